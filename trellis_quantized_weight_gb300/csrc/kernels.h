@@ -53,10 +53,10 @@ bool smem_opt_in(Kernel kernel, int bytes, std::atomic<unsigned long long>& done
 // previous grid has completed and its writes are visible, so stream order is
 // kept for every input and output.
 template <class... Params, class... Args>
-cudaError_t launch_programmatic(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
-                                cudaStream_t stream, Args&&... args) {
+cudaError_t launch_programmatic_grid(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
+                                     cudaStream_t stream, Args&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -66,6 +66,11 @@ cudaError_t launch_programmatic(void (*kernel)(Params...), unsigned grid, unsign
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+template <class... Params, class... Args>
+cudaError_t launch_programmatic(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                                cudaStream_t stream, Args&&... args) {
+    return launch_programmatic_grid(kernel, dim3(grid), block, smem, stream, static_cast<Args&&>(args)...);
 }
 
 // The argument checks of trellis_gemm, in its order (pointers, codes and
@@ -123,6 +128,19 @@ struct CopyBatch {
     unsigned long long count[kCopyBatch];
 };
 int launch_copy_groups(const CopyBatch& batch, int groups, cudaStream_t stream, const DeviceInfo& dev);
+
+// Device of the calling thread, queried once per device.  Returns 0 or a trellis_status.
+int device_info(DeviceInfo& out);
+
+// Paged 8-bit key/value cache (kv_cache.cuh): the checks its operators share,
+// and the view of its tokens that their kernels take.
+constexpr int kKvMaxSeqs = 16384, kKvMaxHeads = 1024;
+int check_kv(const int* starts, const int* kv_len, const int* pages, int tokens, int seqs, int max_q, int page_cols,
+             int num_pages, int q_heads, int kv_heads, int head_dim, int page_size, const void* k_codes,
+             const void* v_codes, const float* k_scales, const float* v_scales);
+struct KvLayout;
+KvLayout kv_layout(const int* starts, const int* kv_len, const int* pages, int tokens, int seqs, int page_cols,
+                   int num_pages, int q_heads, int kv_heads, int page_size);
 
 // Launches one thread whose bounded wait on an mbarrier runs out (nothing
 // arrives), which sets the device error word exactly as a product wait that

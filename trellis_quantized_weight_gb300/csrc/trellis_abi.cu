@@ -14,6 +14,10 @@ using trellis::DeviceInfo;
 
 constexpr int kMaxDevices = 64;
 
+}  // namespace
+
+namespace trellis {
+
 int device_info(DeviceInfo& out) {
     static std::mutex mu;
     static DeviceInfo cache[kMaxDevices];
@@ -34,6 +38,12 @@ int device_info(DeviceInfo& out) {
     out = cache[dev];
     return TRELLIS_OK;
 }
+
+}  // namespace trellis
+
+namespace {
+
+using trellis::device_info;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
