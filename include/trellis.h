@@ -310,6 +310,132 @@ TRELLIS_API int trellis_gemm_packed(const uint16_t *const *xs, const int *rows, 
 TRELLIS_API int trellis_gemm_packed_workspace_size(const int *rows, int groups, int K, int N, int k, int L, int T,
                                                    size_t *bytes);
 
+/* ---- the attention block's cache and adapters ---------------------------------------
+ *
+ * A step's rows ("packed tokens") of several sequences lie one after another;
+ * starts [seqs + 1] (device, int32, starts[0] = 0, starts[seqs] = tokens) says
+ * which are sequence s's.  A sequence may have none.  kv_len [seqs] (device, int32)
+ * is the number of its tokens with this step's, so its last row is position
+ * kv_len - 1; a row whose position comes out negative (an idle slot: one row,
+ * kv_len 0) has no token.
+ *
+ * Paged cache, for keys and for values alike:
+ *   codes   device, e4m3 bytes [num_pages, kv_heads, page_size, head_dim],
+ *           16-byte aligned;
+ *   scales  device, float [num_pages, kv_heads, page_size / 16], a power of two
+ *           for each block of 16 tokens of a page and head.  A stored value is
+ *           code * scale.
+ * Token t of sequence s lies in page pages[s][t / page_size] (device, int32
+ * [seqs, page_cols]) at slot t % page_size.  Every page that the tokens below
+ * kv_len need has to be in the table; page ids outside the pool are clamped into
+ * it and tokens past the table are left out, so that wrong tables give wrong
+ * results but no access outside the arrays.  What unused slots hold does not
+ * matter, NaN codes included.
+ *
+ * Accepted: head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; q_heads a
+ * multiple of kv_heads, at most 1024; 1 <= seqs <= 16384; rows of q, k and v
+ * `stride` elements apart (a multiple of 8, at least heads * head_dim) with the
+ * heads contiguous, 16-byte aligned.  max_q is the number of rows of the
+ * sequence that has most in this step: it shapes the launch only, a wrong one
+ * costs time.  tokens == 0 enqueues nothing and returns TRELLIS_OK.
+ */
+
+/*
+ * trellis_rope_table - cosines and sines of the rotary positions 0 .. rows - 1.
+ *
+ *   table   device, float [rows, rot], 16-byte aligned; row p holds rot / 2
+ *           cosines and then rot / 2 sines, of p times the pair's speed
+ *           base^(-2 i / rot).  rot: a multiple of 16, 16 .. 256.
+ * stretch >= 1 slows the pairs down for longer contexts: all alike when original
+ * is 0; else those that make at most `low` turns over `original` positions by
+ * 1 / stretch, those that make `high` or more not at all, with a linear blend in
+ * between.  gain multiplies every entry.  Angles are fp64, entries rounded once.
+ */
+TRELLIS_API int trellis_rope_table(float *table, int rows, int rot, double base, double stretch, double original,
+                                   double low, double high, double gain, cudaStream_t stream);
+
+/*
+ * trellis_kv_append - rotate a step's queries and keys, and put its keys and
+ * values into the cache.
+ *
+ *   q, k, v   device, bf16 rows of q_heads (kv_heads) heads; q may be NULL (then
+ *             q_out is NULL too).
+ *   rope      device, float [rope_rows, rot] as trellis_rope_table writes it, or
+ *             NULL for no rotation (rope_rows, rot and interleaved are then
+ *             ignored).  The first rot values of each query and key head turn by
+ *             (a, b) -> (a cos - b sin, b cos + a sin), pairs (i, i + rot / 2),
+ *             or (2 i, 2 i + 1) when interleaved.  rot: a multiple of 16, at most
+ *             head_dim.  Positions past the table take its last row.
+ *   q_out     device, bf16 [tokens, q_heads, head_dim]: the rotated queries,
+ *             rounded once (rows without a token: as they are).
+ * A block's scale becomes the smallest power of two s >= 2^-60 with
+ * max|x| <= 448 s over its new tokens, and stays what it was if that is larger and
+ * the block has tokens from before this call; those tokens' codes are rounded
+ * again when it grows.  A NaN or infinity among a block's new values makes its
+ * scale NaN, and with it the whole block.  Earlier tokens are the ones below
+ * kv_len minus the sequence's rows: appending at an earlier position again
+ * (dropping drafted tokens) needs nothing else.
+ * Two sequences of one call must not append to the same page.
+ */
+TRELLIS_API int trellis_kv_append(const uint16_t *q, long long q_stride, const uint16_t *k, long long k_stride,
+                                  const uint16_t *v, long long v_stride, const int *starts, const int *kv_len,
+                                  const int *pages, int tokens, int seqs, int max_q, int page_cols, int num_pages,
+                                  int q_heads, int kv_heads, int head_dim, int page_size, const float *rope,
+                                  int rope_rows, int rot, int interleaved, uint8_t *k_codes, uint8_t *v_codes,
+                                  float *k_scales, float *v_scales, uint16_t *q_out, cudaStream_t stream);
+
+/*
+ * trellis_kv_attention - causal attention of a step's queries over the cache.
+ *
+ *   q       device, bf16 rows of q_heads heads; query head h reads key head
+ *           h / (q_heads / kv_heads).
+ *   scale   factor of the scores (1 / sqrt(head_dim) for most models).
+ *   window  0: a row at position p sees the tokens 0 .. p; w > 0: the last w of them.
+ *   out     device, bf16 [tokens, q_heads, head_dim], rounded once from fp32 sums;
+ *           a row that sees no token is zero.
+ *   workspace  as trellis_gemm_ws: 256-byte aligned, zero-filled before its first
+ *           use, at least trellis_kv_attention_workspace_size bytes; one buffer
+ *           may serve the products too.
+ * The scales of the cache must be powers of two (trellis_kv_append writes no others).
+ * The order of all sums is fixed by the sizes, so equal calls give equal bits.
+ */
+TRELLIS_API int trellis_kv_attention(const uint16_t *q, long long q_stride, const int *starts, const int *kv_len,
+                                     const int *pages, int tokens, int seqs, int max_q, int page_cols, int num_pages,
+                                     int q_heads, int kv_heads, int head_dim, int page_size, float scale, int window,
+                                     const uint8_t *k_codes, const uint8_t *v_codes, const float *k_scales,
+                                     const float *v_scales, uint16_t *out, void *workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+/* Bytes of workspace trellis_kv_attention needs on the current device. */
+TRELLIS_API int trellis_kv_attention_workspace_size(int tokens, int seqs, int max_q, int q_heads, int kv_heads,
+                                                    int head_dim, size_t *bytes);
+
+/*
+ * trellis_lora_add - low-rank adapters of many requests, added to the output of a
+ * projection they share: out[m] = bf16(y[m] + scales[a] * (x[m] A[a]^T) B[a]^T)
+ * with a = which[s] for the rows m of request s (starts[s] .. starts[s + 1] - 1).
+ *
+ *   y, out  device, bf16 [M, N]; out may be y.
+ *   x       device, bf16 [M, K], 16-byte aligned; K a multiple of 8.
+ *   a       device, bf16 [adapters, R, K], 16-byte aligned; b bf16 [adapters, N, R],
+ *           16-byte aligned; R a multiple of 8, at most 128.
+ *   scales  device, float [adapters].
+ *   starts  device, int32 [segments + 1], non-decreasing from 0 to M.
+ *   which   device, int32 [segments]; outside 0 .. adapters - 1: no adapter, and
+ *           the rows of y pass unchanged.
+ *   workspace  256-byte aligned, at least trellis_lora_add_workspace_size bytes;
+ *           its first 1 MiB is not touched, so a product's workspace will do.
+ * M <= 65536 (0: nothing is enqueued), segments <= 65536.  Sums are fp32, with one
+ * rounding of the result.
+ */
+TRELLIS_API int trellis_lora_add(const uint16_t *y, const uint16_t *x, const uint16_t *a, const uint16_t *b,
+                                 const float *scales, const int *starts, const int *which, int M, int K, int N, int R,
+                                 int adapters, int segments, uint16_t *out, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+
+/* Bytes of workspace trellis_lora_add needs on the current device. */
+TRELLIS_API int trellis_lora_add_workspace_size(int M, int K, int N, int R, int adapters, int segments, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

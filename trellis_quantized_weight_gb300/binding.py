@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 from . import build as _build
 
@@ -25,6 +26,8 @@ STATUS = {
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
+_D = ctypes.c_double
 SIGNATURES = {
     "trellis_abi_version": (_I, []),
     "trellis_status_string": (ctypes.c_char_p, [_I]),
@@ -39,6 +42,12 @@ SIGNATURES = {
     "trellis_gemm_gateup_workspace_size": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "trellis_gemm_packed": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "trellis_gemm_packed_workspace_size": (_I, [_P, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "trellis_rope_table": (_I, [_P, _I, _I, _D, _D, _D, _D, _D, _D, _P]),
+    "trellis_kv_append": (_I, [_P, _LL, _P, _LL, _P, _LL, _P, _P, _P, *[_I] * 9, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "trellis_kv_attention": (_I, [_P, _LL, _P, _P, _P, *[_I] * 9, ctypes.c_float, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "trellis_kv_attention_workspace_size": (_I, [*[_I] * 6, ctypes.POINTER(_SZ)]),
+    "trellis_lora_add": (_I, [*[_P] * 7, *[_I] * 6, _P, _P, _SZ, _P]),
+    "trellis_lora_add_workspace_size": (_I, [*[_I] * 6, ctypes.POINTER(_SZ)]),
 }
 
 
@@ -266,3 +275,216 @@ def gemm_packed(xs, codes, scales, k: int, L: int = 12, T: int = 256, outs=None,
                                     ws.data_ptr(), ws.numel(), _stream_handle(xs[0].device, stream))
     _check(rc, "trellis_gemm_packed")
     return outs
+
+
+# ---- the attention block's cache and adapters --------------------------------
+class KVCache(NamedTuple):
+    """A paged key/value cache: e4m3 codes [pages, kv_heads, page_size, head_dim] and, for each
+    16 tokens of a page and head, a power-of-two scale, float32 [pages, kv_heads, page_size / 16].
+    The functions below take any such four tensors in this order."""
+    k: object
+    v: object
+    k_scale: object
+    v_scale: object
+
+
+def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> KVCache:
+    """An empty cache of `pages` pages."""
+    torch = _torch()
+    codes = [torch.zeros((pages, kv_heads, page_size, head_dim), dtype=torch.uint8, device=device)
+             .view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones((pages, kv_heads, page_size // 16), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales)
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, stretch: float = 1.0, original: int = 0,
+               low: float = 1.0, high: float = 32.0, gain: float = 1.0, device="cuda", stream=None):
+    """cos and sin of the rotary positions, float32 [positions, rot], for kv_append.  stretch > 1 slows
+    the pairs for longer contexts: all of them, or with `original` > 0 only those that make few
+    turns over that many positions (fully at `low` turns, not at all from `high` on)."""
+    torch = _torch()
+    if not isinstance(positions, int) or positions < 1 or not isinstance(rot, int) or rot < 1:
+        raise ValueError("positions and rot must be positive ints")
+    table = torch.empty((positions, rot), dtype=torch.float32, device=device)
+    if not table.is_cuda:
+        raise ValueError("device must be a CUDA device")
+    _check(load().trellis_rope_table(table.data_ptr(), positions, rot, base, stretch, float(original), low, high, gain,
+                                     _stream_handle(table.device, stream)), "trellis_rope_table")
+    return table
+
+
+def _require_rows(t, name, device):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a bfloat16 [tokens, heads, head_dim] tensor")
+    d = t.shape[2]
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+
+
+def _row_stride(t):
+    # the stride of a single row is arbitrary: the row's own length then
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _require_cache(cache, starts, kv_len, pages):
+    """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns)."""
+    torch = _torch()
+    k, v, ks, vs = cache
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise ValueError("the cache must be CUDA tensors")
+    dev = k.device
+    shape = k.shape
+    if k.dim() != 4 or v.shape != shape or k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+        raise ValueError("cache codes must be float8_e4m3fn [pages, kv_heads, page_size, head_dim]")
+    want = (shape[0], shape[1], shape[2] // 16)
+    if ks.shape != want or vs.shape != want or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise ValueError("cache scales must be float32 [pages, kv_heads, page_size / 16]")
+    if v.device != dev or ks.device != dev or vs.device != dev:
+        raise ValueError("the cache must be on one device")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("the cache must be contiguous")
+    i32 = torch.int32
+    for name, t in (("starts", starts), ("kv_len", kv_len), ("pages", pages)):
+        if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != i32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
+    seqs = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    if starts.dim() != 1 or pages.dim() != 2 or seqs < 0 or starts.shape[0] != seqs + 1 or pages.shape[0] != seqs:
+        raise ValueError("starts must be [S + 1], kv_len [S] and pages [S, columns]")
+    return shape, seqs, pages.shape[1]
+
+
+def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved: bool = False, max_q=None, q_out=None,
+              stream=None):
+    """Put a step's keys and values into the paged cache, rotated on the way, and return its rotated
+    queries (None without q).
+
+    k, v: bf16 [tokens, kv_heads, head_dim]; q: bf16 [tokens, q_heads, head_dim] (rows may be
+    strided, as slices of one projection's output are).  starts int32 [S + 1]: the rows of each
+    sequence; kv_len int32 [S]: its tokens with these; pages int32 [S, columns]: its pages.
+    rope: float32 [positions, rot] from rope_table, or None.  max_q: rows of the sequence that
+    has most (a hint).  The cache is updated in place."""
+    torch = _torch()
+    (num_pages, hk, page, d), seqs, cols = _require_cache(cache, starts, kv_len, pages)
+    dev = starts.device
+    _require_rows(k, "k", dev)
+    _require_rows(v, "v", dev)
+    tokens = k.shape[0]
+    if tuple(k.shape) != (tokens, hk, d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [tokens, {hk}, {d}]")
+    hq, q_ptr, q_stride = hk, None, 0
+    if q is not None:
+        _require_rows(q, "q", dev)
+        hq = q.shape[1]
+        if q.shape[0] != tokens or q.shape[2] != d:
+            raise ValueError(f"q must be [{tokens}, heads, {d}]")
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=dev)
+        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or q_out.device != dev or not q_out.is_contiguous():
+            raise ValueError("q_out must be a contiguous bfloat16 tensor of q's shape")
+        q_ptr, q_stride = q.data_ptr(), _row_stride(q)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope_ptr, rows, rot = None, 0, 0
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor) or rope.device != dev or rope.dtype != torch.float32 or rope.dim() != 2 \
+                or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 [positions, rot] tensor")
+        rope_ptr, (rows, rot) = rope.data_ptr(), rope.shape
+    if seqs == 0 or tokens == 0:
+        return q_out
+    rc = load().trellis_kv_append(
+        q_ptr, q_stride, k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), starts.data_ptr(),
+        kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, tokens if max_q is None else max_q, cols, num_pages, hq, hk, d,
+        page, rope_ptr, rows, rot, 1 if interleaved else 0, cache[0].data_ptr(), cache[1].data_ptr(),
+        cache[2].data_ptr(), cache[3].data_ptr(), q_out.data_ptr() if q is not None else None,
+        _stream_handle(dev, stream))
+    _check(rc, "trellis_kv_append")
+    return q_out
+
+
+def kv_attention_workspace_bytes(tokens, seqs, max_q, q_heads, kv_heads, head_dim) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().trellis_kv_attention_workspace_size(tokens, seqs, max_q, q_heads, kv_heads, head_dim,
+                                                      ctypes.byref(n)), "trellis_kv_attention_workspace_size")
+    return int(n.value)
+
+
+def kv_attention(q, cache, starts, kv_len, pages, scale=None, window: int = 0, max_q=None, out=None, stream=None):
+    """Causal attention of a step's queries over the paged cache: bf16 [tokens, q_heads, head_dim].
+
+    q: bf16 [tokens, q_heads, head_dim], rows may be strided; the rest as kv_append, whose
+    tokens the cache holds by now.  scale: of the scores, 1 / sqrt(head_dim) by default;
+    window: how many tokens a row sees, itself included (0: all before it)."""
+    torch = _torch()
+    (num_pages, hk, page, d), seqs, cols = _require_cache(cache, starts, kv_len, pages)
+    dev = starts.device
+    _require_rows(q, "q", dev)
+    tokens, hq = q.shape[0], q.shape[1]
+    if q.shape[2] != d:
+        raise ValueError(f"q must be [tokens, heads, {d}]")
+    if out is None:
+        out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=dev)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
+    if seqs == 0 or tokens == 0:
+        return out
+    most = tokens if max_q is None else max_q
+    ws = _workspace(dev, kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), stream)
+    rc = load().trellis_kv_attention(
+        q.data_ptr(), _row_stride(q), starts.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, most, cols,
+        num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
+        cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream_handle(dev, stream))
+    _check(rc, "trellis_kv_attention")
+    return out
+
+
+def lora_add_workspace_bytes(M, K, N, R, adapters, segments) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().trellis_lora_add_workspace_size(M, K, N, R, adapters, segments, ctypes.byref(n)),
+           "trellis_lora_add_workspace_size")
+    return int(n.value)
+
+
+def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
+    """y + scales[w] * (x A[w]^T) B[w]^T for each request's adapter w: bf16 [M, N].
+
+    y: bf16 [M, N], the output of the projection that the requests share; x: bf16 [M, K], its
+    input; a: bf16 [adapters, R, K]; b: bf16 [adapters, N, R]; scales: float32 [adapters].
+    starts int32 [S + 1]: the rows of each request; which int32 [S]: its adapter, -1 for none.
+    out may be y."""
+    torch = _torch()
+    bf16 = (torch.bfloat16,)
+    _require(y, "y", bf16, 2)
+    _require(x, "x", bf16, 2)
+    _require(a, "a", bf16, 3)
+    _require(b, "b", bf16, 3)
+    _require(scales, "scales", (torch.float32,), 1)
+    _require(starts, "starts", (torch.int32,), 1)
+    _require(which, "which", (torch.int32,), 1)
+    (M, N), K = y.shape, x.shape[1]
+    n_ad, R = a.shape[0], a.shape[1]
+    segments = which.shape[0]
+    if x.shape[0] != M or tuple(a.shape) != (n_ad, R, K) or tuple(b.shape) != (n_ad, N, R) or scales.shape[0] != n_ad:
+        raise ValueError("y must be [M, N], x [M, K], a [adapters, R, K], b [adapters, N, R] and scales [adapters]")
+    if starts.shape[0] != segments + 1:
+        raise ValueError("starts must be [S + 1] with which [S]")
+    if any(t.device != y.device for t in (x, a, b, scales, starts, which)):
+        raise ValueError("all tensors must be on one device")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=y.device)
+    else:
+        _require(out, "out", bf16, 2)
+        if out.shape != y.shape or out.device != y.device:
+            raise ValueError("out must be [M, N] on y's device")
+    if M == 0:
+        return out
+    ws = _workspace(y.device, lora_add_workspace_bytes(M, K, N, R, n_ad, segments), stream)
+    rc = load().trellis_lora_add(y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(),
+                                 starts.data_ptr(), which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), _stream_handle(y.device, stream))
+    _check(rc, "trellis_lora_add")
+    return out

@@ -1,0 +1,567 @@
+// Attention over the paged 8-bit cache for few query rows: the form for single
+// tokens and short drafts.
+//
+//   out[i] = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale * q_i . k_j),
+//   over the cached tokens j that row i sees (pos_i - window < j <= pos_i).
+//
+// What bounds it: 2 D bytes of codes a cached token and key head, each read once
+// and used by the head group's few rows, so HBM.  Everything else is arranged
+// around a long stream of 16-byte loads:
+//
+// * Work: a unit is (sequence, NT * 8 query rows of one key head's group, key
+//   head); its tokens are cut into tiles of 16 tokens a warp.  All units' tiles
+//   in a row are dealt to the CTAs in equal contiguous shares, whatever the
+//   lengths, so a CTA holds at most two pieces of units that others share.  The
+//   pieces' sums meet in the workspace; the CTA that finishes last adds them in
+//   CTA order (the same order on every run).
+// * Loads: each lane copies the codes that it will itself use from the cache into
+//   its own slots of a ring in shared memory (cp.async), several steps ahead.
+//   Reading them back needs no barrier and has no bank conflict.
+// * Products: S^T = K Q^T and O^T = V^T P^T on m16n8k16 with f16 operands and fp32
+//   sums.  e4m3 -> f16 is exact.  The order of a sum's terms is free, so a lane's 16
+//   consecutive bytes of a key serve as its operand of four products, the query
+//   fragments being loaded in the same order; the values of two tokens are paired
+//   by byte permutes.  Keys take the 16-row side, so a group of up to 8 rows
+//   pays for 8.  (These products are a few per cent of the tensor rate: at 2 D bytes
+//   a token the legacy matrix instruction is far from being the limit.)
+// * Scales: a power of two times a score is exact.  The key block's scale multiplies
+//   the scores; the value block's is added to them as its log2, so that
+//   p' = p * v_scale comes out of the exponential and no further multiplication
+//   is needed; the denominators add p' / v_scale.
+// * Running maximum: p' is taken against a reference that is only moved when a score
+//   exceeds it by 2^8, so a step has one vote instead of reductions.  p' <= 2^8 in
+//   f16 (11 significant bits, relative to the largest) is the one rounding
+//   between q, k, v and the fp32 sums; queries enter as f16 times a power of
+//   two per row, which is exact for bf16 down to 2^-24 of the row's largest.
+#include <cfloat>
+
+#include "kv_attention.cuh"
+#include "trellis.h"
+
+namespace trellis {
+
+namespace {
+
+constexpr float kMoveBy = 8.0f;          // the reference moves when exceeded by 2^8
+
+// Warps of a CTA and ring steps by head width: about 160 KB in flight an SM.
+template <int D> struct StreamShape;
+template <> struct StreamShape<64>  { static constexpr int kWarps = 8, kSteps = 8; };
+template <> struct StreamShape<128> { static constexpr int kWarps = 8, kSteps = 5; };
+template <> struct StreamShape<256> { static constexpr int kWarps = 8, kSteps = 3; };
+
+template <int D, int NT>
+struct Stream {
+    static constexpr int kWarps = StreamShape<D>::kWarps;
+    static constexpr int kSteps = StreamShape<D>::kSteps;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kRows = 8 * NT;                 // query rows of a unit
+    static constexpr int kTile = kKvBlock * kWarps;      // cached tokens of a tile
+    static constexpr int kStepBytes = 2 * kKvBlock * D;  // codes of one warp's step
+    static constexpr int kRing = kWarps * kSteps * kStepBytes;
+    static constexpr int kScaleOff = kRing;              // [warps][steps][2] floats
+    static constexpr int kScanOff = kScaleOff + kWarps * kSteps * 8;
+    static constexpr int kSmem = kScanOff + 256;
+    // after a unit's last step the ring holds the warps' sums: O [rows][D], then m, l
+    static constexpr int kPart = kRows * D + 2 * kRows;  // floats of a partial result
+    static_assert(kWarps * kPart * 4 <= kRing, "the warps' sums fit the ring");
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Unit {
+    int seq, head, qt;        // query tile
+    int start, n, p0;         // packed rows, and the first one's position
+    int lo, hi;               // cached tokens [lo, hi) that its rows see (lo a multiple of 16)
+    int tiles;
+};
+
+// Query tiles of a sequence with n rows, and the token range of one of them.
+template <int D, int NT>
+__device__ __forceinline__ int unit_tiles(const AttendArgs& a, int n, int total, int p0, int qt, int* lo, int* hi) {
+    using S = Stream<D, NT>;
+    const int g = a.group;
+    const int first = qt * S::kRows / g, last = min(n - 1, (qt * S::kRows + S::kRows - 1) / g);
+    *hi = max(0, min(total, p0 + last + 1));
+    const int low = a.window > 0 ? max(0, p0 + first + 1 - a.window) : 0;
+    *lo = low & ~(kKvBlock - 1);
+    const int span = *hi - *lo;
+    return span > 0 ? (span + S::kTile - 1) / S::kTile : 1;   // an empty unit still writes its zeros
+}
+
+template <int D, int NT>
+__device__ long long seq_tiles(const AttendArgs& a, int s) {
+    int start, n;
+    if (!kv_rows(a.l, s, &start, &n)) return 0;
+    const int total = kv_total(a.l, s), p0 = __ldg(a.l.kv_len + s) - n;
+    const int qts = (n * a.group + Stream<D, NT>::kRows - 1) / Stream<D, NT>::kRows;
+    long long sum = 0;
+    for (int qt = 0; qt < qts; ++qt) {
+        int lo, hi;
+        sum += unit_tiles<D, NT>(a, n, total, p0, qt, &lo, &hi);
+    }
+    return sum * a.l.kv_heads;
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void load_unit(const AttendArgs& a, Unit& u) {
+    kv_rows(a.l, u.seq, &u.start, &u.n);
+    u.p0 = __ldg(a.l.kv_len + u.seq) - u.n;
+    u.tiles = unit_tiles<D, NT>(a, u.n, kv_total(a.l, u.seq), u.p0, u.qt, &u.lo, &u.hi);
+}
+
+// The unit after u (heads, then query tiles, then sequences); the caller knows there is one.
+template <int D, int NT>
+__device__ __forceinline__ void next_unit(const AttendArgs& a, Unit& u) {
+    if (++u.head < a.l.kv_heads) return;                       // the same rows and tokens
+    u.head = 0;
+    if (++u.qt * Stream<D, NT>::kRows >= u.n * a.group) {
+        u.qt = 0;
+        int start, n;
+        do { ++u.seq; } while (u.seq < a.l.seqs && !kv_rows(a.l, u.seq, &start, &n));
+        if (u.seq >= a.l.seqs) { u.seq = a.l.seqs - 1; return; }
+    }
+    load_unit<D, NT>(a, u);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(const __grid_constant__ AttendArgs a) {
+    using S = Stream<D, NT>;
+    constexpr int KJ = D / 64;                  // 16-byte loads of a key row a lane
+    constexpr int VJ = D >= 128 ? D / 128 : 1;  // loads of a value row a lane (8 bytes at D = 64)
+    constexpr int MT = D / 16;                  // 16-row tiles of O^T
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    griddep_wait();
+
+    // ---- this CTA's share of all units' tiles -------------------------------------------
+    // prefix sums over the sequences, a contiguous chunk a thread
+    long long* scan = reinterpret_cast<long long*>(smem + S::kScanOff);   // warps' sums, then the answer
+    const int per = (a.l.seqs + S::kThreads - 1) / S::kThreads;
+    const int s0 = min(a.l.seqs, static_cast<int>(threadIdx.x) * per), s1 = min(a.l.seqs, s0 + per);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += seq_tiles<D, NT>(a, s);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < S::kWarps; ++w) {
+        if (w < warp) before += scan[w];
+        all += scan[w];
+    }
+    const long long ctas = min(static_cast<long long>(gridDim.x), all);
+    const long long cta = blockIdx.x;
+    if (cta >= ctas) { griddep_launch_dependents(); return; }
+    const long long begin = cta * all / ctas, end = (cta + 1) * all / ctas;
+    // the thread whose sequences hold tile `begin` finds the unit
+    int* found = reinterpret_cast<int*>(smem + S::kScanOff + 8 * S::kWarps);   // seq, qt, head, tile
+    long long at = before + incl - mine;
+    if (begin >= at && begin < at + mine) {
+        int s = s0;
+        long long c = seq_tiles<D, NT>(a, s);
+        while (begin >= at + c) { at += c; c = seq_tiles<D, NT>(a, ++s); }
+        int start, n, lo, hi, qt = 0;
+        kv_rows(a.l, s, &start, &n);
+        const int total = kv_total(a.l, s), p0 = __ldg(a.l.kv_len + s) - n;
+        int off = static_cast<int>(begin - at);
+        int tl = unit_tiles<D, NT>(a, n, total, p0, 0, &lo, &hi);
+        while (off >= tl * a.l.kv_heads) {
+            off -= tl * a.l.kv_heads;
+            tl = unit_tiles<D, NT>(a, n, total, p0, ++qt, &lo, &hi);
+        }
+        found[0] = s; found[1] = qt; found[2] = off / tl; found[3] = off % tl;
+    }
+    __syncthreads();
+    Unit u;
+    u.seq = found[0]; u.qt = found[1]; u.head = found[2];
+    load_unit<D, NT>(a, u);
+    int tile0 = found[3];
+    __syncthreads();                            // the ring and the scan area are free from here on
+
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kSteps * S::kStepBytes;
+    const uint32_t ring_sc = static_cast<uint32_t>(__cvta_generic_to_shared(smem + S::kScaleOff)) + warp * S::kSteps * 8;
+    float* part_smem = reinterpret_cast<float*>(smem);
+
+    for (long long done = begin; done < end;) {
+        const int tile1 = static_cast<int>(min(static_cast<long long>(u.tiles), tile0 + (end - done)));
+        // blocks of this warp: first, first + warps, ...
+        const int blocks = (u.hi - u.lo + kKvBlock - 1) / kKvBlock;          // <= 0: nothing to see
+        const int b_first = tile0 * S::kWarps + warp;
+        const int b_end = min(tile1 * S::kWarps, blocks);
+        const int steps = b_first < b_end ? (b_end - b_first + S::kWarps - 1) / S::kWarps : 0;
+        const int blk0 = u.lo / kKvBlock;
+
+        // ---- queries: f16 fragments, each row times a power of two --------------------
+        uint32_t qf[NT][4 * KJ][2];
+        float qmul[NT][2];                      // of this lane's two columns (rows 2t, 2t + 1 of each 8)
+        int limit[NT][2], lower[NT][2];         // cached tokens [lower, limit) that they see
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = u.qt * S::kRows + nt * 8 + g;
+            const int tok = r / a.group;
+            const bool live = tok < u.n;
+            const uint16_t* row = a.q + static_cast<size_t>(u.start + (live ? tok : 0)) * a.q_stride +
+                                  (static_cast<size_t>(u.head) * a.group + r % a.group) * D;
+            uint32_t raw[KJ][8];
+            uint32_t most = 0u;
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+                if (live) {
+                    v0 = __ldg(reinterpret_cast<const uint4*>(row) + 2 * (t + 4 * j));
+                    v1 = __ldg(reinterpret_cast<const uint4*>(row) + 2 * (t + 4 * j) + 1);
+                }
+                const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    raw[j][i] = w[i];
+                    most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                }
+            }
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            const int e = query_exponent(most);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int j = 0; j < KJ; ++j)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t v = raw[j][2 * w + h];
+                        qf[nt][4 * j + w][h] = f32_to_f16x2(bf16_lo(v) * down, bf16_hi(v) * down);
+                    }
+            // the column's factor, from the lane that holds its row
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                qmul[nt][h] = __shfl_sync(0xffffffffu, up, (2 * t + h) * 4);
+                const int tk = min((u.qt * S::kRows + nt * 8 + 2 * t + h) / a.group, u.n - 1);
+                limit[nt][h] = min(u.hi, u.p0 + tk + 1);
+                lower[nt][h] = a.window > 0 ? u.p0 + tk + 1 - a.window : 0;
+            }
+        }
+        // tokens that every row sees
+        const int all_hi = min(u.hi, u.p0 + u.qt * S::kRows / a.group + 1);
+        const int all_lo = a.window > 0
+            ? u.p0 + min((u.qt * S::kRows + S::kRows - 1) / a.group, u.n - 1) + 1 - a.window : 0;
+
+        // ---- the stream ---------------------------------------------------------------
+        const int shift = a.l.page_shift - 4;
+        auto page_of = [&](int i) {             // of this warp's step i
+            return kv_page(a.l, u.seq, (blk0 + b_first + i * S::kWarps) >> shift);
+        };
+        auto issue = [&](int i, int page) {     // start the copies of step i
+            const int blk = blk0 + b_first + i * S::kWarps;
+            const int in_page = blk & ((1 << shift) - 1);
+            const size_t unit = static_cast<size_t>(page) * a.l.kv_heads + u.head;
+            const size_t off = (unit * a.l.page_size + in_page * kKvBlock) * D;
+            const uint32_t dst = ring + (i % S::kSteps) * S::kStepBytes;
+            const uint8_t* k = a.k_codes + off;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int j = 0; j < KJ; ++j)
+                    cp_async16(dst + (r * KJ + j) * 512 + lane * 16, k + (g + 8 * r) * D + (t + 4 * j) * 16);
+            const uint8_t* v = a.v_codes + off;
+            const uint32_t vdst = dst + kKvBlock * D;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {       // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+                const int tok = 2 * t + (r & 1) + (r >> 1) * 8;
+                if constexpr (D == 64) {
+                    cp_async8(vdst + r * 256 + lane * 8, v + tok * D + g * 8);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VJ; ++j)
+                        cp_async16(vdst + (r * VJ + j) * 512 + lane * 16, v + tok * D + (g + 8 * j) * 16);
+                }
+            }
+            const size_t sc = unit * (a.l.page_size / kKvBlock) + in_page;
+            if (lane < 2) cp_async4(ring_sc + (i % S::kSteps) * 8 + lane * 4, (lane == 0 ? a.k_scales : a.v_scales) + sc);
+        };
+
+        float o[NT][MT][4];
+        float m[NT][2], sum[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            sum[nt][0] = sum[nt][1] = 0.0f;
+        }
+
+        int page_next = 0;
+#pragma unroll
+        for (int i = 0; i < S::kSteps - 1; ++i) {
+            if (i < steps) issue(i, page_of(i));
+            cp_async_commit();
+        }
+        if (S::kSteps - 1 < steps) page_next = page_of(S::kSteps - 1);
+
+        for (int i = 0; i < steps; ++i) {
+            __syncwarp();                       // every lane has read the slot that is filled now
+            if (i + S::kSteps - 1 < steps) issue(i + S::kSteps - 1, page_next);
+            cp_async_commit();
+            if (i + S::kSteps < steps) page_next = page_of(i + S::kSteps);
+            cp_async_wait<S::kSteps - 1>();
+            __syncwarp();                       // the scales were copied by lanes 0 and 1
+            const uint32_t src = ring + (i % S::kSteps) * S::kStepBytes;
+            float ks, vs;
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs)
+                         : "r"(ring_sc + (i % S::kSteps) * 8) : "memory");
+            const int tok0 = (blk0 + b_first + i * S::kWarps) * kKvBlock;
+
+            // scores: two chains of products
+            float sc[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sc[nt][h][j] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                const uint4 ka = lds128(src + j * 512 + lane * 16);
+                const uint4 kb = lds128(src + (KJ + j) * 512 + lane * 16);
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16x2(wa[w], a0, a2);
+                    e4m3x4_to_f16x2(wb[w], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(sc[nt][w & 1], a0, a1, a2, a3, qf[nt][4 * j + w][0], qf[nt][4 * j + w][1]);
+                }
+            }
+            const float lv = pow2_log2(vs), iv = pow2_recip(vs);
+            const bool edge = tok0 + kKvBlock > all_hi || tok0 < all_lo;
+            bool over = false;
+            float x[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int h = j & 1;
+                    x[nt][j] = fmaf(sc[nt][0][j] + sc[nt][1][j], qmul[nt][h] * ks, lv);
+                    if (edge) {
+                        const int tok = tok0 + g + (j >> 1) * 8;
+                        if (tok >= limit[nt][h] || tok < lower[nt][h]) x[nt][j] = -INFINITY;
+                    }
+                    over |= x[nt][j] > m[nt][h] + kMoveBy;
+                }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float top = fmaxf(x[nt][h], x[nt][h + 2]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        top = fmaxf(top, m[nt][h]);
+                        const float f = m[nt][h] == -INFINITY ? 0.0f : exp2_approx(m[nt][h] - top);
+                        m[nt][h] = top;
+                        sum[nt][h] *= f;
+#pragma unroll
+                        for (int q = 0; q < MT; ++q) { o[nt][q][h] *= f; o[nt][q][h + 2] *= f; }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
+                const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+                const float p0 = exp2_approx(x[nt][0] - m0), p1 = exp2_approx(x[nt][1] - m1);
+                const float p2 = exp2_approx(x[nt][2] - m0), p3 = exp2_approx(x[nt][3] - m1);
+                sum[nt][0] = fmaf(p0 + p2, iv, sum[nt][0]);
+                sum[nt][1] = fmaf(p1 + p3, iv, sum[nt][1]);
+                pf[nt][0] = movmatrix_trans(f32_to_f16x2(p0, p1));
+                pf[nt][1] = movmatrix_trans(f32_to_f16x2(p2, p3));
+            }
+            // slots past the last token may hold anything, NaN too: their values count as 0
+            const bool tail = tok0 + kKvBlock > u.hi;
+            const uint32_t vsrc = src + kKvBlock * D;
+            auto products = [&](int q, const uint32_t (&w)[4]) {       // 4 values of 4 tokens: tiles 2q, 2q + 1
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16x2(__byte_perm(w[0], w[1], sel), a0, a1);
+                    e4m3x4_to_f16x2(__byte_perm(w[2], w[3], sel), a2, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * q + h], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                }
+            };
+            bool keep[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) keep[r] = !tail || tok0 + 2 * t + (r & 1) + (r >> 1) * 8 < u.hi;
+            if constexpr (D == 64) {
+                uint32_t w[2][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint2 v = lds64(vsrc + r * 256 + lane * 8);
+                    w[0][r] = keep[r] ? v.x : 0u;
+                    w[1][r] = keep[r] ? v.y : 0u;
+                }
+                products(0, w[0]);
+                products(1, w[1]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VJ; ++j) {
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint4 v = lds128(vsrc + (r * VJ + j) * 512 + lane * 16);
+                        w[0][r] = keep[r] ? v.x : 0u;
+                        w[1][r] = keep[r] ? v.y : 0u;
+                        w[2][r] = keep[r] ? v.z : 0u;
+                        w[3][r] = keep[r] ? v.w : 0u;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) products(4 * j + q, w[q]);
+                }
+            }
+        }
+        cp_async_wait<0>();
+
+        // ---- the warps' sums meet ---------------------------------------------------------
+        __syncthreads();                        // every warp is done with its ring
+        {
+            float* mine_o = part_smem + warp * S::kPart;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float l = sum[nt][h];
+                    l += __shfl_xor_sync(0xffffffffu, l, 4);
+                    l += __shfl_xor_sync(0xffffffffu, l, 8);
+                    l += __shfl_xor_sync(0xffffffffu, l, 16);
+                    const int row = nt * 8 + 2 * t + h;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        // tile i, row g: the value index that load and permute gave it
+                        const int d = D == 64 ? 8 * g + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
+                        mine_o[row * D + d] = o[nt][i][h];
+                        mine_o[row * D + d + 1] = o[nt][i][h + 2];
+                    }
+                    if (g == 0) {
+                        mine_o[S::kRows * D + row] = m[nt][h];
+                        mine_o[S::kRows * D + S::kRows + row] = l;
+                    }
+                }
+        }
+        __syncthreads();
+        const bool whole = tile0 == 0 && tile1 == u.tiles;
+        // where the unit's pieces go: CTA c's slot 2c when the unit began before it, else 2c + 1
+        float* slot = a.partials + (2 * cta + (tile0 == 0 ? 1 : 0)) * S::kPart;
+        const int rows = min(S::kRows, u.n * a.group - u.qt * S::kRows);
+        for (int e = threadIdx.x; e < rows * D; e += S::kThreads) {
+            const int row = e / D, d = e % D;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, part_smem[w * S::kPart + S::kRows * D + row]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float acc = 0.0f, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) {
+                const float* p = part_smem + w * S::kPart;
+                const float f = exp2_approx(p[S::kRows * D + row] - ref);
+                acc = fmaf(p[row * D + d], f, acc);
+                l = fmaf(p[S::kRows * D + S::kRows + row], f, l);
+            }
+            if (whole) {
+                store_row(a, u.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
+            } else {
+                slot[row * D + d] = acc;
+                if (d == 0) {
+                    slot[S::kRows * D + row] = top;
+                    slot[S::kRows * D + S::kRows + row] = l;
+                }
+            }
+        }
+        if (!whole) {
+            // the CTAs that hold the unit's first and last tile
+            const long long f0 = done - tile0, f1 = f0 + u.tiles - 1;
+            auto holder = [&](long long tile) {
+                long long c = tile * ctas / all;
+                while (c + 1 < ctas && (c + 1) * all / ctas <= tile) ++c;
+                while (c > 0 && c * all / ctas > tile) --c;
+                return c;
+            };
+            const long long c0 = holder(f0), c1 = holder(f1);
+            __threadfence();
+            __syncthreads();
+            int* ticket = reinterpret_cast<int*>(smem + S::kScanOff);
+            if (threadIdx.x == 0) {
+                const unsigned int pieces = static_cast<unsigned int>(c1 - c0 + 1);
+                const unsigned int got = atomicAdd(a.counters + c0, 1u);
+                if (got == pieces - 1) a.counters[c0] = 0u;      // left ready for the next call
+                *ticket = got == pieces - 1;
+            }
+            __syncthreads();
+            if (*ticket) {
+                __threadfence();
+                for (int e = threadIdx.x; e < rows * D; e += S::kThreads) {
+                    const int row = e / D, d = e % D;
+                    float top = -INFINITY, acc = 0.0f, l = 0.0f;
+                    for (long long c = c0; c <= c1; ++c) {
+                        const float* p = a.partials + (2 * c + (c == c0 ? 1 : 0)) * S::kPart;
+                        const float pm = __ldcg(p + S::kRows * D + row);
+                        const float to = fmaxf(top, pm), ref = to == -INFINITY ? 0.0f : to;
+                        const float f = exp2_approx(top - ref), fp = exp2_approx(pm - ref);
+                        acc = fmaf(acc, f, __ldcg(p + row * D + d) * fp);
+                        l = fmaf(l, f, __ldcg(p + S::kRows * D + S::kRows + row) * fp);
+                        top = to;
+                    }
+                    store_row(a, u.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
+                }
+            }
+        }
+        __syncthreads();                        // the sums are read before the next unit's copies land
+        done += tile1 - tile0;
+        if (done < end) {
+            next_unit<D, NT>(a, u);
+            tile0 = 0;
+        }
+    }
+    griddep_launch_dependents();
+}
+
+template <int D, int NT>
+int launch(const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+    using S = Stream<D, NT>;
+    static std::atomic<unsigned long long> opted{0};
+    if (!smem_opt_in(kv_stream_kernel<D, NT>, S::kSmem, opted)) return TRELLIS_ERR_CUDA;
+    const cudaError_t e = launch_programmatic(kv_stream_kernel<D, NT>, static_cast<unsigned>(dev.num_sms),
+                                              static_cast<unsigned>(S::kThreads), S::kSmem, stream, a);
+    return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
+}
+
+// Rows of a unit: 16 where a sequence has more than 8 rows to a key head, except
+// at D = 256, whose sums for 16 rows do not fit the registers.
+bool two_tiles(int head_dim, int rows) { return rows > 8 && head_dim < 256; }
+
+}  // namespace
+
+size_t kv_stream_workspace_bytes(int head_dim, int rows, const DeviceInfo& dev) {
+    const size_t unit_rows = two_tiles(head_dim, rows) ? 16 : 8;
+    return kKvCounterBytes + static_cast<size_t>(dev.num_sms) * 2 * (unit_rows * head_dim + 2 * unit_rows) * 4;
+}
+
+int launch_kv_stream(const AttendArgs& a, int head_dim, int rows, const DeviceInfo& dev, cudaStream_t stream) {
+    const bool two = two_tiles(head_dim, rows);
+    if (head_dim == 64) return two ? launch<64, 2>(a, dev, stream) : launch<64, 1>(a, dev, stream);
+    if (head_dim == 128) return two ? launch<128, 2>(a, dev, stream) : launch<128, 1>(a, dev, stream);
+    return launch<256, 1>(a, dev, stream);
+}
+
+}  // namespace trellis
