@@ -73,16 +73,8 @@ def test_lora_refuses(lib, change, want):
     assert lib.trellis_lora_add(*{**LORA, **change}.values()) == want
 
 
-@pytest.mark.parametrize("args,want", [
-    ((0, 8, 64, 1e4, 1.0, 0.0, 1.0, 32.0, 1.0), -2), ((8, 0, 64, 1e4, 1.0, 0.0, 1.0, 32.0, 1.0), None),
-    ((8, 24, 0, 1e4, 1.0, 0.0, 1.0, 32.0, 1.0), None)])
-def test_rope_table_refuses_sizes(lib, args, want):
-    rows, rot = args[0], args[1]
-    assert lib.trellis_rope_table(P, rows, rot, *args[3:]) == (want if want is not None else -3)
-
-
 @pytest.mark.parametrize("change,want", [
-    (dict(table=0), -1), (dict(base=0.0), -2), (dict(base=float("nan")), -2), (dict(stretch=0.5), -2),
+    (dict(table=0), -1), (dict(rows=0), -2), (dict(base=0.0), -2), (dict(base=float("nan")), -2), (dict(stretch=0.5), -2),
     (dict(original=-1.0), -2), (dict(gain=0.0), -2), (dict(gain=float("inf")), -2), (dict(original=100.0, low=2.0, high=2.0), -2),
     (dict(rot=264), -3), (dict(rot=8), -3), (dict(table=P + 4), -4)])
 def test_rope_table_refuses(lib, change, want):
