@@ -149,5 +149,7 @@ int launch_wait_selftest(cudaStream_t stream);
 // Reads and clears the tensor-core kernel's device error word (bit 0: a
 // bounded wait gave up).  Returns 0 or a trellis_status.
 int tc_take_device_error(unsigned int* flags);
+// The same for the attention kernel on the tensor cores.
+int kv_take_device_error(unsigned int* flags);
 
 }  // namespace trellis

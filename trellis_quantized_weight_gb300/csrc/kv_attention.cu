@@ -17,6 +17,17 @@ int rows_of(int tokens, int max_q, int q_heads, int kv_heads) {
     return r > (1 << 30) ? 1 << 30 : static_cast<int>(r < 1 ? 1 : r);
 }
 
+// The tensor-core kernel where a sequence has more rows to a key head than one unit
+// of the streaming kernel.
+bool on_tensor_cores(int head_dim, int rows) { return rows > (head_dim < 256 ? 16 : 8); }
+
+size_t workspace_bytes_of(int tokens, int seqs, int rows, int q_heads, int kv_heads, int head_dim,
+                          const DeviceInfo& dev) {
+    return on_tensor_cores(head_dim, rows)
+               ? trellis::kv_tile_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim, dev)
+               : trellis::kv_stream_workspace_bytes(head_dim, rows, dev);
+}
+
 }  // namespace
 
 extern "C" {
@@ -31,7 +42,7 @@ int trellis_kv_attention_workspace_size(int tokens, int seqs, int max_q, int q_h
     DeviceInfo dev;
     const int rc = trellis::device_info(dev);
     if (rc != TRELLIS_OK) return rc;
-    *bytes = trellis::kv_stream_workspace_bytes(head_dim, rows_of(tokens, max_q, q_heads, kv_heads), dev);
+    *bytes = workspace_bytes_of(tokens, seqs, rows_of(tokens, max_q, q_heads, kv_heads), q_heads, kv_heads, head_dim, dev);
     return TRELLIS_OK;
 }
 
@@ -52,7 +63,8 @@ int trellis_kv_attention(const uint16_t* q, long long q_stride, const int* start
     rc = device_info(dev);
     if (rc != TRELLIS_OK) return rc;
     const int rows = rows_of(tokens, max_q, q_heads, kv_heads);
-    if (workspace == nullptr || workspace_bytes < kv_stream_workspace_bytes(head_dim, rows, dev))
+    if (workspace == nullptr ||
+        workspace_bytes < workspace_bytes_of(tokens, seqs, rows, q_heads, kv_heads, head_dim, dev))
         return TRELLIS_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
     if (tokens == 0) return TRELLIS_OK;
@@ -66,7 +78,8 @@ int trellis_kv_attention(const uint16_t* q, long long q_stride, const int* start
     a.out = out;
     a.counters = static_cast<unsigned int*>(workspace);
     a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kKvCounterBytes);
-    return launch_kv_stream(a, head_dim, rows, dev, stream);
+    return on_tensor_cores(head_dim, rows) ? launch_kv_tile(a, head_dim, dev, stream)
+                                           : launch_kv_stream(a, head_dim, rows, dev, stream);
 }
 
 }  // extern "C"

@@ -55,5 +55,7 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int start, int he
 
 size_t kv_stream_workspace_bytes(int head_dim, int rows, const DeviceInfo& dev);
 int launch_kv_stream(const AttendArgs& a, int head_dim, int rows, const DeviceInfo& dev, cudaStream_t stream);
+size_t kv_tile_workspace_bytes(int tokens, int seqs, int q_heads, int kv_heads, int head_dim, const DeviceInfo& dev);
+int launch_kv_tile(const AttendArgs& a, int head_dim, const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace trellis
