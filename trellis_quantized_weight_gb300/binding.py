@@ -313,47 +313,81 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, stretch: float =
     return table
 
 
-def _require_rows(t, name, device):
+# The calls below are made several times a layer and step, so their host side is kept
+# short: one query of the stream, no query of the workspace's size unless the one at hand
+# is refused.
+def _raw_stream(index, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(index)
+
+
+def _with_workspace(call, size, device, index, handle, stream):
+    """call(pointer, bytes) on this stream's workspace; grown to size() bytes if it is too small."""
+    buf = _ws_cache.get((index, handle))
+    rc = -7 if buf is None else call(buf.data_ptr(), buf.numel())
+    if rc == -7:
+        buf = _workspace(device, size(), stream)
+        rc = call(buf.data_ptr(), buf.numel())
+    return rc
+
+
+def _require_rows(t, name, index):
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on cuda:{index}")
+    shape = t.shape
+    if t.dtype != torch.bfloat16 or len(shape) != 3:
         raise ValueError(f"{name} must be a bfloat16 [tokens, heads, head_dim] tensor")
-    d = t.shape[2]
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+    row, head, one = t.stride()
+    if t.numel() and (one != 1 or (shape[1] > 1 and head != shape[2])):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-
-
-def _row_stride(t):
     # the stride of a single row is arbitrary: the row's own length then
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return shape, row if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _require_ints(t, name, index, ndim):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.int32 or t.dim() != ndim \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {ndim}-d int32 tensor on cuda:{index}")
+    return t.shape
 
 
 def _require_cache(cache, starts, kv_len, pages):
-    """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns)."""
+    """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns, device index)."""
     torch = _torch()
     k, v, ks, vs = cache
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise ValueError("the cache must be CUDA tensors")
-    dev = k.device
+    index = k.get_device()
     shape = k.shape
-    if k.dim() != 4 or v.shape != shape or k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if len(shape) != 4 or v.shape != shape or k.dtype != f8 or v.dtype != f8:
         raise ValueError("cache codes must be float8_e4m3fn [pages, kv_heads, page_size, head_dim]")
     want = (shape[0], shape[1], shape[2] // 16)
-    if ks.shape != want or vs.shape != want or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+    if ks.shape != want or vs.shape != want or ks.dtype != f32 or vs.dtype != f32:
         raise ValueError("cache scales must be float32 [pages, kv_heads, page_size / 16]")
-    if v.device != dev or ks.device != dev or vs.device != dev:
+    if v.get_device() != index or ks.get_device() != index or vs.get_device() != index:
         raise ValueError("the cache must be on one device")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("the cache must be contiguous")
-    i32 = torch.int32
-    for name, t in (("starts", starts), ("kv_len", kv_len), ("pages", pages)):
-        if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != i32 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
-    seqs = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    if starts.dim() != 1 or pages.dim() != 2 or seqs < 0 or starts.shape[0] != seqs + 1 or pages.shape[0] != seqs:
+    n, = _require_ints(starts, "starts", index, 1)
+    seqs, = _require_ints(kv_len, "kv_len", index, 1)
+    rows, cols = _require_ints(pages, "pages", index, 2)
+    if n != seqs + 1 or rows != seqs:
         raise ValueError("starts must be [S + 1], kv_len [S] and pages [S, columns]")
-    return shape, seqs, pages.shape[1]
+    return shape, seqs, cols, index
+
+
+def _output(out, name, shape, index, device):
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    if not isinstance(out, torch.Tensor) or out.shape != shape or out.dtype != torch.bfloat16 \
+            or out.get_device() != index or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bfloat16 {tuple(shape)} tensor on cuda:{index}")
+    return out
 
 
 def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved: bool = False, max_q=None, q_out=None,
@@ -367,41 +401,35 @@ def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved
     rope: float32 [positions, rot] from rope_table, or None.  max_q: rows of the sequence that
     has most (a hint).  The cache is updated in place."""
     torch = _torch()
-    (num_pages, hk, page, d), seqs, cols = _require_cache(cache, starts, kv_len, pages)
-    dev = starts.device
-    _require_rows(k, "k", dev)
-    _require_rows(v, "v", dev)
-    tokens = k.shape[0]
-    if tuple(k.shape) != (tokens, hk, d) or v.shape != k.shape:
+    (num_pages, hk, page, d), seqs, cols, index = _require_cache(cache, starts, kv_len, pages)
+    k_shape, k_stride = _require_rows(k, "k", index)
+    v_shape, v_stride = _require_rows(v, "v", index)
+    tokens = k_shape[0]
+    if k_shape != (tokens, hk, d) or v_shape != k_shape:
         raise ValueError(f"k and v must be [tokens, {hk}, {d}]")
-    hq, q_ptr, q_stride = hk, None, 0
+    hq, q_ptr, q_stride, out_ptr = hk, None, 0, None
     if q is not None:
-        _require_rows(q, "q", dev)
-        hq = q.shape[1]
-        if q.shape[0] != tokens or q.shape[2] != d:
+        q_shape, q_stride = _require_rows(q, "q", index)
+        hq = q_shape[1]
+        if q_shape[0] != tokens or q_shape[2] != d:
             raise ValueError(f"q must be [{tokens}, heads, {d}]")
-        if q_out is None:
-            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=dev)
-        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or q_out.device != dev or not q_out.is_contiguous():
-            raise ValueError("q_out must be a contiguous bfloat16 tensor of q's shape")
-        q_ptr, q_stride = q.data_ptr(), _row_stride(q)
+        q_out = _output(q_out, "q_out", q_shape, index, k.device)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     rope_ptr, rows, rot = None, 0, 0
     if rope is not None:
-        if not isinstance(rope, torch.Tensor) or rope.device != dev or rope.dtype != torch.float32 or rope.dim() != 2 \
-                or not rope.is_contiguous():
+        if not isinstance(rope, torch.Tensor) or rope.get_device() != index or rope.dtype != torch.float32 \
+                or rope.dim() != 2 or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous float32 [positions, rot] tensor")
         rope_ptr, (rows, rot) = rope.data_ptr(), rope.shape
     if seqs == 0 or tokens == 0:
         return q_out
-    rc = load().trellis_kv_append(
-        q_ptr, q_stride, k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), starts.data_ptr(),
-        kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, tokens if max_q is None else max_q, cols, num_pages, hq, hk, d,
-        page, rope_ptr, rows, rot, 1 if interleaved else 0, cache[0].data_ptr(), cache[1].data_ptr(),
-        cache[2].data_ptr(), cache[3].data_ptr(), q_out.data_ptr() if q is not None else None,
-        _stream_handle(dev, stream))
-    _check(rc, "trellis_kv_append")
+    _check(load().trellis_kv_append(
+        q_ptr, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, starts.data_ptr(), kv_len.data_ptr(),
+        pages.data_ptr(), tokens, seqs, tokens if max_q is None else max_q, cols, num_pages, hq, hk, d, page, rope_ptr, rows,
+        rot, 1 if interleaved else 0, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
+        out_ptr, _raw_stream(index, stream)), "trellis_kv_append")
     return q_out
 
 
@@ -418,27 +446,23 @@ def kv_attention(q, cache, starts, kv_len, pages, scale=None, window: int = 0, m
     q: bf16 [tokens, q_heads, head_dim], rows may be strided; the rest as kv_append, whose
     tokens the cache holds by now.  scale: of the scores, 1 / sqrt(head_dim) by default;
     window: how many tokens a row sees, itself included (0: all before it)."""
-    torch = _torch()
-    (num_pages, hk, page, d), seqs, cols = _require_cache(cache, starts, kv_len, pages)
-    dev = starts.device
-    _require_rows(q, "q", dev)
-    tokens, hq = q.shape[0], q.shape[1]
-    if q.shape[2] != d:
+    (num_pages, hk, page, d), seqs, cols, index = _require_cache(cache, starts, kv_len, pages)
+    shape, q_stride = _require_rows(q, "q", index)
+    tokens, hq = shape[0], shape[1]
+    if shape[2] != d:
         raise ValueError(f"q must be [tokens, heads, {d}]")
-    if out is None:
-        out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=dev)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
+    dev = q.device
+    out = _output(out, "out", shape, index, dev)
     if seqs == 0 or tokens == 0:
         return out
     most = tokens if max_q is None else max_q
-    ws = _workspace(dev, kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), stream)
-    rc = load().trellis_kv_attention(
-        q.data_ptr(), _row_stride(q), starts.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, most, cols,
-        num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
-        cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream_handle(dev, stream))
-    _check(rc, "trellis_kv_attention")
+    fn, handle = load().trellis_kv_attention, _raw_stream(index, stream)
+    args = (q.data_ptr(), q_stride, starts.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, most, cols,
+            num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
+            cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr())
+    _check(_with_workspace(lambda ptr, size: fn(*args, ptr, size, handle),
+                           lambda: kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), dev, index, handle,
+                           stream), "trellis_kv_attention")
     return out
 
 
@@ -463,28 +487,25 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
     _require(a, "a", bf16, 3)
     _require(b, "b", bf16, 3)
     _require(scales, "scales", (torch.float32,), 1)
-    _require(starts, "starts", (torch.int32,), 1)
-    _require(which, "which", (torch.int32,), 1)
-    (M, N), K = y.shape, x.shape[1]
-    n_ad, R = a.shape[0], a.shape[1]
-    segments = which.shape[0]
-    if x.shape[0] != M or tuple(a.shape) != (n_ad, R, K) or tuple(b.shape) != (n_ad, N, R) or scales.shape[0] != n_ad:
+    dev, index = y.device, y.get_device()
+    n, = _require_ints(starts, "starts", index, 1)
+    segments, = _require_ints(which, "which", index, 1)
+    shape, x_shape = y.shape, x.shape
+    (M, N), K = shape, x_shape[1]
+    n_ad, R, k_a = a.shape
+    if x_shape[0] != M or k_a != K or b.shape != (n_ad, N, R) or scales.shape[0] != n_ad:
         raise ValueError("y must be [M, N], x [M, K], a [adapters, R, K], b [adapters, N, R] and scales [adapters]")
-    if starts.shape[0] != segments + 1:
+    if n != segments + 1:
         raise ValueError("starts must be [S + 1] with which [S]")
-    if any(t.device != y.device for t in (x, a, b, scales, starts, which)):
+    if x.get_device() != index or a.get_device() != index or b.get_device() != index or scales.get_device() != index:
         raise ValueError("all tensors must be on one device")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=y.device)
-    else:
-        _require(out, "out", bf16, 2)
-        if out.shape != y.shape or out.device != y.device:
-            raise ValueError("out must be [M, N] on y's device")
+    out = _output(out, "out", shape, index, dev)
     if M == 0:
         return out
-    ws = _workspace(y.device, lora_add_workspace_bytes(M, K, N, R, n_ad, segments), stream)
-    rc = load().trellis_lora_add(y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(),
-                                 starts.data_ptr(), which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), _stream_handle(y.device, stream))
-    _check(rc, "trellis_lora_add")
+    fn, handle = load().trellis_lora_add, _raw_stream(index, stream)
+    args = (y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), starts.data_ptr(),
+            which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr())
+    _check(_with_workspace(lambda ptr, size: fn(*args, ptr, size, handle),
+                           lambda: lora_add_workspace_bytes(M, K, N, R, n_ad, segments), dev, index, handle, stream),
+           "trellis_lora_add")
     return out
