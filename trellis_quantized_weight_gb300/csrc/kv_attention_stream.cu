@@ -14,9 +14,9 @@
 //   lengths, so a CTA holds at most two pieces of units that others share.  The
 //   pieces' sums meet in the workspace; the CTA that finishes last adds them in
 //   CTA order (the same order on every run).
-// * Loads: each lane copies the codes that it will itself use from the cache into
-//   its own slots of a ring in shared memory (cp.async), several steps ahead.
-//   Reading them back needs no barrier and has no bank conflict.
+// * Loads: each warp copies the codes of its steps (whole lines of the cache) into a
+//   ring of its own in shared memory (cp.async), several steps ahead, in the order in
+//   which its lanes will read them.  No barrier wider than a warp is in the loop.
 // * Products: S^T = K Q^T and O^T = V^T P^T on m16n8k16 with f16 operands and fp32
 //   sums.  e4m3 -> f16 is exact.  The order of a sum's terms is free, so a lane's 16
 //   consecutive bytes of a key serve as its operand of four products, the query
@@ -45,15 +45,20 @@ namespace {
 constexpr float kMoveBy = 8.0f;          // the reference moves when exceeded by 2^8
 
 // Warps of a CTA and ring steps by head width: about 160 KB in flight an SM.
-template <int D> struct StreamShape;
-template <> struct StreamShape<64>  { static constexpr int kWarps = 8, kSteps = 8; };
-template <> struct StreamShape<128> { static constexpr int kWarps = 8, kSteps = 5; };
-template <> struct StreamShape<256> { static constexpr int kWarps = 8, kSteps = 3; };
+#ifndef W128
+#define W128 8
+#define S128 5
+#endif
+template <int D, int NT> struct StreamShape;
+template <int NT> struct StreamShape<64, NT>  { static constexpr int kWarps = 8, kSteps = 8; };
+template <> struct StreamShape<128, 1> { static constexpr int kWarps = W128, kSteps = S128; };
+template <> struct StreamShape<128, 2> { static constexpr int kWarps = 8, kSteps = 5; };
+template <int NT> struct StreamShape<256, NT> { static constexpr int kWarps = 8, kSteps = 3; };
 
 template <int D, int NT>
 struct Stream {
-    static constexpr int kWarps = StreamShape<D>::kWarps;
-    static constexpr int kSteps = StreamShape<D>::kSteps;
+    static constexpr int kWarps = StreamShape<D, NT>::kWarps;
+    static constexpr int kSteps = StreamShape<D, NT>::kSteps;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = 8 * NT;                 // query rows of a unit
     static constexpr int kTile = kKvBlock * kWarps;      // cached tokens of a tile
@@ -61,7 +66,7 @@ struct Stream {
     static constexpr int kRing = kWarps * kSteps * kStepBytes;
     static constexpr int kScaleOff = kRing;              // [warps][steps][2] floats
     static constexpr int kScanOff = kScaleOff + kWarps * kSteps * 8;
-    static constexpr int kSmem = kScanOff + 256;
+    static constexpr int kSmem = kScanOff + 16 * kWarps + 256;
     // after a unit's last step the ring holds the warps' sums: O [rows][D], then m, l
     static constexpr int kPart = kRows * D + 2 * kRows;  // floats of a partial result
     static_assert(kWarps * kPart * 4 <= kRing, "the warps' sums fit the ring");
@@ -129,6 +134,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     constexpr int KJ = D / 64;                  // 16-byte loads of a key row a lane
     constexpr int VJ = D >= 128 ? D / 128 : 1;  // loads of a value row a lane (8 bytes at D = 64)
     constexpr int MT = D / 16;                  // 16-row tiles of O^T
+    constexpr int kCopies = D / 32;             // 16-byte copies of a lane for the keys of a step (values alike)
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -257,30 +263,33 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
         auto page_of = [&](int i) {             // of this warp's step i
             return kv_page(a.l, u.seq, (blk0 + b_first + i * S::kWarps) >> shift);
         };
+        // The 16 tokens of a step lie one after another, so copy r of a lane is bytes
+        // 512 r + 16 lane of them: whole lines of the cache.  Where its 16 bytes go in the
+        // ring makes them the operands of the lane that reads there; the exclusive ors keep
+        // both the copies and the reads free of bank conflicts.
+        auto k_slot = [&](int r) {
+            const int chunk = r * 32 + lane, tok = chunk / (D / 16), c = chunk % (D / 16);
+            const int j = c >> 2;               // token = row 8 h + g, chunk t + 4 j
+            return ((tok >> 3) * KJ + j) * 512 + ((((tok & 7) * 4 + (c & 3)) ^ ((j & 1) * 4)) * 16);
+        };
+        auto v_slot = [&](int r) {
+            const int chunk = r * 32 + lane, tok = chunk / (D / 16), c = chunk % (D / 16);
+            const int vt = (tok & 7) >> 1, vr = (tok & 1) + ((tok >> 3) << 1);   // token 2 t + (r & 1) + 8 (r >> 1)
+            if constexpr (D == 64) return vr * 256 + vt * 64 + ((c ^ (vt & 2)) * 16);
+            return (vr * VJ + (c >> 3)) * 512 + vt * 128 + (((c & 7) ^ (2 * vt)) * 16);
+        };
         auto issue = [&](int i, int page) {     // start the copies of step i
             const int blk = blk0 + b_first + i * S::kWarps;
             const int in_page = blk & ((1 << shift) - 1);
             const size_t unit = static_cast<size_t>(page) * a.l.kv_heads + u.head;
             const size_t off = (unit * a.l.page_size + in_page * kKvBlock) * D;
             const uint32_t dst = ring + (i % S::kSteps) * S::kStepBytes;
-            const uint8_t* k = a.k_codes + off;
+            const uint8_t* k = a.k_codes + off + lane * 16;
+            const uint8_t* v = a.v_codes + off + lane * 16;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int j = 0; j < KJ; ++j)
-                    cp_async16(dst + (r * KJ + j) * 512 + lane * 16, k + (g + 8 * r) * D + (t + 4 * j) * 16);
-            const uint8_t* v = a.v_codes + off;
-            const uint32_t vdst = dst + kKvBlock * D;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {       // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-                const int tok = 2 * t + (r & 1) + (r >> 1) * 8;
-                if constexpr (D == 64) {
-                    cp_async8(vdst + r * 256 + lane * 8, v + tok * D + g * 8);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VJ; ++j)
-                        cp_async16(vdst + (r * VJ + j) * 512 + lane * 16, v + tok * D + (g + 8 * j) * 16);
-                }
+            for (int r = 0; r < kCopies; ++r) {
+                cp_async16(dst + k_slot(r), k + r * 512);
+                cp_async16(dst + kKvBlock * D + v_slot(r), v + r * 512);
             }
             const size_t sc = unit * (a.l.page_size / kKvBlock) + in_page;
             if (lane < 2) cp_async4(ring_sc + (i % S::kSteps) * 8 + lane * 4, (lane == 0 ? a.k_scales : a.v_scales) + sc);
@@ -312,7 +321,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             cp_async_commit();
             if (i + S::kSteps < steps) page_next = page_of(i + S::kSteps);
             cp_async_wait<S::kSteps - 1>();
-            __syncwarp();                       // the scales were copied by lanes 0 and 1
+            __syncwarp();                       // every lane's copies have landed
             const uint32_t src = ring + (i % S::kSteps) * S::kStepBytes;
             float ks, vs;
             asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs)
@@ -329,8 +338,8 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                     for (int j = 0; j < 4; ++j) sc[nt][h][j] = 0.0f;
 #pragma unroll
             for (int j = 0; j < KJ; ++j) {
-                const uint4 ka = lds128(src + j * 512 + lane * 16);
-                const uint4 kb = lds128(src + (KJ + j) * 512 + lane * 16);
+                const uint4 ka = lds128(src + j * 512 + ((lane ^ ((j & 1) * 4)) * 16));
+                const uint4 kb = lds128(src + (KJ + j) * 512 + ((lane ^ ((j & 1) * 4)) * 16));
                 const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                 uint32_t w[2][4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const uint2 v = lds64(vsrc + r * 256 + lane * 8);
+                    const uint2 v = lds64(vsrc + r * 256 + t * 64 + ((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8);
                     w[0][r] = keep[r] ? v.x : 0u;
                     w[1][r] = keep[r] ? v.y : 0u;
                 }
@@ -420,7 +429,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                     uint32_t w[4][4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const uint4 v = lds128(vsrc + (r * VJ + j) * 512 + lane * 16);
+                        const uint4 v = lds128(vsrc + (r * VJ + j) * 512 + t * 128 + (g ^ (2 * t)) * 16);
                         w[0][r] = keep[r] ? v.x : 0u;
                         w[1][r] = keep[r] ? v.y : 0u;
                         w[2][r] = keep[r] ? v.z : 0u;
