@@ -45,12 +45,15 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 }
 
 // Row r of a sequence's rows to a key head (token r / group, query head r % group):
-// value d of the output.  A row that sees nothing (l == 0) is zero.
-__device__ __forceinline__ void store_row(const AttendArgs& a, int start, int head, int r, int D, int d, float acc,
-                                          float l) {
+// values d .. d + 3 of the output.  A row that sees nothing (l == 0) is zero.
+__device__ __forceinline__ void store_row4(const AttendArgs& a, int start, int head, int r, int D, int d, float4 acc,
+                                           float l) {
     const size_t row = static_cast<size_t>(start) + r / a.group;
     const int h = head * a.group + r % a.group;
-    a.out[(row * a.l.q_heads + h) * D + d] = bf16_bits_rn(l == 0.0f ? 0.0f : acc / l);
+    const float inv = 1.0f / l;
+    uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (l == 0.0f) w = make_uint2(0u, 0u);
+    *reinterpret_cast<uint2*>(a.out + (row * a.l.q_heads + h) * D + d) = w;
 }
 
 size_t kv_stream_workspace_bytes(int head_dim, int rows, const DeviceInfo& dev);

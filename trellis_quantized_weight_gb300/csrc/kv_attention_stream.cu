@@ -44,16 +44,13 @@ namespace {
 
 constexpr float kMoveBy = 8.0f;          // the reference moves when exceeded by 2^8
 
-// Warps of a CTA and ring steps by head width: about 160 KB in flight an SM.
-#ifndef W128
-#define W128 8
-#define S128 5
-#endif
+// Warps of a CTA and ring steps by head width and rows: 128 to 160 KB of codes in
+// flight an SM beside the warps' sums.
 template <int D, int NT> struct StreamShape;
-template <int NT> struct StreamShape<64, NT>  { static constexpr int kWarps = 8, kSteps = 8; };
-template <> struct StreamShape<128, 1> { static constexpr int kWarps = W128, kSteps = S128; };
-template <> struct StreamShape<128, 2> { static constexpr int kWarps = 8, kSteps = 5; };
-template <int NT> struct StreamShape<256, NT> { static constexpr int kWarps = 8, kSteps = 3; };
+template <int NT> struct StreamShape<64, NT> { static constexpr int kWarps = 8, kSteps = 8; };
+template <> struct StreamShape<128, 1> { static constexpr int kWarps = 8, kSteps = 5; };
+template <> struct StreamShape<128, 2> { static constexpr int kWarps = 8, kSteps = 4; };
+template <int NT> struct StreamShape<256, NT> { static constexpr int kWarps = 6, kSteps = 3; };
 
 template <int D, int NT>
 struct Stream {
@@ -65,74 +62,92 @@ struct Stream {
     static constexpr int kStepBytes = 2 * kKvBlock * D;  // codes of one warp's step
     static constexpr int kRing = kWarps * kSteps * kStepBytes;
     static constexpr int kScaleOff = kRing;              // [warps][steps][2] floats
-    static constexpr int kScanOff = kScaleOff + kWarps * kSteps * 8;
-    static constexpr int kSmem = kScanOff + 16 * kWarps + 256;
-    // after a unit's last step the ring holds the warps' sums: O [rows][D], then m, l
-    static constexpr int kPart = kRows * D + 2 * kRows;  // floats of a partial result
-    static_assert(kWarps * kPart * 4 <= kRing, "the warps' sums fit the ring");
+    static constexpr int kPart = kRows * D + 2 * kRows;  // floats of a partial result: O [rows][D], m, l
+    static constexpr int kSumsOff = kScaleOff + kWarps * kSteps * 8;
+    static constexpr int kMiscOff = kSumsOff + kWarps * kPart * 4;
+    static constexpr int kSmem = kMiscOff + 256;
+    // the join of a unit's pieces keeps a factor a piece and row where the warps' sums were
+    static constexpr int kMaxPieces = kWarps * kPart / kRows;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
+// A sequence as the units need it.
+struct Seq {
+    int start, n, p0, total;      // packed rows; the first one's position; cached tokens
+};
+
+// n <= 0: no rows.  The four loads do not wait for one another.
+__device__ __forceinline__ Seq load_seq(const AttendArgs& a, int s) {
+    const int b = __ldg(a.l.starts + s), e = __ldg(a.l.starts + s + 1), len = __ldg(a.l.kv_len + s);
+    const long long most = static_cast<long long>(a.l.page_cols) << a.l.page_shift;
+    Seq q;
+    q.start = b;
+    q.n = b >= 0 && e <= a.l.tokens ? e - b : 0;
+    q.p0 = len - q.n;
+    q.total = len < most ? len : static_cast<int>(most);
+    return q;
+}
+
 struct Unit {
     int seq, head, qt;        // query tile
-    int start, n, p0;         // packed rows, and the first one's position
+    Seq s;
     int lo, hi;               // cached tokens [lo, hi) that its rows see (lo a multiple of 16)
     int tiles;
 };
 
-// Query tiles of a sequence with n rows, and the token range of one of them.
+// Tiles of a query tile, and its token range.
 template <int D, int NT>
-__device__ __forceinline__ int unit_tiles(const AttendArgs& a, int n, int total, int p0, int qt, int* lo, int* hi) {
+__device__ __forceinline__ int unit_tiles(const AttendArgs& a, const Seq& s, int qt, int* lo, int* hi) {
     using S = Stream<D, NT>;
-    const int g = a.group;
-    const int first = qt * S::kRows / g, last = min(n - 1, (qt * S::kRows + S::kRows - 1) / g);
-    *hi = max(0, min(total, p0 + last + 1));
-    const int low = a.window > 0 ? max(0, p0 + first + 1 - a.window) : 0;
+    const int first = qt * S::kRows / a.group, last = min(s.n - 1, (qt * S::kRows + S::kRows - 1) / a.group);
+    *hi = max(0, min(s.total, s.p0 + last + 1));
+    const int low = a.window > 0 ? max(0, s.p0 + first + 1 - a.window) : 0;
     *lo = low & ~(kKvBlock - 1);
     const int span = *hi - *lo;
     return span > 0 ? (span + S::kTile - 1) / S::kTile : 1;   // an empty unit still writes its zeros
 }
 
 template <int D, int NT>
-__device__ long long seq_tiles(const AttendArgs& a, int s) {
-    int start, n;
-    if (!kv_rows(a.l, s, &start, &n)) return 0;
-    const int total = kv_total(a.l, s), p0 = __ldg(a.l.kv_len + s) - n;
-    const int qts = (n * a.group + Stream<D, NT>::kRows - 1) / Stream<D, NT>::kRows;
+__device__ long long seq_tiles(const AttendArgs& a, const Seq& s) {
+    if (s.n <= 0) return 0;
+    const int qts = (s.n * a.group + Stream<D, NT>::kRows - 1) / Stream<D, NT>::kRows;
     long long sum = 0;
-    for (int qt = 0; qt < qts; ++qt) {
-        int lo, hi;
-        sum += unit_tiles<D, NT>(a, n, total, p0, qt, &lo, &hi);
-    }
+    int lo, hi;
+    for (int qt = 0; qt < qts; ++qt) sum += unit_tiles<D, NT>(a, s, qt, &lo, &hi);
     return sum * a.l.kv_heads;
 }
 
+// A walk over units in their order: heads, then query tiles, then sequences.
 template <int D, int NT>
-__device__ __forceinline__ void load_unit(const AttendArgs& a, Unit& u) {
-    kv_rows(a.l, u.seq, &u.start, &u.n);
-    u.p0 = __ldg(a.l.kv_len + u.seq) - u.n;
-    u.tiles = unit_tiles<D, NT>(a, u.n, kv_total(a.l, u.seq), u.p0, u.qt, &u.lo, &u.hi);
-}
+struct Walk {
+    Unit u;
+    Seq ahead;                // sequence u.seq + 1, loaded before it is needed
 
-// The unit after u (heads, then query tiles, then sequences); the caller knows there is one.
-template <int D, int NT>
-__device__ __forceinline__ void next_unit(const AttendArgs& a, Unit& u) {
-    if (++u.head < a.l.kv_heads) return;                       // the same rows and tokens
-    u.head = 0;
-    if (++u.qt * Stream<D, NT>::kRows >= u.n * a.group) {
-        u.qt = 0;
-        int start, n;
-        do { ++u.seq; } while (u.seq < a.l.seqs && !kv_rows(a.l, u.seq, &start, &n));
-        if (u.seq >= a.l.seqs) { u.seq = a.l.seqs - 1; return; }
+    __device__ __forceinline__ void begin(const AttendArgs& a, const Unit& first) {
+        u = first;
+        ahead = load_seq(a, min(u.seq + 1, a.l.seqs - 1));
     }
-    load_unit<D, NT>(a, u);
-}
+    // The caller knows that there is a unit after this one.
+    __device__ __forceinline__ void next(const AttendArgs& a) {
+        if (++u.head < a.l.kv_heads) return;               // the same rows and tokens
+        u.head = 0;
+        if (++u.qt * Stream<D, NT>::kRows >= u.s.n * a.group) {
+            u.qt = 0;
+            do {
+                u.seq = min(u.seq + 1, a.l.seqs - 1);
+                u.s = ahead;
+                ahead = load_seq(a, min(u.seq + 1, a.l.seqs - 1));
+            } while (u.s.n <= 0 && u.seq < a.l.seqs - 1);
+        }
+        u.tiles = unit_tiles<D, NT>(a, u.s, u.qt, &u.lo, &u.hi);
+    }
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(const __grid_constant__ AttendArgs a) {
     using S = Stream<D, NT>;
-    constexpr int KJ = D / 64;                  // 16-byte loads of a key row a lane
-    constexpr int VJ = D >= 128 ? D / 128 : 1;  // loads of a value row a lane (8 bytes at D = 64)
+    constexpr int KJ = D / 64;                  // 16-byte pieces of a key row a lane
+    constexpr int VJ = D >= 128 ? D / 128 : 1;  // pieces of a value row a lane (8 bytes at D = 64)
     constexpr int MT = D / 16;                  // 16-row tiles of O^T
     constexpr int kCopies = D / 32;             // 16-byte copies of a lane for the keys of a step (values alike)
     extern __shared__ __align__(128) unsigned char smem[];
@@ -142,11 +157,11 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
 
     // ---- this CTA's share of all units' tiles -------------------------------------------
     // prefix sums over the sequences, a contiguous chunk a thread
-    long long* scan = reinterpret_cast<long long*>(smem + S::kScanOff);   // warps' sums, then the answer
+    long long* scan = reinterpret_cast<long long*>(smem + S::kMiscOff);
     const int per = (a.l.seqs + S::kThreads - 1) / S::kThreads;
     const int s0 = min(a.l.seqs, static_cast<int>(threadIdx.x) * per), s1 = min(a.l.seqs, s0 + per);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += seq_tiles<D, NT>(a, s);
+    for (int s = s0; s < s1; ++s) mine += seq_tiles<D, NT>(a, load_seq(a, s));
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -166,70 +181,143 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     if (cta >= ctas) { griddep_launch_dependents(); return; }
     const long long begin = cta * all / ctas, end = (cta + 1) * all / ctas;
     // the thread whose sequences hold tile `begin` finds the unit
-    int* found = reinterpret_cast<int*>(smem + S::kScanOff + 8 * S::kWarps);   // seq, qt, head, tile
+    Unit* found = reinterpret_cast<Unit*>(smem + S::kMiscOff + 8 * S::kWarps);
+    int* found_tile = reinterpret_cast<int*>(found + 1);
     long long at = before + incl - mine;
     if (begin >= at && begin < at + mine) {
-        int s = s0;
-        long long c = seq_tiles<D, NT>(a, s);
-        while (begin >= at + c) { at += c; c = seq_tiles<D, NT>(a, ++s); }
-        int start, n, lo, hi, qt = 0;
-        kv_rows(a.l, s, &start, &n);
-        const int total = kv_total(a.l, s), p0 = __ldg(a.l.kv_len + s) - n;
-        int off = static_cast<int>(begin - at);
-        int tl = unit_tiles<D, NT>(a, n, total, p0, 0, &lo, &hi);
-        while (off >= tl * a.l.kv_heads) {
-            off -= tl * a.l.kv_heads;
-            tl = unit_tiles<D, NT>(a, n, total, p0, ++qt, &lo, &hi);
+        Unit f;
+        f.seq = s0;
+        f.s = load_seq(a, s0);
+        long long c = seq_tiles<D, NT>(a, f.s);
+        while (begin >= at + c) {
+            at += c;
+            f.s = load_seq(a, ++f.seq);
+            c = seq_tiles<D, NT>(a, f.s);
         }
-        found[0] = s; found[1] = qt; found[2] = off / tl; found[3] = off % tl;
+        long long off = begin - at;
+        f.qt = 0;
+        f.tiles = unit_tiles<D, NT>(a, f.s, 0, &f.lo, &f.hi);
+        while (off >= static_cast<long long>(f.tiles) * a.l.kv_heads) {
+            off -= static_cast<long long>(f.tiles) * a.l.kv_heads;
+            f.tiles = unit_tiles<D, NT>(a, f.s, ++f.qt, &f.lo, &f.hi);
+        }
+        f.head = static_cast<int>(off / f.tiles);
+        *found = f;
+        *found_tile = static_cast<int>(off % f.tiles);
     }
     __syncthreads();
-    Unit u;
-    u.seq = found[0]; u.qt = found[1]; u.head = found[2];
-    load_unit<D, NT>(a, u);
-    int tile0 = found[3];
-    __syncthreads();                            // the ring and the scan area are free from here on
 
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kSteps * S::kStepBytes;
     const uint32_t ring_sc = static_cast<uint32_t>(__cvta_generic_to_shared(smem + S::kScaleOff)) + warp * S::kSteps * 8;
-    float* part_smem = reinterpret_cast<float*>(smem);
+    float* sums = reinterpret_cast<float*>(smem + S::kSumsOff);
+    int* ticket = reinterpret_cast<int*>(smem + S::kMiscOff);
+
+    // ---- copies: a walk of its own, steps ahead of the sums and across units ---------------
+    // The 16 tokens of a step lie one after another, so copy r of a lane is bytes
+    // 512 r + 16 lane of them: whole lines of the cache.  Where its 16 bytes go in the
+    // ring makes them the operands of the lane that reads there; the exclusive ors keep
+    // both the copies and the reads free of bank conflicts.
+    auto k_slot = [&](int r) {
+        const int chunk = r * 32 + lane, tok = chunk / (D / 16), c = chunk % (D / 16);
+        const int j = c >> 2;                   // token = row 8 h + g, chunk t + 4 j
+        return ((tok >> 3) * KJ + j) * 512 + ((((tok & 7) * 4 + (c & 3)) ^ ((j & 1) * 4)) * 16);
+    };
+    auto v_slot = [&](int r) {
+        const int chunk = r * 32 + lane, tok = chunk / (D / 16), c = chunk % (D / 16);
+        const int vt = (tok & 7) >> 1, vr = (tok & 1) + ((tok >> 3) << 1);   // token 2 t + (r & 1) + 8 (r >> 1)
+        if constexpr (D == 64) return vr * 256 + vt * 64 + ((c ^ (vt & 2)) * 16);
+        return (vr * VJ + (c >> 3)) * 512 + vt * 128 + (((c & 7) ^ (2 * vt)) * 16);
+    };
+    const int shift = a.l.page_shift - 4;       // blocks of a page, log2
+    Walk<D, NT> ahead;
+    ahead.begin(a, *found);
+    int ahead_tile = *found_tile;
+    long long ahead_left = end - begin;         // tiles not yet walked over
+    int next_blk = -1, next_page = 0, next_head = 0;
+    // finds this warp's next block and starts the load of its page id
+    auto seek = [&]() {
+        next_blk = -1;
+        while (ahead_left > 0) {
+            if (ahead_tile == ahead.u.tiles) {
+                ahead.next(a);
+                ahead_tile = 0;
+            }
+            const int blk = ahead.u.lo / kKvBlock + ahead_tile * S::kWarps + warp;
+            ++ahead_tile;
+            --ahead_left;
+            if (blk * kKvBlock < ahead.u.hi) {
+                next_blk = blk;
+                next_head = ahead.u.head;
+                next_page = kv_page(a.l, ahead.u.seq, blk >> shift);
+                break;
+            }
+        }
+    };
+    auto issue = [&](int slot) {
+        if (next_blk < 0) return;
+        const int in_page = next_blk & ((1 << shift) - 1);
+        const size_t unit = static_cast<size_t>(next_page) * a.l.kv_heads + next_head;
+        const size_t off = (unit * a.l.page_size + in_page * kKvBlock) * D + lane * 16;
+        const uint32_t dst = ring + slot * S::kStepBytes;
+#pragma unroll
+        for (int r = 0; r < kCopies; ++r) {
+            cp_async16(dst + k_slot(r), a.k_codes + off + r * 512);
+            cp_async16(dst + kKvBlock * D + v_slot(r), a.v_codes + off + r * 512);
+        }
+        const size_t sc = unit * (a.l.page_size / kKvBlock) + in_page;
+        if (lane < 2) cp_async4(ring_sc + slot * 8 + lane * 4, (lane == 0 ? a.k_scales : a.v_scales) + sc);
+        seek();
+    };
+    seek();
+#pragma unroll
+    for (int i = 0; i < S::kSteps - 1; ++i) {
+        issue(i);
+        cp_async_commit();
+    }
+    int slot = 0, fill = S::kSteps - 1;         // ring slots read and filled next
+
+    // ---- queries of a unit: raw, loaded a unit ahead ----------------------------------------
+    Walk<D, NT> walk;
+    walk.begin(a, *found);
+    int tile0 = *found_tile;
+    uint4 raw[NT][KJ][2];
+    auto load_queries = [&](const Unit& u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = u.qt * S::kRows + nt * 8 + g;
+            const int tok = r / a.group;
+            const bool live = tok < u.s.n;
+            const uint4* row = reinterpret_cast<const uint4*>(
+                a.q + static_cast<size_t>(u.s.start + (live ? tok : 0)) * a.q_stride +
+                (static_cast<size_t>(u.head) * a.group + r % a.group) * D);
+#pragma unroll
+            for (int j = 0; j < KJ; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    raw[nt][j][h] = live ? __ldg(row + 2 * (t + 4 * j) + h) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    load_queries(walk.u);
 
     for (long long done = begin; done < end;) {
+        const Unit u = walk.u;
         const int tile1 = static_cast<int>(min(static_cast<long long>(u.tiles), tile0 + (end - done)));
-        // blocks of this warp: first, first + warps, ...
-        const int blocks = (u.hi - u.lo + kKvBlock - 1) / kKvBlock;          // <= 0: nothing to see
-        const int b_first = tile0 * S::kWarps + warp;
-        const int b_end = min(tile1 * S::kWarps, blocks);
-        const int steps = b_first < b_end ? (b_end - b_first + S::kWarps - 1) / S::kWarps : 0;
-        const int blk0 = u.lo / kKvBlock;
 
-        // ---- queries: f16 fragments, each row times a power of two --------------------
+        // f16 fragments, each row times a power of two
         uint32_t qf[NT][4 * KJ][2];
         float qmul[NT][2];                      // of this lane's two columns (rows 2t, 2t + 1 of each 8)
         int limit[NT][2], lower[NT][2];         // cached tokens [lower, limit) that they see
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = u.qt * S::kRows + nt * 8 + g;
-            const int tok = r / a.group;
-            const bool live = tok < u.n;
-            const uint16_t* row = a.q + static_cast<size_t>(u.start + (live ? tok : 0)) * a.q_stride +
-                                  (static_cast<size_t>(u.head) * a.group + r % a.group) * D;
-            uint32_t raw[KJ][8];
             uint32_t most = 0u;
 #pragma unroll
-            for (int j = 0; j < KJ; ++j) {
-                uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-                if (live) {
-                    v0 = __ldg(reinterpret_cast<const uint4*>(row) + 2 * (t + 4 * j));
-                    v1 = __ldg(reinterpret_cast<const uint4*>(row) + 2 * (t + 4 * j) + 1);
-                }
-                const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            for (int j = 0; j < KJ; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    raw[j][i] = w[i];
-                    most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w[4] = {raw[nt][j][h].x, raw[nt][j][h].y, raw[nt][j][h].z, raw[nt][j][h].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
                 }
-            }
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const int e = query_exponent(most);
@@ -237,63 +325,31 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
 #pragma unroll
             for (int j = 0; j < KJ; ++j)
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w[4] = {raw[nt][j][h].x, raw[nt][j][h].y, raw[nt][j][h].z, raw[nt][j][h].w};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t v = raw[j][2 * w + h];
-                        qf[nt][4 * j + w][h] = f32_to_f16x2(bf16_lo(v) * down, bf16_hi(v) * down);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        qf[nt][4 * j + 2 * h + (i >> 1)][i & 1] = f32_to_f16x2(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
+                }
             // the column's factor, from the lane that holds its row
             const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 qmul[nt][h] = __shfl_sync(0xffffffffu, up, (2 * t + h) * 4);
-                const int tk = min((u.qt * S::kRows + nt * 8 + 2 * t + h) / a.group, u.n - 1);
-                limit[nt][h] = min(u.hi, u.p0 + tk + 1);
-                lower[nt][h] = a.window > 0 ? u.p0 + tk + 1 - a.window : 0;
+                const int tk = min((u.qt * S::kRows + nt * 8 + 2 * t + h) / a.group, u.s.n - 1);
+                limit[nt][h] = min(u.hi, u.s.p0 + tk + 1);
+                lower[nt][h] = a.window > 0 ? u.s.p0 + tk + 1 - a.window : 0;
             }
         }
         // tokens that every row sees
-        const int all_hi = min(u.hi, u.p0 + u.qt * S::kRows / a.group + 1);
+        const int all_hi = min(u.hi, u.s.p0 + u.qt * S::kRows / a.group + 1);
         const int all_lo = a.window > 0
-            ? u.p0 + min((u.qt * S::kRows + S::kRows - 1) / a.group, u.n - 1) + 1 - a.window : 0;
-
-        // ---- the stream ---------------------------------------------------------------
-        const int shift = a.l.page_shift - 4;
-        auto page_of = [&](int i) {             // of this warp's step i
-            return kv_page(a.l, u.seq, (blk0 + b_first + i * S::kWarps) >> shift);
-        };
-        // The 16 tokens of a step lie one after another, so copy r of a lane is bytes
-        // 512 r + 16 lane of them: whole lines of the cache.  Where its 16 bytes go in the
-        // ring makes them the operands of the lane that reads there; the exclusive ors keep
-        // both the copies and the reads free of bank conflicts.
-        auto k_slot = [&](int r) {
-            const int chunk = r * 32 + lane, tok = chunk / (D / 16), c = chunk % (D / 16);
-            const int j = c >> 2;               // token = row 8 h + g, chunk t + 4 j
-            return ((tok >> 3) * KJ + j) * 512 + ((((tok & 7) * 4 + (c & 3)) ^ ((j & 1) * 4)) * 16);
-        };
-        auto v_slot = [&](int r) {
-            const int chunk = r * 32 + lane, tok = chunk / (D / 16), c = chunk % (D / 16);
-            const int vt = (tok & 7) >> 1, vr = (tok & 1) + ((tok >> 3) << 1);   // token 2 t + (r & 1) + 8 (r >> 1)
-            if constexpr (D == 64) return vr * 256 + vt * 64 + ((c ^ (vt & 2)) * 16);
-            return (vr * VJ + (c >> 3)) * 512 + vt * 128 + (((c & 7) ^ (2 * vt)) * 16);
-        };
-        auto issue = [&](int i, int page) {     // start the copies of step i
-            const int blk = blk0 + b_first + i * S::kWarps;
-            const int in_page = blk & ((1 << shift) - 1);
-            const size_t unit = static_cast<size_t>(page) * a.l.kv_heads + u.head;
-            const size_t off = (unit * a.l.page_size + in_page * kKvBlock) * D;
-            const uint32_t dst = ring + (i % S::kSteps) * S::kStepBytes;
-            const uint8_t* k = a.k_codes + off + lane * 16;
-            const uint8_t* v = a.v_codes + off + lane * 16;
-#pragma unroll
-            for (int r = 0; r < kCopies; ++r) {
-                cp_async16(dst + k_slot(r), k + r * 512);
-                cp_async16(dst + kKvBlock * D + v_slot(r), v + r * 512);
-            }
-            const size_t sc = unit * (a.l.page_size / kKvBlock) + in_page;
-            if (lane < 2) cp_async4(ring_sc + (i % S::kSteps) * 8 + lane * 4, (lane == 0 ? a.k_scales : a.v_scales) + sc);
-        };
+            ? u.s.p0 + min((u.qt * S::kRows + S::kRows - 1) / a.group, u.s.n - 1) + 1 - a.window : 0;
+        const long long after = done + (tile1 - tile0);
+        if (after < end) {
+            walk.next(a);
+            load_queries(walk.u);
+        }
 
         float o[NT][MT][4];
         float m[NT][2], sum[NT][2];
@@ -307,26 +363,19 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             sum[nt][0] = sum[nt][1] = 0.0f;
         }
 
-        int page_next = 0;
-#pragma unroll
-        for (int i = 0; i < S::kSteps - 1; ++i) {
-            if (i < steps) issue(i, page_of(i));
-            cp_async_commit();
-        }
-        if (S::kSteps - 1 < steps) page_next = page_of(S::kSteps - 1);
-
-        for (int i = 0; i < steps; ++i) {
+        for (int tile = tile0; tile < tile1; ++tile) {
+            const int tok0 = u.lo + (tile * S::kWarps + warp) * kKvBlock;
+            if (tok0 >= u.hi) break;            // the walk of the copies passes over it too
             __syncwarp();                       // every lane has read the slot that is filled now
-            if (i + S::kSteps - 1 < steps) issue(i + S::kSteps - 1, page_next);
+            issue(fill);
             cp_async_commit();
-            if (i + S::kSteps < steps) page_next = page_of(i + S::kSteps);
             cp_async_wait<S::kSteps - 1>();
             __syncwarp();                       // every lane's copies have landed
-            const uint32_t src = ring + (i % S::kSteps) * S::kStepBytes;
+            const uint32_t src = ring + slot * S::kStepBytes;
             float ks, vs;
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs)
-                         : "r"(ring_sc + (i % S::kSteps) * 8) : "memory");
-            const int tok0 = (blk0 + b_first + i * S::kWarps) * kKvBlock;
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(ring_sc + slot * 8) : "memory");
+            slot = slot + 1 == S::kSteps ? 0 : slot + 1;
+            fill = fill + 1 == S::kSteps ? 0 : fill + 1;
 
             // scores: two chains of products
             float sc[NT][2][4];
@@ -440,12 +489,10 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                 }
             }
         }
-        cp_async_wait<0>();
 
-        // ---- the warps' sums meet ---------------------------------------------------------
-        __syncthreads();                        // every warp is done with its ring
+        // ---- the warps' sums meet (the copies of the next unit are under way) ---------------
         {
-            float* mine_o = part_smem + warp * S::kPart;
+            float* mine_o = sums + warp * S::kPart;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -459,8 +506,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                     for (int i = 0; i < MT; ++i) {
                         // tile i, row g: the value index that load and permute gave it
                         const int d = D == 64 ? 8 * g + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
-                        mine_o[row * D + d] = o[nt][i][h];
-                        mine_o[row * D + d + 1] = o[nt][i][h + 2];
+                        *reinterpret_cast<float2*>(mine_o + row * D + d) = make_float2(o[nt][i][h], o[nt][i][h + 2]);
                     }
                     if (g == 0) {
                         mine_o[S::kRows * D + row] = m[nt][h];
@@ -471,29 +517,32 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == u.tiles;
         // where the unit's pieces go: CTA c's slot 2c when the unit began before it, else 2c + 1
-        float* slot = a.partials + (2 * cta + (tile0 == 0 ? 1 : 0)) * S::kPart;
-        const int rows = min(S::kRows, u.n * a.group - u.qt * S::kRows);
-        for (int e = threadIdx.x; e < rows * D; e += S::kThreads) {
+        float* piece = a.partials + (2 * cta + (tile0 == 0 ? 1 : 0)) * S::kPart;
+        const int rows = min(S::kRows, u.s.n * a.group - u.qt * S::kRows);
+        for (int e = threadIdx.x * 4; e < rows * D; e += S::kThreads * 4) {
             const int row = e / D, d = e % D;
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, part_smem[w * S::kPart + S::kRows * D + row]);
+            for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, sums[w * S::kPart + S::kRows * D + row]);
             const float ref = top == -INFINITY ? 0.0f : top;
-            float acc = 0.0f, l = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float l = 0.0f;
 #pragma unroll
             for (int w = 0; w < S::kWarps; ++w) {
-                const float* p = part_smem + w * S::kPart;
+                const float* p = sums + w * S::kPart;
                 const float f = exp2_approx(p[S::kRows * D + row] - ref);
-                acc = fmaf(p[row * D + d], f, acc);
+                const float4 v = *reinterpret_cast<const float4*>(p + row * D + d);
+                acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
                 l = fmaf(p[S::kRows * D + S::kRows + row], f, l);
             }
             if (whole) {
-                store_row(a, u.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
+                store_row4(a, u.s.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
             } else {
-                slot[row * D + d] = acc;
+                *reinterpret_cast<float4*>(piece + row * D + d) = acc;
                 if (d == 0) {
-                    slot[S::kRows * D + row] = top;
-                    slot[S::kRows * D + S::kRows + row] = l;
+                    piece[S::kRows * D + row] = top;
+                    piece[S::kRows * D + S::kRows + row] = l;
                 }
             }
         }
@@ -506,51 +555,67 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                 while (c > 0 && c * all / ctas > tile) --c;
                 return c;
             };
-            const long long c0 = holder(f0), c1 = holder(f1);
+            const long long c0 = holder(f0);
+            const int pieces = static_cast<int>(holder(f1) - c0) + 1;
             __threadfence();
             __syncthreads();
-            int* ticket = reinterpret_cast<int*>(smem + S::kScanOff);
             if (threadIdx.x == 0) {
-                const unsigned int pieces = static_cast<unsigned int>(c1 - c0 + 1);
                 const unsigned int got = atomicAdd(a.counters + c0, 1u);
-                if (got == pieces - 1) a.counters[c0] = 0u;      // left ready for the next call
-                *ticket = got == pieces - 1;
+                *ticket = got == static_cast<unsigned int>(pieces - 1);
+                if (*ticket) a.counters[c0] = 0u;                // left ready for the next call
             }
             __syncthreads();
             if (*ticket) {
+                // a factor a piece and row in shared memory, then all pieces' sums with
+                // independent loads.
                 __threadfence();
-                for (int e = threadIdx.x; e < rows * D; e += S::kThreads) {
-                    const int row = e / D, d = e % D;
-                    float top = -INFINITY, acc = 0.0f, l = 0.0f;
-                    for (long long c = c0; c <= c1; ++c) {
-                        const float* p = a.partials + (2 * c + (c == c0 ? 1 : 0)) * S::kPart;
-                        const float pm = __ldcg(p + S::kRows * D + row);
-                        const float to = fmaxf(top, pm), ref = to == -INFINITY ? 0.0f : to;
-                        const float f = exp2_approx(top - ref), fp = exp2_approx(pm - ref);
-                        acc = fmaf(acc, f, __ldcg(p + row * D + d) * fp);
-                        l = fmaf(l, f, __ldcg(p + S::kRows * D + S::kRows + row) * fp);
-                        top = to;
+                auto part = [&](int p) { return a.partials + (2 * (c0 + p) + (p == 0 ? 1 : 0)) * S::kPart; };
+                float* den = reinterpret_cast<float*>(smem + S::kMiscOff + 64);       // [rows]
+                for (int r = warp; r < rows; r += S::kWarps) {
+                    float top = -INFINITY, l = 0.0f;
+                    for (int p = lane; p < pieces; p += 32) top = fmaxf(top, __ldcg(part(p) + S::kRows * D + r));
+#pragma unroll
+                    for (int q = 16; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
+                    const float ref = top == -INFINITY ? 0.0f : top;
+                    for (int p = lane; p < pieces; p += 32) {
+                        const float f = exp2_approx(__ldcg(part(p) + S::kRows * D + r) - ref);
+                        l = fmaf(__ldcg(part(p) + S::kRows * D + S::kRows + r), f, l);
+                        sums[p * S::kRows + r] = f;
                     }
-                    store_row(a, u.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
+#pragma unroll
+                    for (int q = 16; q > 0; q >>= 1) l += __shfl_xor_sync(0xffffffffu, l, q);
+                    if (lane == 0) den[r] = l;
+                }
+                __syncthreads();
+                for (int e = threadIdx.x * 4; e < rows * D; e += S::kThreads * 4) {
+                    const int row = e / D, d = e % D;
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                    for (int p = 0; p < pieces; ++p) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(p) + e));
+                        const float f = sums[p * S::kRows + row];
+                        acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
+                        acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+                    }
+                    store_row4(a, u.s.start, u.head, u.qt * S::kRows + row, D, d, acc, den[row]);
                 }
             }
         }
-        __syncthreads();                        // the sums are read before the next unit's copies land
-        done += tile1 - tile0;
-        if (done < end) {
-            next_unit<D, NT>(a, u);
-            tile0 = 0;
-        }
+        __syncthreads();                        // the sums are read before the next unit's are stored
+        done = after;
+        tile0 = 0;
     }
+    cp_async_wait<0>();
     griddep_launch_dependents();
 }
 
 template <int D, int NT>
 int launch(const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
     using S = Stream<D, NT>;
+    const int ctas = dev.num_sms < S::kMaxPieces ? dev.num_sms : S::kMaxPieces;   // a unit has at most a piece a CTA
     static std::atomic<unsigned long long> opted{0};
     if (!smem_opt_in(kv_stream_kernel<D, NT>, S::kSmem, opted)) return TRELLIS_ERR_CUDA;
-    const cudaError_t e = launch_programmatic(kv_stream_kernel<D, NT>, static_cast<unsigned>(dev.num_sms),
+    const cudaError_t e = launch_programmatic(kv_stream_kernel<D, NT>, static_cast<unsigned>(ctas),
                                               static_cast<unsigned>(S::kThreads), S::kSmem, stream, a);
     return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
 }
