@@ -95,6 +95,32 @@ struct Unit {
     int tiles;
 };
 
+// A unit costs a CTA at least about as much as streaming kMinTiles tiles (its warps'
+// sums meet, its result is stored), so a shorter one counts as that many in the
+// shares: tile k of a unit stands at its unit's first place + lead + k.
+constexpr int kMinTiles = 3;
+__device__ __forceinline__ int lead_of(int tiles) { return tiles < kMinTiles ? kMinTiles - tiles : 0; }
+
+// Quotient of two counts of places: 32 bits wide but for enormous batches.
+__device__ __forceinline__ long long div_places(long long x, long long y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
+
+// Equal shares of `all` places: the first `rest` of the CTAs hold one more.
+struct Shares {
+    long long each, rest;
+    __device__ __forceinline__ Shares(long long all, long long ctas) {
+        each = div_places(all, ctas);
+        rest = all - each * ctas;
+    }
+    __device__ __forceinline__ long long first(long long cta) const { return cta * each + min(cta, rest); }
+    __device__ __forceinline__ long long holder(long long place) const {
+        const long long wide = rest * (each + 1);
+        return place < wide ? div_places(place, each + 1) : rest + div_places(place - wide, each);
+    }
+};
+
 // Tiles of a query tile, and its token range.
 template <int D, int NT>
 __device__ __forceinline__ int unit_tiles(const AttendArgs& a, const Seq& s, int qt, int* lo, int* hi) {
@@ -108,13 +134,13 @@ __device__ __forceinline__ int unit_tiles(const AttendArgs& a, const Seq& s, int
 }
 
 template <int D, int NT>
-__device__ long long seq_tiles(const AttendArgs& a, const Seq& s) {
+__device__ long long seq_places(const AttendArgs& a, const Seq& s) {
     if (s.n <= 0) return 0;
     const int qts = (s.n * a.group + Stream<D, NT>::kRows - 1) / Stream<D, NT>::kRows;
     long long sum = 0;
     int lo, hi;
-    for (int qt = 0; qt < qts; ++qt) sum += unit_tiles<D, NT>(a, s, qt, &lo, &hi);
-    return sum * a.l.kv_heads;
+    for (int qt = 0; qt < qts; ++qt) sum += max(kMinTiles, unit_tiles<D, NT>(a, s, qt, &lo, &hi));
+    return sum * a.l.kv_heads;                             // places
 }
 
 // A walk over units in their order: heads, then query tiles, then sequences.
@@ -161,7 +187,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     const int per = (a.l.seqs + S::kThreads - 1) / S::kThreads;
     const int s0 = min(a.l.seqs, static_cast<int>(threadIdx.x) * per), s1 = min(a.l.seqs, s0 + per);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += seq_tiles<D, NT>(a, load_seq(a, s));
+    for (int s = s0; s < s1; ++s) mine += seq_places<D, NT>(a, load_seq(a, s));
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -179,31 +205,33 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     const long long ctas = min(static_cast<long long>(gridDim.x), all);
     const long long cta = blockIdx.x;
     if (cta >= ctas) { griddep_launch_dependents(); return; }
-    const long long begin = cta * all / ctas, end = (cta + 1) * all / ctas;
-    // the thread whose sequences hold tile `begin` finds the unit
+    const Shares shares(all, ctas);
+    const long long begin = shares.first(cta), end = shares.first(cta + 1);
+    // the thread whose sequences hold place `begin` finds the unit
     Unit* found = reinterpret_cast<Unit*>(smem + S::kMiscOff + 8 * S::kWarps);
-    int* found_tile = reinterpret_cast<int*>(found + 1);
+    int* found_off = reinterpret_cast<int*>(found + 1);
     long long at = before + incl - mine;
     if (begin >= at && begin < at + mine) {
         Unit f;
         f.seq = s0;
         f.s = load_seq(a, s0);
-        long long c = seq_tiles<D, NT>(a, f.s);
+        long long c = seq_places<D, NT>(a, f.s);
         while (begin >= at + c) {
             at += c;
             f.s = load_seq(a, ++f.seq);
-            c = seq_tiles<D, NT>(a, f.s);
+            c = seq_places<D, NT>(a, f.s);
         }
         long long off = begin - at;
         f.qt = 0;
         f.tiles = unit_tiles<D, NT>(a, f.s, 0, &f.lo, &f.hi);
-        while (off >= static_cast<long long>(f.tiles) * a.l.kv_heads) {
-            off -= static_cast<long long>(f.tiles) * a.l.kv_heads;
+        while (off >= static_cast<long long>(max(kMinTiles, f.tiles)) * a.l.kv_heads) {
+            off -= static_cast<long long>(max(kMinTiles, f.tiles)) * a.l.kv_heads;
             f.tiles = unit_tiles<D, NT>(a, f.s, ++f.qt, &f.lo, &f.hi);
         }
-        f.head = static_cast<int>(off / f.tiles);
+        const int places = max(kMinTiles, f.tiles);
+        f.head = static_cast<int>(div_places(off, places));
         *found = f;
-        *found_tile = static_cast<int>(off % f.tiles);
+        *found_off = static_cast<int>(off - static_cast<long long>(f.head) * places);
     }
     __syncthreads();
 
@@ -231,32 +259,34 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     const int shift = a.l.page_shift - 4;       // blocks of a page, log2
     Walk<D, NT> ahead;
     ahead.begin(a, *found);
-    int ahead_tile = *found_tile;
-    long long ahead_left = end - begin;         // tiles not yet walked over
-    int next_blk = -1, next_page = 0, next_head = 0;
-    // finds this warp's next block and starts the load of its page id
-    auto seek = [&]() {
-        next_blk = -1;
-        while (ahead_left > 0) {
+    long long ahead_base = begin - *found_off;  // first place of the walk's unit
+    int ahead_tile = max(0, *found_off - lead_of(ahead.u.tiles));
+    // this warp's next block; -1: none is left.  Starts the load of its page id.
+    auto seek = [&](int& blk, int& page, int& head) {
+        blk = -1;
+        while (true) {
+            if (ahead_base + lead_of(ahead.u.tiles) + ahead_tile >= end) return;
             if (ahead_tile == ahead.u.tiles) {
+                ahead_base += max(kMinTiles, ahead.u.tiles);
+                if (ahead_base >= end) return;
                 ahead.next(a);
                 ahead_tile = 0;
+                continue;
             }
-            const int blk = ahead.u.lo / kKvBlock + ahead_tile * S::kWarps + warp;
+            const int b = ahead.u.lo / kKvBlock + ahead_tile * S::kWarps + warp;
             ++ahead_tile;
-            --ahead_left;
-            if (blk * kKvBlock < ahead.u.hi) {
-                next_blk = blk;
-                next_head = ahead.u.head;
-                next_page = kv_page(a.l, ahead.u.seq, blk >> shift);
-                break;
+            if (b * kKvBlock < ahead.u.hi) {
+                blk = b;
+                head = ahead.u.head;
+                page = kv_page(a.l, ahead.u.seq, b >> shift);
+                return;
             }
         }
     };
-    auto issue = [&](int slot) {
-        if (next_blk < 0) return;
-        const int in_page = next_blk & ((1 << shift) - 1);
-        const size_t unit = static_cast<size_t>(next_page) * a.l.kv_heads + next_head;
+    auto issue = [&](int slot, int blk, int page, int head) {
+        if (blk < 0) return;
+        const int in_page = blk & ((1 << shift) - 1);
+        const size_t unit = static_cast<size_t>(page) * a.l.kv_heads + head;
         const size_t off = (unit * a.l.page_size + in_page * kKvBlock) * D + lane * 16;
         const uint32_t dst = ring + slot * S::kStepBytes;
 #pragma unroll
@@ -266,20 +296,27 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
         }
         const size_t sc = unit * (a.l.page_size / kKvBlock) + in_page;
         if (lane < 2) cp_async4(ring_sc + slot * 8 + lane * 4, (lane == 0 ? a.k_scales : a.v_scales) + sc);
-        seek();
     };
-    seek();
+    int next_blk, next_page = 0, next_head = 0;
+    {
+        // the first steps' page ids are loaded side by side
+        int blk[S::kSteps - 1], page[S::kSteps - 1] = {}, head[S::kSteps - 1] = {};
 #pragma unroll
-    for (int i = 0; i < S::kSteps - 1; ++i) {
-        issue(i);
-        cp_async_commit();
+        for (int i = 0; i < S::kSteps - 1; ++i) seek(blk[i], page[i], head[i]);
+        seek(next_blk, next_page, next_head);
+#pragma unroll
+        for (int i = 0; i < S::kSteps - 1; ++i) {
+            issue(i, blk[i], page[i], head[i]);
+            cp_async_commit();
+        }
     }
     int slot = 0, fill = S::kSteps - 1;         // ring slots read and filled next
 
     // ---- queries of a unit: raw, loaded a unit ahead ----------------------------------------
     Walk<D, NT> walk;
     walk.begin(a, *found);
-    int tile0 = *found_tile;
+    long long base = begin - *found_off;        // first place of the unit
+    int tile0 = max(0, *found_off - lead_of(walk.u.tiles));
     uint4 raw[NT][KJ][2];
     auto load_queries = [&](const Unit& u) {
 #pragma unroll
@@ -299,9 +336,11 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     };
     load_queries(walk.u);
 
-    for (long long done = begin; done < end;) {
+    while (base < end) {
         const Unit u = walk.u;
-        const int tile1 = static_cast<int>(min(static_cast<long long>(u.tiles), tile0 + (end - done)));
+        // the unit's tiles that stand before this CTA's end; none where only its lead does
+        const int tile1 = static_cast<int>(min(static_cast<long long>(u.tiles), end - base - lead_of(u.tiles)));
+        if (tile1 <= tile0) break;
 
         // f16 fragments, each row times a power of two
         uint32_t qf[NT][4 * KJ][2];
@@ -345,8 +384,9 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
         const int all_hi = min(u.hi, u.s.p0 + u.qt * S::kRows / a.group + 1);
         const int all_lo = a.window > 0
             ? u.s.p0 + min((u.qt * S::kRows + S::kRows - 1) / a.group, u.s.n - 1) + 1 - a.window : 0;
-        const long long after = done + (tile1 - tile0);
-        if (after < end) {
+        const long long unit_base = base;
+        base += max(kMinTiles, u.tiles);
+        if (base < end) {
             walk.next(a);
             load_queries(walk.u);
         }
@@ -367,7 +407,8 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             const int tok0 = u.lo + (tile * S::kWarps + warp) * kKvBlock;
             if (tok0 >= u.hi) break;            // the walk of the copies passes over it too
             __syncwarp();                       // every lane has read the slot that is filled now
-            issue(fill);
+            issue(fill, next_blk, next_page, next_head);
+            if (next_blk >= 0) seek(next_blk, next_page, next_head);
             cp_async_commit();
             cp_async_wait<S::kSteps - 1>();
             __syncwarp();                       // every lane's copies have landed
@@ -548,15 +589,8 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
         }
         if (!whole) {
             // the CTAs that hold the unit's first and last tile
-            const long long f0 = done - tile0, f1 = f0 + u.tiles - 1;
-            auto holder = [&](long long tile) {
-                long long c = tile * ctas / all;
-                while (c + 1 < ctas && (c + 1) * all / ctas <= tile) ++c;
-                while (c > 0 && c * all / ctas > tile) --c;
-                return c;
-            };
-            const long long c0 = holder(f0);
-            const int pieces = static_cast<int>(holder(f1) - c0) + 1;
+            const long long c0 = shares.holder(unit_base + lead_of(u.tiles));
+            const int pieces = static_cast<int>(shares.holder(unit_base + lead_of(u.tiles) + u.tiles - 1) - c0) + 1;
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
@@ -602,7 +636,6 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             }
         }
         __syncthreads();                        // the sums are read before the next unit's are stored
-        done = after;
         tile0 = 0;
     }
     cp_async_wait<0>();
