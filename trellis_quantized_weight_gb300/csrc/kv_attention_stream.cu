@@ -66,8 +66,6 @@ struct Stream {
     static constexpr int kSumsOff = kScaleOff + kWarps * kSteps * 8;
     static constexpr int kMiscOff = kSumsOff + kWarps * kPart * 4;
     static constexpr int kSmem = kMiscOff + 256;
-    // the join of a unit's pieces keeps a factor a piece and row where the warps' sums were
-    static constexpr int kMaxPieces = kWarps * kPart / kRows;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -298,17 +296,12 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
         if (lane < 2) cp_async4(ring_sc + slot * 8 + lane * 4, (lane == 0 ? a.k_scales : a.v_scales) + sc);
     };
     int next_blk, next_page = 0, next_head = 0;
-    {
-        // the first steps' page ids are loaded side by side
-        int blk[S::kSteps - 1], page[S::kSteps - 1] = {}, head[S::kSteps - 1] = {};
-#pragma unroll
-        for (int i = 0; i < S::kSteps - 1; ++i) seek(blk[i], page[i], head[i]);
-        seek(next_blk, next_page, next_head);
-#pragma unroll
-        for (int i = 0; i < S::kSteps - 1; ++i) {
-            issue(i, blk[i], page[i], head[i]);
-            cp_async_commit();
-        }
+    seek(next_blk, next_page, next_head);
+#pragma unroll 1
+    for (int i = 0; i < S::kSteps - 1; ++i) {   // the page ids are neighbours: one miss serves most
+        issue(i, next_blk, next_page, next_head);
+        cp_async_commit();
+        if (next_blk >= 0) seek(next_blk, next_page, next_head);
     }
     int slot = 0, fill = S::kSteps - 1;         // ring slots read and filled next
 
@@ -600,38 +593,45 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             }
             __syncthreads();
             if (*ticket) {
-                // a factor a piece and row in shared memory, then all pieces' sums with
-                // independent loads.
+                // all pieces' sums in their order, eight at a time with independent loads
                 __threadfence();
-                auto part = [&](int p) { return a.partials + (2 * (c0 + p) + (p == 0 ? 1 : 0)) * S::kPart; };
-                float* den = reinterpret_cast<float*>(smem + S::kMiscOff + 64);       // [rows]
-                for (int r = warp; r < rows; r += S::kWarps) {
-                    float top = -INFINITY, l = 0.0f;
-                    for (int p = lane; p < pieces; p += 32) top = fmaxf(top, __ldcg(part(p) + S::kRows * D + r));
-#pragma unroll
-                    for (int q = 16; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    for (int p = lane; p < pieces; p += 32) {
-                        const float f = exp2_approx(__ldcg(part(p) + S::kRows * D + r) - ref);
-                        l = fmaf(__ldcg(part(p) + S::kRows * D + S::kRows + r), f, l);
-                        sums[p * S::kRows + r] = f;
-                    }
-#pragma unroll
-                    for (int q = 16; q > 0; q >>= 1) l += __shfl_xor_sync(0xffffffffu, l, q);
-                    if (lane == 0) den[r] = l;
-                }
-                __syncthreads();
                 for (int e = threadIdx.x * 4; e < rows * D; e += S::kThreads * 4) {
                     const int row = e / D, d = e % D;
+                    float top = -INFINITY, l = 0.0f;
                     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                    for (int p = 0; p < pieces; ++p) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(p) + e));
-                        const float f = sums[p * S::kRows + row];
-                        acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
-                        acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+#pragma unroll 1
+                    for (int p0 = 0; p0 < pieces; p0 += 8) {
+                        float pm[8], pl[8];
+                        float4 v[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int p = min(p0 + q, pieces - 1);
+                            const float* from = a.partials + (2 * (c0 + p) + (p == 0 ? 1 : 0)) * S::kPart;
+                            pm[q] = __ldcg(from + S::kRows * D + row);
+                            pl[q] = __ldcg(from + S::kRows * D + S::kRows + row);
+                            v[q] = __ldcg(reinterpret_cast<const float4*>(from + e));
+                        }
+                        float to = top;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (p0 + q >= pieces) pm[q] = -INFINITY;
+                            to = fmaxf(to, pm[q]);
+                        }
+                        const float ref = to == -INFINITY ? 0.0f : to;
+                        float f = exp2_approx(top - ref);
+                        top = to;
+                        l *= f;
+                        acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            f = exp2_approx(pm[q] - ref);
+                            if (p0 + q >= pieces) continue;
+                            acc.x = fmaf(v[q].x, f, acc.x); acc.y = fmaf(v[q].y, f, acc.y);
+                            acc.z = fmaf(v[q].z, f, acc.z); acc.w = fmaf(v[q].w, f, acc.w);
+                            l = fmaf(pl[q], f, l);
+                        }
                     }
-                    store_row4(a, u.s.start, u.head, u.qt * S::kRows + row, D, d, acc, den[row]);
+                    store_row4(a, u.s.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
                 }
             }
         }
@@ -645,10 +645,9 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
 template <int D, int NT>
 int launch(const AttendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
     using S = Stream<D, NT>;
-    const int ctas = dev.num_sms < S::kMaxPieces ? dev.num_sms : S::kMaxPieces;   // a unit has at most a piece a CTA
     static std::atomic<unsigned long long> opted{0};
     if (!smem_opt_in(kv_stream_kernel<D, NT>, S::kSmem, opted)) return TRELLIS_ERR_CUDA;
-    const cudaError_t e = launch_programmatic(kv_stream_kernel<D, NT>, static_cast<unsigned>(ctas),
+    const cudaError_t e = launch_programmatic(kv_stream_kernel<D, NT>, static_cast<unsigned>(dev.num_sms),
                                               static_cast<unsigned>(S::kThreads), S::kSmem, stream, a);
     return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
 }
