@@ -43,12 +43,21 @@ namespace trellis {
 namespace {
 
 constexpr float kMoveBy = 8.0f;          // the reference moves when exceeded by 2^8
+constexpr int kJoin = 16;                // pieces of a unit that one CTA joins
 
 // Warps of a CTA and ring steps by head width and rows: 128 to 160 KB of codes in
 // flight an SM beside the warps' sums.
 template <int D, int NT> struct StreamShape;
-template <int NT> struct StreamShape<64, NT> { static constexpr int kWarps = 8, kSteps = 8; };
-template <> struct StreamShape<128, 1> { static constexpr int kWarps = 8, kSteps = 5; };
+#ifndef W64
+#define W64 8
+#define S64 8
+#endif
+template <int NT> struct StreamShape<64, NT> { static constexpr int kWarps = W64, kSteps = S64; };
+#ifndef W128
+#define W128 8
+#define S128 5
+#endif
+template <> struct StreamShape<128, 1> { static constexpr int kWarps = W128, kSteps = S128; };
 template <> struct StreamShape<128, 2> { static constexpr int kWarps = 8, kSteps = 4; };
 template <int NT> struct StreamShape<256, NT> { static constexpr int kWarps = 6, kSteps = 3; };
 
@@ -237,6 +246,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     const uint32_t ring_sc = static_cast<uint32_t>(__cvta_generic_to_shared(smem + S::kScaleOff)) + warp * S::kSteps * 8;
     float* sums = reinterpret_cast<float*>(smem + S::kSumsOff);
     int* ticket = reinterpret_cast<int*>(smem + S::kMiscOff);
+    float* joined = reinterpret_cast<float*>(smem + S::kMiscOff + 64);     // [2][rows]
 
     // ---- copies: a walk of its own, steps ahead of the sums and across units ---------------
     // The 16 tokens of a step lie one after another, so copy r of a lane is bytes
@@ -277,6 +287,10 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                 blk = b;
                 head = ahead.u.head;
                 page = kv_page(a.l, ahead.u.seq, b >> shift);
+                // and of the line that the ids of the steps to come lie in
+                const int later = min((b >> shift) + 32, a.l.page_cols - 1);
+                asm volatile("prefetch.global.L1 [%0];"
+                             :: "l"(a.l.pages + static_cast<size_t>(ahead.u.seq) * a.l.page_cols + later));
                 return;
             }
         }
@@ -584,54 +598,84 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             // the CTAs that hold the unit's first and last tile
             const long long c0 = shares.holder(unit_base + lead_of(u.tiles));
             const int pieces = static_cast<int>(shares.holder(unit_base + lead_of(u.tiles) + u.tiles - 1) - c0) + 1;
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const unsigned int got = atomicAdd(a.counters + c0, 1u);
-                *ticket = got == static_cast<unsigned int>(pieces - 1);
-                if (*ticket) a.counters[c0] = 0u;                // left ready for the next call
-            }
-            __syncthreads();
-            if (*ticket) {
-                // all pieces' sums in their order, eight at a time with independent loads
+            // Groups of kJoin pieces are joined by their last CTA into the slot of their first
+            // piece, and the groups by the last of those: the order of the sums is always the
+            // same, and a long sequence's many pieces are not one CTA's chain of loads.
+            auto part = [&](int p) { return a.partials + (2 * (c0 + p) + (p == 0 ? 1 : 0)) * S::kPart; };
+            auto last_of = [&](unsigned int* counter, int of) {
                 __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    const unsigned int got = atomicAdd(counter, 1u);
+                    *ticket = got == static_cast<unsigned int>(of - 1);
+                    if (*ticket) *counter = 0u;                  // left ready for the next call
+                }
+                __syncthreads();
+                const bool yes = *ticket != 0;
+                if (yes) __threadfence();
+                return yes;
+            };
+            // joins pieces from, from + step, ... below to; `final` stores the unit's rows
+            auto join = [&](int from, int to, int step, bool final) {
                 for (int e = threadIdx.x * 4; e < rows * D; e += S::kThreads * 4) {
                     const int row = e / D, d = e % D;
                     float top = -INFINITY, l = 0.0f;
                     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-                    for (int p0 = 0; p0 < pieces; p0 += 8) {
+                    for (int p0 = from; p0 < to; p0 += 8 * step) {
                         float pm[8], pl[8];
                         float4 v[8];
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const int p = min(p0 + q, pieces - 1);
-                            const float* from = a.partials + (2 * (c0 + p) + (p == 0 ? 1 : 0)) * S::kPart;
-                            pm[q] = __ldcg(from + S::kRows * D + row);
-                            pl[q] = __ldcg(from + S::kRows * D + S::kRows + row);
-                            v[q] = __ldcg(reinterpret_cast<const float4*>(from + e));
+                            const int p = p0 + q * step;
+                            const float* src = part(p < to ? p : from);
+                            pm[q] = __ldcg(src + S::kRows * D + row);
+                            pl[q] = __ldcg(src + S::kRows * D + S::kRows + row);
+                            v[q] = __ldcg(reinterpret_cast<const float4*>(src + e));
                         }
-                        float to = top;
+                        float high = top;
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            if (p0 + q >= pieces) pm[q] = -INFINITY;
-                            to = fmaxf(to, pm[q]);
+                            if (p0 + q * step >= to) pm[q] = -INFINITY;
+                            high = fmaxf(high, pm[q]);
                         }
-                        const float ref = to == -INFINITY ? 0.0f : to;
+                        const float ref = high == -INFINITY ? 0.0f : high;
                         float f = exp2_approx(top - ref);
-                        top = to;
+                        top = high;
                         l *= f;
                         acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             f = exp2_approx(pm[q] - ref);
-                            if (p0 + q >= pieces) continue;
+                            if (p0 + q * step >= to) continue;
                             acc.x = fmaf(v[q].x, f, acc.x); acc.y = fmaf(v[q].y, f, acc.y);
                             acc.z = fmaf(v[q].z, f, acc.z); acc.w = fmaf(v[q].w, f, acc.w);
                             l = fmaf(pl[q], f, l);
                         }
                     }
-                    store_row4(a, u.s.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
+                    if (final) {
+                        store_row4(a, u.s.start, u.head, u.qt * S::kRows + row, D, d, acc, l);
+                        continue;
+                    }
+                    // the row's maximum and denominator in its first piece are still read by the
+                    // other threads of the row: they are replaced below, from shared memory
+                    *reinterpret_cast<float4*>(part(from) + e) = acc;
+                    if (d == 0) { joined[row] = top; joined[S::kRows + row] = l; }
+                }
+                if (!final) {
+                    __syncthreads();
+                    if (threadIdx.x < 2 * S::kRows) part(from)[S::kRows * D + threadIdx.x] = joined[threadIdx.x];
+                }
+            };
+            const int mine_p = static_cast<int>(cta - c0);
+            if (pieces <= kJoin) {
+                if (last_of(a.counters + 2 * c0 + 1, pieces)) join(0, pieces, 1, true);
+            } else {
+                const int first = mine_p / kJoin * kJoin, to = min(first + kJoin, pieces);
+                if (last_of(a.counters + 2 * (c0 + first) + (first == 0 ? 1 : 0), to - first)) {
+                    join(first, to, 1, false);
+                    if (last_of(a.counters + 2 * (gridDim.x + c0), (pieces + kJoin - 1) / kJoin))
+                        join(0, pieces, kJoin, true);
                 }
             }
         }
