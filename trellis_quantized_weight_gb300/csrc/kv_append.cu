@@ -12,11 +12,14 @@
 //   codes      e4m3(x / s), nearest even.  When a block's scale grows, the codes from
 //              before are multiplied by the (power of two) ratio and rounded again.
 //
-// One warp owns one (sequence, cache block, key or value head) or one (sequence,
-// 16 new tokens, query head): it holds the block's values in registers between
-// the maximum and the codes, so every input is read from HBM once.  A lane takes
-// 8 consecutive values (16 bytes in, 8 bytes of codes out); a pair's other half in
-// the half layout is read from the neighbour's 16 bytes, an L1 hit.
+// What bounds it: at prompts the bytes (2 in and 1 or 2 out a value); for a step of
+// single tokens the latency of lengths -> page -> values.  A CTA takes one block of 16
+// positions of a sequence and some of its heads ("tasks": a key head, a value head
+// or a query head), a warp a task at a time.  The block's rows of the table are read once a
+// CTA into shared memory.  A lane takes 8 consecutive values a token (16 bytes in, 8 of
+// codes out).  A block's codes need its maximum first: its 16 tokens are read and rotated
+// twice, the second time from L1.  In the half layout a pair's other half comes from another
+// lane by shuffles.
 #include "kv_cache.cuh"
 #include "trellis.h"
 
@@ -25,57 +28,70 @@ namespace trellis {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kAppendCtas = 8;           // an SM: 32 warps at 64 registers
 
 struct AppendArgs {
     KvLayout l;
     const uint16_t *q, *k, *v;
     long long q_stride, k_stride, v_stride;   // elements between packed rows
     const float* rope;                        // [rope_rows, rot]: cosines, then sines; or NULL
-    int rope_rows, rot, interleaved;
+    int rope_rows, rot, interleaved;          // rot = 0 without a table
+    int per_warp;                             // tasks of a warp
     uint8_t *k_codes, *v_codes;
     float *k_scales, *v_scales;
     uint16_t* q_out;                          // [tokens, q_heads, D]
 };
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
-    x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
-    x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+__device__ __forceinline__ void unpack8(uint4 v, float2 (&x)[4]) {
+    x[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+    x[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    x[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+    x[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
 }
 
-// Values 8c .. 8c+7 of a head's row, rotated when they belong to its first `rot`
-// values (rot is a multiple of 16, so a chunk lies in one half).
-__device__ __forceinline__ void load_rotated(const uint16_t* __restrict__ row, int c, const float* __restrict__ table,
-                                             int rot, int interleaved, float (&x)[8]) {
-    const uint4* r4 = reinterpret_cast<const uint4*>(row);
-    const uint4 own = __ldg(r4 + c);
-    unpack8(own, x);
-    if (table == nullptr || 8 * c >= rot) return;
-    const int half = rot >> 1;
+// (x c + y s) for two values: products and sums rounded one by one.  (Two-wide products
+// would be fused into the two-wide sums by the assembler.)
+__device__ __forceinline__ float2 turn2(float2 x, float2 y, float c0, float c1, float s0, float s1) {
+    return make_float2(__fadd_rn(__fmul_rn(x.x, c0), __fmul_rn(y.x, s0)),
+                       __fadd_rn(__fmul_rn(x.y, c1), __fmul_rn(y.y, s1)));
+}
+
+// Where float4 k (two of cosines, two of sines) of the 8 pairs cc of a table row stands in
+// shared memory: 64 bytes for 8 pairs, turned so that the lanes of a quarter warp, which
+// read the same k of neighbouring cc, hit different banks.
+__device__ __forceinline__ int table_slot(int cc, int k) { return 4 * cc + (k ^ ((cc >> 1) & 3)); }
+
+// The 8 values of chunk c of a head's row, rotated by the token's table row in shared
+// memory when they belong to the first `rot` (a multiple of 16, so a chunk lies in one
+// half).  Every lane of the warp calls it; in the half layout lane + `other` holds the
+// chunk of the pairs' other halves.
+__device__ __forceinline__ void rotated(uint4 raw, int c, const float* row, int rot, int interleaved, bool turn,
+                                        float2 (&x)[4]) {
+    unpack8(raw, x);
+    if (rot == 0) return;
+    const int half = rot >> 1, n = half / 8;
+    const float4* row4 = reinterpret_cast<const float4*>(row);
     if (interleaved) {
-        const float4 co = __ldg(reinterpret_cast<const float4*>(table + 4 * c));
-        const float4 si = __ldg(reinterpret_cast<const float4*>(table + half + 4 * c));
+        if (!turn || 8 * c >= rot) return;
+        const float4 co = row4[table_slot(c >> 1, c & 1)], si = row4[table_slot(c >> 1, 2 + (c & 1))];
         const float cs[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cs[i]), __fmul_rn(a, sn[i]));
-        }
+        for (int i = 0; i < 4; ++i) x[i] = turn2(x[i], make_float2(x[i].y, x[i].x), cs[i], cs[i], -sn[i], sn[i]);
     } else {
-        const bool low = 8 * c < half;
-        const int i0 = low ? 8 * c : 8 * c - half;
-        float y[8];
-        unpack8(__ldg(r4 + (low ? c + half / 8 : c - half / 8)), y);
+        const int src = static_cast<int>(threadIdx.x & 31) + (c < n ? n : -n);
+        const uint32_t minus = c < n ? 0x80008000u : 0u;       // a turns to a cos + (-b) sin
+        uint4 o;
+        o.x = __shfl_sync(0xffffffffu, raw.x, src) ^ minus; o.y = __shfl_sync(0xffffffffu, raw.y, src) ^ minus;
+        o.z = __shfl_sync(0xffffffffu, raw.z, src) ^ minus; o.w = __shfl_sync(0xffffffffu, raw.w, src) ^ minus;
+        if (!turn || c >= 2 * n) return;
+        float2 y[4];
+        unpack8(o, y);
+        const int cc = c < n ? c : c - n;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float4 co = __ldg(reinterpret_cast<const float4*>(table + i0) + h);
-            const float4 si = __ldg(reinterpret_cast<const float4*>(table + half + i0) + h);
-            const float cs[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float own_c = __fmul_rn(x[4 * h + i], cs[i]), other_s = __fmul_rn(y[4 * h + i], sn[i]);
-                x[4 * h + i] = low ? __fsub_rn(own_c, other_s) : __fadd_rn(own_c, other_s);
-            }
+            const float4 co = row4[table_slot(cc, h)], si = row4[table_slot(cc, 2 + h)];
+            x[2 * h] = turn2(x[2 * h], y[2 * h], co.x, co.y, si.x, si.y);
+            x[2 * h + 1] = turn2(x[2 * h + 1], y[2 * h + 1], co.z, co.w, si.z, si.w);
         }
     }
 }
@@ -91,121 +107,143 @@ __device__ __forceinline__ float block_scale(uint32_t abits) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_constant__ AppendArgs a) {
-    griddep_wait();
+__global__ void __launch_bounds__(kWarps * 32, kAppendCtas) kv_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kChunks = D / 8;                       // 16-byte chunks of a row
     constexpr int kPer = 32 / kChunks;                   // tokens a warp covers in a pass
-    constexpr int kPasses = kKvBlock / kPer;
+    constexpr int kGroup = 4;                            // passes loaded side by side
+    __shared__ __align__(16) float table[kKvBlock * D];  // the block's rows of `rot` values
     const KvLayout& l = a.l;
-    const int lane = threadIdx.x & 31;
-    const int task = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int s = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = lane % kChunks, sub = lane / kChunks;
-    int start, n;
-    const int kv_tasks = 2 * l.kv_heads;
-    const int tasks = kv_tasks + (a.q_out != nullptr ? l.q_heads : 0);
-    if (task < tasks && kv_rows(l, s, &start, &n)) {
-        const int total = kv_total(l, s);
-        const int p0 = __ldg(l.kv_len + s) - n;          // position of the first new token
-        if (task >= kv_tasks) {
-            // ---- a query head: rotate and store
-            const int h = task - kv_tasks;
-            for (int b = blockIdx.z; b * kKvBlock < n; b += gridDim.z) {
-#pragma unroll 4
-                for (int i = 0; i < kPasses; ++i) {
-                    const int tok = b * kKvBlock + i * kPer + sub;
-                    if (tok >= n) continue;
-                    const int pos = p0 + tok;
-                    // a row before position 0 (an idle slot) is stored as it is
-                    const float* table = a.rope == nullptr || pos < 0
-                        ? nullptr : a.rope + static_cast<size_t>(min(pos, a.rope_rows - 1)) * a.rot;
-                    const size_t row = static_cast<size_t>(start) + tok;
-                    float x[8];
-                    load_rotated(a.q + row * a.q_stride + h * D, c, table, a.rot, a.interleaved, x);
-                    uint4 o;
-                    o.x = pack_bf16x2(x[0], x[1]); o.y = pack_bf16x2(x[2], x[3]);
-                    o.z = pack_bf16x2(x[4], x[5]); o.w = pack_bf16x2(x[6], x[7]);
-                    reinterpret_cast<uint4*>(a.q_out + (row * l.q_heads + h) * D)[c] = o;
-                }
+    const int kv_tasks = 2 * l.kv_heads, tasks = kv_tasks + (a.q_out != nullptr ? l.q_heads : 0);
+    griddep_wait();
+    const int s = blockIdx.y;
+    const Seq q = load_seq(l, s);
+    const int len = q.p0 + q.n;                          // tokens with these, past the table too
+    // blocks of 16 positions (negative ones for rows before position 0), floor division
+    const int b0 = q.p0 >> 4, b1 = (len - 1) >> 4;
+    if (q.n > 0)
+        for (int b = b0 + static_cast<int>(blockIdx.z); b <= b1; b += gridDim.z) {
+            const int first = b * kKvBlock;
+            const int lo = max(q.p0, first), hi = min(len, first + kKvBlock);
+            if (b != b0 + static_cast<int>(blockIdx.z)) __syncthreads();     // the table is read no more
+            for (int e = threadIdx.x; e < (hi - lo) * (a.rot / 4); e += kWarps * 32) {
+                const int tok = e / (a.rot / 4), at = e % (a.rot / 4);
+                const int pos = min(max(lo + tok, 0), a.rope_rows - 1);
+                const bool sine = at >= a.rot / 8;
+                const int f = sine ? at - a.rot / 8 : at;
+                reinterpret_cast<float4*>(table + (lo + tok - first) * a.rot)[table_slot(f >> 1, (sine ? 2 : 0) + (f & 1))] =
+                    __ldg(reinterpret_cast<const float4*>(a.rope + static_cast<size_t>(pos) * a.rot) + at);
             }
-        } else {
-            const bool key = task < l.kv_heads;
-            const int h = key ? task : task - l.kv_heads;
-            const uint16_t* src = key ? a.k : a.v;
-            const long long stride = key ? a.k_stride : a.v_stride;
-            uint8_t* codes = key ? a.k_codes : a.v_codes;
-            float* scales = key ? a.k_scales : a.v_scales;
-            const float* rope = key ? a.rope : nullptr;
-            const int first = max(p0, 0);
-            for (int b = first / kKvBlock + static_cast<int>(blockIdx.z); b * kKvBlock < total; b += gridDim.z) {
-                const int lo = max(first, b * kKvBlock), hi = min(total, (b + 1) * kKvBlock);
-                const int kept = lo - b * kKvBlock;       // tokens of the block from before
-                const int slot0 = (b * kKvBlock) & (l.page_size - 1);
-                const size_t unit = static_cast<size_t>(kv_page(l, s, (b * kKvBlock) >> l.page_shift)) * l.kv_heads + h;
-                uint8_t* out = codes + (unit * l.page_size + slot0) * D;
-                float* scale = scales + unit * (l.page_size / kKvBlock) + slot0 / kKvBlock;
-                float x[kPasses][8];
-                uint32_t most = 0u;
+            if (a.rot > 0) __syncthreads();
+            for (int i = 0; i < a.per_warp; ++i) {
+                const int task = (blockIdx.x * a.per_warp + i) * kWarps + warp;
+                if (task >= tasks) break;
+                const bool query = task >= kv_tasks, key = task < l.kv_heads;
+                const int h = query ? task - kv_tasks : key ? task : task - l.kv_heads;
+                const uint16_t* src = query ? a.q : key ? a.k : a.v;
+                const long long stride = query ? a.q_stride : key ? a.k_stride : a.v_stride;
+                const int rot = query || key ? a.rot : 0;
+                // this lane's chunk of the block's slot 0 (before the rows where the block starts earlier)
+                const uint16_t* lane_src = src + (static_cast<long long>(q.start) + (first + sub - q.p0)) * stride + h * D + 8 * c;
+                // kGroup passes' inputs are loaded side by side
+                auto load = [&](int p0, uint4 (&raw)[kGroup]) {
+                    const uint16_t* at = lane_src + p0 * kPer * stride;
 #pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int pos = b * kKvBlock + i * kPer + sub;
-                    if (pos < lo || pos >= hi) continue;
-                    const float* table = rope == nullptr
-                        ? nullptr : rope + static_cast<size_t>(min(pos, a.rope_rows - 1)) * a.rot;
-                    const size_t row = static_cast<size_t>(start) + (pos - p0);
-                    load_rotated(src + row * stride + h * D, c, table, a.rot, a.interleaved, x[i]);
+                    for (int p = 0; p < kGroup; ++p) {
+                        const int pos = first + (p0 + p) * kPer + sub;
+                        raw[p] = make_uint4(0u, 0u, 0u, 0u);
+                        if (pos >= lo && pos < hi) raw[p] = __ldg(reinterpret_cast<const uint4*>(at));
+                        at += kPer * stride;
+                    }
+                };
+                // passes that hold tokens [from, to) of the block
+                auto passes = [&](int from, int to, auto&& body) {
+#pragma unroll 1
+                    for (int p0 = (from - first) / (kPer * kGroup) * kGroup; first + p0 * kPer < to; p0 += kGroup) {
+                        uint4 raw[kGroup];
+                        load(p0, raw);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(x[i][j]) & 0x7fffffffu);
+                        for (int p = 0; p < kGroup; ++p) {
+                            const int row = (p0 + p) * kPer + sub, pos = first + row;
+                            float2 x[4];
+                            // a query row before position 0 (an idle slot) is stored as it is
+                            rotated(raw[p], c, table + row * a.rot, rot, a.interleaved, pos >= 0, x);
+                            if (pos >= from && pos < to) body(pos, x);
+                        }
+                    }
+                };
+                if (query) {
+                    uint16_t* lane_out = a.q_out + ((static_cast<long long>(q.start) + (first - q.p0)) * l.q_heads + h) * D + 8 * c;
+                    const int out_stride = l.q_heads * D;
+                    passes(lo, hi, [&](int pos, float2 (&x)[4]) {
+                        *reinterpret_cast<uint4*>(lane_out + (pos - first) * out_stride) =
+                            make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                                       pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
+                    });
+                    continue;
                 }
+                // tokens of the block that have a slot: from max(p0, 0) to the table's end
+                const int from = max(lo, 0), to = min(hi, q.total);
+                if (from >= to) continue;
+                const int kept = from - first;            // tokens of the block from before
+                const int slot0 = first & (l.page_size - 1);
+                const size_t unit = static_cast<size_t>(kv_page(l, s, first >> l.page_shift)) * l.kv_heads + h;
+                uint8_t* out = (key ? a.k_codes : a.v_codes) + (unit * l.page_size + slot0) * D;
+                float* scale = (key ? a.k_scales : a.v_scales) + unit * (l.page_size / kKvBlock) + slot0 / kKvBlock;
+                float had = 0.0f;
+                if (kept > 0) had = *scale;
+                uint32_t most = 0u;
+                passes(from, to, [&](int, float2 (&x)[4]) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        most = max(most, max(__float_as_uint(x[j].x) & 0x7fffffffu, __float_as_uint(x[j].y) & 0x7fffffffu));
+                });
                 most = __reduce_max_sync(0xffffffffu, most);
                 float sc = block_scale(most);
                 if (kept > 0) {
-                    const float had = *scale;
                     // NaN on either side stays NaN
                     const float now = (had != had || sc != sc) ? __uint_as_float(0x7fc00000u) : fmaxf(had, sc);
                     if (now != had) {
                         const float ratio = __fdiv_rn(had, now);
-                        for (int t = sub; t < kept; t += kPer) {
-                            uint2* p = reinterpret_cast<uint2*>(out + t * D) + c;
-                            uint2 w = *p;
-                            uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+                        for (int tok = sub; tok < kept; tok += kPer) {
+                            uint2* at = reinterpret_cast<uint2*>(out + tok * D) + c;
+                            uint2 w = *at;
+                            uint32_t ww[2] = {w.x, w.y};
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
+                            for (int j = 0; j < 2; ++j) {
                                 uint32_t u0, u1;
-                                e4m3x4_to_f16x2(ww[q], u0, u1);
+                                e4m3x4_to_f16x2(ww[j], u0, u1);
                                 const float2 f0 = f16x2_to_f32(u0), f1 = f16x2_to_f32(u1);
-                                ww[q] = static_cast<uint32_t>(f32_to_e4m3x2(f0.x * ratio, f0.y * ratio)) |
+                                ww[j] = static_cast<uint32_t>(f32_to_e4m3x2(f0.x * ratio, f0.y * ratio)) |
                                         (static_cast<uint32_t>(f32_to_e4m3x2(f1.x * ratio, f1.y * ratio)) << 16);
                             }
-                            *p = w;
+                            *at = make_uint2(ww[0], ww[1]);
                         }
                     }
                     sc = now;
                 }
                 const float inv = pow2_recip(sc);         // exact: the scale is a power of two
-#pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int pos = b * kKvBlock + i * kPer + sub;
-                    if (pos < lo || pos >= hi) continue;
+                passes(from, to, [&](int pos, float2 (&x)[4]) {
                     uint2 w;
-                    w.x = static_cast<uint32_t>(f32_to_e4m3x2(x[i][0] * inv, x[i][1] * inv)) |
-                          (static_cast<uint32_t>(f32_to_e4m3x2(x[i][2] * inv, x[i][3] * inv)) << 16);
-                    w.y = static_cast<uint32_t>(f32_to_e4m3x2(x[i][4] * inv, x[i][5] * inv)) |
-                          (static_cast<uint32_t>(f32_to_e4m3x2(x[i][6] * inv, x[i][7] * inv)) << 16);
-                    reinterpret_cast<uint2*>(out + (pos - b * kKvBlock) * D)[c] = w;
-                }
+                    w.x = static_cast<uint32_t>(f32_to_e4m3x2(x[0].x * inv, x[0].y * inv)) |
+                          (static_cast<uint32_t>(f32_to_e4m3x2(x[1].x * inv, x[1].y * inv)) << 16);
+                    w.y = static_cast<uint32_t>(f32_to_e4m3x2(x[2].x * inv, x[2].y * inv)) |
+                          (static_cast<uint32_t>(f32_to_e4m3x2(x[3].x * inv, x[3].y * inv)) << 16);
+                    reinterpret_cast<uint2*>(out + (pos - first) * D)[c] = w;
+                });
                 __syncwarp();                             // `had` was read by every lane
                 if (lane == 0) *scale = sc;
             }
         }
-    }
     griddep_launch_dependents();
 }
 
 template <int D>
 cudaError_t launch(const AppendArgs& a, int blocks, cudaStream_t stream) {
     const int tasks = 2 * a.l.kv_heads + (a.q_out != nullptr ? a.l.q_heads : 0);
-    return launch_programmatic_grid(kv_append_kernel<D>, dim3((tasks + kWarps - 1) / kWarps, a.l.seqs, blocks),
+    const int warps = (tasks + a.per_warp - 1) / a.per_warp;
+    return launch_programmatic_grid(kv_append_kernel<D>, dim3((warps + kWarps - 1) / kWarps, a.l.seqs, blocks),
                                     kWarps * 32, 0, stream, a);
 }
 
@@ -283,6 +321,16 @@ extern "C" int trellis_kv_append(const uint16_t* q, long long q_stride, const ui
     const long long deep = 8ll * (tokens / kKvBlock + 2ll * seqs) / seqs;
     if (blocks > deep) blocks = static_cast<int>(deep);
     if (blocks > 16384) blocks = 16384;
+    // tasks of a warp: two, so that fewer CTAs read the same table rows (8165 prompt tokens
+    // and 48 heads: 45.5 us with 2, 46.9 with 1, 49.7 with 4, whose last wave is ragged);
+    // one where that would leave fewer than 16 warps an SM
+    const int tasks = 2 * kv_heads + (q != nullptr ? q_heads : 0);
+    const long long units = (static_cast<long long>(tokens) + kKvBlock - 1) / kKvBlock * tasks;
+    DeviceInfo dev;
+    const int rc_dev = device_info(dev);
+    if (rc_dev != TRELLIS_OK) return rc_dev;
+    const long long per = units / (16ll * dev.num_sms);
+    a.per_warp = static_cast<int>(per < 1 ? 1 : per > 2 ? 2 : per);
     const cudaError_t e = head_dim == 64 ? launch<64>(a, blocks, stream)
                           : head_dim == 128 ? launch<128>(a, blocks, stream) : launch<256>(a, blocks, stream);
     return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;

@@ -78,23 +78,6 @@ struct Stream {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// A sequence as the units need it.
-struct Seq {
-    int start, n, p0, total;      // packed rows; the first one's position; cached tokens
-};
-
-// n <= 0: no rows.  The four loads do not wait for one another.
-__device__ __forceinline__ Seq load_seq(const AttendArgs& a, int s) {
-    const int b = __ldg(a.l.starts + s), e = __ldg(a.l.starts + s + 1), len = __ldg(a.l.kv_len + s);
-    const long long most = static_cast<long long>(a.l.page_cols) << a.l.page_shift;
-    Seq q;
-    q.start = b;
-    q.n = b >= 0 && e <= a.l.tokens ? e - b : 0;
-    q.p0 = len - q.n;
-    q.total = len < most ? len : static_cast<int>(most);
-    return q;
-}
-
 struct Unit {
     int seq, head, qt;        // query tile
     Seq s;
@@ -158,7 +141,7 @@ struct Walk {
 
     __device__ __forceinline__ void begin(const AttendArgs& a, const Unit& first) {
         u = first;
-        ahead = load_seq(a, min(u.seq + 1, a.l.seqs - 1));
+        ahead = load_seq(a.l, min(u.seq + 1, a.l.seqs - 1));
     }
     // The caller knows that there is a unit after this one.
     __device__ __forceinline__ void next(const AttendArgs& a) {
@@ -169,7 +152,7 @@ struct Walk {
             do {
                 u.seq = min(u.seq + 1, a.l.seqs - 1);
                 u.s = ahead;
-                ahead = load_seq(a, min(u.seq + 1, a.l.seqs - 1));
+                ahead = load_seq(a.l, min(u.seq + 1, a.l.seqs - 1));
             } while (u.s.n <= 0 && u.seq < a.l.seqs - 1);
         }
         u.tiles = unit_tiles<D, NT>(a, u.s, u.qt, &u.lo, &u.hi);
@@ -194,7 +177,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     const int per = (a.l.seqs + S::kThreads - 1) / S::kThreads;
     const int s0 = min(a.l.seqs, static_cast<int>(threadIdx.x) * per), s1 = min(a.l.seqs, s0 + per);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += seq_places<D, NT>(a, load_seq(a, s));
+    for (int s = s0; s < s1; ++s) mine += seq_places<D, NT>(a, load_seq(a.l, s));
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -221,11 +204,11 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
     if (begin >= at && begin < at + mine) {
         Unit f;
         f.seq = s0;
-        f.s = load_seq(a, s0);
+        f.s = load_seq(a.l, s0);
         long long c = seq_places<D, NT>(a, f.s);
         while (begin >= at + c) {
             at += c;
-            f.s = load_seq(a, ++f.seq);
+            f.s = load_seq(a.l, ++f.seq);
             c = seq_places<D, NT>(a, f.s);
         }
         long long off = begin - at;

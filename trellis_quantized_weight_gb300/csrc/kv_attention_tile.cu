@@ -179,8 +179,9 @@ __device__ bool find_part(const AttendArgs& a, long long item, int splits, Part&
     int got = -1, qt = 0;
     for (int s1 = a.l.seqs; s1 > 0 && got < 0; s1 -= 32) {
         const int s = s1 - 1 - lane;
-        int start, n, qts = 0;
-        if (s >= 0 && kv_rows(a.l, s, &start, &n)) qts = (n * a.group + kRows - 1) / kRows;
+        Seq q = {};
+        if (s >= 0) q = load_seq(a.l, s);
+        const int qts = q.n > 0 ? (q.n * a.group + kRows - 1) / kRows : 0;
         int incl = qts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -192,15 +193,16 @@ __device__ bool find_part(const AttendArgs& a, long long item, int splits, Part&
             const int src = __ffs(hit) - 1;
             qt = __shfl_sync(0xffffffffu, qts - 1 - static_cast<int>(tile - (incl - qts)), src);
             got = s1 - 1 - src;
+            u.start = __shfl_sync(0xffffffffu, q.start, src);
+            u.n = __shfl_sync(0xffffffffu, q.n, src);
+            u.p0 = __shfl_sync(0xffffffffu, q.p0, src);
+            u.total = __shfl_sync(0xffffffffu, q.total, src);
         }
         tile -= __shfl_sync(0xffffffffu, incl, 31);
     }
     if (got < 0) return false;
     u.seq = got;
     u.qt = qt;
-    kv_rows(a.l, got, &u.start, &u.n);
-    u.total = kv_total(a.l, got);
-    u.p0 = __ldg(a.l.kv_len + got) - u.n;
     const int first = qt * kRows / a.group, last = min(u.n - 1, (qt * kRows + kRows - 1) / a.group);
     u.hi = max(0, min(u.total, u.p0 + last + 1));
     const int low = a.window > 0 ? max(0, u.p0 + first + 1 - a.window) : 0;

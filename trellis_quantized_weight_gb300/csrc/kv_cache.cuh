@@ -27,20 +27,23 @@ struct KvLayout {
     int q_heads, kv_heads, page_size, page_shift;
 };
 
-// Sequence s's packed rows; false when it has none or its range is not inside
-// the packed tokens (nothing of it is touched then).
-__device__ __forceinline__ bool kv_rows(const KvLayout& l, int s, int* start, int* count) {
-    const int a = __ldg(l.starts + s), b = __ldg(l.starts + s + 1);
-    *start = a;
-    *count = b - a;
-    return a >= 0 && b > a && b <= l.tokens;
-}
+// A sequence's rows and tokens.
+struct Seq {
+    int start, n, p0, total;      // packed rows; the first one's position; cached tokens
+};
 
-// Tokens of sequence s that the page table can hold.
-__device__ __forceinline__ int kv_total(const KvLayout& l, int s) {
+// n <= 0: it has no rows, or a range that is not inside the packed tokens (nothing of it
+// is touched then).  Tokens past the page table are left out of `total`.  The three loads
+// do not wait for one another.
+__device__ __forceinline__ Seq load_seq(const KvLayout& l, int s) {
+    const int b = __ldg(l.starts + s), e = __ldg(l.starts + s + 1), len = __ldg(l.kv_len + s);
     const long long most = static_cast<long long>(l.page_cols) << l.page_shift;
-    const int n = __ldg(l.kv_len + s);
-    return n < most ? n : static_cast<int>(most);
+    Seq q;
+    q.start = b;
+    q.n = b >= 0 && e <= l.tokens ? e - b : 0;
+    q.p0 = len - q.n;
+    q.total = len < most ? len : static_cast<int>(most);
+    return q;
 }
 
 // Page of column c of sequence s, clamped into the pool: a wrong id reads or
