@@ -2,32 +2,38 @@
 // longer drafts, on the tensor cores (tcgen05).
 //
 // The same function as the streaming kernel (kv_attention_stream.cu), whose notes on
-// scales, f16 queries and weights and the seldom-moved reference hold here too.  With
-// 128 rows to a key head's tile the products are a dense contraction:
+// scales and on the seldom-moved reference hold here too.  With 128 rows to a key head's
+// tile the products are a dense contraction:
 //
-//   S[row, key] = Q K^T    Q [128, D] and K [64, D] f16 in shared memory, both K-major
-//   O[row, d]  += P V      P [128, 64] f16 in tensor memory, V [64, D] f16 in shared
-//                          memory as the cache has it (tokens x D: "MN-major" for this
-//                          product, so nothing is transposed)
+//   S[row, key] = Q K^T    K: the cache's e4m3 codes as they are, [64 keys, D] in shared
+//                          memory.  A bf16 query has 8 significant bits and e4m3 4, so
+//                          q = hi + lo in two e4m3 numbers, exactly (down to 2^-17 of the
+//                          row's largest value, the row being scaled by a power of
+//                          two): two 8-bit products at twice the rate of one 16-bit
+//                          product, and keys need no conversion.  Q lies in tensor memory.
+//   O[row, d]  += P V      P [128, 64] f16 in tensor memory over the columns that S had,
+//                          V converted to f16 in shared memory as the cache has it
+//                          (tokens x D: "MN-major" for this product, nothing is transposed).
+//                          Weights need more than e4m3's bits; f16 keeps 11.
 //
-// A CTA takes one (sequence, 128 query rows of one key head's group, key head), or a
-// part of its tokens where there are too few units for the SMs, and runs three roles:
+// A CTA an SM works through items: (sequence, QT x 128 query rows of one key head's
+// group, key head), or a part of its tokens where there are too few units for the SMs.
+// QT = 2 query tiles share every loaded tile of keys and values (1 at D = 256, whose sums
+// fill tensor memory), and one's softmax runs beside the other's products.  Roles:
 //
-// * 4 conversion warps: warp w loads the codes of tokens 16w .. 16w+15 of each 64-token
-//   tile (one block of the cache, so one page and one pair of scales), a tile ahead in
-//   registers, and stores them as f16 in the 128-byte-swizzled layout that both
-//   products read: row = token, 64 values (128 bytes) a row, 16-byte chunk c of row r at
-//   c ^ (r % 8), one such panel for each 64 values of D.
-// * 1 thread issues the products.  S is double buffered: S of tile i + 1 is issued
-//   before the wait for P of tile i.
-// * 4 softmax warps, a row a thread: scores from tensor memory, p' = 2^(x - m), sums in
-//   registers, P over the columns that S had.  O is rescaled in tensor memory only when
-//   a row's reference moves.
+// * 1 warp plans: takes the next item from a counter and finds its rows, one item ahead.
+// * 4 warps load: warp w the codes of tokens 16w .. 16w+15 of each 64-token tile (one
+//   block of the cache, so one page and one pair of scales), a tile ahead in registers;
+//   K goes to shared memory as it is, V as f16, both in the 128-byte-swizzled layout:
+//   row = token, 128 bytes a row (a panel), 16-byte chunk c of row r at c ^ (r % 8).
+// * 1 thread issues the products.
+// * 4 warps a query tile do the softmax, a row a thread: scores from tensor memory,
+//   p' = 2^(x - m), sums in registers.  O is rescaled in tensor memory only when a row's
+//   reference moves.  They also store the result and bring in the next item's queries.
 //
-// What bounds it: at long contexts the 4 D flops a (row, key) pair, against 16
-// exponentials a clock and SM at 1 / (4 D) of that rate: for D = 128 the products of a
-// 64-key tile and its 8192 exponentials take about equally long.  Two CTAs an SM
-// (D <= 128) let one's softmax run beside the other's products.
+// What bounds it: per 64-key tile and 128 rows at D = 128 the products take 512 clocks,
+// the exponentials 256 (32 a clock and SM), and the softmax warps' instructions come near
+// the products' time; the tile's shared-memory traffic is 384 clocks.
 //
 // Waits are bounded as in gemm_tc_kernel.cu: one that gives up sets the device error
 // word and its role leaves; the issuing thread always waits for its last products
@@ -42,38 +48,46 @@ __device__ unsigned int g_kv_error = 0u;
 namespace {
 
 constexpr float kMoveBy = 8.0f;
-constexpr int kRows = 128;               // query rows of a unit
+constexpr int kRows = 128;               // query rows of a tile (lanes of tensor memory)
 constexpr int kKeys = 64;                // cached tokens of a tile
-constexpr int kSoftWarps = 4, kConvWarps = 4;
-constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
-constexpr int kScaleSlots = 4;           // tiles whose scales are held
+constexpr int kLoadWarps = 4;
+constexpr int kScaleSlots = 8;           // tiles whose scales are held
 constexpr int kMinChunk = 4;             // fewest tiles of a split unit's part
 
 template <int D>
 struct Tile {
-    static constexpr int kQBytes = kRows * D * 2;
-    static constexpr int kKvBytes = kKeys * D * 2;       // a converted key or value tile
-    static constexpr int kPanel = kKeys * 128;           // 64 values of each of its tokens
-    static constexpr int kQPanel = kRows * 128;
-    static constexpr int kOffK = kQBytes;                // two stages each
-    static constexpr int kOffV = kOffK + 2 * kKvBytes;
-    static constexpr int kOffScale = kOffV + 2 * kKvBytes;
-    static constexpr int kOffBar = kOffScale + kScaleSlots * 4 * 16;
+    static constexpr int kQt = D <= 128 ? 2 : 1;         // query tiles of a CTA
+    static constexpr int kSBufs = D == 128 ? 1 : 2;      // score buffers of a query tile
+    static constexpr int kSoftWarps = 4 * kQt;
+    static constexpr int kThreads = (kSoftWarps + kLoadWarps + 2) * 32;
+    static constexpr int kStages = 3;                    // of keys, and of values
+    static constexpr int kPanel = kKeys * 128;           // 128 bytes of each token of a tile
+    static constexpr int kKPanels = D <= 128 ? 1 : 2;    // a D = 64 row takes half of its 128 bytes
+    static constexpr int kVPanels = D / 64;
+    static constexpr int kOffV = kStages * kKPanels * kPanel;
+    static constexpr int kOffScale = kOffV + kStages * kVPanels * kPanel;
+    static constexpr int kOffPart = kOffScale + kScaleSlots * 4 * 16;
+    static constexpr int kOffBar = kOffPart + 2 * 64;
     // barriers
-    static constexpr int kQFull = 0, kKFull = 1, kSFull = 3, kVFull = 5, kPvDone = 7, kPFull = 9, kDone = 11;
-    static constexpr int kOffTaddr = kOffBar + 12 * 8;
+    static constexpr int kQFull = 0, kJoin = kQt, kKFull = 2 * kQt, kKFree = kKFull + kStages, kVFull = kKFree + kStages,
+                         kVFree = kVFull + kStages, kSFull = kVFree + kStages, kPFull = kSFull + 2 * kQt,
+                         kPvDone = kPFull + kQt, kPartFull = kPvDone + 2 * kQt, kPartFree = kPartFull + 2,
+                         kDone = kPartFree + 2, kBars = kDone + 1;
+    static constexpr int kOffTaddr = kOffBar + kBars * 8;
     static constexpr int kSmem = kOffTaddr + 32 + 1024;  // + rounding of the base to 1 KB
-    static constexpr int kSCol = 0;                      // S / P: 2 x 64 columns
-    static constexpr int kOCol = 2 * kKeys;              // O: D columns
-    static constexpr int kCols = 2 * kKeys + D <= 256 ? 256 : 512;
-    static constexpr int kCtas = D <= 128 ? 2 : 1;       // an SM
-    // f16 operands, fp32 sums; N in bits 17-22, M in 24-28; bit 16: B is MN-major
+    // tensor memory: queries (two terms of D / 4 columns), scores, sums of each query tile
+    static constexpr int kQCols = D / 2;
+    static constexpr int kSCol = kQt * kQCols;
+    static constexpr int kOCol = kSCol + kQt * kSBufs * kKeys;
+    static constexpr int kCols = 512;
+    // fp32 sums; N in bits 17-22, M in 24-28; formats 0 are e4m3 and f16; bit 16: B is MN-major
     static constexpr uint32_t kIdescS = (1u << 4) | (static_cast<uint32_t>(kKeys >> 3) << 17) |
                                         (static_cast<uint32_t>(kRows >> 4) << 24);
     static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) |
                                         (static_cast<uint32_t>(kRows >> 4) << 24);
-    static constexpr size_t kPart = static_cast<size_t>(kRows) * D + 2 * kRows;   // floats of a part's result
-    static_assert(kSmem * kCtas <= 232448, "shared memory");
+    static constexpr size_t kPart = static_cast<size_t>(kRows) * D + 2 * kRows;   // floats of a query tile's partial result
+    static_assert(kOCol + kQt * D <= kCols, "tensor memory");
+    static_assert(kSmem <= 232448, "shared memory");
 };
 
 // ---- PTX wrappers ------------------------------------------------------------------
@@ -115,17 +129,18 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Shared-memory descriptor, 128-byte swizzle: start, leading and stride byte offsets.
-// K-major (both operands of S): 1 KB between groups of 8 rows.  MN-major (V): the
-// stride offset separates groups of 8 tokens, the leading offset panels of 64 values.
+// K-major (keys): 1 KB between groups of 8 tokens.  MN-major (values): the stride offset
+// separates groups of 8 tokens, the leading offset panels of 64 values.
 __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
            (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// Products with A in tensor memory: 8-bit (K = 32 a product) and f16 (K = 16).
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
@@ -159,29 +174,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
                    "r"(r[15]) : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 struct Part {
-    int seq, head, qt;
-    int start, n, p0, total;
+    int seq, head, qt;       // qt: in units of kQt query tiles
+    int start, n, p0;
     int lo, hi;              // cached tokens that the unit's rows see, lo a multiple of 64
     int t0, t1;              // its tiles [t0, t1)
-    int parts;               // of the unit
+    int parts, index;        // of the unit, and this one's
+    int live;                // query tiles that have rows; 0: no more items
+    int unit;
 };
+static_assert(sizeof(Part) <= 64, "part slot");
 
 // The unit and part of work item `item`; false when there is none.  Units are counted
-// from the last query tile of the last sequence, so that the long ones of a causal
+// from the last query tiles of the last sequence, so that the long ones of a causal
 // prompt come first.  One warp calls it.
-__device__ bool find_part(const AttendArgs& a, long long item, int splits, Part& u) {
+template <int kUnitRows>
+__device__ bool find_part(const AttendArgs& a, unsigned int item, int splits, Part& u) {
     const int lane = threadIdx.x & 31;
-    const int split = static_cast<int>(item % splits);
-    item /= splits;
-    u.head = static_cast<int>(item % a.l.kv_heads);
-    long long tile = item / a.l.kv_heads;
-    int got = -1, qt = 0;
+    u.index = static_cast<int>(item % splits);
+    u.unit = static_cast<int>(item / splits);
+    u.head = u.unit % a.l.kv_heads;
+    int tile = u.unit / a.l.kv_heads;
+    int got = -1;
     for (int s1 = a.l.seqs; s1 > 0 && got < 0; s1 -= 32) {
         const int s = s1 - 1 - lane;
         Seq q = {};
         if (s >= 0) q = load_seq(a.l, s);
-        const int qts = q.n > 0 ? (q.n * a.group + kRows - 1) / kRows : 0;
+        const int qts = q.n > 0 ? (q.n * a.group + kUnitRows - 1) / kUnitRows : 0;
         int incl = qts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -191,67 +216,71 @@ __device__ bool find_part(const AttendArgs& a, long long item, int splits, Part&
         const unsigned hit = __ballot_sync(0xffffffffu, tile >= incl - qts && tile < incl);
         if (hit != 0u) {
             const int src = __ffs(hit) - 1;
-            qt = __shfl_sync(0xffffffffu, qts - 1 - static_cast<int>(tile - (incl - qts)), src);
+            u.qt = __shfl_sync(0xffffffffu, qts - 1 - (tile - (incl - qts)), src);
             got = s1 - 1 - src;
             u.start = __shfl_sync(0xffffffffu, q.start, src);
             u.n = __shfl_sync(0xffffffffu, q.n, src);
             u.p0 = __shfl_sync(0xffffffffu, q.p0, src);
-            u.total = __shfl_sync(0xffffffffu, q.total, src);
+            u.hi = __shfl_sync(0xffffffffu, q.total, src);
         }
         tile -= __shfl_sync(0xffffffffu, incl, 31);
     }
     if (got < 0) return false;
     u.seq = got;
-    u.qt = qt;
-    const int first = qt * kRows / a.group, last = min(u.n - 1, (qt * kRows + kRows - 1) / a.group);
-    u.hi = max(0, min(u.total, u.p0 + last + 1));
+    const int row0 = u.qt * kUnitRows, rows = u.n * a.group;
+    const int first = row0 / a.group, last = min(u.n - 1, (row0 + kUnitRows - 1) / a.group);
+    u.hi = max(0, min(u.hi, u.p0 + last + 1));
     const int low = a.window > 0 ? max(0, u.p0 + first + 1 - a.window) : 0;
     u.lo = low & ~(kKeys - 1);
+    u.live = min(kUnitRows, rows - row0 + kRows - 1) / kRows;
     const int tiles = u.hi > u.lo ? (u.hi - u.lo + kKeys - 1) / kKeys : 0;
     const int chunk = max(kMinChunk, (tiles + splits - 1) / splits);
     u.parts = max(1, (tiles + chunk - 1) / chunk);
-    u.t0 = split * chunk;
+    u.t0 = u.index * chunk;
     u.t1 = min(tiles, u.t0 + chunk);
-    return split < u.parts;
+    return u.index < u.parts;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, Tile<D>::kCtas)
-kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits) {
+__global__ void __launch_bounds__(Tile<D>::kThreads, 1)
+kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int items) {
     using T = Tile<D>;
+    constexpr int kQt = T::kQt, kSB = T::kSBufs, kSt = T::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ Part shared_part;
-    __shared__ int shared_ok;
+    __shared__ int joins[kQt];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sraw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
     unsigned char* const smem = smem_raw + (sbase - sraw);
     const uint32_t bars = sbase + T::kOffBar;
     auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+    constexpr int kMmaWarp = T::kSoftWarps + kLoadWarps;   // and the planner's after it
 
-    griddep_wait();
-    if (warp == 0) {
-        Part p;
-        const bool ok = find_part(a, blockIdx.x, splits, p);
-        if (lane == 0) { shared_part = p; shared_ok = ok; }
-    } else if (threadIdx.x == 32) {
-        bar_init(bar(T::kQFull), kSoftWarps);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSt; ++s) {
+            bar_init(bar(T::kKFull + s), kLoadWarps);
+            bar_init(bar(T::kKFree + s), 1);
+            bar_init(bar(T::kVFull + s), kLoadWarps);
+            bar_init(bar(T::kVFree + s), 1);
+        }
+        for (int q = 0; q < kQt; ++q) {
+            bar_init(bar(T::kQFull + q), 4);
+            bar_init(bar(T::kJoin + q), 4);
+            bar_init(bar(T::kSFull + 2 * q), 1);
+            bar_init(bar(T::kSFull + 2 * q + 1), 1);
+            bar_init(bar(T::kPFull + q), 4);
+            bar_init(bar(T::kPvDone + 2 * q), 1);
+            bar_init(bar(T::kPvDone + 2 * q + 1), 1);
+        }
         for (int s = 0; s < 2; ++s) {
-            bar_init(bar(T::kKFull + s), kConvWarps);
-            bar_init(bar(T::kSFull + s), 1);
-            bar_init(bar(T::kVFull + s), kConvWarps);
-            bar_init(bar(T::kPvDone + s), 1);
-            bar_init(bar(T::kPFull + s), kSoftWarps);
+            bar_init(bar(T::kPartFull + s), 1);
+            bar_init(bar(T::kPartFree + s), T::kSoftWarps + kLoadWarps + 1);
         }
         bar_init(bar(T::kDone), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
-    __syncthreads();
-    if (!shared_ok) { griddep_launch_dependents(); return; }
-    const Part u = shared_part;
-    const int tiles = u.t1 - u.t0;                       // 0: the rows see nothing
-    if (warp == kSoftWarps + kConvWarps) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :: "r"(sbase + T::kOffTaddr), "r"(T::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -261,235 +290,306 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits) {
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + T::kOffTaddr);
     float4* const scales = reinterpret_cast<float4*>(smem + T::kOffScale);   // [slot][block]: k scale, log2 v, 1 / v
+    griddep_wait();
 
-    if (warp < kSoftWarps) {
+    // Every role walks the same items: the planner's slot k & 1 holds item k.
+    auto part_at = [&](int k) { return reinterpret_cast<volatile Part*>(smem + T::kOffPart + (k & 1) * 64); };
+    auto take_part = [&](int k, Part& u) {
+        if (!bar_wait(bar(T::kPartFull + (k & 1)), (k >> 1) & 1)) return false;
+        const volatile int* from = reinterpret_cast<const volatile int*>(part_at(k));
+        int* to = reinterpret_cast<int*>(&u);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(Part) / 4); ++i) to[i] = from[i];
+        return u.live > 0;
+    };
+
+    if (warp < T::kSoftWarps) {
         // ------------------------------------------------------------------ softmax
-        const int r = u.qt * kRows + static_cast<int>(threadIdx.x);
-        const int tok = r / a.group;
-        const bool live = tok < u.n;
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        // this row's query: f16 times a power of two, into the swizzled K-major tile
-        float qmul;
-        {
-            const uint16_t* row = a.q + static_cast<size_t>(u.start + (live ? tok : 0)) * a.q_stride +
-                                  (static_cast<size_t>(u.head) * a.group + r % a.group) * D;
-            const uint4* r4 = reinterpret_cast<const uint4*>(row);
-            uint32_t most = 0u;
+        const int qi = warp >> 2;                        // query tile
+        const int row = static_cast<int>(threadIdx.x) & (kRows - 1);
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t q_addr = lane_base + qi * T::kQCols;
+        const uint32_t s_base = lane_base + T::kSCol + qi * kSB * kKeys;
+        const uint32_t o_addr = lane_base + T::kOCol + qi * D;
+        uint32_t meets = 0;
+        uint32_t tiles_all = 0, tiles_mine = 0;          // walked over before this item: by the loaders, by this query tile
+        // Waits for the product with P of this query tile's tile n.  Two barriers in turn: a
+        // parity tells one phase from the next only, and the product before may be running too
+        auto pv_done = [&](uint32_t n) { return bar_wait(bar(T::kPvDone + 2 * qi + (n & 1)), (n >> 1) & 1); };
+        Part u;
+        bool have = take_part(0, u);
+        have = __all_sync(0xffffffffu, have);
+        for (int k = 0; have; ++k) {
+            const bool live_tile = qi < u.live;
+            const int r = (u.qt * kQt + qi) * kRows + row;
+            const int tok = r / a.group;
+            const bool live = tok < u.n;
+            const int tiles = u.t1 - u.t0;               // 0: the rows see nothing
+            // this row's query: a power of two times hi + lo, into tensor memory
+            float qmul = 0.0f;
+            if (live_tile && tiles > 0) {
+                const uint4* r4 = reinterpret_cast<const uint4*>(
+                    a.q + static_cast<size_t>(u.start + (live ? tok : 0)) * a.q_stride +
+                    (static_cast<size_t>(u.head) * a.group + r % a.group) * D);
+                uint32_t most = 0u;
 #pragma unroll 8
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = __ldg(r4 + c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = __ldg(r4 + c);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-            }
-            const int e = query_exponent(most);
-            const float down = live ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.0f;
-            qmul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
-            const uint32_t dst = sbase + threadIdx.x * 128;
-#pragma unroll 8
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = __ldg(r4 + c);
-                const uint32_t at = dst + (c >> 3) * T::kQPanel + ((static_cast<uint32_t>(c & 7) ^ (threadIdx.x & 7)) << 4);
-                sts128(at, f32_to_f16x2(bf16_lo(v.x) * down, bf16_hi(v.x) * down),
-                       f32_to_f16x2(bf16_lo(v.y) * down, bf16_hi(v.y) * down),
-                       f32_to_f16x2(bf16_lo(v.z) * down, bf16_hi(v.z) * down),
-                       f32_to_f16x2(bf16_lo(v.w) * down, bf16_hi(v.w) * down));
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(T::kQFull));
-        }
-        const int limit = min(u.hi, u.p0 + tok + 1);
-        const int lower = a.window > 0 ? u.p0 + tok + 1 - a.window : 0;
-        // tokens that every row of the unit sees
-        const int all_hi = min(u.hi, u.p0 + u.qt * kRows / a.group + 1);
-        const int all_lo = a.window > 0 ? u.p0 + min(u.n - 1, (u.qt * kRows + kRows - 1) / a.group) + 1 - a.window : 0;
-        float m = -INFINITY, l = 0.0f;
-        bool ok = true;
-        for (int i = 0; i < tiles && ok; ++i) {
-            const int b = i & 1;
-            const uint32_t par = (i >> 1) & 1;
-            // the conversion warps stored the scales before they arrived for V; that barrier
-            // cannot run ahead of this wait (V of tile i + 2 needs the product with P of tile
-            // i), as the one for K could
-            ok = bar_wait(bar(T::kSFull + b), par) && bar_wait(bar(T::kVFull + b), par);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            fence_after();
-            const uint32_t s_addr = lane_base + T::kSCol + b * kKeys;
-            uint32_t s0[32], s1[32];
-            tmem_ld32(s0, s_addr);
-            tmem_ld32(s1, s_addr + 32);
-            float4 sc[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sc[k] = scales[(i % kScaleSlots) * 4 + k];
-            wait_ld();
-            const int tok0 = u.lo + (u.t0 + i) * kKeys;
-            float top = -INFINITY;
-            auto score = [&](uint32_t v, int k, int j) {
-                float x = fmaf(__uint_as_float(v), sc[k].x * qmul, sc[k].y);
-                return x;
-            };
-            if (tok0 + kKeys > all_hi || tok0 < all_lo) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float x0 = score(s0[j], j >> 4, j), x1 = score(s1[j], 2 + (j >> 4), j);
-                    const int k0 = tok0 + j, k1 = k0 + 32;
-                    s0[j] = __float_as_uint(k0 < limit && k0 >= lower ? x0 : -INFINITY);
-                    s1[j] = __float_as_uint(k1 < limit && k1 >= lower ? x1 : -INFINITY);
+                    for (int i = 0; i < 4; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    s0[j] = __float_as_uint(score(s0[j], j >> 4, j));
-                    s1[j] = __float_as_uint(score(s1[j], 2 + (j >> 4), j));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
-            if (__any_sync(0xffffffffu, top > m + kMoveBy)) {
-                const float to = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.0f : exp2_approx(m - to);
-                m = to;
-                l *= f;
-                if (i > 0) {
-                    // O holds the tiles before this one
-                    ok = bar_wait(bar(T::kPvDone + (b ^ 1)), ((i - 1) >> 1) & 1);
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    fence_after();
+                // the largest lands in [128, 256); a negative score factor turns the query's sign
+                const int e = query_exponent(most);
+                float down = live ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 128.0f : 0.0f;
+                if (a.scale_log2 < 0.0f) down = -down;
+                qmul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (fabsf(a.scale_log2) * 0.0078125f);
+                if (most >= 0x7f80u) qmul = __uint_as_float(0x7fc00000u);    // e4m3 has no infinity: the row is NaN
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o, lane_base + T::kOCol + c);
-                        wait_ld();
+                for (int c = 0; c < D / 64; ++c) {       // 64 values: 16 columns of each term
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st16(lane_base + T::kOCol + c, o);
-                    }
-                }
-            }
-            const float ref = m == -INFINITY ? 0.0f : m;
-            uint32_t p[16];
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 v = __ldg(r4 + 8 * c + i);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float part = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float p0 = exp2_approx(__uint_as_float(s0[16 * k + 2 * j]) - ref);
-                    const float p1 = exp2_approx(__uint_as_float(s0[16 * k + 2 * j + 1]) - ref);
-                    part += p0 + p1;
-                    p[8 * k + j] = f32_to_f16x2(p0, p1);
-                }
-                l = fmaf(part, sc[k].z, l);
-            }
-            tmem_st16(s_addr, p);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float part = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float p0 = exp2_approx(__uint_as_float(s1[16 * k + 2 * j]) - ref);
-                    const float p1 = exp2_approx(__uint_as_float(s1[16 * k + 2 * j + 1]) - ref);
-                    part += p0 + p1;
-                    p[8 * k + j] = f32_to_f16x2(p0, p1);
-                }
-                l = fmaf(part, sc[2 + k].z, l);
-            }
-            tmem_st16(s_addr + 16, p);
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(T::kPFull + b));
-        }
-        // ---- result -------------------------------------------------------------------
-        if (ok && tiles > 0) {
-            ok = bar_wait(bar(T::kPvDone + ((tiles - 1) & 1)), ((tiles - 1) >> 1) & 1);
-            fence_after();
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        const bool whole = u.parts == 1;
-        const long long unit = blockIdx.x / splits;
-        float* part = whole ? nullptr : a.partials + (unit * splits + blockIdx.x % splits) * T::kPart;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* out = a.out + ((static_cast<size_t>(u.start) + (live ? tok : 0)) * a.l.q_heads +
-                                 static_cast<size_t>(u.head) * a.group + r % a.group) * D;
-        if (ok) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                if (tiles > 0) {
-                    tmem_ld16(o, lane_base + T::kOCol + c);
-                    wait_ld();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = 0u;
-                }
-                if (whole) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        // a row that sees nothing is zero, whatever its sums are
-                        w[j] = l == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-                    if (live) {
-                        reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c + j) * kRows + threadIdx.x] = __uint_as_float(o[j]);
-                }
-            }
-            if (!whole) {
-                part[D * kRows + threadIdx.x] = m;
-                part[D * kRows + kRows + threadIdx.x] = l;
-                // the part that finishes last adds them all, in their order
-                __threadfence();
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (threadIdx.x == 0) {
-                    const unsigned int got = atomicAdd(a.counters + unit, 1u);
-                    shared_ok = got == static_cast<unsigned int>(u.parts - 1);
-                    if (shared_ok) a.counters[unit] = 0u;
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (shared_ok && live) {
-                    __threadfence();
-                    const float* base = a.partials + unit * splits * T::kPart + threadIdx.x;
-                    float top = -INFINITY;
-                    for (int q = 0; q < u.parts; ++q) top = fmaxf(top, __ldcg(base + q * T::kPart + D * kRows));
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    float den = 0.0f;
-                    for (int q = 0; q < u.parts; ++q) {
-                        const float* p = base + q * T::kPart + D * kRows;
-                        den = fmaf(__ldcg(p + kRows), exp2_approx(__ldcg(p) - ref), den);
-                    }
-                    const float s = 1.0f / den;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        float acc[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-                        for (int q = 0; q < u.parts; ++q) {
-                            const float* p = base + q * T::kPart;
-                            const float f = exp2_approx(__ldcg(p + D * kRows) - ref);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[j] = fmaf(__ldcg(p + (c + j) * kRows), f, acc[j]);
+                        for (int h = 0; h < 2; ++h) {
+                            const float x0 = bf16_lo(w[2 * h]) * down, x1 = bf16_hi(w[2 * h]) * down;
+                            const float x2 = bf16_lo(w[2 * h + 1]) * down, x3 = bf16_hi(w[2 * h + 1]) * down;
+                            const uint32_t c01 = f32_to_e4m3x2(x0, x1), c23 = f32_to_e4m3x2(x2, x3);
+                            uint32_t u01 = e4m3x2_to_f16x2(static_cast<uint16_t>(c01));
+                            uint32_t u23 = e4m3x2_to_f16x2(static_cast<uint16_t>(c23));
+                            const float2 f01 = f16x2_to_f32(u01), f23 = f16x2_to_f32(u23);
+                            hi[2 * i + h] = c01 | (c23 << 16);
+                            lo[2 * i + h] = static_cast<uint32_t>(f32_to_e4m3x2(x0 - f01.x, x1 - f01.y)) |
+                                            (static_cast<uint32_t>(f32_to_e4m3x2(x2 - f23.x, x3 - f23.y)) << 16);
                         }
+                    }
+                    tmem_st16(q_addr + 16 * c, hi);
+                    tmem_st16(q_addr + D / 4 + 16 * c, lo);
+                }
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(T::kQFull + qi));
+            }
+            const int limit = min(u.hi, u.p0 + tok + 1);
+            const int lower = a.window > 0 ? u.p0 + tok + 1 - a.window : 0;
+            // tokens that every row of the query tile sees
+            const int row0 = (u.qt * kQt + qi) * kRows;
+            const int all_hi = min(u.hi, u.p0 + row0 / a.group + 1);
+            const int all_lo = a.window > 0 ? u.p0 + min(u.n - 1, (row0 + kRows - 1) / a.group) + 1 - a.window : 0;
+            float m = -INFINITY, l = 0.0f;
+            bool ok = true;
+            for (int i = 0; live_tile && i < tiles; ++i) {
+                const uint32_t sn = tiles_mine + i, gn = tiles_all + i;
+                const uint32_t b = sn % kSB;
+                // the loaders stored the scales before they arrived for V; that barrier cannot
+                // run ahead of this wait (its next use needs the product with this tile's P), as
+                // the one for K could
+                ok = bar_wait(bar(T::kSFull + 2 * qi + b), (sn / kSB) & 1) && bar_wait(bar(T::kVFull + gn % kSt), (gn / kSt) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fence_after();
+                const uint32_t s_addr = s_base + b * kKeys;
+                uint32_t s0[32], s1[32];
+                tmem_ld32(s0, s_addr);
+                tmem_ld32(s1, s_addr + 32);
+                float mul[4], lv[4], iv[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 v = scales[(gn % kScaleSlots) * 4 + c];
+                    mul[c] = v.x * qmul; lv[c] = v.y; iv[c] = v.z;
+                }
+                wait_ld();
+                const int tok0 = u.lo + (u.t0 + i) * kKeys;
+                if (tok0 + kKeys > all_hi || tok0 < all_lo) {
+                    // finished scores in the scores' place where some are hidden
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float x0 = fmaf(__uint_as_float(s0[j]), mul[j >> 4], lv[j >> 4]);
+                        const float x1 = fmaf(__uint_as_float(s1[j]), mul[2 + (j >> 4)], lv[2 + (j >> 4)]);
+                        const int k0 = tok0 + j, k1 = k0 + 32;
+                        s0[j] = __float_as_uint(k0 < limit && k0 >= lower ? x0 : -INFINITY);
+                        s1[j] = __float_as_uint(k1 < limit && k1 >= lower ? x1 : -INFINITY);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) { mul[c] = 1.0f; lv[c] = 0.0f; }
+                }
+                // the largest score: scales are positive, so a block's is that of its largest product
+                float top = -INFINITY;
+                auto block_top = [&](const uint32_t* s, int c) {
+                    float x = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+#pragma unroll
+                    for (int j = 3; j < 15; j += 2) x = max3(x, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                    x = fmaxf(x, __uint_as_float(s[15]));
+                    top = fmaxf(top, fmaf(x, mul[c], lv[c]));
+                };
+                block_top(s0, 0); block_top(s0 + 16, 1); block_top(s1, 2); block_top(s1 + 16, 3);
+                if (__any_sync(0xffffffffu, top > m + kMoveBy)) {
+                    const float to = fmaxf(m, top);
+                    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - to);
+                    m = to;
+                    l *= f;
+                    if (i > 0) {
+                        // O holds the tiles before this one
+                        ok = pv_done(sn - 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o, o_addr + c);
+                            wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st16(o_addr + c, o);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;
+                auto weights = [&](const uint32_t* s, int c, uint32_t* p) {
+                    const float2 mm = make_float2(mul[c], mul[c]), sh = make_float2(lv[c] - ref, lv[c] - ref);
+                    float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), mm, sh);
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        part = __fadd2_rn(part, x);
+                        p[j] = f32_to_f16x2(x.x, x.y);
+                    }
+                    l = fmaf(part.x + part.y, iv[c], l);
+                };
+                uint32_t p[16];
+                weights(s0, 0, p); weights(s0 + 16, 1, p + 8);
+                tmem_st16(s_addr, p);
+                weights(s1, 2, p); weights(s1 + 16, 3, p + 8);
+                tmem_st16(s_addr + 16, p);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(T::kPFull + qi));
+            }
+            if (!ok) break;
+            tiles_all += tiles;
+            if (live_tile) tiles_mine += tiles;
+            // ---- result ---------------------------------------------------------------
+            if (live_tile && tiles > 0) {
+                ok = pv_done(tiles_mine - 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fence_after();
+            }
+            // the next item is known by now; this one's slot is free after its last use
+            const Part v = u;
+            if (live_tile) {
+                const bool whole = v.parts == 1;
+                float* part = a.partials + ((static_cast<size_t>(v.unit) * splits + v.index) * kQt + qi) * T::kPart;
+                const float inv = 1.0f / l;
+                uint16_t* out = a.out + ((static_cast<size_t>(v.start) + (live ? tok : 0)) * a.l.q_heads +
+                                         static_cast<size_t>(v.head) * a.group + r % a.group) * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    if (tiles > 0) {
+                        tmem_ld16(o, o_addr + c);
+                        wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = 0u;
+                    }
+                    if (whole) {
                         uint32_t w[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) w[j] = den == 0.0f ? 0u : pack_bf16x2(acc[2 * j] * s, acc[2 * j + 1] * s);
-                        reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        for (int j = 0; j < 8; ++j)
+                            // a row that sees nothing is zero, whatever its sums are
+                            w[j] = l == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        if (live) {
+                            reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = __uint_as_float(o[j]);
+                    }
+                }
+                fence_before();                          // O is read before the next item's products
+                if (!whole) {
+                    part[D * kRows + row] = m;
+                    part[D * kRows + kRows + row] = l;
+                    // the part that finishes last adds them all, in their order
+                    __threadfence();
+                    // the query tile's four warps: bounded like every wait here
+                    auto meet = [&]() {
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(bar(T::kJoin + qi));
+                        const bool met = bar_wait(bar(T::kJoin + qi), meets & 1);
+                        ++meets;
+                        return __all_sync(0xffffffffu, met) != 0;
+                    };
+                    if (!meet()) break;
+                    if (row == 0) {
+                        unsigned int* counter = a.counters + 2 + static_cast<size_t>(v.unit) * kQt + qi;
+                        joins[qi] = atomicAdd(counter, 1u) == static_cast<unsigned int>(v.parts - 1);
+                        if (joins[qi]) *counter = 0u;
+                    }
+                    if (!meet()) break;
+                    const bool join = joins[qi] != 0;
+                    if (!meet()) break;                  // it is read before the next item's is written
+                    if (join && live) {
+                        __threadfence();
+                        const size_t step = kQt * T::kPart;
+                        const float* base = a.partials + (static_cast<size_t>(v.unit) * splits * kQt + qi) * T::kPart + row;
+                        float top = -INFINITY;
+#pragma unroll 8
+                        for (int q = 0; q < v.parts; ++q) top = fmaxf(top, __ldcg(base + q * step + D * kRows));
+                        const float ref = top == -INFINITY ? 0.0f : top;
+                        float den = 0.0f;
+#pragma unroll 8
+                        for (int q = 0; q < v.parts; ++q) {
+                            const float* from = base + q * step + D * kRows;
+                            den = fmaf(__ldcg(from + kRows), exp2_approx(__ldcg(from) - ref), den);
+                        }
+                        const float s = 1.0f / den;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float acc[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
+#pragma unroll 2
+                            for (int q = 0; q < v.parts; ++q) {
+                                const float* from = base + q * step;
+                                const float f = exp2_approx(__ldcg(from + D * kRows) - ref);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) acc[j] = fmaf(__ldcg(from + (c + j) * kRows), f, acc[j]);
+                            }
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) w[j] = den == 0.0f ? 0u : pack_bf16x2(acc[2 * j] * s, acc[2 * j + 1] * s);
+                            reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
+            have = __all_sync(0xffffffffu, take_part(k + 1, u));
         }
-    } else if (warp < kSoftWarps + kConvWarps) {
-        // --------------------------------------------------------------- conversion
-        constexpr int P = D / 64;                        // panels of 64 values
-        const int w = warp - kSoftWarps;                 // tokens 16w .. 16w + 15 of a tile
-        const int c4 = lane & 3, r8 = lane >> 2;         // 16 codes c4 of a panel's 64, tokens r8 and r8 + 8
-        uint4 kraw[2][P], vraw[2][P];
-        float ks = 0.0f, vs = 0.0f;
-        // codes of tile i: base of this warp's block (null past the last token)
+    } else if (warp < T::kSoftWarps + kLoadWarps) {
+        // ------------------------------------------------------------------ loads
+        const int w = warp - T::kSoftWarps;              // tokens 16w .. 16w + 15 of a tile
+        constexpr int kKc = D / 16;                      // 16-byte chunks of a token's codes
+        constexpr int kKLoads = kKvBlock * kKc / 32;     // of a lane: whole lines, for K
+        constexpr int P = T::kVPanels;
+        const int c4 = lane & 3, r8 = lane >> 2;         // for V: 16 codes c4 of a panel's 64, tokens r8 and r8 + 8
+        uint4 kraw[kKLoads], vraw[2][P];
+        float ks = 1.0f, vs = 1.0f;
+        Part u = {};
+        uint32_t gn = 0;                                 // tiles so far
+        // this warp's block of tile i; false past the last token
         auto block_of = [&](int i, size_t* unit, int* in_page) {
             const int t = u.lo + (u.t0 + i) * kKeys + 16 * w;
             if (t >= u.hi) return false;
@@ -497,161 +597,234 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits) {
             *in_page = t & (a.l.page_size - 1);
             return true;
         };
-        auto load = [&](const uint8_t* codes, size_t unit, int in_page, bool in, uint4 (&raw)[2][P]) {
-            const uint8_t* src = codes + (unit * a.l.page_size + in_page) * D + c4 * 16;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    raw[h][p] = in ? __ldg(reinterpret_cast<const uint4*>(src + (r8 + 8 * h) * D + p * 64))
-                                   : make_uint4(0u, 0u, 0u, 0u);
-        };
-        // store as f16: token row 16w + 8h + r8 of panel p, chunks 2 c4 and 2 c4 + 1
-        auto store = [&](uint32_t dst, const uint4 (&raw)[2][P], int valid) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool keep = r8 + 8 * h < valid;
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const uint32_t in[4] = {raw[h][p].x, raw[h][p].y, raw[h][p].z, raw[h][p].w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) e4m3x4_to_f16x2(keep ? in[j] : 0u, o[2 * j], o[2 * j + 1]);
-                    const uint32_t row = dst + p * T::kPanel + (16 * w + 8 * h + r8) * 128;
-                    const uint32_t c = 2 * c4;
-                    sts128(row + (((c) ^ r8) << 4), o[0], o[1], o[2], o[3]);
-                    sts128(row + (((c + 1) ^ r8) << 4), o[4], o[5], o[6], o[7]);
-                }
-            }
-        };
         size_t unit = 0;
         int in_page = 0;
-        bool in = tiles > 0 && block_of(0, &unit, &in_page);
-        auto load_scales = [&]() {
+        bool in = false;
+        auto load_k = [&]() {
+            const uint8_t* src = a.k_codes + (unit * a.l.page_size + in_page) * D + lane * 16;
+#pragma unroll
+            for (int r = 0; r < kKLoads; ++r)
+                kraw[r] = in ? __ldg(reinterpret_cast<const uint4*>(src + r * 512)) : make_uint4(0u, 0u, 0u, 0u);
             const size_t at = unit * (a.l.page_size / kKvBlock) + in_page / kKvBlock;
             ks = in ? __ldg(a.k_scales + at) : 1.0f;
             vs = in ? __ldg(a.v_scales + at) : 1.0f;
         };
-        load(a.k_codes, unit, in_page, in, kraw);
-        load(a.v_codes, unit, in_page, in, vraw);
-        load_scales();
-        for (int i = 0; i < tiles; ++i) {
-            const int b = i & 1;
-            const int valid = u.hi - (u.lo + (u.t0 + i) * kKeys + 16 * w);   // tokens of the block that count
-            // stage b is free when the products of tile i - 2 are done
-            bool ok = i < 2 || bar_wait(bar(T::kSFull + b), ((i - 2) >> 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) scales[(i % kScaleSlots) * 4 + w] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
-            store(sbase + T::kOffK + b * T::kKvBytes, kraw, valid);
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(T::kKFull + b));
-            const bool more = i + 1 < tiles;
-            in = more && block_of(i + 1, &unit, &in_page);
-            load(a.k_codes, unit, in_page, in, kraw);
-            load_scales();
-            ok = i < 2 || bar_wait(bar(T::kPvDone + b), ((i - 2) >> 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            store(sbase + T::kOffV + b * T::kKvBytes, vraw, valid);
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(T::kVFull + b));
-            load(a.v_codes, unit, in_page, in, vraw);
-        }
-    } else if (lane == 0) {
-        // ----------------------------------------------------------------- products
-        bool ok = tiles == 0 || bar_wait(bar(T::kQFull), 0);
-        auto scores = [&](int i) {
-            const uint32_t kb = sbase + T::kOffK + (i & 1) * T::kKvBytes;
+        auto load_v = [&]() {
+            const uint8_t* src = a.v_codes + (unit * a.l.page_size + in_page) * D + c4 * 16;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k & 3) * 32;       // 16 values inside a panel's 128-byte row
-                mma_ss(tmem + T::kSCol + (i & 1) * kKeys, desc(sbase + (k >> 2) * T::kQPanel + off, 16),
-                       desc(kb + (k >> 2) * T::kPanel + off, 16), T::kIdescS, k > 0);
-            }
-            commit(bar(T::kSFull + (i & 1)));
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    vraw[h][p] = in ? __ldg(reinterpret_cast<const uint4*>(src + (r8 + 8 * h) * D + p * 64))
+                                    : make_uint4(0u, 0u, 0u, 0u);
         };
-        if (ok && tiles > 0) {
-            ok = bar_wait(bar(T::kKFull), 0);
-            if (ok) { fence_after(); scores(0); }
-        }
-        for (int i = 0; i < tiles && ok; ++i) {
-            const int b = i & 1;
-            const uint32_t par = (i >> 1) & 1;
-            if (i + 1 < tiles) {
-                // S of tile i + 1 takes the columns that P of tile i - 1 had: its product
-                // was issued before by this thread, and the tensor pipe runs in order
-                ok = bar_wait(bar(T::kKFull + (b ^ 1)), ((i + 1) >> 1) & 1);
-                if (!ok) break;
-                fence_after();
-                scores(i + 1);
-            }
-            ok = bar_wait(bar(T::kVFull + b), par) && bar_wait(bar(T::kPFull + b), par);
-            if (!ok) break;
-            fence_after();
-            const uint32_t vb = sbase + T::kOffV + b * T::kKvBytes;
+        bool run = true;
+        for (int k = 0; run; ++k) {
+            if (!__all_sync(0xffffffffu, take_part(k, u))) break;
+            const int tiles = u.t1 - u.t0;
+            in = tiles > 0 && block_of(0, &unit, &in_page);
+            load_k();
+            load_v();
+            for (int i = 0; i < tiles; ++i, ++gn) {
+                const uint32_t st = gn % kSt, turn = gn / kSt;
+                // a stage is free when its last tile's products are done
+                bool ok = turn == 0 || bar_wait(bar(T::kKFree + st), (turn - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
+                if (lane == 0) scales[(gn % kScaleSlots) * 4 + w] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
+                const uint32_t kdst = sbase + st * T::kKPanels * T::kPanel;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-                mma_ts(tmem + T::kOCol, tmem + T::kSCol + b * kKeys + k * 8, desc(vb + k * 2048, T::kPanel), T::kIdescO,
-                       i > 0 || k > 0);
-            commit(bar(T::kPvDone + b));
+                for (int r = 0; r < kKLoads; ++r) {
+                    const int chunk = r * 32 + lane, tk = chunk / kKc, c = chunk % kKc;
+                    sts128(kdst + (c >> 3) * T::kPanel + (16 * w + tk) * 128 + (((c & 7) ^ (tk & 7)) << 4), kraw[r].x, kraw[r].y,
+                           kraw[r].z, kraw[r].w);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(T::kKFull + st));
+                // tokens of the block that count: what lies past them may be anything, NaN
+                // codes too, and 0 times NaN is not 0.  (Scores of such keys are masked.)
+                const int valid = u.hi - (u.lo + (u.t0 + i) * kKeys + 16 * w);
+                in = i + 1 < tiles && block_of(i + 1, &unit, &in_page);
+                load_k();
+                ok = turn == 0 || bar_wait(bar(T::kVFree + st), (turn - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
+                if (valid < kKvBlock) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+                            if (r8 + 8 * h >= valid) vraw[h][p] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                const uint32_t vdst = sbase + T::kOffV + st * T::kVPanels * T::kPanel;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const uint32_t code[4] = {vraw[h][p].x, vraw[h][p].y, vraw[h][p].z, vraw[h][p].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) e4m3x4_to_f16x2(code[j], o[2 * j], o[2 * j + 1]);
+                        const uint32_t at = vdst + p * T::kPanel + (16 * w + 8 * h + r8) * 128;
+                        sts128(at + (((2 * c4) ^ r8) << 4), o[0], o[1], o[2], o[3]);
+                        sts128(at + (((2 * c4 + 1) ^ r8) << 4), o[4], o[5], o[6], o[7]);
+                    }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(T::kVFull + st));
+                load_v();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
         }
-        // nothing is in flight when the tensor memory is released
-        commit(bar(T::kDone));
-        (void)bar_wait(bar(T::kDone), 0);
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            // ------------------------------------------------------------- products
+            // so far: tiles of the loaders and of each query tile, and its items
+            uint32_t gn = 0, sn[kQt], qn[kQt];
+#pragma unroll
+            for (int q = 0; q < kQt; ++q) sn[q] = qn[q] = 0;
+            Part u;
+            bool ok = true;
+            for (int k = 0; ok && take_part(k, u); ++k) {
+                const int tiles = u.t1 - u.t0;
+                // S of query tile q with tile i of this item.  It takes the columns of an earlier
+                // tile's P, whose product this thread issued before: the tensor pipe runs in order
+                auto scores = [&](int q, int i) {
+                    const uint32_t st = (gn + i) % kSt, n = sn[q] + i;
+                    if (q == 0) {
+                        if (!bar_wait(bar(T::kKFull + st), ((gn + i) / kSt) & 1)) return false;
+                        fence_after();
+                    }
+                    const uint32_t kb = sbase + st * T::kKPanels * T::kPanel;
+                    const uint32_t d = tmem + T::kSCol + (q * kSB + n % kSB) * kKeys;
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int s = 0; s < D / 32; ++s)
+                            mma_e4m3(d, tmem + q * T::kQCols + term * (D / 4) + s * 8,
+                                     desc(kb + (s >> 2) * T::kPanel + (s & 3) * 32, 16), T::kIdescS, term + s > 0);
+                    commit(bar(T::kSFull + 2 * q + n % kSB));
+                    if (q == u.live - 1) commit(bar(T::kKFree + st));
+                    return true;
+                };
+#pragma unroll
+                for (int q = 0; q < kQt; ++q)
+                    if (ok && q < u.live && tiles > 0) {
+                        ok = bar_wait(bar(T::kQFull + q), qn[q]++ & 1);
+                        fence_after();
+                        ok = ok && scores(q, 0);
+                    }
+                for (int i = 0; ok && i < tiles; ++i) {
+                    const uint32_t st = (gn + i) % kSt;
+#pragma unroll
+                    for (int q = 0; q < kQt; ++q) {
+                        if (!ok || q >= u.live) break;
+                        if (kSB == 2 && i + 1 < tiles && !(ok = scores(q, i + 1))) break;
+                        ok = (q > 0 || bar_wait(bar(T::kVFull + st), ((gn + i) / kSt) & 1)) &&
+                             bar_wait(bar(T::kPFull + q), (sn[q] + i) & 1);
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t vb = sbase + T::kOffV + st * T::kVPanels * T::kPanel;
+                        const uint32_t p = tmem + T::kSCol + (q * kSB + (sn[q] + i) % kSB) * kKeys;
+#pragma unroll
+                        for (int s = 0; s < kKeys / 16; ++s)
+                            mma_f16_ts(tmem + T::kOCol + q * D, p + s * 8, desc(vb + s * 2048, T::kPanel), T::kIdescO,
+                                       i > 0 || s > 0);
+                        commit(bar(T::kPvDone + 2 * q + ((sn[q] + i) & 1)));
+                        if (q == u.live - 1) commit(bar(T::kVFree + st));
+                        if (kSB == 1 && i + 1 < tiles) ok = scores(q, i + 1);
+                    }
+                }
+                gn += tiles;
+#pragma unroll
+                for (int q = 0; q < kQt; ++q)
+                    if (q < u.live) sn[q] += tiles;
+                bar_arrive(bar(T::kPartFree + (k & 1)));
+            }
+            // nothing is in flight when the tensor memory is released
+            commit(bar(T::kDone));
+            (void)bar_wait(bar(T::kDone), 0);
+        }
+    } else {
+        // ---------------------------------------------------------------------- plan
+        for (int k = 0;; ++k) {
+            if (k >= 2 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPartFree + (k & 1)), ((k >> 1) - 1) & 1))) break;
+            Part u = {};
+            bool found = false, last = false;
+            while (!found) {
+                unsigned int item = 0;
+                if (lane == 0) item = atomicAdd(a.counters, 1u);
+                item = __shfl_sync(0xffffffffu, item, 0);
+                if (item >= items) { last = true; break; }
+                found = find_part<kQt * kRows>(a, item, splits, u);
+            }
+            if (last) u.live = 0;
+            if (lane == 0) {
+                *const_cast<Part*>(part_at(k)) = u;
+                bar_arrive(bar(T::kPartFull + (k & 1)));
+            }
+            if (last) break;
+        }
+        // the CTA that leaves last puts the counters back
+        if (lane == 0 && atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
+            a.counters[0] = 0u;
+            a.counters[1] = 0u;
+        }
     }
 
     griddep_launch_dependents();
     fence_before();
     __syncthreads();
-    if (warp == kSoftWarps + kConvWarps) {
+    if (warp == kMmaWarp) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(T::kCols) : "memory");
     }
 }
 
+int unit_rows(int head_dim) { return head_dim <= 128 ? 2 * kRows : kRows; }
+
 // Units that the packed rows can make (their lengths are on the device): a partial tile
 // a sequence at most.
-long long unit_bound(int tokens, int seqs, int group, int kv_heads) {
+long long unit_bound(int tokens, int seqs, int group, int kv_heads, int head_dim) {
     const long long rows = static_cast<long long>(tokens) * group;
-    const long long t = rows / kRows + seqs, most = rows;
-    return (t < most ? t : most) * kv_heads;
+    const long long t = rows / unit_rows(head_dim) + seqs;
+    return (t < rows ? t : rows) * kv_heads;
 }
 
-// Parts that a unit's tokens are cut into: one where the units fill the SMs' CTAs
-// twice, else enough for that.
-int split_count(long long units, int ctas) {
-    const long long want = 2ll * ctas;
-    if (units >= want) return 1;
-    const long long s = (want + units - 1) / units;
-    return static_cast<int>(s);
+// Parts that a unit's tokens are cut into: one where the units fill the SMs four
+// times, else enough for that.
+int split_count(long long units, int sms) {
+    const long long want = 4ll * sms;
+    return units >= want ? 1 : static_cast<int>((want + units - 1) / units);
 }
 
 template <int D>
-int launch(const AttendArgs& a, long long units, int splits, cudaStream_t stream) {
+int launch(const AttendArgs& a, long long units, int splits, int sms, cudaStream_t stream) {
     using T = Tile<D>;
     static std::atomic<unsigned long long> opted{0};
     if (!smem_opt_in(kv_tile_kernel<D>, T::kSmem, opted)) return TRELLIS_ERR_CUDA;
-    const cudaError_t e = launch_programmatic(kv_tile_kernel<D>, static_cast<unsigned>(units * splits),
-                                              static_cast<unsigned>(kThreads), T::kSmem, stream, a, splits);
+    const unsigned items = static_cast<unsigned>(units * splits);
+    const cudaError_t e = launch_programmatic(kv_tile_kernel<D>, items < static_cast<unsigned>(sms) ? items : static_cast<unsigned>(sms),
+                                              static_cast<unsigned>(T::kThreads), T::kSmem, stream, a, splits, items);
     return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
 }
 
 }  // namespace
 
 size_t kv_tile_workspace_bytes(int tokens, int seqs, int q_heads, int kv_heads, int head_dim, const DeviceInfo& dev) {
-    const long long units = unit_bound(tokens > 0 ? tokens : 1, seqs, q_heads / kv_heads, kv_heads);
-    const int splits = split_count(units, dev.num_sms * (head_dim <= 128 ? 2 : 1));
+    const long long units = unit_bound(tokens > 0 ? tokens : 1, seqs, q_heads / kv_heads, kv_heads, head_dim);
+    const int splits = split_count(units, dev.num_sms);
     if (splits == 1) return kKvCounterBytes;
-    return kKvCounterBytes + static_cast<size_t>(units) * splits * (static_cast<size_t>(kRows) * head_dim + 2 * kRows) * 4;
+    return kKvCounterBytes + static_cast<size_t>(units) * splits * unit_rows(head_dim) * (static_cast<size_t>(head_dim) + 2) * 4;
 }
 
 int launch_kv_tile(const AttendArgs& a, int head_dim, const DeviceInfo& dev, cudaStream_t stream) {
-    const long long units = unit_bound(a.l.tokens, a.l.seqs, a.group, a.l.kv_heads);
-    const int splits = split_count(units, dev.num_sms * (head_dim <= 128 ? 2 : 1));
+    const long long units = unit_bound(a.l.tokens, a.l.seqs, a.group, a.l.kv_heads, head_dim);
+    const int splits = split_count(units, dev.num_sms);
     if (units * splits >= (1ll << 31)) return TRELLIS_ERR_SHAPE;
-    return head_dim == 64 ? launch<64>(a, units, splits, stream)
-           : head_dim == 128 ? launch<128>(a, units, splits, stream) : launch<256>(a, units, splits, stream);
+    return head_dim == 64 ? launch<64>(a, units, splits, dev.num_sms, stream)
+           : head_dim == 128 ? launch<128>(a, units, splits, dev.num_sms, stream)
+                             : launch<256>(a, units, splits, dev.num_sms, stream);
 }
 
 int kv_take_device_error(unsigned int* flags) {
