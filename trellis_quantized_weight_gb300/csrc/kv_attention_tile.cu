@@ -57,14 +57,19 @@ constexpr int kMinChunk = 4;             // fewest tiles of a split unit's part
 template <int D>
 struct Tile {
     static constexpr int kQt = D <= 128 ? 2 : 1;         // query tiles of a CTA
-    static constexpr int kSBufs = D == 128 ? 1 : 2;      // score buffers of a query tile
+    static constexpr int kSBufs = 2;                     // score buffers of a query tile
     static constexpr int kSoftWarps = 4 * kQt;
     static constexpr int kThreads = (kSoftWarps + kLoadWarps + 2) * 32;
     static constexpr int kStages = 3;                    // of keys, and of values
     static constexpr int kPanel = kKeys * 128;           // 128 bytes of each token of a tile
     static constexpr int kKPanels = D <= 128 ? 1 : 2;    // a D = 64 row takes half of its 128 bytes
     static constexpr int kVPanels = D / 64;
-    static constexpr int kOffV = kStages * kKPanels * kPanel;
+    // queries: hi and lo terms of 128 bytes a row and panel; at D = 64 one row holds both
+    static constexpr int kQPanel = kRows * 128;
+    static constexpr int kQTerm = kKPanels * kQPanel;    // from a row's hi term to its lo term (64 bytes at D = 64)
+    static constexpr int kQBytes = D == 64 ? kQPanel : 2 * kQTerm;
+    static constexpr int kOffK = kQt * kQBytes;
+    static constexpr int kOffV = kOffK + kStages * kKPanels * kPanel;
     static constexpr int kOffScale = kOffV + kStages * kVPanels * kPanel;
     static constexpr int kOffPart = kOffScale + kScaleSlots * 4 * 16;
     static constexpr int kOffBar = kOffPart + 2 * 64;
@@ -75,9 +80,8 @@ struct Tile {
                          kDone = kPartFree + 2, kBars = kDone + 1;
     static constexpr int kOffTaddr = kOffBar + kBars * 8;
     static constexpr int kSmem = kOffTaddr + 32 + 1024;  // + rounding of the base to 1 KB
-    // tensor memory: queries (two terms of D / 4 columns), scores, sums of each query tile
-    static constexpr int kQCols = D / 2;
-    static constexpr int kSCol = kQt * kQCols;
+    // tensor memory: scores (P over them) and sums of each query tile
+    static constexpr int kSCol = 0;
     static constexpr int kOCol = kSCol + kQt * kSBufs * kKeys;
     static constexpr int kCols = 512;
     // fp32 sums; N in bits 17-22, M in 24-28; formats 0 are e4m3 and f16; bit 16: B is MN-major
@@ -135,14 +139,35 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
            (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// Products with A in tensor memory: 8-bit (K = 32 a product) and f16 (K = 16).
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// One 8-bit product (K = 32) with both operands in shared memory, and one f16 product
+// (K = 16) with A in tensor memory.  The issuing thread is the bottleneck if an issue
+// costs it more than the product (48 and 64 clocks here), so descriptors are a base and
+// an immediate: offsets (in 16 bytes) only reach the address field.
+template <int kOffA, int kOffB, bool kAcc>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n add.s64 x, %1, %5;\n add.s64 y, %2, %6;\n"
+                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "n"(kAcc ? 1 : 0), "n"(kOffA >> 4), "n"(kOffB >> 4) : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+template <int kOffA, int kOffB>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n .reg .b32 x;\n setp.ne.b32 p, %4, 0;\n add.s32 x, %1, %5;\n add.s64 y, %2, %6;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kOffA), "n"(kOffB >> 4) : "memory");
+}
+// Every 32 (16) steps of the sums of a tile, unrolled.
+template <int D, int kTerm, int kStep>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k) {
+    using T = Tile<D>;
+    constexpr int off = (kStep >> 2) * T::kQPanel + (kStep & 3) * 32;
+    mma_e4m3<off + kTerm * (D == 64 ? 64 : T::kQTerm), (kStep >> 2) * T::kPanel + (kStep & 3) * 32, (kTerm + kStep > 0)>(d, q, k, T::kIdescS);
+    if constexpr (kStep + 1 < D / 32) mma_scores<D, kTerm, kStep + 1>(d, q, k);
+    else if constexpr (kTerm == 0) mma_scores<D, 1, 0>(d, q, k);
+}
+template <int D, int kStep>
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t p, uint64_t v, uint32_t acc) {
+    mma_f16<kStep * 8, kStep * 2048>(d, p, v, Tile<D>::kIdescO, acc);
+    if constexpr (kStep + 1 < kKeys / 16) mma_values<D, kStep + 1>(d, p, v, 1u);
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -308,7 +333,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         const int qi = warp >> 2;                        // query tile
         const int row = static_cast<int>(threadIdx.x) & (kRows - 1);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t q_addr = lane_base + qi * T::kQCols;
+        const uint32_t q_row = sbase + qi * T::kQBytes + row * 128;
         const uint32_t s_base = lane_base + T::kSCol + qi * kSB * kKeys;
         const uint32_t o_addr = lane_base + T::kOCol + qi * D;
         uint32_t meets = 0;
@@ -325,7 +350,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             const int tok = r / a.group;
             const bool live = tok < u.n;
             const int tiles = u.t1 - u.t0;               // 0: the rows see nothing
-            // this row's query: a power of two times hi + lo, into tensor memory
+            // this row's query: a power of two times hi + lo, swizzled K-major rows
             float qmul = 0.0f;
             if (live_tile && tiles > 0) {
                 const uint4* r4 = reinterpret_cast<const uint4*>(
@@ -345,31 +370,31 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (a.scale_log2 < 0.0f) down = -down;
                 qmul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (fabsf(a.scale_log2) * 0.0078125f);
                 if (most >= 0x7f80u) qmul = __uint_as_float(0x7fc00000u);    // e4m3 has no infinity: the row is NaN
-#pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {       // 64 values: 16 columns of each term
-                    uint32_t hi[16], lo[16];
+#pragma unroll 4
+                for (int c = 0; c < D / 16; ++c) {       // 16 values: a 16-byte chunk of each term
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 v = __ldg(r4 + 8 * c + i);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 v = __ldg(r4 + 2 * c + i);
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float x0 = bf16_lo(w[2 * h]) * down, x1 = bf16_hi(w[2 * h]) * down;
                             const float x2 = bf16_lo(w[2 * h + 1]) * down, x3 = bf16_hi(w[2 * h + 1]) * down;
                             const uint32_t c01 = f32_to_e4m3x2(x0, x1), c23 = f32_to_e4m3x2(x2, x3);
-                            uint32_t u01 = e4m3x2_to_f16x2(static_cast<uint16_t>(c01));
-                            uint32_t u23 = e4m3x2_to_f16x2(static_cast<uint16_t>(c23));
-                            const float2 f01 = f16x2_to_f32(u01), f23 = f16x2_to_f32(u23);
+                            const float2 f01 = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(c01)));
+                            const float2 f23 = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(c23)));
                             hi[2 * i + h] = c01 | (c23 << 16);
                             lo[2 * i + h] = static_cast<uint32_t>(f32_to_e4m3x2(x0 - f01.x, x1 - f01.y)) |
                                             (static_cast<uint32_t>(f32_to_e4m3x2(x2 - f23.x, x3 - f23.y)) << 16);
                         }
                     }
-                    tmem_st16(q_addr + 16 * c, hi);
-                    tmem_st16(q_addr + D / 4 + 16 * c, lo);
+                    const uint32_t panel = q_row + (c >> 3) * T::kQPanel;
+                    sts128(panel + (((c & 7) ^ (row & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (D == 64) sts128(panel + (((c + 4) ^ (row & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+                    else sts128(panel + T::kQTerm + (((c & 7) ^ (row & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
                 }
-                wait_st();
-                fence_before();
+                fence_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(T::kQFull + qi));
             }
@@ -631,7 +656,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 bool ok = turn == 0 || bar_wait(bar(T::kKFree + st), (turn - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
                 if (lane == 0) scales[(gn % kScaleSlots) * 4 + w] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
-                const uint32_t kdst = sbase + st * T::kKPanels * T::kPanel;
+                const uint32_t kdst = sbase + T::kOffK + st * T::kKPanels * T::kPanel;
 #pragma unroll
                 for (int r = 0; r < kKLoads; ++r) {
                     const int chunk = r * 32 + lane, tk = chunk / kKc, c = chunk % kKc;
@@ -679,66 +704,58 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
             // ------------------------------------------------------------- products
-            // so far: tiles of the loaders and of each query tile, and its items
-            uint32_t gn = 0, sn[kQt], qn[kQt];
+            // stage and turn of the next keys and values; tiles and items of each query tile so far
+            uint32_t kst = 0, kturn = 0, vst = 0, vturn = 0, sn[kQt], qn[kQt];
 #pragma unroll
             for (int q = 0; q < kQt; ++q) sn[q] = qn[q] = 0;
+            const uint64_t q0 = desc(sbase, 16), k0 = desc(sbase + T::kOffK, 16), v0 = desc(sbase + T::kOffV, T::kPanel);
             Part u;
             bool ok = true;
             for (int k = 0; ok && take_part(k, u); ++k) {
-                const int tiles = u.t1 - u.t0;
-                // S of query tile q with tile i of this item.  It takes the columns of an earlier
-                // tile's P, whose product this thread issued before: the tensor pipe runs in order
-                auto scores = [&](int q, int i) {
-                    const uint32_t st = (gn + i) % kSt, n = sn[q] + i;
+                const int tiles = u.t1 - u.t0, live = u.live;
+                // S of every query tile with the item's next tile of keys.  It takes the columns
+                // that P had two tiles ago, whose product this thread issued before: the tensor
+                // pipe runs in order
+                auto scores = [&](int q, uint32_t n) {
                     if (q == 0) {
-                        if (!bar_wait(bar(T::kKFull + st), ((gn + i) / kSt) & 1)) return false;
+                        if (!bar_wait(bar(T::kKFull) + 8 * kst, kturn)) return false;
                         fence_after();
                     }
-                    const uint32_t kb = sbase + st * T::kKPanels * T::kPanel;
-                    const uint32_t d = tmem + T::kSCol + (q * kSB + n % kSB) * kKeys;
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-#pragma unroll
-                        for (int s = 0; s < D / 32; ++s)
-                            mma_e4m3(d, tmem + q * T::kQCols + term * (D / 4) + s * 8,
-                                     desc(kb + (s >> 2) * T::kPanel + (s & 3) * 32, 16), T::kIdescS, term + s > 0);
-                    commit(bar(T::kSFull + 2 * q + n % kSB));
-                    if (q == u.live - 1) commit(bar(T::kKFree + st));
+                    mma_scores<D, 0, 0>(tmem + T::kSCol + (2 * q + (n & 1)) * kKeys, q0 + q * (T::kQBytes >> 4),
+                                        k0 + kst * (T::kKPanels * T::kPanel >> 4));
+                    commit(bar(T::kSFull + 2 * q) + 8 * (n & 1));
+                    if (q == live - 1) {
+                        commit(bar(T::kKFree) + 8 * kst);
+                        if (++kst == kSt) { kst = 0; kturn ^= 1; }
+                    }
                     return true;
                 };
 #pragma unroll
                 for (int q = 0; q < kQt; ++q)
-                    if (ok && q < u.live && tiles > 0) {
+                    if (ok && q < live && tiles > 0) {
                         ok = bar_wait(bar(T::kQFull + q), qn[q]++ & 1);
                         fence_after();
-                        ok = ok && scores(q, 0);
+                        ok = ok && scores(q, sn[q]);
                     }
                 for (int i = 0; ok && i < tiles; ++i) {
-                    const uint32_t st = (gn + i) % kSt;
 #pragma unroll
                     for (int q = 0; q < kQt; ++q) {
-                        if (!ok || q >= u.live) break;
-                        if (kSB == 2 && i + 1 < tiles && !(ok = scores(q, i + 1))) break;
-                        ok = (q > 0 || bar_wait(bar(T::kVFull + st), ((gn + i) / kSt) & 1)) &&
-                             bar_wait(bar(T::kPFull + q), (sn[q] + i) & 1);
+                        if (!ok || q >= live) break;
+                        const uint32_t n = sn[q];
+                        if (i + 1 < tiles && !(ok = scores(q, n + 1))) break;
+                        ok = (q > 0 || bar_wait(bar(T::kVFull) + 8 * vst, vturn)) && bar_wait(bar(T::kPFull + q), n & 1);
                         if (!ok) break;
                         fence_after();
-                        const uint32_t vb = sbase + T::kOffV + st * T::kVPanels * T::kPanel;
-                        const uint32_t p = tmem + T::kSCol + (q * kSB + (sn[q] + i) % kSB) * kKeys;
-#pragma unroll
-                        for (int s = 0; s < kKeys / 16; ++s)
-                            mma_f16_ts(tmem + T::kOCol + q * D, p + s * 8, desc(vb + s * 2048, T::kPanel), T::kIdescO,
-                                       i > 0 || s > 0);
-                        commit(bar(T::kPvDone + 2 * q + ((sn[q] + i) & 1)));
-                        if (q == u.live - 1) commit(bar(T::kVFree + st));
-                        if (kSB == 1 && i + 1 < tiles) ok = scores(q, i + 1);
+                        mma_values<D, 0>(tmem + T::kOCol + q * D, tmem + T::kSCol + (2 * q + (n & 1)) * kKeys,
+                                         v0 + vst * (T::kVPanels * T::kPanel >> 4), i > 0 ? 1u : 0u);
+                        commit(bar(T::kPvDone + 2 * q) + 8 * (n & 1));
+                        if (q == live - 1) {
+                            commit(bar(T::kVFree) + 8 * vst);
+                            if (++vst == kSt) { vst = 0; vturn ^= 1; }
+                        }
+                        sn[q] = n + 1;
                     }
                 }
-                gn += tiles;
-#pragma unroll
-                for (int q = 0; q < kQt; ++q)
-                    if (q < u.live) sn[q] += tiles;
                 bar_arrive(bar(T::kPartFree + (k & 1)));
             }
             // nothing is in flight when the tensor memory is released
