@@ -26,7 +26,7 @@
 //   block of the cache, so one page and one pair of scales), a tile ahead in registers;
 //   K goes to shared memory as it is, V as f16, both in the 128-byte-swizzled layout:
 //   row = token, 128 bytes a row (a panel), 16-byte chunk c of row r at c ^ (r % 8).
-// * 1 thread issues the products.
+// * 1 warp issues the products.
 // * 4 warps a query tile do the softmax, a row a thread: scores from tensor memory,
 //   p' = 2^(x - m), sums in registers.  O is rescaled in tensor memory only when a row's
 //   reference moves.  They also store the result and bring in the next item's queries.
@@ -36,7 +36,7 @@
 // the products' time; the tile's shared-memory traffic is 384 clocks.
 //
 // Waits are bounded as in gemm_tc_kernel.cu: one that gives up sets the device error
-// word and its role leaves; the issuing thread always waits for its last products
+// word and its role leaves; the issuing warp always waits for its last products
 // before the tensor memory is released.
 #include "kv_attention.cuh"
 #include "trellis.h"
@@ -60,7 +60,7 @@ struct Tile {
     static constexpr int kSBufs = 2;                     // score buffers of a query tile
     static constexpr int kSoftWarps = 4 * kQt;
     static constexpr int kThreads = (kSoftWarps + kLoadWarps + 2) * 32;
-    static constexpr int kStages = 3;                    // of keys, and of values
+    static constexpr int kKStages = 2, kVStages = 2;     // tiles of keys and of values in shared memory
     static constexpr int kPanel = kKeys * 128;           // 128 bytes of each token of a tile
     static constexpr int kKPanels = D <= 128 ? 1 : 2;    // a D = 64 row takes half of its 128 bytes
     static constexpr int kVPanels = D / 64;
@@ -69,14 +69,13 @@ struct Tile {
     static constexpr int kQTerm = kKPanels * kQPanel;    // from a row's hi term to its lo term (64 bytes at D = 64)
     static constexpr int kQBytes = D == 64 ? kQPanel : 2 * kQTerm;
     static constexpr int kOffK = kQt * kQBytes;
-    static constexpr int kOffV = kOffK + kStages * kKPanels * kPanel;
-    static constexpr int kOffScale = kOffV + kStages * kVPanels * kPanel;
+    static constexpr int kOffV = kOffK + kKStages * kKPanels * kPanel;
+    static constexpr int kOffScale = kOffV + kVStages * kVPanels * kPanel;
     static constexpr int kOffPart = kOffScale + kScaleSlots * 4 * 16;
     static constexpr int kOffBar = kOffPart + 2 * 64;
     // barriers
-    static constexpr int kQFull = 0, kJoin = kQt, kKFull = 2 * kQt, kKFree = kKFull + kStages, kVFull = kKFree + kStages,
-                         kVFree = kVFull + kStages, kSFull = kVFree + kStages, kPFull = kSFull + 2 * kQt,
-                         kPvDone = kPFull + kQt, kPartFull = kPvDone + 2 * kQt, kPartFree = kPartFull + 2,
+    static constexpr int kQFull = 0, kJoin = kQt, kKFull = 2 * kQt, kVFull = kKFull + kKStages, kSFull = kVFull + kVStages,
+                         kPFull = kSFull + 2 * kQt, kPvDone = kPFull + kQt, kPartFull = kPvDone + 2 * kQt, kPartFree = kPartFull + 2,
                          kDone = kPartFree + 2, kBars = kDone + 1;
     static constexpr int kOffTaddr = kOffBar + kBars * 8;
     static constexpr int kSmem = kOffTaddr + 32 + 1024;  // + rounding of the base to 1 KB
@@ -124,8 +123,18 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0u || bar_wait_slow(bar, parity);
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+// The products' instructions below are executed by the elected lane of a warp whose
+// lanes all walk the same path: their operands then live in uniform registers, which a
+// branch of one lane would have to fill one by one before every product.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t elected) {
+    asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+                 " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+                 :: "r"(bar), "r"(elected) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -140,34 +149,38 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead) {
            (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 // One 8-bit product (K = 32) with both operands in shared memory, and one f16 product
-// (K = 16) with A in tensor memory.  The issuing thread is the bottleneck if an issue
-// costs it more than the product (48 and 64 clocks here), so descriptors are a base and
-// an immediate: offsets (in 16 bytes) only reach the address field.
+// (K = 16) with A in tensor memory.  The issuing warp is the bottleneck if an issue costs
+// it more than the product (48 and 64 clocks here), so descriptors are a base and an
+// immediate: offsets (in 16 bytes) only reach the address field.
 template <int kOffA, int kOffB, bool kAcc>
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-    asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n add.s64 x, %1, %5;\n add.s64 y, %2, %6;\n"
-                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "n"(kAcc ? 1 : 0), "n"(kOffA >> 4), "n"(kOffB >> 4) : "memory");
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t elected) {
+    asm volatile("{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %7, 0;\n"
+                 " add.s64 x, %1, %5;\n add.s64 y, %2, %6;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "n"(kAcc ? 1 : 0), "n"(kOffA >> 4), "n"(kOffB >> 4), "r"(elected)
+                 : "memory");
 }
 template <int kOffA, int kOffB>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n .reg .b32 x;\n setp.ne.b32 p, %4, 0;\n add.s32 x, %1, %5;\n add.s64 y, %2, %6;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kOffA), "n"(kOffB >> 4) : "memory");
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t elected) {
+    asm volatile("{\n .reg .pred p, e;\n .reg .b64 y;\n .reg .b32 x;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %7, 0;\n"
+                 " add.s32 x, %1, %5;\n add.s64 y, %2, %6;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kOffA), "n"(kOffB >> 4), "r"(elected) : "memory");
 }
-// Every 32 (16) steps of the sums of a tile, unrolled.
+// A tile's products, unrolled.
 template <int D, int kTerm, int kStep>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k) {
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t elected) {
     using T = Tile<D>;
     constexpr int off = (kStep >> 2) * T::kQPanel + (kStep & 3) * 32;
-    mma_e4m3<off + kTerm * (D == 64 ? 64 : T::kQTerm), (kStep >> 2) * T::kPanel + (kStep & 3) * 32, (kTerm + kStep > 0)>(d, q, k, T::kIdescS);
-    if constexpr (kStep + 1 < D / 32) mma_scores<D, kTerm, kStep + 1>(d, q, k);
-    else if constexpr (kTerm == 0) mma_scores<D, 1, 0>(d, q, k);
+    mma_e4m3<off + kTerm * (D == 64 ? 64 : T::kQTerm), (kStep >> 2) * T::kPanel + (kStep & 3) * 32, (kTerm + kStep > 0)>(
+        d, q, k, T::kIdescS, elected);
+    if constexpr (kStep + 1 < D / 32) mma_scores<D, kTerm, kStep + 1>(d, q, k, elected);
+    else if constexpr (kTerm == 0) mma_scores<D, 1, 0>(d, q, k, elected);
 }
 template <int D, int kStep>
-__device__ __forceinline__ void mma_values(uint32_t d, uint32_t p, uint64_t v, uint32_t acc) {
-    mma_f16<kStep * 8, kStep * 2048>(d, p, v, Tile<D>::kIdescO, acc);
-    if constexpr (kStep + 1 < kKeys / 16) mma_values<D, kStep + 1>(d, p, v, 1u);
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t p, uint64_t v, uint32_t acc, uint32_t elected) {
+    mma_f16<kStep * 8, kStep * 2048>(d, p, v, Tile<D>::kIdescO, acc, elected);
+    if constexpr (kStep + 1 < kKeys / 16) mma_values<D, kStep + 1>(d, p, v, 1u, elected);
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -270,7 +283,7 @@ template <int D>
 __global__ void __launch_bounds__(Tile<D>::kThreads, 1)
 kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int items) {
     using T = Tile<D>;
-    constexpr int kQt = T::kQt, kSB = T::kSBufs, kSt = T::kStages;
+    constexpr int kQt = T::kQt;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ int joins[kQt];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -282,12 +295,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
     constexpr int kMmaWarp = T::kSoftWarps + kLoadWarps;   // and the planner's after it
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kSt; ++s) {
-            bar_init(bar(T::kKFull + s), kLoadWarps);
-            bar_init(bar(T::kKFree + s), 1);
-            bar_init(bar(T::kVFull + s), kLoadWarps);
-            bar_init(bar(T::kVFree + s), 1);
-        }
+        for (int s = 0; s < T::kKStages; ++s) bar_init(bar(T::kKFull + s), kLoadWarps);
+        for (int s = 0; s < T::kVStages; ++s) bar_init(bar(T::kVFull + s), kLoadWarps);
         for (int q = 0; q < kQt; ++q) {
             bar_init(bar(T::kQFull + q), 4);
             bar_init(bar(T::kJoin + q), 4);
@@ -313,7 +322,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + T::kOffTaddr);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + T::kOffTaddr), 0);
     float4* const scales = reinterpret_cast<float4*>(smem + T::kOffScale);   // [slot][block]: k scale, log2 v, 1 / v
     griddep_wait();
 
@@ -334,13 +343,15 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         const int row = static_cast<int>(threadIdx.x) & (kRows - 1);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t q_row = sbase + qi * T::kQBytes + row * 128;
-        const uint32_t s_base = lane_base + T::kSCol + qi * kSB * kKeys;
+        const uint32_t s_base = lane_base + T::kSCol + qi * 2 * kKeys;
         const uint32_t o_addr = lane_base + T::kOCol + qi * D;
         uint32_t meets = 0;
-        uint32_t tiles_all = 0, tiles_mine = 0;          // walked over before this item: by the loaders, by this query tile
-        // Waits for the product with P of this query tile's tile n.  Two barriers in turn: a
-        // parity tells one phase from the next only, and the product before may be running too
-        auto pv_done = [&](uint32_t n) { return bar_wait(bar(T::kPvDone + 2 * qi + (n & 1)), (n >> 1) & 1); };
+        uint32_t done = 0;                               // this query tile's tiles before this item
+        uint32_t vst = 0, vturn = 0, slot = 0;           // value stage and its turn, scale slot, of the next tile
+        // S, and the product with P, of this query tile's tile n.  Two barriers in turn each: a
+        // parity tells a phase from the next only, so a wait must not be two of them early or late
+        auto s_full = [&](uint32_t n) { return bar_wait(bar(T::kSFull + 2 * qi) + 8 * (n & 1), (n >> 1) & 1); };
+        auto pv_done = [&](uint32_t n) { return bar_wait(bar(T::kPvDone + 2 * qi) + 8 * (n & 1), (n >> 1) & 1); };
         Part u;
         bool have = take_part(0, u);
         have = __all_sync(0xffffffffu, have);
@@ -407,25 +418,26 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int i = 0; live_tile && i < tiles; ++i) {
-                const uint32_t sn = tiles_mine + i, gn = tiles_all + i;
-                const uint32_t b = sn % kSB;
+                const uint32_t n = done + i;
                 // the loaders stored the scales before they arrived for V; that barrier cannot
                 // run ahead of this wait (its next use needs the product with this tile's P), as
                 // the one for K could
-                ok = bar_wait(bar(T::kSFull + 2 * qi + b), (sn / kSB) & 1) && bar_wait(bar(T::kVFull + gn % kSt), (gn / kSt) & 1);
+                ok = s_full(n) && bar_wait(bar(T::kVFull) + 8 * vst, vturn);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
-                const uint32_t s_addr = s_base + b * kKeys;
+                const uint32_t s_addr = s_base + (n & 1) * kKeys;
                 uint32_t s0[32], s1[32];
                 tmem_ld32(s0, s_addr);
                 tmem_ld32(s1, s_addr + 32);
                 float mul[4], lv[4], iv[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float4 v = scales[(gn % kScaleSlots) * 4 + c];
+                    const float4 v = scales[slot * 4 + c];
                     mul[c] = v.x * qmul; lv[c] = v.y; iv[c] = v.z;
                 }
+                if (++vst == T::kVStages) { vst = 0; vturn ^= 1; }
+                slot = (slot + 1) % kScaleSlots;
                 wait_ld();
                 const int tok0 = u.lo + (u.t0 + i) * kKeys;
                 if (tok0 + kKeys > all_hi || tok0 < all_lo) {
@@ -458,7 +470,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                     l *= f;
                     if (i > 0) {
                         // O holds the tiles before this one
-                        ok = pv_done(sn - 1);
+                        ok = pv_done(n - 1);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         fence_after();
@@ -498,11 +510,16 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (lane == 0) bar_arrive(bar(T::kPFull + qi));
             }
             if (!ok) break;
-            tiles_all += tiles;
-            if (live_tile) tiles_mine += tiles;
+            if (!live_tile) {                            // the tiles passed by without this query tile
+                for (int i = 0; i < tiles; ++i) {
+                    if (++vst == T::kVStages) { vst = 0; vturn ^= 1; }
+                    slot = (slot + 1) % kScaleSlots;
+                }
+            }
             // ---- result ---------------------------------------------------------------
             if (live_tile && tiles > 0) {
-                ok = pv_done(tiles_mine - 1);
+                done += tiles;
+                ok = pv_done(done - 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
@@ -613,18 +630,27 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         uint4 kraw[kKLoads], vraw[2][P];
         float ks = 1.0f, vs = 1.0f;
         Part u = {};
-        uint32_t gn = 0;                                 // tiles so far
-        // this warp's block of tile i; false past the last token
-        auto block_of = [&](int i, size_t* unit, int* in_page) {
-            const int t = u.lo + (u.t0 + i) * kKeys + 16 * w;
-            if (t >= u.hi) return false;
-            *unit = static_cast<size_t>(kv_page(a.l, u.seq, t >> a.l.page_shift)) * a.l.kv_heads + u.head;
-            *in_page = t & (a.l.page_size - 1);
-            return true;
-        };
+        // stages and scale slot of the next tile; the tiles of each query tile so far
+        uint32_t kst = 0, vst = 0, slot = 0, done[kQt];
+#pragma unroll
+        for (int q = 0; q < kQt; ++q) done[q] = 0;
+        int last = 0;                                    // last query tile of the item before, and its tiles
+        uint32_t last_done = 0;
+        // this warp's block of the tile that is loaded, and the page id of the next
         size_t unit = 0;
-        int in_page = 0;
+        int in_page = 0, page_next = 0;
         bool in = false;
+        auto token_of = [&](int i) { return u.lo + (u.t0 + i) * kKeys + 16 * w; };
+        auto seek_page = [&](int i, int tiles) {
+            if (i < tiles && token_of(i) < u.hi) page_next = kv_page(a.l, u.seq, token_of(i) >> a.l.page_shift);
+        };
+        auto seek = [&](int i, int tiles) {
+            const int t = token_of(i);
+            in = i < tiles && t < u.hi;                  // false past the last token
+            unit = static_cast<size_t>(page_next) * a.l.kv_heads + u.head;
+            in_page = t & (a.l.page_size - 1);
+            seek_page(i + 1, tiles);
+        };
         auto load_k = [&]() {
             const uint8_t* src = a.k_codes + (unit * a.l.page_size + in_page) * D + lane * 16;
 #pragma unroll
@@ -647,16 +673,32 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         for (int k = 0; run; ++k) {
             if (!__all_sync(0xffffffffu, take_part(k, u))) break;
             const int tiles = u.t1 - u.t0;
-            in = tiles > 0 && block_of(0, &unit, &in_page);
+            seek_page(0, tiles);
+            seek(0, tiles);
             load_k();
             load_v();
-            for (int i = 0; i < tiles; ++i, ++gn) {
-                const uint32_t st = gn % kSt, turn = gn / kSt;
-                // a stage is free when its last tile's products are done
-                bool ok = turn == 0 || bar_wait(bar(T::kKFree + st), (turn - 1) & 1);
+            const int q_last = u.live - 1;
+            uint32_t base = 0;
+#pragma unroll
+            for (int q = 0; q < kQt; ++q)
+                if (q == q_last) base = done[q];
+            auto s_full = [&](int q, uint32_t n) { return bar_wait(bar(T::kSFull + 2 * q) + 8 * (n & 1), (n >> 1) & 1); };
+            auto pv_done = [&](int q, uint32_t n) { return bar_wait(bar(T::kPvDone + 2 * q) + 8 * (n & 1), (n >> 1) & 1); };
+            for (int i = 0; i < tiles; ++i) {
+                // The stage of keys is free when S of the tile two before is done, the stage of
+                // values when the product with P of the tile two before is; an item starts when
+                // the one before is done.  (Its last two products one after the other: a wait must
+                // not be two phases of a barrier early.)
+                bool ok = true;
+                if (i >= 2) {
+                    ok = s_full(q_last, base + i - 2);
+                } else if (i == 0 && last_done > 0) {
+                    ok = (last_done < 2 || pv_done(last, last_done - 2)) && pv_done(last, last_done - 1);
+                }
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
-                if (lane == 0) scales[(gn % kScaleSlots) * 4 + w] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
-                const uint32_t kdst = sbase + T::kOffK + st * T::kKPanels * T::kPanel;
+                if (lane == 0) scales[slot * 4 + w] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
+                slot = (slot + 1) % kScaleSlots;
+                const uint32_t kdst = sbase + T::kOffK + kst * T::kKPanels * T::kPanel;
 #pragma unroll
                 for (int r = 0; r < kKLoads; ++r) {
                     const int chunk = r * 32 + lane, tk = chunk / kKc, c = chunk % kKc;
@@ -665,13 +707,14 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 }
                 fence_async();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(T::kKFull + st));
+                if (lane == 0) bar_arrive(bar(T::kKFull) + 8 * kst);
+                if (++kst == T::kKStages) kst = 0;
                 // tokens of the block that count: what lies past them may be anything, NaN
                 // codes too, and 0 times NaN is not 0.  (Scores of such keys are masked.)
                 const int valid = u.hi - (u.lo + (u.t0 + i) * kKeys + 16 * w);
-                in = i + 1 < tiles && block_of(i + 1, &unit, &in_page);
+                seek(i + 1, tiles);
                 load_k();
-                ok = turn == 0 || bar_wait(bar(T::kVFree + st), (turn - 1) & 1);
+                ok = i < 2 || pv_done(q_last, base + i - 2);
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
                 if (valid < kKvBlock) {
 #pragma unroll
@@ -680,7 +723,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                         for (int p = 0; p < P; ++p)
                             if (r8 + 8 * h >= valid) vraw[h][p] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                const uint32_t vdst = sbase + T::kOffV + st * T::kVPanels * T::kPanel;
+                const uint32_t vdst = sbase + T::kOffV + vst * T::kVPanels * T::kPanel;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -695,73 +738,84 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                     }
                 fence_async();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(T::kVFull + st));
+                if (lane == 0) bar_arrive(bar(T::kVFull) + 8 * vst);
+                if (++vst == T::kVStages) vst = 0;
                 load_v();
+            }
+            if (tiles > 0) {
+#pragma unroll
+                for (int q = 0; q < kQt; ++q)
+                    if (q < u.live) {
+                        done[q] += tiles;
+                        last_done = done[q];
+                    }
+                last = q_last;
             }
             __syncwarp();
             if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            // ------------------------------------------------------------- products
-            // stage and turn of the next keys and values; tiles and items of each query tile so far
-            uint32_t kst = 0, kturn = 0, vst = 0, vturn = 0, sn[kQt], qn[kQt];
+        // ----------------------------------------------------------------- products
+        // stage and turn of the next keys and values; tiles and items of each query tile so far
+        uint32_t kst = 0, kturn = 0, vst = 0, vturn = 0, sn[kQt], qn[kQt];
 #pragma unroll
-            for (int q = 0; q < kQt; ++q) sn[q] = qn[q] = 0;
-            const uint64_t q0 = desc(sbase, 16), k0 = desc(sbase + T::kOffK, 16), v0 = desc(sbase + T::kOffV, T::kPanel);
-            Part u;
-            bool ok = true;
-            for (int k = 0; ok && take_part(k, u); ++k) {
-                const int tiles = u.t1 - u.t0, live = u.live;
-                // S of every query tile with the item's next tile of keys.  It takes the columns
-                // that P had two tiles ago, whose product this thread issued before: the tensor
-                // pipe runs in order
-                auto scores = [&](int q, uint32_t n) {
-                    if (q == 0) {
-                        if (!bar_wait(bar(T::kKFull) + 8 * kst, kturn)) return false;
-                        fence_after();
-                    }
-                    mma_scores<D, 0, 0>(tmem + T::kSCol + (2 * q + (n & 1)) * kKeys, q0 + q * (T::kQBytes >> 4),
-                                        k0 + kst * (T::kKPanels * T::kPanel >> 4));
-                    commit(bar(T::kSFull + 2 * q) + 8 * (n & 1));
+        for (int q = 0; q < kQt; ++q) sn[q] = qn[q] = 0;
+        const uint64_t q0 = desc(sbase, 16), k0 = desc(sbase + T::kOffK, 16), v0 = desc(sbase + T::kOffV, T::kPanel);
+        const uint32_t elected = elect_lane();
+        Part u;
+        bool ok = true;
+        for (int k = 0; ok && __all_sync(0xffffffffu, take_part(k, u)); ++k) {
+            const int tiles = __shfl_sync(0xffffffffu, u.t1 - u.t0, 0), live = __shfl_sync(0xffffffffu, u.live, 0);
+            // S of query tile q with the item's next tile of keys, its tile n.  It takes the columns
+            // that P had two tiles ago.  Products of different kinds (8-bit and f16) do not wait for
+            // one another, neither in the pipe nor in a commit: what the product with that P still
+            // reads is only free when its own commit says so.  (Some 50 clocks a commit; with two
+            // query tiles that product is long over.)
+            auto scores = [&](int q, uint32_t n) {
+                if (q == 0) {
+                    if (!__all_sync(0xffffffffu, bar_wait(bar(T::kKFull) + 8 * kst, kturn))) return false;
+                }
+                if (n >= 2 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPvDone + 2 * q) + 8 * (n & 1), ((n - 2) >> 1) & 1))) return false;
+                fence_after();
+                mma_scores<D, 0, 0>(tmem + T::kSCol + (2 * q + (n & 1)) * kKeys, q0 + q * (T::kQBytes >> 4),
+                                    k0 + kst * (T::kKPanels * T::kPanel >> 4), elected);
+                commit(bar(T::kSFull + 2 * q) + 8 * (n & 1), elected);
+                if (q == live - 1) {
+                    if (++kst == T::kKStages) { kst = 0; kturn ^= 1; }
+                }
+                return true;
+            };
+#pragma unroll
+            for (int q = 0; q < kQt; ++q)
+                if (ok && q < live && tiles > 0) {
+                    ok = __all_sync(0xffffffffu, bar_wait(bar(T::kQFull + q), qn[q]++ & 1));
+                    fence_after();
+                    ok = ok && scores(q, sn[q]);
+                }
+            for (int i = 0; ok && i < tiles; ++i) {
+#pragma unroll
+                for (int q = 0; q < kQt; ++q) {
+                    if (!ok || q >= live) break;
+                    const uint32_t n = sn[q]++;
+                    if (i + 1 < tiles && !(ok = scores(q, n + 1))) break;
+                    ok = (q > 0 || bar_wait(bar(T::kVFull) + 8 * vst, vturn)) && bar_wait(bar(T::kPFull + q), n & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    fence_after();
+                    mma_values<D, 0>(tmem + T::kOCol + q * D, tmem + T::kSCol + (2 * q + (n & 1)) * kKeys,
+                                     v0 + vst * (T::kVPanels * T::kPanel >> 4), i > 0 ? 1u : 0u, elected);
+                    commit(bar(T::kPvDone + 2 * q) + 8 * (n & 1), elected);
                     if (q == live - 1) {
-                        commit(bar(T::kKFree) + 8 * kst);
-                        if (++kst == kSt) { kst = 0; kturn ^= 1; }
-                    }
-                    return true;
-                };
-#pragma unroll
-                for (int q = 0; q < kQt; ++q)
-                    if (ok && q < live && tiles > 0) {
-                        ok = bar_wait(bar(T::kQFull + q), qn[q]++ & 1);
-                        fence_after();
-                        ok = ok && scores(q, sn[q]);
-                    }
-                for (int i = 0; ok && i < tiles; ++i) {
-#pragma unroll
-                    for (int q = 0; q < kQt; ++q) {
-                        if (!ok || q >= live) break;
-                        const uint32_t n = sn[q];
-                        if (i + 1 < tiles && !(ok = scores(q, n + 1))) break;
-                        ok = (q > 0 || bar_wait(bar(T::kVFull) + 8 * vst, vturn)) && bar_wait(bar(T::kPFull + q), n & 1);
-                        if (!ok) break;
-                        fence_after();
-                        mma_values<D, 0>(tmem + T::kOCol + q * D, tmem + T::kSCol + (2 * q + (n & 1)) * kKeys,
-                                         v0 + vst * (T::kVPanels * T::kPanel >> 4), i > 0 ? 1u : 0u);
-                        commit(bar(T::kPvDone + 2 * q) + 8 * (n & 1));
-                        if (q == live - 1) {
-                            commit(bar(T::kVFree) + 8 * vst);
-                            if (++vst == kSt) { vst = 0; vturn ^= 1; }
-                        }
-                        sn[q] = n + 1;
+                        if (++vst == T::kVStages) { vst = 0; vturn ^= 1; }
                     }
                 }
-                bar_arrive(bar(T::kPartFree + (k & 1)));
             }
-            // nothing is in flight when the tensor memory is released
-            commit(bar(T::kDone));
-            (void)bar_wait(bar(T::kDone), 0);
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
         }
+        // nothing is in flight when the tensor memory is released
+        commit(bar(T::kDone), elected);
+        (void)bar_wait(bar(T::kDone), 0);
     } else {
         // ---------------------------------------------------------------------- plan
         for (int k = 0;; ++k) {
