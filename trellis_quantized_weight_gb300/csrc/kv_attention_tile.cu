@@ -21,7 +21,8 @@
 // QT = 2 query tiles share every loaded tile of keys and values (1 at D = 256, whose sums
 // fill tensor memory), and one's softmax runs beside the other's products.  Roles:
 //
-// * 1 warp plans: takes the next item from a counter and finds its rows, one item ahead.
+// * 1 warp plans: takes the next item from a counter and finds its rows, shortly before
+//   the one at hand ends.
 // * 4 warps load: warp w the codes of tokens 16w .. 16w+15 of each 64-token tile (one
 //   block of the cache, so one page and one pair of scales), a tile ahead in registers;
 //   K goes to shared memory as it is, V as f16, both in the 128-byte-swizzled layout:
@@ -60,7 +61,7 @@ struct Tile {
     static constexpr int kSBufs = 2;                     // score buffers of a query tile
     static constexpr int kSoftWarps = 4 * kQt;
     static constexpr int kThreads = (kSoftWarps + kLoadWarps + 2) * 32;
-    static constexpr int kKStages = 2, kVStages = 2;     // tiles of keys and of values in shared memory
+    static constexpr int kKStages = 2, kVStages = 3;     // tiles of keys and of values in shared memory
     static constexpr int kPanel = kKeys * 128;           // 128 bytes of each token of a tile
     static constexpr int kKPanels = D <= 128 ? 1 : 2;    // a D = 64 row takes half of its 128 bytes
     static constexpr int kVPanels = D / 64;
@@ -70,12 +71,16 @@ struct Tile {
     static constexpr int kQBytes = D == 64 ? kQPanel : 2 * kQTerm;
     static constexpr int kOffK = kQt * kQBytes;
     static constexpr int kOffV = kOffK + kKStages * kKPanels * kPanel;
-    static constexpr int kOffScale = kOffV + kVStages * kVPanels * kPanel;
-    static constexpr int kOffPart = kOffScale + kScaleSlots * 4 * 16;
+    static constexpr int kOffStage = kOffV + kVStages * kVPanels * kPanel;   // results on their way out: 32 rows a warp
+    static constexpr int kStageD = D == 128 ? 128 : 64;                     // values of a row at a time
+    static constexpr int kStageWarp = 32 * kStageD * 2;
+    static constexpr int kOffScale = kOffStage + kSoftWarps * kStageWarp;
+    static constexpr int kOffMul = kOffScale + kScaleSlots * 4 * 16;         // a float a query row
+    static constexpr int kOffPart = kOffMul + kQt * kRows * 4;
     static constexpr int kOffBar = kOffPart + 2 * 64;
     // barriers
     static constexpr int kQFull = 0, kJoin = kQt, kKFull = 2 * kQt, kVFull = kKFull + kKStages, kSFull = kVFull + kVStages,
-                         kPFull = kSFull + 2 * kQt, kPvDone = kPFull + kQt, kPartFull = kPvDone + 2 * kQt, kPartFree = kPartFull + 2,
+                         kPFull = kSFull + 2 * kQt, kItem = kPFull + 2 * kQt, kPartFull = kItem + kQt, kPartFree = kPartFull + 2,
                          kDone = kPartFree + 2, kBars = kDone + 1;
     static constexpr int kOffTaddr = kOffBar + kBars * 8;
     static constexpr int kSmem = kOffTaddr + 32 + 1024;  // + rounding of the base to 1 KB
@@ -212,6 +217,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
                    "r"(r[15]) : "memory");
 }
 
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(addr), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -302,9 +310,9 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             bar_init(bar(T::kJoin + q), 4);
             bar_init(bar(T::kSFull + 2 * q), 1);
             bar_init(bar(T::kSFull + 2 * q + 1), 1);
-            bar_init(bar(T::kPFull + q), 4);
-            bar_init(bar(T::kPvDone + 2 * q), 1);
-            bar_init(bar(T::kPvDone + 2 * q + 1), 1);
+            bar_init(bar(T::kItem + q), 1);
+            bar_init(bar(T::kPFull + 2 * q), 4);
+            bar_init(bar(T::kPFull + 2 * q + 1), 4);
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(bar(T::kPartFull + s), 1);
@@ -328,6 +336,10 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
 
     // Every role walks the same items: the planner's slot k & 1 holds item k.
     auto part_at = [&](int k) { return reinterpret_cast<volatile Part*>(smem + T::kOffPart + (k & 1) * 64); };
+    auto free_part = [&](int k) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
+    };
     auto take_part = [&](int k, Part& u) {
         if (!bar_wait(bar(T::kPartFull + (k & 1)), (k >> 1) & 1)) return false;
         const volatile int* from = reinterpret_cast<const volatile int*>(part_at(k));
@@ -342,73 +354,115 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         const int qi = warp >> 2;                        // query tile
         const int row = static_cast<int>(threadIdx.x) & (kRows - 1);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t q_row = sbase + qi * T::kQBytes + row * 128;
         const uint32_t s_base = lane_base + T::kSCol + qi * 2 * kKeys;
         const uint32_t o_addr = lane_base + T::kOCol + qi * D;
         uint32_t meets = 0;
-        uint32_t done = 0;                               // this query tile's tiles before this item
+        uint32_t turns = 0, tiles_so_far = 0, items = 0; // this query tile's, before this item
         uint32_t vst = 0, vturn = 0, slot = 0;           // value stage and its turn, scale slot, of the next tile
-        // S, and the product with P, of this query tile's tile n.  Two barriers in turn each: a
-        // parity tells a phase from the next only, so a wait must not be two of them early or late
-        auto s_full = [&](uint32_t n) { return bar_wait(bar(T::kSFull + 2 * qi) + 8 * (n & 1), (n >> 1) & 1); };
-        auto pv_done = [&](uint32_t n) { return bar_wait(bar(T::kPvDone + 2 * qi) + 8 * (n & 1), (n >> 1) & 1); };
-        Part u;
-        bool have = take_part(0, u);
-        have = __all_sync(0xffffffffu, have);
+        // The score barriers take turns, one a tile and one more an item (see the products).  Two
+        // barriers: a parity tells a turn from the next only, so a wait must never be two turns
+        // of a barrier early or late
+        auto turn_done = [&](uint32_t n) { return bar_wait(bar(T::kSFull + 2 * qi) + 8 * (n & 1), (n >> 1) & 1); };
+        // The queries of an item: its 32 rows of this warp, whole lines at a time, as a power of
+        // two times hi + lo in swizzled K-major rows.
+        constexpr int kLanes = D / 8;                    // lanes of a row, 8 values each
+        const int w0 = (warp & 3) * 32;                  // this warp's first row of the query tile
+        float* const muls = reinterpret_cast<float*>(smem + T::kOffMul) + qi * kRows;
+        auto load_queries = [&](const Part& v) {
+            if (qi >= v.live || v.t1 <= v.t0) return;
+            const int c = lane % kLanes, sub = lane / kLanes;
+            constexpr int kPer = 32 / kLanes;            // rows of a pass
+            const int r0 = (v.qt * kQt + qi) * kRows + w0 + sub;
+            constexpr int kSide = kLanes < 16 ? kLanes : 16;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kLanes; i0 += kSide) { // 32 / kPer passes, loaded side by side
+                uint4 raw[kSide];
+#pragma unroll
+                for (int i = 0; i < kSide; ++i) {
+                    const int r = r0 + (i0 + i) * kPer, tok = r / a.group;
+                    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (tok < v.n)
+                        raw[i] = __ldg(reinterpret_cast<const uint4*>(
+                            a.q + static_cast<size_t>(v.start + tok) * a.q_stride +
+                            (static_cast<size_t>(v.head) * a.group + (r - tok * a.group)) * D) + c);
+                }
+#pragma unroll
+                for (int i = 0; i < kSide; ++i) {
+                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    uint32_t most = 0u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) most = max(most, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    // the largest lands in [128, 256); a negative score factor turns the query's sign
+                    const int e = query_exponent(most);
+                    float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 128.0f;
+                    if (a.scale_log2 < 0.0f) down = -down;
+                    const int row_in = w0 + (i0 + i) * kPer + sub;
+                    // e4m3 has no infinity: a row that holds one, or a NaN, is NaN
+                    if (c == 0)
+                        muls[row_in] = most >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                            : __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (fabsf(a.scale_log2) * 0.0078125f);
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float x0 = bf16_lo(w[2 * h]) * down, x1 = bf16_hi(w[2 * h]) * down;
+                        const float x2 = bf16_lo(w[2 * h + 1]) * down, x3 = bf16_hi(w[2 * h + 1]) * down;
+                        const uint32_t c01 = f32_to_e4m3x2(x0, x1), c23 = f32_to_e4m3x2(x2, x3);
+                        const float2 f01 = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(c01)));
+                        const float2 f23 = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(c23)));
+                        hi[h] = c01 | (c23 << 16);
+                        lo[h] = static_cast<uint32_t>(f32_to_e4m3x2(x0 - f01.x, x1 - f01.y)) |
+                                (static_cast<uint32_t>(f32_to_e4m3x2(x2 - f23.x, x3 - f23.y)) << 16);
+                    }
+                    // 8 bytes of each term: half of 16-byte chunk c / 2
+                    const uint32_t at = sbase + qi * T::kQBytes + (c >> 4) * T::kQPanel + row_in * 128 + (c & 1) * 8;
+                    const uint32_t ch = (c >> 1) & 7, r7 = row_in & 7;
+                    sts64(at + ((ch ^ r7) << 4), hi[0], hi[1]);
+                    if constexpr (D == 64) sts64(at + (((ch + 4) ^ r7) << 4), lo[0], lo[1]);
+                    else sts64(at + T::kQTerm + ((ch ^ r7) << 4), lo[0], lo[1]);
+                }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(T::kQFull + qi));
+        };
+        // Rows of results leave through shared memory, so that stores are whole lines.
+        const uint32_t stage = sbase + T::kOffStage + warp * T::kStageWarp;
+        auto stage_row = [&](int c, const uint32_t (&w)[8]) {          // values c .. c + 15 of this lane's row
+            const uint32_t at = stage + ((c % T::kStageD) >> 6) * 4096 + lane * 128;
+            const uint32_t ch = (c >> 3) & 7, r7 = lane & 7;
+            sts128(at + ((ch ^ r7) << 4), w[0], w[1], w[2], w[3]);
+            sts128(at + (((ch + 1) ^ r7) << 4), w[4], w[5], w[6], w[7]);
+        };
+        // after the values up to c + 15: stores the last kStageD of the rows when they are complete
+        auto store_rows = [&](const Part& v, int c_last) {
+            if ((c_last + 16) % T::kStageD != 0) return;
+            __syncwarp();
+            constexpr int kChunks = T::kStageD / 8;
+            const int r0 = (v.qt * kQt + qi) * kRows + w0, c0 = (c_last + 16 - T::kStageD) / 8;
+#pragma unroll 4
+            for (int i = 0; i < kChunks; ++i) {
+                const int at = i * 32 + lane, c = at % kChunks, rr = at / kChunks;
+                const int r = r0 + rr, tok = r / a.group;
+                const uint4 x = lds128(stage + (c >> 3) * 4096 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
+                if (tok < v.n)
+                    reinterpret_cast<uint4*>(a.out + ((static_cast<size_t>(v.start) + tok) * a.l.q_heads +
+                                                      static_cast<size_t>(v.head) * a.group + (r - tok * a.group)) * D)[c0 + c] = x;
+            }
+            __syncwarp();
+        };
+        Part u, next;
+        bool have = __all_sync(0xffffffffu, take_part(0, u)), have_next = false;
+        free_part(0);
+        if (have) load_queries(u);
         for (int k = 0; have; ++k) {
             const bool live_tile = qi < u.live;
             const int r = (u.qt * kQt + qi) * kRows + row;
             const int tok = r / a.group;
-            const bool live = tok < u.n;
             const int tiles = u.t1 - u.t0;               // 0: the rows see nothing
-            // this row's query: a power of two times hi + lo, swizzled K-major rows
-            float qmul = 0.0f;
-            if (live_tile && tiles > 0) {
-                const uint4* r4 = reinterpret_cast<const uint4*>(
-                    a.q + static_cast<size_t>(u.start + (live ? tok : 0)) * a.q_stride +
-                    (static_cast<size_t>(u.head) * a.group + r % a.group) * D);
-                uint32_t most = 0u;
-#pragma unroll 8
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = __ldg(r4 + c);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-                }
-                // the largest lands in [128, 256); a negative score factor turns the query's sign
-                const int e = query_exponent(most);
-                float down = live ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 128.0f : 0.0f;
-                if (a.scale_log2 < 0.0f) down = -down;
-                qmul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (fabsf(a.scale_log2) * 0.0078125f);
-                if (most >= 0x7f80u) qmul = __uint_as_float(0x7fc00000u);    // e4m3 has no infinity: the row is NaN
-#pragma unroll 4
-                for (int c = 0; c < D / 16; ++c) {       // 16 values: a 16-byte chunk of each term
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 v = __ldg(r4 + 2 * c + i);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float x0 = bf16_lo(w[2 * h]) * down, x1 = bf16_hi(w[2 * h]) * down;
-                            const float x2 = bf16_lo(w[2 * h + 1]) * down, x3 = bf16_hi(w[2 * h + 1]) * down;
-                            const uint32_t c01 = f32_to_e4m3x2(x0, x1), c23 = f32_to_e4m3x2(x2, x3);
-                            const float2 f01 = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(c01)));
-                            const float2 f23 = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(c23)));
-                            hi[2 * i + h] = c01 | (c23 << 16);
-                            lo[2 * i + h] = static_cast<uint32_t>(f32_to_e4m3x2(x0 - f01.x, x1 - f01.y)) |
-                                            (static_cast<uint32_t>(f32_to_e4m3x2(x2 - f23.x, x3 - f23.y)) << 16);
-                        }
-                    }
-                    const uint32_t panel = q_row + (c >> 3) * T::kQPanel;
-                    sts128(panel + (((c & 7) ^ (row & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
-                    if constexpr (D == 64) sts128(panel + (((c + 4) ^ (row & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
-                    else sts128(panel + T::kQTerm + (((c & 7) ^ (row & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(T::kQFull + qi));
-            }
+            __syncwarp();
+            const float qmul = muls[row];
             const int limit = min(u.hi, u.p0 + tok + 1);
             const int lower = a.window > 0 ? u.p0 + tok + 1 - a.window : 0;
             // tokens that every row of the query tile sees
@@ -418,11 +472,11 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int i = 0; live_tile && i < tiles; ++i) {
-                const uint32_t n = done + i;
+                const uint32_t n = turns + i, pn = tiles_so_far + i;
                 // the loaders stored the scales before they arrived for V; that barrier cannot
                 // run ahead of this wait (its next use needs the product with this tile's P), as
                 // the one for K could
-                ok = s_full(n) && bar_wait(bar(T::kVFull) + 8 * vst, vturn);
+                ok = turn_done(n) && bar_wait(bar(T::kVFull) + 8 * vst, vturn);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
@@ -469,8 +523,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                     m = to;
                     l *= f;
                     if (i > 0) {
-                        // O holds the tiles before this one
-                        ok = pv_done(n - 1);
+                        // O holds the tiles before this one once the next turn is over
+                        ok = turn_done(n + 1);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         fence_after();
@@ -507,7 +561,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(T::kPFull + qi));
+                // in turn two barriers: a warp may be a tile ahead of the others
+                if (lane == 0) bar_arrive(bar(T::kPFull + 2 * qi) + 8 * (pn & 1));
             }
             if (!ok) break;
             if (!live_tile) {                            // the tiles passed by without this query tile
@@ -516,22 +571,26 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                     slot = (slot + 1) % kScaleSlots;
                 }
             }
+            if (live_tile && tiles > 0) {                // every S of the item is done: its queries' place is free
+                turns += tiles + 1;
+                tiles_so_far += tiles;
+                if (!__all_sync(0xffffffffu, turn_done(turns - 1))) break;
+            }
+            // the next item's queries first: its first scores are made while this one's results leave
+            have_next = __all_sync(0xffffffffu, take_part(k + 1, next));
+            free_part(k + 1);
+            if (have_next) load_queries(next);
             // ---- result ---------------------------------------------------------------
             if (live_tile && tiles > 0) {
-                done += tiles;
-                ok = pv_done(done - 1);
+                ok = bar_wait(bar(T::kItem + qi), items++ & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
             }
-            // the next item is known by now; this one's slot is free after its last use
-            const Part v = u;
             if (live_tile) {
-                const bool whole = v.parts == 1;
-                float* part = a.partials + ((static_cast<size_t>(v.unit) * splits + v.index) * kQt + qi) * T::kPart;
+                const bool whole = u.parts == 1;
+                float* part = a.partials + ((static_cast<size_t>(u.unit) * splits + u.index) * kQt + qi) * T::kPart;
                 const float inv = 1.0f / l;
-                uint16_t* out = a.out + ((static_cast<size_t>(v.start) + (live ? tok : 0)) * a.l.q_heads +
-                                         static_cast<size_t>(v.head) * a.group + r % a.group) * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
                     uint32_t o[16];
@@ -548,10 +607,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                         for (int j = 0; j < 8; ++j)
                             // a row that sees nothing is zero, whatever its sums are
                             w[j] = l == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-                        if (live) {
-                            reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
+                        stage_row(c, w);
+                        store_rows(u, c);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = __uint_as_float(o[j]);
@@ -573,24 +630,25 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                     };
                     if (!meet()) break;
                     if (row == 0) {
-                        unsigned int* counter = a.counters + 2 + static_cast<size_t>(v.unit) * kQt + qi;
-                        joins[qi] = atomicAdd(counter, 1u) == static_cast<unsigned int>(v.parts - 1);
+                        unsigned int* counter = a.counters + 2 + static_cast<size_t>(u.unit) * kQt + qi;
+                        joins[qi] = atomicAdd(counter, 1u) == static_cast<unsigned int>(u.parts - 1);
                         if (joins[qi]) *counter = 0u;
                     }
                     if (!meet()) break;
                     const bool join = joins[qi] != 0;
                     if (!meet()) break;                  // it is read before the next item's is written
-                    if (join && live) {
+                    // (a warp whose rows are all past the last has nothing to store)
+                    if (join && (u.qt * kQt + qi) * kRows + w0 < u.n * a.group) {
                         __threadfence();
                         const size_t step = kQt * T::kPart;
-                        const float* base = a.partials + (static_cast<size_t>(v.unit) * splits * kQt + qi) * T::kPart + row;
+                        const float* base = a.partials + (static_cast<size_t>(u.unit) * splits * kQt + qi) * T::kPart + row;
                         float top = -INFINITY;
 #pragma unroll 8
-                        for (int q = 0; q < v.parts; ++q) top = fmaxf(top, __ldcg(base + q * step + D * kRows));
+                        for (int q = 0; q < u.parts; ++q) top = fmaxf(top, __ldcg(base + q * step + D * kRows));
                         const float ref = top == -INFINITY ? 0.0f : top;
                         float den = 0.0f;
 #pragma unroll 8
-                        for (int q = 0; q < v.parts; ++q) {
+                        for (int q = 0; q < u.parts; ++q) {
                             const float* from = base + q * step + D * kRows;
                             den = fmaf(__ldcg(from + kRows), exp2_approx(__ldcg(from) - ref), den);
                         }
@@ -601,7 +659,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
 #pragma unroll
                             for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
 #pragma unroll 2
-                            for (int q = 0; q < v.parts; ++q) {
+                            for (int q = 0; q < u.parts; ++q) {
                                 const float* from = base + q * step;
                                 const float f = exp2_approx(__ldcg(from + D * kRows) - ref);
 #pragma unroll
@@ -610,15 +668,14 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                             uint32_t w[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) w[j] = den == 0.0f ? 0u : pack_bf16x2(acc[2 * j] * s, acc[2 * j + 1] * s);
-                            reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            stage_row(c, w);
+                            store_rows(u, c);
                         }
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
-            have = __all_sync(0xffffffffu, take_part(k + 1, u));
+            u = next;
+            have = have_next;
         }
     } else if (warp < T::kSoftWarps + kLoadWarps) {
         // ------------------------------------------------------------------ loads
@@ -630,12 +687,15 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         uint4 kraw[kKLoads], vraw[2][P];
         float ks = 1.0f, vs = 1.0f;
         Part u = {};
-        // stages and scale slot of the next tile; the tiles of each query tile so far
-        uint32_t kst = 0, vst = 0, slot = 0, done[kQt];
+        // stages and scale slot of the next tile; the turns of each query tile's score barriers
+        uint32_t kst = 0, vst = 0, slot = 0, turns[kQt];
 #pragma unroll
-        for (int q = 0; q < kQt; ++q) done[q] = 0;
-        int last = 0;                                    // last query tile of the item before, and its tiles
-        uint32_t last_done = 0;
+        for (int q = 0; q < kQt; ++q) turns[q] = 0;
+        int q_before = -1;                               // last query tile of the item before (-1: none)
+        uint32_t turns_before = 0, items[kQt];           // its turns up to that item's end; items of each query tile
+#pragma unroll
+        for (int q = 0; q < kQt; ++q) items[q] = 0;
+        auto turn_done = [&](int q, uint32_t n) { return bar_wait(bar(T::kSFull + 2 * q) + 8 * (n & 1), (n >> 1) & 1); };
         // this warp's block of the tile that is loaded, and the page id of the next
         size_t unit = 0;
         int in_page = 0, page_next = 0;
@@ -681,20 +741,23 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             uint32_t base = 0;
 #pragma unroll
             for (int q = 0; q < kQt; ++q)
-                if (q == q_last) base = done[q];
-            auto s_full = [&](int q, uint32_t n) { return bar_wait(bar(T::kSFull + 2 * q) + 8 * (n & 1), (n >> 1) & 1); };
-            auto pv_done = [&](int q, uint32_t n) { return bar_wait(bar(T::kPvDone + 2 * q) + 8 * (n & 1), (n >> 1) & 1); };
+                if (q == q_last) base = turns[q];
+            auto item_done = [&]() {                     // all products of the item before
+                uint32_t n = 0;
+#pragma unroll
+                for (int q = 0; q < kQt; ++q)
+                    if (q == q_before) n = items[q];
+                return bar_wait(bar(T::kItem + q_before), (n - 1) & 1);
+            };
+            if (tiles == 0) free_part(k);
             for (int i = 0; i < tiles; ++i) {
-                // The stage of keys is free when S of the tile two before is done, the stage of
-                // values when the product with P of the tile two before is; an item starts when
-                // the one before is done.  (Its last two products one after the other: a wait must
-                // not be two phases of a barrier early.)
+                // the next item is taken when this one nears its end, not before: it may be long
+                if (i == max(0, tiles - 4)) free_part(k);
+                // The stage of keys is free when S of the tile two before is done (turn base + i - 2),
+                // at an item's start when the last turn of the one before is over
                 bool ok = true;
-                if (i >= 2) {
-                    ok = s_full(q_last, base + i - 2);
-                } else if (i == 0 && last_done > 0) {
-                    ok = (last_done < 2 || pv_done(last, last_done - 2)) && pv_done(last, last_done - 1);
-                }
+                if (i >= 2) ok = turn_done(q_last, base + i - 2);
+                else if (i == 0 && q_before >= 0) ok = turn_done(q_before, turns_before - 1);
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
                 if (lane == 0) scales[slot * 4 + w] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
                 slot = (slot + 1) % kScaleSlots;
@@ -714,7 +777,10 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 const int valid = u.hi - (u.lo + (u.t0 + i) * kKeys + 16 * w);
                 seek(i + 1, tiles);
                 load_k();
-                ok = i < 2 || pv_done(q_last, base + i - 2);
+                // the stage of values is free when the product with P of the tile three before is:
+                // turn base + i - 1; of the last tile of the item before: that item's own barrier
+                ok = i == 0 || turn_done(q_last, base + i - 1);
+                if (i == 1 && q_before >= 0) ok = ok && item_done();
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
                 if (valid < kKvBlock) {
 #pragma unroll
@@ -742,40 +808,44 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (++vst == T::kVStages) vst = 0;
                 load_v();
             }
+            if (tiles == 1 && q_before >= 0 && !__all_sync(0xffffffffu, item_done())) break;
             if (tiles > 0) {
 #pragma unroll
                 for (int q = 0; q < kQt; ++q)
                     if (q < u.live) {
-                        done[q] += tiles;
-                        last_done = done[q];
+                        turns[q] += tiles + 1;
+                        turns_before = turns[q];
+                        ++items[q];
                     }
-                last = q_last;
+                q_before = q_last;
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
         }
     } else if (warp == kMmaWarp) {
         // ----------------------------------------------------------------- products
-        // stage and turn of the next keys and values; tiles and items of each query tile so far
-        uint32_t kst = 0, kturn = 0, vst = 0, vturn = 0, sn[kQt], qn[kQt];
+        // stage and turn of the next keys and values; turns of the score barriers, tiles and
+        // items of each query tile so far
+        uint32_t kst = 0, kturn = 0, vst = 0, vturn = 0, turns[kQt], pn[kQt], qn[kQt];
 #pragma unroll
-        for (int q = 0; q < kQt; ++q) sn[q] = qn[q] = 0;
+        for (int q = 0; q < kQt; ++q) turns[q] = pn[q] = qn[q] = 0;
         const uint64_t q0 = desc(sbase, 16), k0 = desc(sbase + T::kOffK, 16), v0 = desc(sbase + T::kOffV, T::kPanel);
         const uint32_t elected = elect_lane();
         Part u;
         bool ok = true;
         for (int k = 0; ok && __all_sync(0xffffffffu, take_part(k, u)); ++k) {
+            free_part(k);
             const int tiles = __shfl_sync(0xffffffffu, u.t1 - u.t0, 0), live = __shfl_sync(0xffffffffu, u.live, 0);
-            // S of query tile q with the item's next tile of keys, its tile n.  It takes the columns
-            // that P had two tiles ago.  Products of different kinds (8-bit and f16) do not wait for
-            // one another, neither in the pipe nor in a commit: what the product with that P still
-            // reads is only free when its own commit says so.  (Some 50 clocks a commit; with two
-            // query tiles that product is long over.)
+            // S of query tile q with the item's next tile of keys, turn n.  It takes the columns that P
+            // had two tiles ago, whose product was issued before: the tensor pipe works in the
+            // order of issue, whatever the products' kinds.
+            //
+            // A commit costs the pipe some 50 clocks, so there is one a tile and query tile:
+            // after S of tile i (turn i), which says too that every product issued before is done,
+            // that with P of tile i - 2 among them.  A turn without scores and a barrier of its own
+            // end an item: when P of its last tile but one is used up, and when P of its last is.
             auto scores = [&](int q, uint32_t n) {
                 if (q == 0) {
                     if (!__all_sync(0xffffffffu, bar_wait(bar(T::kKFull) + 8 * kst, kturn))) return false;
                 }
-                if (n >= 2 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPvDone + 2 * q) + 8 * (n & 1), ((n - 2) >> 1) & 1))) return false;
                 fence_after();
                 mma_scores<D, 0, 0>(tmem + T::kSCol + (2 * q + (n & 1)) * kKeys, q0 + q * (T::kQBytes >> 4),
                                     k0 + kst * (T::kKPanels * T::kPanel >> 4), elected);
@@ -790,28 +860,36 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (ok && q < live && tiles > 0) {
                     ok = __all_sync(0xffffffffu, bar_wait(bar(T::kQFull + q), qn[q]++ & 1));
                     fence_after();
-                    ok = ok && scores(q, sn[q]);
+                    ok = ok && scores(q, turns[q]);
                 }
             for (int i = 0; ok && i < tiles; ++i) {
 #pragma unroll
                 for (int q = 0; q < kQt; ++q) {
                     if (!ok || q >= live) break;
-                    const uint32_t n = sn[q]++;
-                    if (i + 1 < tiles && !(ok = scores(q, n + 1))) break;
-                    ok = (q > 0 || bar_wait(bar(T::kVFull) + 8 * vst, vturn)) && bar_wait(bar(T::kPFull + q), n & 1);
+                    const uint32_t n = turns[q] + i, p = pn[q]++;
+                    if (i + 1 < tiles) {
+                        if (!(ok = scores(q, n + 1))) break;
+                    } else {
+                        commit(bar(T::kSFull + 2 * q) + 8 * ((n + 1) & 1), elected);
+                    }
+                    ok = (q > 0 || bar_wait(bar(T::kVFull) + 8 * vst, vturn)) &&
+                         bar_wait(bar(T::kPFull + 2 * q) + 8 * (p & 1), (p >> 1) & 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     fence_after();
                     mma_values<D, 0>(tmem + T::kOCol + q * D, tmem + T::kSCol + (2 * q + (n & 1)) * kKeys,
                                      v0 + vst * (T::kVPanels * T::kPanel >> 4), i > 0 ? 1u : 0u, elected);
-                    commit(bar(T::kPvDone + 2 * q) + 8 * (n & 1), elected);
                     if (q == live - 1) {
                         if (++vst == T::kVStages) { vst = 0; vturn ^= 1; }
                     }
+                    if (i + 1 == tiles) commit(bar(T::kItem + q), elected);
                 }
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(T::kPartFree + (k & 1)));
+            if (tiles > 0) {
+#pragma unroll
+                for (int q = 0; q < kQt; ++q)
+                    if (q < live) turns[q] += tiles + 1;
+            }
         }
         // nothing is in flight when the tensor memory is released
         commit(bar(T::kDone), elected);
@@ -819,7 +897,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
     } else {
         // ---------------------------------------------------------------------- plan
         for (int k = 0;; ++k) {
-            if (k >= 2 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPartFree + (k & 1)), ((k >> 1) - 1) & 1))) break;
+            // every role has the item before, and the loaders are nearly done with it
+            if (k >= 1 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPartFree + ((k - 1) & 1)), ((k - 1) >> 1) & 1))) break;
             Part u = {};
             bool found = false, last = false;
             while (!found) {
