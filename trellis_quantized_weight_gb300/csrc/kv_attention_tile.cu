@@ -79,7 +79,7 @@ struct Tile {
     static constexpr int kOffPart = kOffMul + kQt * kRows * 4;
     static constexpr int kOffBar = kOffPart + 2 * 64;
     // barriers
-    static constexpr int kQFull = 0, kJoin = kQt, kKFull = 2 * kQt, kVFull = kKFull + kKStages, kSFull = kVFull + kVStages,
+    static constexpr int kQFull = 0, kKFull = kQt, kVFull = kKFull + kKStages, kSFull = kVFull + kVStages,
                          kPFull = kSFull + 2 * kQt, kItem = kPFull + 2 * kQt, kPartFull = kItem + kQt, kPartFree = kPartFull + 2,
                          kDone = kPartFree + 2, kBars = kDone + 1;
     static constexpr int kOffTaddr = kOffBar + kBars * 8;
@@ -241,7 +241,7 @@ static_assert(sizeof(Part) <= 64, "part slot");
 // from the last query tiles of the last sequence, so that the long ones of a causal
 // prompt come first.  One warp calls it.
 template <int kUnitRows>
-__device__ bool find_part(const AttendArgs& a, unsigned int item, int splits, Part& u) {
+__device__ bool find_part(const AttendArgs& a, unsigned int item, int splits, int least, Part& u) {
     const int lane = threadIdx.x & 31;
     u.index = static_cast<int>(item % splits);
     u.unit = static_cast<int>(item / splits);
@@ -280,11 +280,29 @@ __device__ bool find_part(const AttendArgs& a, unsigned int item, int splits, Pa
     u.lo = low & ~(kKeys - 1);
     u.live = min(kUnitRows, rows - row0 + kRows - 1) / kRows;
     const int tiles = u.hi > u.lo ? (u.hi - u.lo + kKeys - 1) / kKeys : 0;
-    const int chunk = max(kMinChunk, (tiles + splits - 1) / splits);
+    const int chunk = max(least, (tiles + splits - 1) / splits);
     u.parts = max(1, (tiles + chunk - 1) / chunk);
     u.t0 = u.index * chunk;
     u.t1 = min(tiles, u.t0 + chunk);
     return u.index < u.parts;
+}
+
+// Tiles of a part where units are split: equal parts whatever the sequences' lengths,
+// some three for two CTAs.  (An item costs a CTA some ten tiles' time of its own.)
+template <int kUnitRows>
+__device__ int least_chunk(const AttendArgs& a, int ctas) {
+    const int lane = threadIdx.x & 31;
+    long long sum = 0;
+    for (int s = lane; s < a.l.seqs; s += 32) {
+        const Seq q = load_seq(a.l, s);
+        if (q.n <= 0 || q.total <= 0) continue;
+        const int seen = a.window > 0 ? min(q.total, a.window + q.n) : q.total;
+        sum += static_cast<long long>((q.n * a.group + kUnitRows - 1) / kUnitRows) * ((seen + kKeys - 1) / kKeys);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const long long each = 2 * sum * a.l.kv_heads / (3ll * ctas) + 1;
+    return static_cast<int>(max(static_cast<long long>(kMinChunk), min(each, 1ll << 24)));
 }
 
 template <int D>
@@ -293,7 +311,6 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
     using T = Tile<D>;
     constexpr int kQt = T::kQt;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ int joins[kQt];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sraw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
@@ -307,7 +324,6 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         for (int s = 0; s < T::kVStages; ++s) bar_init(bar(T::kVFull + s), kLoadWarps);
         for (int q = 0; q < kQt; ++q) {
             bar_init(bar(T::kQFull + q), 4);
-            bar_init(bar(T::kJoin + q), 4);
             bar_init(bar(T::kSFull + 2 * q), 1);
             bar_init(bar(T::kSFull + 2 * q + 1), 1);
             bar_init(bar(T::kItem + q), 1);
@@ -356,7 +372,6 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t s_base = lane_base + T::kSCol + qi * 2 * kKeys;
         const uint32_t o_addr = lane_base + T::kOCol + qi * D;
-        uint32_t meets = 0;
         uint32_t turns = 0, tiles_so_far = 0, items = 0; // this query tile's, before this item
         uint32_t vst = 0, vturn = 0, slot = 0;           // value stage and its turn, scale slot, of the next tile
         // The score barriers take turns, one a tile and one more an item (see the products).  Two
@@ -374,6 +389,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             constexpr int kPer = 32 / kLanes;            // rows of a pass
             const int r0 = (v.qt * kQt + qi) * kRows + w0 + sub;
             constexpr int kSide = kLanes < 16 ? kLanes : 16;
+            // (a warp without rows leaves what is there: its rows of S are not looked at)
+            if ((v.qt * kQt + qi) * kRows + w0 < v.n * a.group)
 #pragma unroll 1
             for (int i0 = 0; i0 < kLanes; i0 += kSide) { // 32 / kPer passes, loaded side by side
                 uint4 raw[kSide];
@@ -469,6 +486,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             const int row0 = (u.qt * kQt + qi) * kRows;
             const int all_hi = min(u.hi, u.p0 + row0 / a.group + 1);
             const int all_lo = a.window > 0 ? u.p0 + min(u.n - 1, (row0 + kRows - 1) / a.group) + 1 - a.window : 0;
+            const bool has_rows = row0 + w0 < u.n * a.group;
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int i = 0; live_tile && i < tiles; ++i) {
@@ -493,6 +511,11 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (++vst == T::kVStages) { vst = 0; vturn ^= 1; }
                 slot = (slot + 1) % kScaleSlots;
                 wait_ld();
+                if (!has_rows) {                         // P of rows that are not there: whatever it is
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(T::kPFull + 2 * qi) + 8 * (pn & 1));
+                    continue;
+                }
                 const int tok0 = u.lo + (u.t0 + i) * kKeys;
                 if (tok0 + kKeys > all_hi || tok0 < all_lo) {
                     // finished scores in the scores' place where some are hidden
@@ -592,7 +615,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 float* part = a.partials + ((static_cast<size_t>(u.unit) * splits + u.index) * kQt + qi) * T::kPart;
                 const float inv = 1.0f / l;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
+                for (int c = 0; has_rows && c < D; c += 16) {
                     uint32_t o[16];
                     if (tiles > 0) {
                         tmem_ld16(o, o_addr + c);
@@ -610,68 +633,17 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                         stage_row(c, w);
                         store_rows(u, c);
                     } else {
+                        if (r < u.n * a.group) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = __uint_as_float(o[j]);
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<uint4*>(part + row * D + c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
                     }
                 }
                 fence_before();                          // O is read before the next item's products
-                if (!whole) {
+                if (!whole && r < u.n * a.group) {
                     part[D * kRows + row] = m;
                     part[D * kRows + kRows + row] = l;
-                    // the part that finishes last adds them all, in their order
-                    __threadfence();
-                    // the query tile's four warps: bounded like every wait here
-                    auto meet = [&]() {
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(bar(T::kJoin + qi));
-                        const bool met = bar_wait(bar(T::kJoin + qi), meets & 1);
-                        ++meets;
-                        return __all_sync(0xffffffffu, met) != 0;
-                    };
-                    if (!meet()) break;
-                    if (row == 0) {
-                        unsigned int* counter = a.counters + 2 + static_cast<size_t>(u.unit) * kQt + qi;
-                        joins[qi] = atomicAdd(counter, 1u) == static_cast<unsigned int>(u.parts - 1);
-                        if (joins[qi]) *counter = 0u;
-                    }
-                    if (!meet()) break;
-                    const bool join = joins[qi] != 0;
-                    if (!meet()) break;                  // it is read before the next item's is written
-                    // (a warp whose rows are all past the last has nothing to store)
-                    if (join && (u.qt * kQt + qi) * kRows + w0 < u.n * a.group) {
-                        __threadfence();
-                        const size_t step = kQt * T::kPart;
-                        const float* base = a.partials + (static_cast<size_t>(u.unit) * splits * kQt + qi) * T::kPart + row;
-                        float top = -INFINITY;
-#pragma unroll 8
-                        for (int q = 0; q < u.parts; ++q) top = fmaxf(top, __ldcg(base + q * step + D * kRows));
-                        const float ref = top == -INFINITY ? 0.0f : top;
-                        float den = 0.0f;
-#pragma unroll 8
-                        for (int q = 0; q < u.parts; ++q) {
-                            const float* from = base + q * step + D * kRows;
-                            den = fmaf(__ldcg(from + kRows), exp2_approx(__ldcg(from) - ref), den);
-                        }
-                        const float s = 1.0f / den;
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            float acc[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-#pragma unroll 2
-                            for (int q = 0; q < u.parts; ++q) {
-                                const float* from = base + q * step;
-                                const float f = exp2_approx(__ldcg(from + D * kRows) - ref);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) acc[j] = fmaf(__ldcg(from + (c + j) * kRows), f, acc[j]);
-                            }
-                            uint32_t w[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = den == 0.0f ? 0u : pack_bf16x2(acc[2 * j] * s, acc[2 * j + 1] * s);
-                            stage_row(c, w);
-                            store_rows(u, c);
-                        }
-                    }
                 }
             }
             u = next;
@@ -896,6 +868,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         (void)bar_wait(bar(T::kDone), 0);
     } else {
         // ---------------------------------------------------------------------- plan
+        const int least = splits > 1 ? least_chunk<kQt * kRows>(a, gridDim.x) : kMinChunk;
         for (int k = 0;; ++k) {
             // every role has the item before, and the loaders are nearly done with it
             if (k >= 1 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPartFree + ((k - 1) & 1)), ((k - 1) >> 1) & 1))) break;
@@ -906,7 +879,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (lane == 0) item = atomicAdd(a.counters, 1u);
                 item = __shfl_sync(0xffffffffu, item, 0);
                 if (item >= items) { last = true; break; }
-                found = find_part<kQt * kRows>(a, item, splits, u);
+                found = find_part<kQt * kRows>(a, item, splits, least, u);
             }
             if (last) u.live = 0;
             if (lane == 0) {
@@ -929,6 +902,69 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(T::kCols) : "memory");
     }
+}
+
+// The parts of split units, added in their order: a CTA for 32 values of a query tile's
+// rows, after the kernel above (whose last CTA would else add a long unit's parts alone).
+constexpr int kJoinThreads = 128, kJoinCols = 32;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ AttendArgs a, int splits, int ctas) {
+    using T = Tile<D>;
+    __shared__ Part shared_part;
+    __shared__ int shared_ok;
+    griddep_wait();
+    const int qi = blockIdx.x % T::kQt;
+    if (threadIdx.x < 32) {
+        Part p = {};
+        const int least = least_chunk<T::kQt * kRows>(a, ctas);
+        const bool ok = find_part<T::kQt * kRows>(a, static_cast<unsigned>(blockIdx.x / T::kQt) * splits, splits, least, p);
+        if (threadIdx.x == 0) { shared_part = p; shared_ok = ok && p.parts > 1 && qi < p.live; }
+    }
+    __syncthreads();
+    if (shared_ok) {
+        const Part& u = shared_part;
+        const int row0 = (u.qt * T::kQt + qi) * kRows, rows = min(kRows, u.n * a.group - row0), parts = u.parts;
+        const size_t step = T::kQt * T::kPart;
+        const float* base = a.partials + (static_cast<size_t>(u.unit) * splits * T::kQt + qi) * T::kPart;
+        const int d = blockIdx.y * kJoinCols + threadIdx.x % 8 * 4;
+        for (int row = threadIdx.x / 8; row < rows; row += kJoinThreads / 8) {
+            float top = -INFINITY, l = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int p0 = 0; p0 < parts; p0 += 8) {      // eight parts' loads side by side
+                float pm[8], pl[8];
+                float4 v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float* from = base + min(p0 + q, parts - 1) * step;
+                    pm[q] = __ldcg(from + D * kRows + row);
+                    pl[q] = __ldcg(from + D * kRows + kRows + row);
+                    v[q] = __ldcg(reinterpret_cast<const float4*>(from + row * D + d));
+                }
+                float high = top;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (p0 + q >= parts) pm[q] = -INFINITY;
+                    high = fmaxf(high, pm[q]);
+                }
+                const float ref = high == -INFINITY ? 0.0f : high;
+                float f = exp2_approx(top - ref);
+                top = high;
+                l *= f;
+                acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    f = exp2_approx(pm[q] - ref);
+                    if (p0 + q >= parts) continue;
+                    acc.x = fmaf(v[q].x, f, acc.x); acc.y = fmaf(v[q].y, f, acc.y);
+                    acc.z = fmaf(v[q].z, f, acc.z); acc.w = fmaf(v[q].w, f, acc.w);
+                    l = fmaf(pl[q], f, l);
+                }
+            }
+            store_row4(a, u.start, u.head, row0 + row, D, d, acc, l);
+        }
+    }
+    griddep_launch_dependents();
 }
 
 int unit_rows(int head_dim) { return head_dim <= 128 ? 2 * kRows : kRows; }
@@ -956,7 +992,11 @@ int launch(const AttendArgs& a, long long units, int splits, int sms, cudaStream
     const unsigned items = static_cast<unsigned>(units * splits);
     const cudaError_t e = launch_programmatic(kv_tile_kernel<D>, items < static_cast<unsigned>(sms) ? items : static_cast<unsigned>(sms),
                                               static_cast<unsigned>(T::kThreads), T::kSmem, stream, a, splits, items);
-    return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
+    if (e != cudaSuccess) return TRELLIS_ERR_CUDA;
+    if (splits == 1) return TRELLIS_OK;
+    const int ctas = items < static_cast<unsigned>(sms) ? static_cast<int>(items) : sms;
+    return launch_programmatic_grid(kv_join_kernel<D>, dim3(static_cast<unsigned>(units) * T::kQt, D / kJoinCols), kJoinThreads, 0,
+                                    stream, a, splits, ctas) == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
 }
 
 }  // namespace
