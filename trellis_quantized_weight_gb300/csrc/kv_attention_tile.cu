@@ -23,8 +23,8 @@
 //
 // * 1 warp plans: takes the next item from a counter and finds its rows, shortly before
 //   the one at hand ends.
-// * 4 warps load: warp w the codes of tokens 16w .. 16w+15 of each 64-token tile (one
-//   block of the cache, so one page and one pair of scales), a tile ahead in registers;
+// * 4 warps load (8 at D = 256): warp w the codes of tokens 16w .. 16w+15 of each 64-token
+//   tile (one block of the cache, so one page and one pair of scales), a tile ahead in registers;
 //   K goes to shared memory as it is, V as f16, both in the 128-byte-swizzled layout:
 //   row = token, 128 bytes a row (a panel), 16-byte chunk c of row r at c ^ (r % 8).
 // * 1 warp issues the products.
@@ -51,8 +51,8 @@ namespace {
 constexpr float kMoveBy = 8.0f;
 constexpr int kRows = 128;               // query rows of a tile (lanes of tensor memory)
 constexpr int kKeys = 64;                // cached tokens of a tile
-constexpr int kLoadWarps = 4;
 constexpr int kScaleSlots = 8;           // tiles whose scales are held
+constexpr int kFar = 4;                  // tiles ahead that are brought to L2
 constexpr int kMinChunk = 4;             // fewest tiles of a split unit's part
 
 template <int D>
@@ -60,6 +60,9 @@ struct Tile {
     static constexpr int kQt = D <= 128 ? 2 : 1;         // query tiles of a CTA
     static constexpr int kSBufs = 2;                     // score buffers of a query tile
     static constexpr int kSoftWarps = 4 * kQt;
+    // loading warps: 16 tokens of a tile each, or 8 where the one query tile leaves room for more warps
+    static constexpr int kLoadWarps = D == 256 ? 8 : 4;
+    static constexpr int kLoadToks = kKeys / kLoadWarps;
     static constexpr int kThreads = (kSoftWarps + kLoadWarps + 2) * 32;
     static constexpr int kKStages = 2, kVStages = 3;     // tiles of keys and of values in shared memory
     static constexpr int kPanel = kKeys * 128;           // 128 bytes of each token of a tile
@@ -317,11 +320,11 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
     unsigned char* const smem = smem_raw + (sbase - sraw);
     const uint32_t bars = sbase + T::kOffBar;
     auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
-    constexpr int kMmaWarp = T::kSoftWarps + kLoadWarps;   // and the planner's after it
+    constexpr int kMmaWarp = T::kSoftWarps + T::kLoadWarps;   // and the planner's after it
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < T::kKStages; ++s) bar_init(bar(T::kKFull + s), kLoadWarps);
-        for (int s = 0; s < T::kVStages; ++s) bar_init(bar(T::kVFull + s), kLoadWarps);
+        for (int s = 0; s < T::kKStages; ++s) bar_init(bar(T::kKFull + s), T::kLoadWarps);
+        for (int s = 0; s < T::kVStages; ++s) bar_init(bar(T::kVFull + s), T::kLoadWarps);
         for (int q = 0; q < kQt; ++q) {
             bar_init(bar(T::kQFull + q), 4);
             bar_init(bar(T::kSFull + 2 * q), 1);
@@ -332,7 +335,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(bar(T::kPartFull + s), 1);
-            bar_init(bar(T::kPartFree + s), T::kSoftWarps + kLoadWarps + 1);
+            bar_init(bar(T::kPartFree + s), T::kSoftWarps + T::kLoadWarps + 1);
         }
         bar_init(bar(T::kDone), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -649,14 +652,16 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             u = next;
             have = have_next;
         }
-    } else if (warp < T::kSoftWarps + kLoadWarps) {
+    } else if (warp < T::kSoftWarps + T::kLoadWarps) {
         // ------------------------------------------------------------------ loads
-        const int w = warp - T::kSoftWarps;              // tokens 16w .. 16w + 15 of a tile
+        constexpr int kToks = T::kLoadToks, kH = kToks / 8;
+        const int w = warp - T::kSoftWarps;              // tokens kToks w .. of a tile
         constexpr int kKc = D / 16;                      // 16-byte chunks of a token's codes
-        constexpr int kKLoads = kKvBlock * kKc / 32;     // of a lane: whole lines, for K
+        constexpr int kKLoads = kToks * kKc / 32;        // of a lane: whole lines, for K
         constexpr int P = T::kVPanels;
-        const int c4 = lane & 3, r8 = lane >> 2;         // for V: 16 codes c4 of a panel's 64, tokens r8 and r8 + 8
-        uint4 kraw[kKLoads], vraw[2][P];
+        const int c4 = lane & 3, r8 = lane >> 2;         // for V: 16 codes c4 of a panel's 64, tokens r8 (and r8 + 8)
+        // the next tile, on its way in registers (two tiles there measured no faster)
+        uint4 kraw[kKLoads], vraw[kH][P];
         float ks = 1.0f, vs = 1.0f;
         Part u = {};
         // stages and scale slot of the next tile; the turns of each query tile's score barriers
@@ -670,9 +675,9 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         auto turn_done = [&](int q, uint32_t n) { return bar_wait(bar(T::kSFull + 2 * q) + 8 * (n & 1), (n >> 1) & 1); };
         // this warp's block of the tile that is loaded, and the page id of the next
         size_t unit = 0;
-        int in_page = 0, page_next = 0;
+        int in_page = 0, page_next = 0, page_far = 0;
         bool in = false;
-        auto token_of = [&](int i) { return u.lo + (u.t0 + i) * kKeys + 16 * w; };
+        auto token_of = [&](int i) { return u.lo + (u.t0 + i) * kKeys + kToks * w; };
         auto seek_page = [&](int i, int tiles) {
             if (i < tiles && token_of(i) < u.hi) page_next = kv_page(a.l, u.seq, token_of(i) >> a.l.page_shift);
         };
@@ -682,33 +687,43 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             unit = static_cast<size_t>(page_next) * a.l.kv_heads + u.head;
             in_page = t & (a.l.page_size - 1);
             seek_page(i + 1, tiles);
+            // The registers hold a tile ahead; lines of the tiles after it are brought to L2.
+            // (The page id asked for here serves the next call: nothing waits for it.)
+            constexpr int kLines = kToks * D / 128;
+            const int far = i + kFar, tf = token_of(far);
+            if (splits == 1) return;                     // many units: what one reads others have read
+            if (i > 0 && far < tiles && tf < u.hi && lane < kLines) {
+                const size_t at = ((static_cast<size_t>(page_far) * a.l.kv_heads + u.head) * a.l.page_size +
+                                   (tf & (a.l.page_size - 1))) * D + lane * 128;
+                asm volatile("prefetch.global.L2 [%0];" :: "l"(a.k_codes + at));
+                asm volatile("prefetch.global.L2 [%0];" :: "l"(a.v_codes + at));
+            }
+            if (far + 1 < tiles && token_of(far + 1) < u.hi) page_far = kv_page(a.l, u.seq, token_of(far + 1) >> a.l.page_shift);
         };
-        auto load_k = [&]() {
-            const uint8_t* src = a.k_codes + (unit * a.l.page_size + in_page) * D + lane * 16;
+        auto load = [&](int i, int tiles) {
+            seek(i, tiles);
+            const size_t base = (unit * a.l.page_size + in_page) * D;
+            const uint8_t* src = a.k_codes + base + lane * 16;
 #pragma unroll
             for (int r = 0; r < kKLoads; ++r)
                 kraw[r] = in ? __ldg(reinterpret_cast<const uint4*>(src + r * 512)) : make_uint4(0u, 0u, 0u, 0u);
-            const size_t at = unit * (a.l.page_size / kKvBlock) + in_page / kKvBlock;
-            ks = in ? __ldg(a.k_scales + at) : 1.0f;
-            vs = in ? __ldg(a.v_scales + at) : 1.0f;
-        };
-        auto load_v = [&]() {
-            const uint8_t* src = a.v_codes + (unit * a.l.page_size + in_page) * D + c4 * 16;
+            src = a.v_codes + base + c4 * 16;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kH; ++h)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     vraw[h][p] = in ? __ldg(reinterpret_cast<const uint4*>(src + (r8 + 8 * h) * D + p * 64))
-                                    : make_uint4(0u, 0u, 0u, 0u);
+                                  : make_uint4(0u, 0u, 0u, 0u);
+            const size_t at = unit * (a.l.page_size / kKvBlock) + in_page / kKvBlock;
+            ks = in ? __ldg(a.k_scales + at) : 1.0f;
+            vs = in ? __ldg(a.v_scales + at) : 1.0f;
         };
         bool run = true;
         for (int k = 0; run; ++k) {
             if (!__all_sync(0xffffffffu, take_part(k, u))) break;
             const int tiles = u.t1 - u.t0;
             seek_page(0, tiles);
-            seek(0, tiles);
-            load_k();
-            load_v();
+            load(0, tiles);
             const int q_last = u.live - 1;
             uint32_t base = 0;
 #pragma unroll
@@ -731,13 +746,14 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (i >= 2) ok = turn_done(q_last, base + i - 2);
                 else if (i == 0 && q_before >= 0) ok = turn_done(q_before, turns_before - 1);
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
-                if (lane == 0) scales[slot * 4 + w] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
+                if (lane == 0 && kToks * w % kKvBlock == 0)
+                    scales[slot * 4 + kToks * w / kKvBlock] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
                 slot = (slot + 1) % kScaleSlots;
                 const uint32_t kdst = sbase + T::kOffK + kst * T::kKPanels * T::kPanel;
 #pragma unroll
                 for (int r = 0; r < kKLoads; ++r) {
                     const int chunk = r * 32 + lane, tk = chunk / kKc, c = chunk % kKc;
-                    sts128(kdst + (c >> 3) * T::kPanel + (16 * w + tk) * 128 + (((c & 7) ^ (tk & 7)) << 4), kraw[r].x, kraw[r].y,
+                    sts128(kdst + (c >> 3) * T::kPanel + (kToks * w + tk) * 128 + (((c & 7) ^ (tk & 7)) << 4), kraw[r].x, kraw[r].y,
                            kraw[r].z, kraw[r].w);
                 }
                 fence_async();
@@ -746,31 +762,29 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (++kst == T::kKStages) kst = 0;
                 // tokens of the block that count: what lies past them may be anything, NaN
                 // codes too, and 0 times NaN is not 0.  (Scores of such keys are masked.)
-                const int valid = u.hi - (u.lo + (u.t0 + i) * kKeys + 16 * w);
-                seek(i + 1, tiles);
-                load_k();
+                const int valid = u.hi - token_of(i);
                 // the stage of values is free when the product with P of the tile three before is:
                 // turn base + i - 1; of the last tile of the item before: that item's own barrier
                 ok = i == 0 || turn_done(q_last, base + i - 1);
                 if (i == 1 && q_before >= 0) ok = ok && item_done();
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
-                if (valid < kKvBlock) {
+                if (valid < kToks) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < kH; ++h)
 #pragma unroll
                         for (int p = 0; p < P; ++p)
                             if (r8 + 8 * h >= valid) vraw[h][p] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 const uint32_t vdst = sbase + T::kOffV + vst * T::kVPanels * T::kPanel;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < kH; ++h)
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         const uint32_t code[4] = {vraw[h][p].x, vraw[h][p].y, vraw[h][p].z, vraw[h][p].w};
                         uint32_t o[8];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) e4m3x4_to_f16x2(code[j], o[2 * j], o[2 * j + 1]);
-                        const uint32_t at = vdst + p * T::kPanel + (16 * w + 8 * h + r8) * 128;
+                        const uint32_t at = vdst + p * T::kPanel + (kToks * w + 8 * h + r8) * 128;
                         sts128(at + (((2 * c4) ^ r8) << 4), o[0], o[1], o[2], o[3]);
                         sts128(at + (((2 * c4 + 1) ^ r8) << 4), o[4], o[5], o[6], o[7]);
                     }
@@ -778,7 +792,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(T::kVFull) + 8 * vst);
                 if (++vst == T::kVStages) vst = 0;
-                load_v();
+                load(i + 1, tiles);
             }
             if (tiles == 1 && q_before >= 0 && !__all_sync(0xffffffffu, item_done())) break;
             if (tiles > 0) {
@@ -868,7 +882,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         (void)bar_wait(bar(T::kDone), 0);
     } else {
         // ---------------------------------------------------------------------- plan
-        const int least = splits > 1 ? least_chunk<kQt * kRows>(a, gridDim.x) : kMinChunk;
+        int least = 0;
         for (int k = 0;; ++k) {
             // every role has the item before, and the loaders are nearly done with it
             if (k >= 1 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPartFree + ((k - 1) & 1)), ((k - 1) >> 1) & 1))) break;
@@ -877,6 +891,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             while (!found) {
                 unsigned int item = 0;
                 if (lane == 0) item = atomicAdd(a.counters, 1u);
+                if (least == 0) least = splits > 1 ? least_chunk<kQt * kRows>(a, gridDim.x) : kMinChunk;
                 item = __shfl_sync(0xffffffffu, item, 0);
                 if (item >= items) { last = true; break; }
                 found = find_part<kQt * kRows>(a, item, splits, least, u);
