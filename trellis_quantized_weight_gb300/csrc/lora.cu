@@ -8,14 +8,22 @@
 // adapter), at many rows x, y and out, and the tensor work is a few per cent of
 // either time, so m16n8k16 with bf16 operands and fp32 sums is enough.
 //
-// * Fragments come straight from global memory: the order of a sum's terms is free,
-//   so a lane's 8 consecutive elements (16 bytes) serve as its operands of two
-//   products, in both factors alike.
+// * The order of a sum's terms is free, so a lane's 8 consecutive elements (16 bytes) serve
+//   as its operands of two products, in both factors alike: fragments need no
+//   rearrangement.  They come through rings in shared memory that cp.async fills some
+//   steps ahead, by whole 128-byte lines.  The two halves of a line change places in odd
+//   rows, so that the 16-byte reads (8 rows by 64 bytes a warp) meet no bank conflict.
 // * h is summed over K by the warps of a CTA and over K splits by the second kernel,
 //   always in the same order.  It stays fp32; the second product takes it as the
 //   sum of two bf16 (16 significant bits), so that it rounds far below the one
 //   rounding of the result.
-// * Rows are cut into tiles inside each request's rows, 16 or 64 rows a CTA.
+// * Rows are cut into tiles inside each request's rows.  A warp of the first kernel takes
+//   a tile's 16, 32 or 64 rows by all of the rank and a share of K of its own, so that no
+//   two warps read the same.  In the second kernel's tiles of 128 rows the warps, 16 rows
+//   each, share B's columns.
+// * The first kernel lets the second start once all of its blocks run, after its own wait
+//   for what came before: so the second may find its tile and fetch y and B while the
+//   first still works, and waits only before it reads h.
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "trellis.h"
@@ -23,9 +31,6 @@
 namespace trellis {
 
 namespace {
-
-constexpr int kLoraWarps = 8;
-constexpr int kLoraThreads = kLoraWarps * 32;
 
 struct LoraArgs {
     const uint16_t *y, *x, *a, *b;
@@ -43,6 +48,21 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes, or zeros (nothing is read then).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lora_lds(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void lora_sts(uint32_t addr, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
 // Segment and rows [row, end) of row tile `tile` (tiles of kTileRows rows, counted
@@ -88,176 +108,289 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& p, int seg) {
     return w >= 0 && w < p.adapters ? w : -1;
 }
 
-// h[split][row][r] = sum over the split's k of x[row][k] a[r][k].  kRowGroups groups of
-// 16 rows; the other warps of the CTA, and the splits, share the sum over k in slabs of 32.
-template <int NT, int kRowGroups>
-__global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_constant__ LoraArgs p) {
-    constexpr int kKGroups = kLoraWarps / kRowGroups;
-    constexpr int kTileRows = 16 * kRowGroups;
-    extern __shared__ __align__(16) float sums[];        // [kKGroups][kTileRows][R]
+// Offset in a 128-byte line of its 16-byte piece, in row `row`.
+__device__ __forceinline__ uint32_t line_piece(int piece, int row) { return (piece ^ ((row & 1) << 2)) * 16; }
+
+// h[split][row][r] = sum over the split's k of x[row][k] a[r][k], for a tile of 16 MT rows
+// and a rank of at most 8 NT.  The warps of the CTA, and the splits, share the sum over k
+// in slabs of 64: 128 bytes of every row of x and of a, in a ring of the warp's own.
+template <int NT, int MT>
+struct Down {
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kStepBytes = (kRows + 8 * NT) * 128;
+    static constexpr int kWarps = kStepBytes <= 6144 ? 8 : 4;
+    // two CTAs an SM for tiles of 16 rows, which are many; one of the largest
+    static constexpr int kFit = (MT == 1 ? 112 : 200) * 1024 / (kWarps * kStepBytes);
+    static constexpr int kSteps = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    static constexpr int kRing = kWarps * kSteps * kStepBytes;
+    static constexpr int kSums = kWarps * kRows * (8 * NT + 8) * 4;          // [warp][row][R + 8], where the ring was
+    static constexpr int kSmem = kRing > kSums ? kRing : kSums;
+    static_assert(kSmem <= 232448 - 1024, "shared memory");
+};
+
+template <int NT, int MT>
+__global__ void __launch_bounds__(Down<NT, MT>::kWarps * 32) lora_down_kernel(const __grid_constant__ LoraArgs p) {
+    using S = Down<NT, MT>;
+    extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int found[4];
     griddep_wait();
+    griddep_launch_dependents();
     int seg, row0, end;
-    const bool any = find_tile<kTileRows>(p, blockIdx.x, found, &seg, &row0, &end);
-    const int w = any ? adapter_of(p, seg) : -1;
-    if (w >= 0) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const int rg = warp % kRowGroups, kg = warp / kRowGroups;
-        const int r0 = row0 + rg * 16 + g, r1 = r0 + 8;
-        const uint16_t* x0 = p.x + static_cast<size_t>(min(r0, end - 1)) * p.K;
-        const uint16_t* x1 = p.x + static_cast<size_t>(min(r1, end - 1)) * p.K;
-        const uint16_t* a = p.a + static_cast<size_t>(w) * p.R * p.K;
-        float acc[NT][4];
+    if (!find_tile<S::kRows>(p, blockIdx.x, found, &seg, &row0, &end)) return;
+    const int w = adapter_of(p, seg);
+    if (w < 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint16_t* a = p.a + static_cast<size_t>(w) * p.R * p.K;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kSteps * S::kStepBytes;
+    const int slabs = (p.K + 63) / 64, stride = p.splits * S::kWarps;
+    const int sl0 = blockIdx.y * S::kWarps + warp;
+    const int crow = lane >> 3, cpiece = lane & 7;       // a copy covers 4 rows by 8 pieces
+    auto issue = [&](int sl, int step) {
+        const int k = sl * 64 + cpiece * 8;
+        const bool in = k < p.K;                         // K is a multiple of 8: a piece is in or out
+        const uint32_t dst = ring + step * S::kStepBytes + crow * 128 + line_piece(cpiece, crow);
+#pragma unroll
+        for (int i = 0; i < S::kRows / 4; ++i) {         // rows past the tile's last repeat it
+            const int row = min(row0 + 4 * i + crow, end - 1);
+            cp_async16_or_zero(dst + i * 512, p.x + static_cast<size_t>(row) * p.K + (in ? k : 0), in);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+            const int r = 4 * i + crow;
+            const bool have = in && r < p.R;
+            cp_async16_or_zero(dst + (S::kRows / 4 + i) * 512, a + (have ? static_cast<size_t>(r) * p.K + k : 0), have);
+        }
+    };
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        const int slabs = (p.K + 31) / 32;
-        for (int sl = blockIdx.y * kKGroups + kg; sl < slabs; sl += p.splits * kKGroups) {
-            const int k = sl * 32 + t * 8;
-            const bool in = k < p.K;
-            uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0, b[NT];
-            if (in) {
-                u0 = __ldg(reinterpret_cast<const uint4*>(x0 + k));
-                u1 = __ldg(reinterpret_cast<const uint4*>(x1 + k));
-            }
+            for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S::kSteps - 1; ++i) {
+        if (sl0 + i * stride < slabs) issue(sl0 + i * stride, i);
+        cp_async_commit();
+    }
+    int step = 0, fill = S::kSteps - 1;
+    for (int sl = sl0; sl < slabs; sl += stride) {
+        cp_async_wait<S::kSteps - 2>();
+        __syncwarp();                                    // the copies of every lane; and its reads of the slot to fill
+        const int ahead = sl + (S::kSteps - 1) * stride;
+        if (ahead < slabs) issue(ahead, fill);
+        cp_async_commit();
+        const uint32_t src = ring + step * S::kStepBytes + g * 128;
+        step = step + 1 == S::kSteps ? 0 : step + 1;
+        fill = fill + 1 == S::kSteps ? 0 : fill + 1;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t at = src + line_piece(4 * q + t, g);
+            uint4 u[2 * MT];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) u[i] = lora_lds(at + i * 1024);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                b[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (in && 8 * i + g < p.R)
-                    b[i] = __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(8 * i + g) * p.K + k));
-            }
+                const uint4 b = lora_lds(at + (2 * MT + i) * 1024);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                mma_bf16(acc[i], u0.x, u1.x, u0.y, u1.y, b[i].x, b[i].y);
-                mma_bf16(acc[i], u0.z, u1.z, u0.w, u1.w, b[i].z, b[i].w);
+                for (int m = 0; m < MT; ++m) {
+                    mma_bf16(acc[m][i], u[2 * m].x, u[2 * m + 1].x, u[2 * m].y, u[2 * m + 1].y, b.x, b.y);
+                    mma_bf16(acc[m][i], u[2 * m].z, u[2 * m + 1].z, u[2 * m].w, u[2 * m + 1].w, b.z, b.w);
+                }
             }
         }
-        float* mine = sums + (kg * kTileRows + rg * 16) * p.R;
+    }
+    cp_async_wait<0>();
+    __syncthreads();                                     // every warp is done with its ring
+    // 8 floats between rows: 4 rows of a half warp's pairs fall into different banks
+    const int pitch = p.R + 8;
+    float* sums = reinterpret_cast<float*>(smem);
+    float* mine = sums + warp * S::kRows * pitch;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int c = 8 * i + 2 * t;
             if (c < p.R) {
-                *reinterpret_cast<float2*>(mine + g * p.R + c) = make_float2(acc[i][0], acc[i][1]);
-                *reinterpret_cast<float2*>(mine + (g + 8) * p.R + c) = make_float2(acc[i][2], acc[i][3]);
+                *reinterpret_cast<float2*>(mine + (16 * m + g) * pitch + c) = make_float2(acc[m][i][0], acc[m][i][1]);
+                *reinterpret_cast<float2*>(mine + (16 * m + g + 8) * pitch + c) = make_float2(acc[m][i][2], acc[m][i][3]);
             }
         }
-        __syncthreads();
-        const int live = (end - row0) * p.R;
-        float* h = p.h + (static_cast<size_t>(blockIdx.y) * p.M + row0) * p.R;
-        for (int e = threadIdx.x; e < live; e += kLoraThreads) {
-            float v = 0.0f;
+    __syncthreads();
+    const int quads = p.R / 4, live = (end - row0) * quads;
+    float* h = p.h + (static_cast<size_t>(blockIdx.y) * p.M + row0) * p.R;
+    for (int e = threadIdx.x; e < live; e += S::kWarps * 32) {
+        const int row = e / quads, at = row * pitch + (e - row * quads) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int q = 0; q < kKGroups; ++q) v += sums[q * kTileRows * p.R + e];
-            h[e] = v;
+        for (int q = 0; q < S::kWarps; ++q) {
+            const float4 s = *reinterpret_cast<const float4*>(sums + q * S::kRows * pitch + at);
+            v.x += s.x; v.y += s.y; v.z += s.z; v.w += s.w;
         }
+        *reinterpret_cast<float4*>(h + static_cast<size_t>(e) * 4) = v;
     }
-    griddep_launch_dependents();
 }
 
-// out = y + s h B^T for a tile of rows and kCols columns a pass; NT slabs of 32 of the rank.
-template <int NS, int kRowGroups, bool kVec>
-__global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_constant__ LoraArgs p, int cols_per_cta) {
-    constexpr int kColGroups = kLoraWarps / kRowGroups;
-    constexpr int kTileRows = 16 * kRowGroups;
+// out = y + s h B^T for a tile of 16 RG rows, a warp's 16 rows by 64 columns at a step.
+// RG warps share the step's B; RG = 1: each warp has columns of its own.  NS: slabs of 32
+// of the rank.
+template <int NS, int RG, bool kVec>
+struct Up {
+    static constexpr int kWarps = RG == 1 ? 4 : RG;
+    static constexpr int kCols = 64 * (kWarps / RG);                         // of the CTA's warps in a step
+    static constexpr int kB = 64 * NS * 64, kY = kVec ? 16 * 128 : 0;
+    static constexpr int kStepBytes = kB * (kWarps / RG) + kY * kWarps;
+    static constexpr int kFit = 112 * 1024 / kStepBytes;                     // two CTAs an SM
+    static constexpr int kSteps = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    static constexpr int kSmem = kSteps * kStepBytes;
+    static_assert(kSmem <= 232448 - 1024, "shared memory");
+};
+
+template <int NS, int RG, bool kVec>
+__global__ void __launch_bounds__(Up<NS, RG, kVec>::kWarps * 32, 2)
+lora_up_kernel(const __grid_constant__ LoraArgs p, int cols_per_cta) {
+    using S = Up<NS, RG, kVec>;
+    extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int found[4];
-    griddep_wait();
     int seg, row0, end;
-    const bool any = find_tile<kTileRows>(p, blockIdx.x, found, &seg, &row0, &end);
-    if (any) {
-        const int w = adapter_of(p, seg);
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const int rg = warp % kRowGroups, cg = warp / kRowGroups;
-        const int ra = row0 + rg * 16 + g, rb = ra + 8;
-        const bool la = ra < end, lb = rb < end;
-        const float s = w >= 0 ? __ldg(p.scales + w) : 0.0f;
-        // h as the sum of two bf16: fragments hi, lo of 2 products a slab
-        uint32_t hi[NS][2][4], lo[NS][2][4];
+    if (!find_tile<16 * RG>(p, blockIdx.x, found, &seg, &row0, &end)) {
+        griddep_wait();                                  // what follows may rely on what came before this kernel
+        return;
+    }
+    const int w = adapter_of(p, seg);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rg = warp % RG, cg = warp / RG;
+    const int wrow = row0 + rg * 16;                     // the warp's rows: it may have none
+    const int ra = wrow + g, rb = ra + 8;
+    const bool la = ra < end, lb = rb < end;
+    const uint16_t* B = p.b + (w >= 0 ? static_cast<size_t>(w) * p.N * p.R : 0);
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const uint32_t ring_b = base + cg * S::kB, ring_y = base + S::kB * (S::kWarps / RG) + warp * S::kY;
+    const int c_end = min(p.N, (static_cast<int>(blockIdx.y) + 1) * cols_per_cta);
+    const int first = blockIdx.y * cols_per_cta + cg * 64;
+    const int crow = lane >> 3, cpiece = lane & 7;
+    auto sync = [] {
+        if constexpr (RG == 1) __syncwarp();
+        else __syncthreads();
+    };
+    auto issue = [&](int c0, int step) {
+        if (w >= 0) {
+            const uint32_t dst = ring_b + step * S::kStepBytes;
+            // B's rows, NS 64 bytes each; odd ones with the halves of their lines exchanged
 #pragma unroll
-        for (int sl = 0; sl < NS; ++sl) {
-            const int r = sl * 32 + t * 8;
-            float v[2][8];
+            for (int i = 0; i < 64 * 4 * NS / (RG * 32); ++i) {
+                const int e = i * RG * 32 + rg * 32 + lane, n = e / (4 * NS), piece = e % (4 * NS);
+                const bool have = piece * 8 < p.R;
+                cp_async16_or_zero(dst + n * (NS * 64) + (NS == 1 ? piece * 16 : line_piece(piece, n)),
+                                   B + (have ? static_cast<size_t>(min(c0 + n, p.N - 1)) * p.R + piece * 8 : 0), have);
+            }
+        }
+        if constexpr (kVec) {
+            const uint32_t dst = ring_y + step * S::kStepBytes + crow * 128 + line_piece(cpiece, crow);
+            const int col = c0 + cpiece * 8;
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int i = 0; i < 4; ++i) {
+                const int row = wrow + 4 * i + crow;
+                if (row < end && col < p.N)
+                    cp_async16_or_zero(dst + i * 512, p.y + static_cast<size_t>(row) * p.N + col, true);
+            }
+        }
+    };
+    constexpr int kHop = S::kCols;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
-            if (w >= 0 && r < p.R) {
-                for (int sp = 0; sp < p.splits; ++sp) {
-                    const float* h = p.h + static_cast<size_t>(sp) * p.M * p.R + r;
+    for (int i = 0; i < S::kSteps - 1; ++i) {
+        if (first + i * kHop < c_end) issue(first + i * kHop, i);
+        cp_async_commit();
+    }
+    const float s = w >= 0 ? __ldg(p.scales + w) : 0.0f;
+    griddep_wait();
+    // h as the sum of two bf16: fragments hi, lo of 2 products a slab
+    uint32_t hi[NS][2][4], lo[NS][2][4];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (q == 0 ? la : lb) {
-                            const float4* h4 = reinterpret_cast<const float4*>(h + static_cast<size_t>(q == 0 ? ra : rb) * p.R);
-                            const float4 f0 = h4[0], f1 = h4[1];
-                            v[q][0] += f0.x; v[q][1] += f0.y; v[q][2] += f0.z; v[q][3] += f0.w;
-                            v[q][4] += f1.x; v[q][5] += f1.y; v[q][6] += f1.z; v[q][7] += f1.w;
-                        }
+    for (int sl = 0; sl < NS; ++sl) {
+        const int r = sl * 32 + t * 8;
+        float v[2][8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
+        if (w >= 0 && r < p.R) {
+#pragma unroll 4
+            for (int sp = 0; sp < p.splits; ++sp) {
+                const float* h = p.h + static_cast<size_t>(sp) * p.M * p.R + r;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (q == 0 ? la : lb) {
+                        const float4* h4 = reinterpret_cast<const float4*>(h + static_cast<size_t>(q == 0 ? ra : rb) * p.R);
+                        const float4 f0 = h4[0], f1 = h4[1];
+                        v[q][0] += f0.x; v[q][1] += f0.y; v[q][2] += f0.z; v[q][3] += f0.w;
+                        v[q][4] += f1.x; v[q][5] += f1.y; v[q][6] += f1.z; v[q][7] += f1.w;
                     }
                 }
             }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float v0 = s * v[q][2 * i], v1 = s * v[q][2 * i + 1];
+                const uint32_t h2 = pack_bf16x2(v0, v1);
+                // product i / 2; registers: row g then row g + 8, first pair then second.
+                // An infinite sum has no rest (inf - inf would make it NaN)
+                const float e0 = v0 - bf16_lo(h2), e1 = v1 - bf16_hi(h2);
+                hi[sl][i >> 1][(i & 1) * 2 + q] = h2;
+                lo[sl][i >> 1][(i & 1) * 2 + q] = pack_bf16x2(e0 == e0 ? e0 : 0.0f, e1 == e1 ? e1 : 0.0f);
+            }
+    }
+    int step = 0, fill = S::kSteps - 1;
+    for (int c0 = first; c0 < c_end; c0 += kHop) {
+        cp_async_wait<S::kSteps - 2>();
+        sync();                                          // every copy of the step; and all are done with the slot to fill
+        const int ahead = c0 + (S::kSteps - 1) * kHop;
+        if (ahead < c_end) issue(ahead, fill);
+        cp_async_commit();
+        const uint32_t src_b = ring_b + step * S::kStepBytes, src_y = ring_y + step * S::kStepBytes;
+        step = step + 1 == S::kSteps ? 0 : step + 1;
+        fill = fill + 1 == S::kSteps ? 0 : fill + 1;
+        if (wrow >= end) continue;
+        // column c0 + 32 q + 8 t + 2 i + e belongs to tile i, so a lane's columns are 8 neighbours
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float acc[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float v0 = s * v[q][2 * i], v1 = s * v[q][2 * i + 1];
-                    const uint32_t h2 = pack_bf16x2(v0, v1);
-                    // product i / 2; registers: row g then row g + 8, first pair then second.
-                    // An infinite sum has no rest (inf - inf would make it NaN)
-                    const float e0 = v0 - bf16_lo(h2), e1 = v1 - bf16_hi(h2);
-                    hi[sl][i >> 1][(i & 1) * 2 + q] = h2;
-                    lo[sl][i >> 1][(i & 1) * 2 + q] = pack_bf16x2(e0 == e0 ? e0 : 0.0f, e1 == e1 ? e1 : 0.0f);
-                }
-        }
-        const uint16_t* B = p.b + (w >= 0 ? static_cast<size_t>(w) * p.N * p.R : 0);
-        const int c_end = min(p.N, (static_cast<int>(blockIdx.y) + 1) * cols_per_cta);
-        for (int c0 = blockIdx.y * cols_per_cta + cg * 32; c0 < c_end; c0 += kColGroups * 32) {
-            float acc[4][4];
-            // column c0 + 8 t + 2 i + e belongs to tile i, so a lane's columns are 8 neighbours
-            uint4 b[4][NS];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-                const int n = min(c0 + 8 * (g >> 1) + 2 * i + (g & 1), p.N - 1);
-#pragma unroll
-                for (int sl = 0; sl < NS; ++sl) {
-                    const int r = sl * 32 + t * 8;
-                    b[i][sl] = make_uint4(0u, 0u, 0u, 0u);
-                    if (w >= 0 && r < p.R)
-                        b[i][sl] = __ldg(reinterpret_cast<const uint4*>(B + static_cast<size_t>(n) * p.R + r));
-                }
-            }
-            const int col = c0 + 8 * t;
-            uint4 ya = make_uint4(0u, 0u, 0u, 0u), yb = ya;
-            const size_t ia = static_cast<size_t>(ra) * p.N + col, ib = static_cast<size_t>(rb) * p.N + col;
-            if (kVec) {
-                if (la && col < p.N) ya = *reinterpret_cast<const uint4*>(p.y + ia);
-                if (lb && col < p.N) yb = *reinterpret_cast<const uint4*>(p.y + ib);
-            }
             if (w >= 0) {
 #pragma unroll
                 for (int sl = 0; sl < NS; ++sl)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 q = b[i][sl];
-                        mma_bf16(acc[i], lo[sl][0][0], lo[sl][0][1], lo[sl][0][2], lo[sl][0][3], q.x, q.y);
-                        mma_bf16(acc[i], lo[sl][1][0], lo[sl][1][1], lo[sl][1][2], lo[sl][1][3], q.z, q.w);
-                        mma_bf16(acc[i], hi[sl][0][0], hi[sl][0][1], hi[sl][0][2], hi[sl][0][3], q.x, q.y);
-                        mma_bf16(acc[i], hi[sl][1][0], hi[sl][1][1], hi[sl][1][2], hi[sl][1][3], q.z, q.w);
+                        const int n = 32 * q + 8 * (g >> 1) + 2 * i + (g & 1), piece = sl * 4 + t;
+                        const uint4 b = lora_lds(src_b + n * (NS * 64) + (NS == 1 ? piece * 16 : line_piece(piece, g)));
+                        mma_bf16(acc[i], lo[sl][0][0], lo[sl][0][1], lo[sl][0][2], lo[sl][0][3], b.x, b.y);
+                        mma_bf16(acc[i], lo[sl][1][0], lo[sl][1][1], lo[sl][1][2], lo[sl][1][3], b.z, b.w);
+                        mma_bf16(acc[i], hi[sl][0][0], hi[sl][0][1], hi[sl][0][2], hi[sl][0][3], b.x, b.y);
+                        mma_bf16(acc[i], hi[sl][1][0], hi[sl][1][1], hi[sl][1][2], hi[sl][1][3], b.z, b.w);
                     }
             }
-            if (kVec) {
-                const uint32_t y0[4] = {ya.x, ya.y, ya.z, ya.w}, y1[4] = {yb.x, yb.y, yb.z, yb.w};
-                uint32_t o0[4], o1[4];
+            if constexpr (kVec) {
+                // y's piece gives way to the result's; without an adapter y passes, whatever its bits
+                if (w >= 0) {
+                    const uint32_t at = src_y + g * 128 + line_piece(4 * q + t, g);
+                    const uint4 ya = lora_lds(at), yb = lora_lds(at + 1024);
+                    const uint32_t y0[4] = {ya.x, ya.y, ya.z, ya.w}, y1[4] = {yb.x, yb.y, yb.z, yb.w};
+                    uint32_t o0[4], o1[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // without an adapter y passes as it is, whatever its bits
-                    o0[i] = w < 0 ? y0[i] : pack_bf16x2(bf16_lo(y0[i]) + acc[i][0], bf16_hi(y0[i]) + acc[i][1]);
-                    o1[i] = w < 0 ? y1[i] : pack_bf16x2(bf16_lo(y1[i]) + acc[i][2], bf16_hi(y1[i]) + acc[i][3]);
+                    for (int i = 0; i < 4; ++i) {
+                        o0[i] = pack_bf16x2(bf16_lo(y0[i]) + acc[i][0], bf16_hi(y0[i]) + acc[i][1]);
+                        o1[i] = pack_bf16x2(bf16_lo(y1[i]) + acc[i][2], bf16_hi(y1[i]) + acc[i][3]);
+                    }
+                    lora_sts(at, o0);
+                    lora_sts(at + 1024, o1);
                 }
-                if (la && col < p.N) *reinterpret_cast<uint4*>(p.out + ia) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                if (lb && col < p.N) *reinterpret_cast<uint4*>(p.out + ib) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
             } else {
+                const int col = c0 + 32 * q + 8 * t;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -277,62 +410,100 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
                     }
             }
         }
+        if constexpr (kVec) {
+            __syncwarp();
+            const uint32_t src = src_y + crow * 128 + line_piece(cpiece, crow);
+            const int col = c0 + cpiece * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = wrow + 4 * i + crow;
+                if (row < end && col < p.N)
+                    *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * p.N + col) = lora_lds(src + i * 512);
+            }
+        }
     }
+    cp_async_wait<0>();
     griddep_launch_dependents();
 }
 
 struct LoraShape {
-    bool wide;          // 64-row tiles
-    int tiles;          // upper bound: the segments' lengths are on the device
-    int splits;
-    int cols;           // columns of a CTA of the second kernel
+    bool wide;                       // tiles of many rows
+    int down_tiles, splits;          // of the first kernel: tiles are an upper bound, the lengths are on the device
+    int up_tiles, cols;              // of the second: columns of a CTA
 };
 
-LoraShape lora_shape(int M, int K, int N, int segments, const DeviceInfo& dev) {
+// NT of the first kernel: eighths of the rank, rounded up to what is compiled.
+int down_nt(int R) { return R <= 16 ? 2 : R <= 32 ? 4 : R <= 64 ? 8 : 16; }
+
+template <int NT>
+void down_size(bool wide, int* rows, int* warps, int* steps) {
+    using W = Down<NT, NT == 16 ? 2 : 4>;
+    using F = Down<NT, 1>;
+    *rows = wide ? W::kRows : F::kRows;
+    *warps = wide ? W::kWarps : F::kWarps;
+    *steps = wide ? W::kSteps : F::kSteps;
+}
+
+#ifndef WIDE_ROWS
+#define WIDE_ROWS 64
+#endif
+#ifndef UPW
+#define UPW 2
+#endif
+LoraShape lora_shape(int M, int K, int N, int R, int segments, const DeviceInfo& dev) {
     LoraShape s;
-    // a tile of 64 rows reads its adapter once for four row groups (through L1); with
-    // fewer than 64 rows a segment on average it would mostly hold padding
-    s.wide = M / segments >= 64;
-    const int rows = s.wide ? 64 : 16;
-    // at most one partial tile a segment, and no tile without a row
-    const long long bound = static_cast<long long>(M) / rows + segments;
-    s.tiles = static_cast<int>(bound < M ? bound : M);
-    const int slabs = (K + 31) / 32;
-    const int groups = kLoraWarps / (rows / 16);
-    int splits = (2 * dev.num_sms + s.tiles - 1) / s.tiles;
-    const int most = slabs / (2 * groups) > 0 ? slabs / (2 * groups) : 1;
-    splits = splits < most ? splits : most;
-    s.splits = splits > 32 ? 32 : splits;
-    const int unit = 32 * groups;
-    int parts = (4 * dev.num_sms + s.tiles - 1) / s.tiles;
+    // large tiles read an adapter once for all of their rows; with fewer rows a segment on
+    // average they would mostly hold padding
+    s.wide = M / segments >= WIDE_ROWS;
+    auto tiles = [&](int rows) {     // at most one partial tile a segment, and no tile without a row
+        const long long bound = static_cast<long long>(M) / rows + segments;
+        return static_cast<int>(bound < M ? bound : M);
+    };
+    int rows, warps, steps;
+    switch (down_nt(R)) {
+        case 2: down_size<2>(s.wide, &rows, &warps, &steps); break;
+        case 4: down_size<4>(s.wide, &rows, &warps, &steps); break;
+        case 8: down_size<8>(s.wide, &rows, &warps, &steps); break;
+        default: down_size<16>(s.wide, &rows, &warps, &steps); break;
+    }
+    s.down_tiles = tiles(rows);
+    s.up_tiles = tiles(s.wide ? 128 : 16);
+    // K is split until the CTAs fill the SMs, or each warp's first copies cover its share:
+    // more splits would only be more to add up
+    const int slabs = (K + 63) / 64;
+    const int fill = (s.wide ? 1 : 2) * dev.num_sms / s.down_tiles;
+    const int most = (slabs + warps * (steps - 1) - 1) / (warps * (steps - 1));
+    const int splits = fill < most ? fill : most;
+    s.splits = splits < 1 ? 1 : splits > 32 ? 32 : splits;
+    const int unit = s.wide ? 64 : 256;                  // columns of a CTA's warps in a step
     const int col_units = (N + unit - 1) / unit;
+    int parts = (UPW * dev.num_sms + s.up_tiles - 1) / s.up_tiles;
     parts = parts < col_units ? parts : col_units;
     s.cols = (col_units + parts - 1) / parts * unit;
     return s;
 }
 
-template <int NT>
+template <int NT, int MT>
 cudaError_t launch_down(const LoraArgs& p, const LoraShape& s, cudaStream_t stream) {
-    const dim3 grid(s.tiles, s.splits);
-    const size_t smem = static_cast<size_t>(kLoraWarps) * 16 * p.R * 4;
-    if (s.wide) {
-        static std::atomic<unsigned long long> opted{0};
-        if (!smem_opt_in(lora_down_kernel<NT, 4>, kLoraWarps * 16 * 8 * NT * 4, opted)) return cudaErrorInvalidValue;
-        return launch_programmatic_grid(lora_down_kernel<NT, 4>, grid, kLoraThreads, smem, stream, p);
-    }
+    using S = Down<NT, MT>;
     static std::atomic<unsigned long long> opted{0};
-    if (!smem_opt_in(lora_down_kernel<NT, 1>, kLoraWarps * 16 * 8 * NT * 4, opted)) return cudaErrorInvalidValue;
-    return launch_programmatic_grid(lora_down_kernel<NT, 1>, grid, kLoraThreads, smem, stream, p);
+    if (!smem_opt_in(lora_down_kernel<NT, MT>, S::kSmem, opted)) return cudaErrorInvalidValue;
+    return launch_programmatic_grid(lora_down_kernel<NT, MT>, dim3(s.down_tiles, s.splits), S::kWarps * 32, S::kSmem, stream, p);
+}
+
+template <int NS, int RG, bool kVec>
+cudaError_t launch_up_as(const LoraArgs& p, const LoraShape& s, cudaStream_t stream) {
+    using S = Up<NS, RG, kVec>;
+    static std::atomic<unsigned long long> opted{0};
+    if (!smem_opt_in(lora_up_kernel<NS, RG, kVec>, S::kSmem, opted)) return cudaErrorInvalidValue;
+    return launch_programmatic_grid(lora_up_kernel<NS, RG, kVec>, dim3(s.up_tiles, (p.N + s.cols - 1) / s.cols), S::kWarps * 32,
+                                    S::kSmem, stream, p, s.cols);
 }
 
 template <int NS>
 cudaError_t launch_up(const LoraArgs& p, const LoraShape& s, bool vec, cudaStream_t stream) {
-    const dim3 grid(s.tiles, (p.N + s.cols - 1) / s.cols);
-    if (s.wide)
-        return vec ? launch_programmatic_grid(lora_up_kernel<NS, 4, true>, grid, kLoraThreads, 0, stream, p, s.cols)
-                   : launch_programmatic_grid(lora_up_kernel<NS, 4, false>, grid, kLoraThreads, 0, stream, p, s.cols);
-    return vec ? launch_programmatic_grid(lora_up_kernel<NS, 1, true>, grid, kLoraThreads, 0, stream, p, s.cols)
-               : launch_programmatic_grid(lora_up_kernel<NS, 1, false>, grid, kLoraThreads, 0, stream, p, s.cols);
+    if (s.wide) return vec ? launch_up_as<NS, 8, true>(p, s, stream) : launch_up_as<NS, 8, false>(p, s, stream);
+    return vec ? launch_up_as<NS, 1, true>(p, s, stream) : launch_up_as<NS, 1, false>(p, s, stream);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -358,7 +529,7 @@ int trellis_lora_add_workspace_size(int M, int K, int N, int R, int adapters, in
     DeviceInfo dev;
     rc = device_info(dev);
     if (rc != TRELLIS_OK) return rc;
-    const LoraShape s = lora_shape(M > 0 ? M : 1, K, N, segments, dev);
+    const LoraShape s = lora_shape(M > 0 ? M : 1, K, N, R, segments, dev);
     // the products' counter region stays free (and zero) in front
     *bytes = (size_t(1) << 20) + static_cast<size_t>(s.splits) * M * R * 4;
     return TRELLIS_OK;
@@ -385,13 +556,18 @@ int trellis_lora_add(const uint16_t* y, const uint16_t* x, const uint16_t* a, co
     DeviceInfo dev;
     rc = device_info(dev);
     if (rc != TRELLIS_OK) return rc;
-    const LoraShape s = lora_shape(M, K, N, segments, dev);
+    const LoraShape s = lora_shape(M, K, N, R, segments, dev);
     LoraArgs p;
     p.y = y; p.x = x; p.a = a; p.b = b; p.scales = scales; p.starts = starts; p.which = which; p.out = out;
     p.h = reinterpret_cast<float*>(static_cast<char*>(workspace) + (size_t(1) << 20));
     p.M = M; p.K = K; p.N = N; p.R = R; p.adapters = adapters; p.segments = segments; p.splits = s.splits;
-    cudaError_t e = R <= 16 ? launch_down<2>(p, s, stream) : R <= 32 ? launch_down<4>(p, s, stream)
-                    : R <= 64 ? launch_down<8>(p, s, stream) : launch_down<16>(p, s, stream);
+    cudaError_t e = cudaSuccess;
+    switch (down_nt(R)) {
+        case 2: e = s.wide ? launch_down<2, 4>(p, s, stream) : launch_down<2, 1>(p, s, stream); break;
+        case 4: e = s.wide ? launch_down<4, 4>(p, s, stream) : launch_down<4, 1>(p, s, stream); break;
+        case 8: e = s.wide ? launch_down<8, 4>(p, s, stream) : launch_down<8, 1>(p, s, stream); break;
+        default: e = s.wide ? launch_down<16, 2>(p, s, stream) : launch_down<16, 1>(p, s, stream); break;
+    }
     if (e != cudaSuccess) return TRELLIS_ERR_CUDA;
     // 16-byte accesses of y and out
     const bool vec = N % 8 == 0 && aligned(y, 16) && aligned(out, 16);
