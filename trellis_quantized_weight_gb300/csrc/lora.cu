@@ -118,7 +118,7 @@ template <int NT, int MT>
 struct Down {
     static constexpr int kRows = 16 * MT;
     static constexpr int kStepBytes = (kRows + 8 * NT) * 128;
-    static constexpr int kWarps = kStepBytes <= 6144 ? 8 : 4;
+    static constexpr int kWarps = 4;
     // two CTAs an SM for tiles of 16 rows, which are many; one of the largest
     static constexpr int kFit = (MT == 1 ? 112 : 200) * 1024 / (kWarps * kStepBytes);
     static constexpr int kSteps = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
@@ -145,22 +145,26 @@ __global__ void __launch_bounds__(Down<NT, MT>::kWarps * 32) lora_down_kernel(co
     const int slabs = (p.K + 63) / 64, stride = p.splits * S::kWarps;
     const int sl0 = blockIdx.y * S::kWarps + warp;
     const int crow = lane >> 3, cpiece = lane & 7;       // a copy covers 4 rows by 8 pieces
+    const uint32_t mine_at = ring + crow * 128 + line_piece(cpiece, crow);
+    const int x_rows = end - row0 - crow, a_rows = p.R - crow;
+    const size_t hop = static_cast<size_t>(p.K) * 4;
+    const uint16_t* x_at = p.x + static_cast<size_t>(row0 + (x_rows > 0 ? crow : 0)) * p.K;
+    const uint16_t* a_at = a + static_cast<size_t>(crow) * p.K;
     auto issue = [&](int sl, int step) {
         const int k = sl * 64 + cpiece * 8;
         const bool in = k < p.K;                         // K is a multiple of 8: a piece is in or out
-        const uint32_t dst = ring + step * S::kStepBytes + crow * 128 + line_piece(cpiece, crow);
+        const uint32_t dst = mine_at + step * S::kStepBytes;
+        const uint16_t *xs = x_at + (in ? k : 0), *as = a_at + (in ? k : 0);
 #pragma unroll
-        for (int i = 0; i < S::kRows / 4; ++i) {         // rows past the tile's last repeat it
-            const int row = min(row0 + 4 * i + crow, end - 1);
-            cp_async16_or_zero(dst + i * 512, p.x + static_cast<size_t>(row) * p.K + (in ? k : 0), in);
-        }
+        for (int i = 0; i < S::kRows / 4; ++i, xs += hop)        // past the tile's last row anything may stand
+            if (4 * i < x_rows) cp_async16_or_zero(dst + i * 512, xs, in);
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-            const int r = 4 * i + crow;
-            const bool have = in && r < p.R;
-            cp_async16_or_zero(dst + (S::kRows / 4 + i) * 512, a + (have ? static_cast<size_t>(r) * p.K + k : 0), have);
-        }
+        for (int i = 0; i < 2 * NT; ++i, as += hop)
+            if (4 * i < a_rows) cp_async16_or_zero(dst + (S::kRows / 4 + i) * 512, as, in);
     };
+    for (int i = 0; i < 2 * NT; ++i)                     // rows past the rank: zero, once
+        if (4 * i >= a_rows)
+            for (int q = 0; q < S::kSteps; ++q) lora_sts(mine_at + q * S::kStepBytes + (S::kRows / 4 + i) * 512, {0, 0, 0, 0});
     float acc[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -273,29 +277,38 @@ lora_up_kernel(const __grid_constant__ LoraArgs p, int cols_per_cta) {
         if constexpr (RG == 1) __syncwarp();
         else __syncthreads();
     };
+    // B: a copy covers kBRows of its rows, which are NS 64 bytes each; odd ones have the halves of their lines exchanged
+    constexpr int kBRows = RG * 8 / NS;
+    const int bn = (rg * 32 + lane) / (4 * NS), bpiece = (rg * 32 + lane) % (4 * NS);
+    const uint32_t b_at = ring_b + bn * (NS * 64) + (NS == 1 ? bpiece * 16 : line_piece(bpiece, bn));
+    const bool b_have = w >= 0 && bpiece * 8 < p.R;
+    const uint16_t* b_from = B + static_cast<size_t>(bn) * p.R + bpiece * 8;
+    const size_t b_hop = static_cast<size_t>(kBRows) * p.R;
+    // y: 4 rows by 8 pieces
+    const uint32_t y_at = ring_y + crow * 128 + line_piece(cpiece, crow);
+    const int y_rows = end - wrow - crow;
+    const size_t y_from = static_cast<size_t>(wrow + crow) * p.N + cpiece * 8, y_hop = static_cast<size_t>(p.N) * 4;
     auto issue = [&](int c0, int step) {
-        if (w >= 0) {
-            const uint32_t dst = ring_b + step * S::kStepBytes;
-            // B's rows, NS 64 bytes each; odd ones with the halves of their lines exchanged
+        if (b_have) {
+            const uint32_t dst = b_at + step * S::kStepBytes;
+            const uint16_t* src = b_from + static_cast<size_t>(c0) * p.R;
+            const int left = p.N - c0 - bn;              // past the last column anything may stand
 #pragma unroll
-            for (int i = 0; i < 64 * 4 * NS / (RG * 32); ++i) {
-                const int e = i * RG * 32 + rg * 32 + lane, n = e / (4 * NS), piece = e % (4 * NS);
-                const bool have = piece * 8 < p.R;
-                cp_async16_or_zero(dst + n * (NS * 64) + (NS == 1 ? piece * 16 : line_piece(piece, n)),
-                                   B + (have ? static_cast<size_t>(min(c0 + n, p.N - 1)) * p.R + piece * 8 : 0), have);
-            }
+            for (int i = 0; i < 64 / kBRows; ++i, src += b_hop)
+                if (i * kBRows < left) cp_async16_or_zero(dst + i * kBRows * NS * 64, src, true);
         }
         if constexpr (kVec) {
-            const uint32_t dst = ring_y + step * S::kStepBytes + crow * 128 + line_piece(cpiece, crow);
-            const int col = c0 + cpiece * 8;
+            const uint32_t dst = y_at + step * S::kStepBytes;
+            const uint16_t* src = p.y + y_from + c0;
+            const int rows = c0 + cpiece * 8 < p.N ? y_rows : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = wrow + 4 * i + crow;
-                if (row < end && col < p.N)
-                    cp_async16_or_zero(dst + i * 512, p.y + static_cast<size_t>(row) * p.N + col, true);
-            }
+            for (int i = 0; i < 4; ++i, src += y_hop)
+                if (4 * i < rows) cp_async16_or_zero(dst + i * 512, src, true);
         }
     };
+    if (bpiece * 8 >= p.R)                               // past the rank: zero, once
+        for (int q = 0; q < S::kSteps; ++q)
+            for (int i = 0; i < 64 / kBRows; ++i) lora_sts(b_at + q * S::kStepBytes + i * kBRows * NS * 64, {0, 0, 0, 0});
     constexpr int kHop = S::kCols;
 #pragma unroll
     for (int i = 0; i < S::kSteps - 1; ++i) {
@@ -413,13 +426,11 @@ lora_up_kernel(const __grid_constant__ LoraArgs p, int cols_per_cta) {
         if constexpr (kVec) {
             __syncwarp();
             const uint32_t src = src_y + crow * 128 + line_piece(cpiece, crow);
-            const int col = c0 + cpiece * 8;
+            uint16_t* dst = p.out + y_from + c0;
+            const int rows = c0 + cpiece * 8 < p.N ? y_rows : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = wrow + 4 * i + crow;
-                if (row < end && col < p.N)
-                    *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * p.N + col) = lora_lds(src + i * 512);
-            }
+            for (int i = 0; i < 4; ++i, dst += y_hop)
+                if (4 * i < rows) *reinterpret_cast<uint4*>(dst) = lora_lds(src + i * 512);
         }
     }
     cp_async_wait<0>();
@@ -446,9 +457,6 @@ void down_size(bool wide, int* rows, int* warps, int* steps) {
 
 #ifndef WIDE_ROWS
 #define WIDE_ROWS 64
-#endif
-#ifndef UPW
-#define UPW 2
 #endif
 LoraShape lora_shape(int M, int K, int N, int R, int segments, const DeviceInfo& dev) {
     LoraShape s;
@@ -477,7 +485,9 @@ LoraShape lora_shape(int M, int K, int N, int R, int segments, const DeviceInfo&
     s.splits = splits < 1 ? 1 : splits > 32 ? 32 : splits;
     const int unit = s.wide ? 64 : 256;                  // columns of a CTA's warps in a step
     const int col_units = (N + unit - 1) / unit;
-    int parts = (UPW * dev.num_sms + s.up_tiles - 1) / s.up_tiles;
+    // two CTAs an SM; ragged tiles of many rows even out in shorter turns (4k rows: 74 us at
+    // 6, 92 at 2 or one wave, 78 at 10), 16-row ones are alike (64 rows: 19 at 2, 23 at 10)
+    int parts = ((s.wide ? 6 : 2) * dev.num_sms + s.up_tiles - 1) / s.up_tiles;
     parts = parts < col_units ? parts : col_units;
     s.cols = (col_units + parts - 1) / parts * unit;
     return s;
