@@ -244,14 +244,15 @@ struct Up {
     static constexpr int kCols = 64 * (kWarps / RG);                         // of the CTA's warps in a step
     static constexpr int kB = 64 * NS * 64, kY = kVec ? 16 * 128 : 0;
     static constexpr int kStepBytes = kB * (kWarps / RG) + kY * kWarps;
-    static constexpr int kFit = 112 * 1024 / kStepBytes;                     // two CTAs an SM
+    static constexpr int kCtas = RG == 1 ? 2 : 4;                           // an SM
+    static constexpr int kFit = 224 / kCtas * 1024 / kStepBytes;
     static constexpr int kSteps = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
     static constexpr int kSmem = kSteps * kStepBytes;
     static_assert(kSmem <= 232448 - 1024, "shared memory");
 };
 
 template <int NS, int RG, bool kVec>
-__global__ void __launch_bounds__(Up<NS, RG, kVec>::kWarps * 32, 2)
+__global__ void __launch_bounds__(Up<NS, RG, kVec>::kWarps * 32, Up<NS, RG, kVec>::kCtas)
 lora_up_kernel(const __grid_constant__ LoraArgs p, int cols_per_cta) {
     using S = Up<NS, RG, kVec>;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -475,7 +476,7 @@ LoraShape lora_shape(int M, int K, int N, int R, int segments, const DeviceInfo&
         default: down_size<16>(s.wide, &rows, &warps, &steps); break;
     }
     s.down_tiles = tiles(rows);
-    s.up_tiles = tiles(s.wide ? 128 : 16);
+    s.up_tiles = tiles(s.wide ? 64 : 16);
     // K is split until the CTAs fill the SMs, or each warp's first copies cover its share:
     // more splits would only be more to add up
     const int slabs = (K + 63) / 64;
@@ -487,7 +488,7 @@ LoraShape lora_shape(int M, int K, int N, int R, int segments, const DeviceInfo&
     const int col_units = (N + unit - 1) / unit;
     // two CTAs an SM; ragged tiles of many rows even out in shorter turns (4k rows: 74 us at
     // 6, 92 at 2 or one wave, 78 at 10), 16-row ones are alike (64 rows: 19 at 2, 23 at 10)
-    int parts = ((s.wide ? 6 : 2) * dev.num_sms + s.up_tiles - 1) / s.up_tiles;
+    int parts = ((s.wide ? 8 : 2) * dev.num_sms + s.up_tiles - 1) / s.up_tiles;
     parts = parts < col_units ? parts : col_units;
     s.cols = (col_units + parts - 1) / parts * unit;
     return s;
@@ -512,7 +513,7 @@ cudaError_t launch_up_as(const LoraArgs& p, const LoraShape& s, cudaStream_t str
 
 template <int NS>
 cudaError_t launch_up(const LoraArgs& p, const LoraShape& s, bool vec, cudaStream_t stream) {
-    if (s.wide) return vec ? launch_up_as<NS, 8, true>(p, s, stream) : launch_up_as<NS, 8, false>(p, s, stream);
+    if (s.wide) return vec ? launch_up_as<NS, 4, true>(p, s, stream) : launch_up_as<NS, 4, false>(p, s, stream);
     return vec ? launch_up_as<NS, 1, true>(p, s, stream) : launch_up_as<NS, 1, false>(p, s, stream);
 }
 
