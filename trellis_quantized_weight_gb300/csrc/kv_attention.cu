@@ -1,4 +1,7 @@
 // trellis_kv_attention: argument checks and the choice of kernel.
+#ifndef TCR
+#define TCR 16
+#endif
 #include <cmath>
 
 #include "kv_attention.cuh"
@@ -19,7 +22,7 @@ int rows_of(int tokens, int max_q, int q_heads, int kv_heads) {
 
 // The tensor-core kernel where a sequence has more rows to a key head than one unit
 // of the streaming kernel.
-bool on_tensor_cores(int head_dim, int rows) { return rows > (head_dim < 256 ? 16 : 8); }
+bool on_tensor_cores(int head_dim, int rows) { return rows > TCR; }
 
 size_t workspace_bytes_of(int tokens, int seqs, int rows, int q_heads, int kv_heads, int head_dim,
                           const DeviceInfo& dev) {

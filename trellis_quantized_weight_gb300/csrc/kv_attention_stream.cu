@@ -48,16 +48,8 @@ constexpr int kJoin = 16;                // pieces of a unit that one CTA joins
 // Warps of a CTA and ring steps by head width and rows: 128 to 160 KB of codes in
 // flight an SM beside the warps' sums.
 template <int D, int NT> struct StreamShape;
-#ifndef W64
-#define W64 8
-#define S64 8
-#endif
-template <int NT> struct StreamShape<64, NT> { static constexpr int kWarps = W64, kSteps = S64; };
-#ifndef W128
-#define W128 8
-#define S128 5
-#endif
-template <> struct StreamShape<128, 1> { static constexpr int kWarps = W128, kSteps = S128; };
+template <int NT> struct StreamShape<64, NT> { static constexpr int kWarps = 8, kSteps = 8; };
+template <> struct StreamShape<128, 1> { static constexpr int kWarps = 8, kSteps = 5; };
 template <> struct StreamShape<128, 2> { static constexpr int kWarps = 8, kSteps = 4; };
 template <int NT> struct StreamShape<256, NT> { static constexpr int kWarps = 6, kSteps = 3; };
 

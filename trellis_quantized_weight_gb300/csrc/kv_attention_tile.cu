@@ -676,16 +676,17 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         // this warp's block of the tile that is loaded, and the page id of the next
         size_t unit = 0;
         int in_page = 0, page_next = 0, page_far = 0;
-        bool in = false;
         auto token_of = [&](int i) { return u.lo + (u.t0 + i) * kKeys + kToks * w; };
         auto seek_page = [&](int i, int tiles) {
             if (i < tiles && token_of(i) < u.hi) page_next = kv_page(a.l, u.seq, token_of(i) >> a.l.page_shift);
         };
         auto seek = [&](int i, int tiles) {
             const int t = token_of(i);
-            in = i < tiles && t < u.hi;                  // false past the last token
-            unit = static_cast<size_t>(page_next) * a.l.kv_heads + u.head;
-            in_page = t & (a.l.page_size - 1);
+            // past the last token: the cache's first block, which nothing looks at (a choice of
+            // values instead of addresses would wait for the loads)
+            const bool in = i < tiles && t < u.hi;
+            unit = in ? static_cast<size_t>(page_next) * a.l.kv_heads + u.head : 0;
+            in_page = in ? t & (a.l.page_size - 1) : 0;
             seek_page(i + 1, tiles);
             // The registers hold a tile ahead; lines of the tiles after it are brought to L2.
             // (The page id asked for here serves the next call: nothing waits for it.)
@@ -706,17 +707,16 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             const uint8_t* src = a.k_codes + base + lane * 16;
 #pragma unroll
             for (int r = 0; r < kKLoads; ++r)
-                kraw[r] = in ? __ldg(reinterpret_cast<const uint4*>(src + r * 512)) : make_uint4(0u, 0u, 0u, 0u);
+                kraw[r] = __ldg(reinterpret_cast<const uint4*>(src + r * 512));
             src = a.v_codes + base + c4 * 16;
 #pragma unroll
             for (int h = 0; h < kH; ++h)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    vraw[h][p] = in ? __ldg(reinterpret_cast<const uint4*>(src + (r8 + 8 * h) * D + p * 64))
-                                  : make_uint4(0u, 0u, 0u, 0u);
+                    vraw[h][p] = __ldg(reinterpret_cast<const uint4*>(src + (r8 + 8 * h) * D + p * 64));
             const size_t at = unit * (a.l.page_size / kKvBlock) + in_page / kKvBlock;
-            ks = in ? __ldg(a.k_scales + at) : 1.0f;
-            vs = in ? __ldg(a.v_scales + at) : 1.0f;
+            ks = __ldg(a.k_scales + at);
+            vs = __ldg(a.v_scales + at);
         };
         bool run = true;
         for (int k = 0; run; ++k) {
@@ -746,8 +746,12 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 if (i >= 2) ok = turn_done(q_last, base + i - 2);
                 else if (i == 0 && q_before >= 0) ok = turn_done(q_before, turns_before - 1);
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
+                // tokens of the block that count: what lies past them may be anything, NaN
+                // codes too, and 0 times NaN is not 0.  (Scores of such keys are masked.)
+                const int valid = u.hi - token_of(i);
                 if (lane == 0 && kToks * w % kKvBlock == 0)
-                    scales[slot * 4 + kToks * w / kKvBlock] = make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f);
+                    scales[slot * 4 + kToks * w / kKvBlock] =
+                        valid > 0 ? make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
                 slot = (slot + 1) % kScaleSlots;
                 const uint32_t kdst = sbase + T::kOffK + kst * T::kKPanels * T::kPanel;
 #pragma unroll
@@ -760,9 +764,6 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(T::kKFull) + 8 * kst);
                 if (++kst == T::kKStages) kst = 0;
-                // tokens of the block that count: what lies past them may be anything, NaN
-                // codes too, and 0 times NaN is not 0.  (Scores of such keys are masked.)
-                const int valid = u.hi - token_of(i);
                 // the stage of values is free when the product with P of the tile three before is:
                 // turn base + i - 1; of the last tile of the item before: that item's own barrier
                 ok = i == 0 || turn_done(q_last, base + i - 1);

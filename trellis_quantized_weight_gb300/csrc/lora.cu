@@ -5,8 +5,16 @@
 //
 // Two launches: h = x A^T (sums over K, the long axis), then out = y + s h B^T (over
 // the rank).  Both are skinny: at few rows they read A and B (2 R (K + N) bytes an
-// adapter), at many rows x, y and out, and the tensor work is a few per cent of
-// either time, so m16n8k16 with bf16 operands and fp32 sums is enough.
+// adapter), at many rows x, y and out.  The tensor work is 2 M R (K + 2 N) multiply-adds
+// (h counts twice, see below); m16n8k16 issues one in 8 cycles a quarter of an SM, which
+// stays below the time of the bytes up to a rank of 64 and is no further step from it at 128.
+//
+// Measured (GPU time of both launches; the least bytes at 6.69 TB/s): 1 row, K 5120, N 17408,
+// rank 16: 4.6 us, two launches in a row; 64 requests of one row on 24 adapters, K 17408,
+// N 5120, rank 32: 17 us (5.7), half of it start and the reads of 64 tiles, which do not
+// share an adapter; 4068 rows of 4 requests, K 5120, N 17408, rank 64: 78 us (53), of which
+// the first kernel 20 (chain of copy, shared memory and mma of 4 warps an SM) and the second
+// 58 at 4.9 TB/s.  Rows without an adapter are copied at 6.2 TB/s by the same loop.
 //
 // * The order of a sum's terms is free, so a lane's 8 consecutive elements (16 bytes) serve
 //   as its operands of two products, in both factors alike: fragments need no
@@ -456,14 +464,15 @@ void down_size(bool wide, int* rows, int* warps, int* steps) {
     *steps = wide ? W::kSteps : F::kSteps;
 }
 
-#ifndef WIDE_ROWS
-#define WIDE_ROWS 64
-#endif
 LoraShape lora_shape(int M, int K, int N, int R, int segments, const DeviceInfo& dev) {
     LoraShape s;
-    // large tiles read an adapter once for all of their rows; with fewer rows a segment on
-    // average they would mostly hold padding
-    s.wide = M / segments >= WIDE_ROWS;
+    // Large tiles read an adapter once for all of their rows, but there are few of them, and
+    // short segments leave them half empty.  Measured, us with large tiles / with 16 rows
+    // (K = N = 5120): rank 64, 4 segments of 128 rows 20.5 / 11.6, of 256 24.7 / 21.6, of 512
+    // 27.6 / 35.0, 16 of 128 30.5 / 35.0, 64 of 64 52.7 / 47.9; rank 16, 4 of 256 12.8 / 12.9,
+    // of 512 20.5 / 23.2, 64 of 64 34.1 / 30.9; rank 128, 4 of 128 32.0 / 29.1, of 256
+    // 29.1 / 42.8, 64 of 64 64.9 / 101.5.
+    s.wide = R > 64 ? M > 512 && M / segments >= 48 : M > 1024 && M / segments >= 96;
     auto tiles = [&](int rows) {     // at most one partial tile a segment, and no tile without a row
         const long long bound = static_cast<long long>(M) / rows + segments;
         return static_cast<int>(bound < M ? bound : M);
@@ -486,8 +495,9 @@ LoraShape lora_shape(int M, int K, int N, int R, int segments, const DeviceInfo&
     s.splits = splits < 1 ? 1 : splits > 32 ? 32 : splits;
     const int unit = s.wide ? 64 : 256;                  // columns of a CTA's warps in a step
     const int col_units = (N + unit - 1) / unit;
-    // two CTAs an SM; ragged tiles of many rows even out in shorter turns (4k rows: 74 us at
-    // 6, 92 at 2 or one wave, 78 at 10), 16-row ones are alike (64 rows: 19 at 2, 23 at 10)
+    // Ragged tiles of many rows even out in shorter turns: 4k rows by 17408 columns, rank 64,
+    // 75 us (both kernels) at twice what is resident, 80 at four times.  Of 16-row tiles one
+    // wave is best (64 rows: 19 us; 23 at 10 CTAs an SM).
     int parts = ((s.wide ? 8 : 2) * dev.num_sms + s.up_tiles - 1) / s.up_tiles;
     parts = parts < col_units ? parts : col_units;
     s.cols = (col_units + parts - 1) / parts * unit;
