@@ -101,6 +101,11 @@ struct Tile {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
+__device__ __forceinline__ uint4 ldg_once(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 // ---- PTX wrappers ------------------------------------------------------------------
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
@@ -701,29 +706,43 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             }
             if (far + 1 < tiles && token_of(far + 1) < u.hi) page_far = kv_page(a.l, u.seq, token_of(far + 1) >> a.l.page_shift);
         };
-        auto load = [&](int i, int tiles) {
+        auto load_keys = [&](int i, int tiles) {
             seek(i, tiles);
-            const size_t base = (unit * a.l.page_size + in_page) * D;
-            const uint8_t* src = a.k_codes + base + lane * 16;
+            const uint8_t* src = a.k_codes + (unit * a.l.page_size + in_page) * D + lane * 16;
 #pragma unroll
-            for (int r = 0; r < kKLoads; ++r)
-                kraw[r] = __ldg(reinterpret_cast<const uint4*>(src + r * 512));
-            src = a.v_codes + base + c4 * 16;
+            for (int r = 0; r < kKLoads; ++r) kraw[r] = ldg_once(src + r * 512);
+        };
+        // the values of the tile that was sought last
+        auto load_values = [&] {
+            const uint8_t* src = a.v_codes + (unit * a.l.page_size + in_page) * D + c4 * 16;
 #pragma unroll
             for (int h = 0; h < kH; ++h)
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    vraw[h][p] = __ldg(reinterpret_cast<const uint4*>(src + (r8 + 8 * h) * D + p * 64));
+                for (int p = 0; p < P; ++p) vraw[h][p] = ldg_once(src + (r8 + 8 * h) * D + p * 64);
             const size_t at = unit * (a.l.page_size / kKvBlock) + in_page / kKvBlock;
             ks = __ldg(a.k_scales + at);
             vs = __ldg(a.v_scales + at);
+        };
+        auto store_keys = [&] {
+            const uint32_t kdst = sbase + T::kOffK + kst * T::kKPanels * T::kPanel;
+#pragma unroll
+            for (int r = 0; r < kKLoads; ++r) {
+                const int chunk = r * 32 + lane, tk = chunk / kKc, c = chunk % kKc;
+                sts128(kdst + (c >> 3) * T::kPanel + (kToks * w + tk) * 128 + (((c & 7) ^ (tk & 7)) << 4), kraw[r].x, kraw[r].y,
+                       kraw[r].z, kraw[r].w);
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(T::kKFull) + 8 * kst);
+            if (++kst == T::kKStages) kst = 0;
         };
         bool run = true;
         for (int k = 0; run; ++k) {
             if (!__all_sync(0xffffffffu, take_part(k, u))) break;
             const int tiles = u.t1 - u.t0;
             seek_page(0, tiles);
-            load(0, tiles);
+            load_keys(0, tiles);
+            load_values();
             const int q_last = u.live - 1;
             uint32_t base = 0;
 #pragma unroll
@@ -737,15 +756,23 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 return bar_wait(bar(T::kItem + q_before), (n - 1) & 1);
             };
             if (tiles == 0) free_part(k);
+            // Keys go a tile ahead of the values: their product is wanted first.  At an item's
+            // start the stages are free when the last turn of the one before is over
+            if (tiles > 0) {
+                if (!__all_sync(0xffffffffu, q_before < 0 || turn_done(q_before, turns_before - 1))) break;
+                store_keys();
+                load_keys(1, tiles);
+            }
             for (int i = 0; i < tiles; ++i) {
                 // the next item is taken when this one nears its end, not before: it may be long
                 if (i == max(0, tiles - 4)) free_part(k);
-                // The stage of keys is free when S of the tile two before is done (turn base + i - 2),
-                // at an item's start when the last turn of the one before is over
-                bool ok = true;
-                if (i >= 2) ok = turn_done(q_last, base + i - 2);
-                else if (i == 0 && q_before >= 0) ok = turn_done(q_before, turns_before - 1);
+                // turn base + i - 1: S of the tile before is done, and the product with P of the
+                // one two before that.  So a stage of keys is free, for tile i + 1, and one of values.
+                // The turn two later cannot pass before this wait, since it takes tile i + 1's keys;
+                // at the last tile, which has none to follow, the turn after (S of this tile) serves
+                bool ok = i == 0 || turn_done(q_last, base + i - (i + 1 < tiles ? 1 : 0));
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
+                if (i + 1 < tiles) store_keys();
                 // tokens of the block that count: what lies past them may be anything, NaN
                 // codes too, and 0 times NaN is not 0.  (Scores of such keys are masked.)
                 const int valid = u.hi - token_of(i);
@@ -753,21 +780,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                     scales[slot * 4 + kToks * w / kKvBlock] =
                         valid > 0 ? make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
                 slot = (slot + 1) % kScaleSlots;
-                const uint32_t kdst = sbase + T::kOffK + kst * T::kKPanels * T::kPanel;
-#pragma unroll
-                for (int r = 0; r < kKLoads; ++r) {
-                    const int chunk = r * 32 + lane, tk = chunk / kKc, c = chunk % kKc;
-                    sts128(kdst + (c >> 3) * T::kPanel + (kToks * w + tk) * 128 + (((c & 7) ^ (tk & 7)) << 4), kraw[r].x, kraw[r].y,
-                           kraw[r].z, kraw[r].w);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(T::kKFull) + 8 * kst);
-                if (++kst == T::kKStages) kst = 0;
-                // the stage of values is free when the product with P of the tile three before is:
-                // turn base + i - 1; of the last tile of the item before: that item's own barrier
-                ok = i == 0 || turn_done(q_last, base + i - 1);
-                if (i == 1 && q_before >= 0) ok = ok && item_done();
+                // the last tile of the item before frees its stage at that item's own barrier
+                ok = !(i == 1 && q_before >= 0) || item_done();
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
                 if (valid < kToks) {
 #pragma unroll
@@ -793,7 +807,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(T::kVFull) + 8 * vst);
                 if (++vst == T::kVStages) vst = 0;
-                load(i + 1, tiles);
+                load_values();                           // of tile i + 1
+                load_keys(i + 2, tiles);
             }
             if (tiles == 1 && q_before >= 0 && !__all_sync(0xffffffffu, item_done())) break;
             if (tiles > 0) {
