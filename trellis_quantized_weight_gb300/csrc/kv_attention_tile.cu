@@ -678,19 +678,20 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
 #pragma unroll
         for (int q = 0; q < kQt; ++q) items[q] = 0;
         auto turn_done = [&](int q, uint32_t n) { return bar_wait(bar(T::kSFull + 2 * q) + 8 * (n & 1), (n >> 1) & 1); };
-        // this warp's block of the tile that is loaded, and the page id of the next
+        // this warp's block of the tile that is loaded, and the page ids of the next and of a later
+        // one, as they were read (they are clamped where they are used: nothing waits before)
         size_t unit = 0;
         int in_page = 0, page_next = 0, page_far = 0;
         auto token_of = [&](int i) { return u.lo + (u.t0 + i) * kKeys + kToks * w; };
         auto seek_page = [&](int i, int tiles) {
-            if (i < tiles && token_of(i) < u.hi) page_next = kv_page(a.l, u.seq, token_of(i) >> a.l.page_shift);
+            if (i < tiles && token_of(i) < u.hi) page_next = kv_page_id(a.l, u.seq, token_of(i) >> a.l.page_shift);
         };
         auto seek = [&](int i, int tiles) {
             const int t = token_of(i);
             // past the last token: the cache's first block, which nothing looks at (a choice of
             // values instead of addresses would wait for the loads)
             const bool in = i < tiles && t < u.hi;
-            unit = in ? static_cast<size_t>(page_next) * a.l.kv_heads + u.head : 0;
+            unit = in ? static_cast<size_t>(kv_page_of_id(a.l, page_next)) * a.l.kv_heads + u.head : 0;
             in_page = in ? t & (a.l.page_size - 1) : 0;
             seek_page(i + 1, tiles);
             // The registers hold a tile ahead; lines of the tiles after it are brought to L2.
@@ -699,12 +700,12 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             const int far = i + kFar, tf = token_of(far);
             if (splits == 1) return;                     // many units: what one reads others have read
             if (i > 0 && far < tiles && tf < u.hi && lane < kLines) {
-                const size_t at = ((static_cast<size_t>(page_far) * a.l.kv_heads + u.head) * a.l.page_size +
+                const size_t at = ((static_cast<size_t>(kv_page_of_id(a.l, page_far)) * a.l.kv_heads + u.head) * a.l.page_size +
                                    (tf & (a.l.page_size - 1))) * D + lane * 128;
                 asm volatile("prefetch.global.L2 [%0];" :: "l"(a.k_codes + at));
                 asm volatile("prefetch.global.L2 [%0];" :: "l"(a.v_codes + at));
             }
-            if (far + 1 < tiles && token_of(far + 1) < u.hi) page_far = kv_page(a.l, u.seq, token_of(far + 1) >> a.l.page_shift);
+            if (far + 1 < tiles && token_of(far + 1) < u.hi) page_far = kv_page_id(a.l, u.seq, token_of(far + 1) >> a.l.page_shift);
         };
         auto load_keys = [&](int i, int tiles) {
             seek(i, tiles);

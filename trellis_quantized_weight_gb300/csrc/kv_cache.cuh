@@ -48,10 +48,11 @@ __device__ __forceinline__ Seq load_seq(const KvLayout& l, int s) {
 
 // Page of column c of sequence s, clamped into the pool: a wrong id reads or
 // writes a wrong page, never outside the cache.
-__device__ __forceinline__ int kv_page(const KvLayout& l, int s, int c) {
-    const int id = __ldg(l.pages + static_cast<size_t>(s) * l.page_cols + c);
-    return min(max(id, 0), l.num_pages - 1);
+__device__ __forceinline__ int kv_page_id(const KvLayout& l, int s, int c) {
+    return __ldg(l.pages + static_cast<size_t>(s) * l.page_cols + c);
 }
+__device__ __forceinline__ int kv_page_of_id(const KvLayout& l, int id) { return min(max(id, 0), l.num_pages - 1); }
+__device__ __forceinline__ int kv_page(const KvLayout& l, int s, int c) { return kv_page_of_id(l, kv_page_id(l, s, c)); }
 
 // ---- conversions ------------------------------------------------------------------
 // Two e4m3 codes (low byte first) -> f16x2, exact.
