@@ -239,83 +239,169 @@ struct Part {
     int start, n, p0;
     int lo, hi;              // cached tokens that the unit's rows see, lo a multiple of 64
     int t0, t1;              // its tiles [t0, t1)
-    int parts, index;        // of the unit, and this one's
     int live;                // query tiles that have rows; 0: no more items
-    int unit;
+    int slot;                // of its partial result; -1: it is all of its unit
 };
 static_assert(sizeof(Part) <= 64, "part slot");
 
-// The unit and part of work item `item`; false when there is none.  Units are counted
-// from the last query tiles of the last sequence, so that the long ones of a causal
-// prompt come first.  One warp calls it.
+// Tiles of query tile group `qt` of a sequence, and the tokens [lo, hi) that its rows see.
 template <int kUnitRows>
-__device__ bool find_part(const AttendArgs& a, unsigned int item, int splits, int least, Part& u) {
+__device__ __forceinline__ int unit_tiles(const AttendArgs& a, const Seq& q, int qt, int* lo, int* hi) {
+    const int first = qt * kUnitRows / a.group, last = min(q.n - 1, (qt * kUnitRows + kUnitRows - 1) / a.group);
+    *hi = max(0, min(q.total, q.p0 + last + 1));
+    const int low = a.window > 0 ? max(0, q.p0 + first + 1 - a.window) : 0;
+    *lo = low & ~(kKeys - 1);
+    return *hi > *lo ? (*hi - *lo + kKeys - 1) / kKeys : 0;
+}
+template <int kUnitRows>
+__device__ __forceinline__ int unit_count(const AttendArgs& a, const Seq& q) {   // of a sequence and head
+    return q.n > 0 ? (q.n * a.group + kUnitRows - 1) / kUnitRows : 0;
+}
+template <int kUnitRows>
+__device__ __forceinline__ int fill_part(const AttendArgs& a, const Seq& q, int seq, int head, int qt, Part& u) {
+    u.seq = seq; u.head = head; u.qt = qt;
+    u.start = q.start; u.n = q.n; u.p0 = q.p0;
+    u.live = min(kUnitRows, q.n * a.group - qt * kUnitRows + kRows - 1) / kRows;
+    u.slot = -1;
+    return unit_tiles<kUnitRows>(a, q, qt, &u.lo, &u.hi);
+}
+__device__ __forceinline__ Seq seq_of_lane(const Seq& q, int src) {
+    Seq r;
+    r.start = __shfl_sync(0xffffffffu, q.start, src);
+    r.n = __shfl_sync(0xffffffffu, q.n, src);
+    r.p0 = __shfl_sync(0xffffffffu, q.p0, src);
+    r.total = __shfl_sync(0xffffffffu, q.total, src);
+    return r;
+}
+
+// Many units: item `item` is a whole one; false past the last.  They are counted from the
+// last query tiles of the last sequence, so that the long ones of a causal prompt come
+// first.  One warp calls it.
+template <int kUnitRows>
+__device__ bool find_unit(const AttendArgs& a, unsigned int item, Part& u) {
     const int lane = threadIdx.x & 31;
-    u.index = static_cast<int>(item % splits);
-    u.unit = static_cast<int>(item / splits);
-    u.head = u.unit % a.l.kv_heads;
-    int tile = u.unit / a.l.kv_heads;
-    int got = -1;
-    for (int s1 = a.l.seqs; s1 > 0 && got < 0; s1 -= 32) {
+    int at = static_cast<int>(item / a.l.kv_heads);
+    for (int s1 = a.l.seqs; s1 > 0; s1 -= 32) {
         const int s = s1 - 1 - lane;
         Seq q = {};
         if (s >= 0) q = load_seq(a.l, s);
-        const int qts = q.n > 0 ? (q.n * a.group + kUnitRows - 1) / kUnitRows : 0;
+        const int qts = unit_count<kUnitRows>(a, q);
         int incl = qts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, tile >= incl - qts && tile < incl);
+        const unsigned hit = __ballot_sync(0xffffffffu, at >= incl - qts && at < incl);
         if (hit != 0u) {
             const int src = __ffs(hit) - 1;
-            u.qt = __shfl_sync(0xffffffffu, qts - 1 - (tile - (incl - qts)), src);
-            got = s1 - 1 - src;
-            u.start = __shfl_sync(0xffffffffu, q.start, src);
-            u.n = __shfl_sync(0xffffffffu, q.n, src);
-            u.p0 = __shfl_sync(0xffffffffu, q.p0, src);
-            u.hi = __shfl_sync(0xffffffffu, q.total, src);
+            const int qt = __shfl_sync(0xffffffffu, qts - 1 - (at - (incl - qts)), src);
+            u.t0 = 0;
+            u.t1 = fill_part<kUnitRows>(a, seq_of_lane(q, src), s1 - 1 - src, static_cast<int>(item % a.l.kv_heads), qt, u);
+            return true;
         }
-        tile -= __shfl_sync(0xffffffffu, incl, 31);
+        at -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (got < 0) return false;
-    u.seq = got;
-    const int row0 = u.qt * kUnitRows, rows = u.n * a.group;
-    const int first = row0 / a.group, last = min(u.n - 1, (row0 + kUnitRows - 1) / a.group);
-    u.hi = max(0, min(u.hi, u.p0 + last + 1));
-    const int low = a.window > 0 ? max(0, u.p0 + first + 1 - a.window) : 0;
-    u.lo = low & ~(kKeys - 1);
-    u.live = min(kUnitRows, rows - row0 + kRows - 1) / kRows;
-    const int tiles = u.hi > u.lo ? (u.hi - u.lo + kKeys - 1) / kKeys : 0;
-    const int chunk = max(least, (tiles + splits - 1) / splits);
-    u.parts = max(1, (tiles + chunk - 1) / chunk);
-    u.t0 = u.index * chunk;
-    u.t1 = min(tiles, u.t0 + chunk);
-    return u.index < u.parts;
+    return false;
 }
 
-// Tiles of a part where units are split: equal parts whatever the sequences' lengths,
-// some three for two CTAs.  (An item costs a CTA some ten tiles' time of its own.)
+// Few units: their tiles in a row, and kLead places before each unit's for what an item
+// costs a CTA beside its tiles (its queries, its result), are cut into equal shares, one a
+// CTA.  So a CTA holds at most one part that began before it and one that goes on
+// after it: its two slots of partial results.
+constexpr int kLead = 10;
 template <int kUnitRows>
-__device__ int least_chunk(const AttendArgs& a, int ctas) {
+__device__ __forceinline__ int unit_places(const AttendArgs& a, const Seq& q, int qt) {
+    int lo, hi;
+    return kLead + max(1, unit_tiles<kUnitRows>(a, q, qt, &lo, &hi));    // an empty unit still writes its zeros
+}
+// Places of a head of each lane's sequence.  The warp shares those of many units.
+template <int kUnitRows>
+__device__ long long head_places(const AttendArgs& a, const Seq& q) {
+    const int lane = threadIdx.x & 31, qts = unit_count<kUnitRows>(a, q);
+    long long sum = 0;
+    if (qts <= 4)
+        for (int qt = 0; qt < qts; ++qt) sum += unit_places<kUnitRows>(a, q, qt);
+    for (unsigned many = __ballot_sync(0xffffffffu, qts > 4); many != 0u; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        const Seq of = seq_of_lane(q, src);
+        const int n = __shfl_sync(0xffffffffu, qts, src);
+        long long part = 0;
+        for (int qt = lane; qt < n; qt += 32) part += unit_places<kUnitRows>(a, of, qt);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        if (lane == src) sum = part;
+    }
+    return sum;
+}
+// Places of a CTA's share.  One warp calls it, as the next.
+template <int kUnitRows>
+__device__ long long share_places(const AttendArgs& a, int ctas, long long* all) {
     const int lane = threadIdx.x & 31;
     long long sum = 0;
-    for (int s = lane; s < a.l.seqs; s += 32) {
-        const Seq q = load_seq(a.l, s);
-        if (q.n <= 0 || q.total <= 0) continue;
-        const int seen = a.window > 0 ? min(q.total, a.window + q.n) : q.total;
-        sum += static_cast<long long>((q.n * a.group + kUnitRows - 1) / kUnitRows) * ((seen + kKeys - 1) / kKeys);
+    for (int s0 = 0; s0 < a.l.seqs; s0 += 32) {
+        Seq q = {};
+        if (s0 + lane < a.l.seqs) q = load_seq(a.l, s0 + lane);
+        sum += head_places<kUnitRows>(a, q);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const long long each = 2 * sum * a.l.kv_heads / (3ll * ctas) + 1;
-    return static_cast<int>(max(static_cast<long long>(kMinChunk), min(each, 1ll << 24)));
+    *all = sum * a.l.kv_heads;
+    return max(static_cast<long long>(kLead + kMinChunk), (*all + ctas - 1) / ctas);
+}
+// The unit that holds a place (of [0, all)), as a part with all of its tiles, and its first place.
+template <int kUnitRows>
+__device__ long long find_place(const AttendArgs& a, long long place, Part& u) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int s0 = 0; s0 < a.l.seqs; s0 += 32) {
+        Seq q = {};
+        if (s0 + lane < a.l.seqs) q = load_seq(a.l, s0 + lane);
+        const long long each = head_places<kUnitRows>(a, q), mine = each * a.l.kv_heads;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const long long first = before + incl - mine;
+        const unsigned hit = __ballot_sync(0xffffffffu, place >= first && place < first + mine);
+        if (hit != 0u) {
+            const int src = __ffs(hit) - 1;
+            const Seq of = seq_of_lane(q, src);
+            const long long per = __shfl_sync(0xffffffffu, each, src);
+            long long at = __shfl_sync(0xffffffffu, first, src);
+            const int head = static_cast<int>((place - at) / per);
+            at += head * per;
+            const int qts = unit_count<kUnitRows>(a, of);
+            for (int qt0 = 0; qt0 < qts; qt0 += 32) {
+                const int w = qt0 + lane < qts ? unit_places<kUnitRows>(a, of, qt0 + lane) : 0;
+                int upto = w;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += up;
+                }
+                const unsigned in = __ballot_sync(0xffffffffu, place < at + upto);
+                if (in != 0u) {
+                    const int k = __ffs(in) - 1;
+                    at += __shfl_sync(0xffffffffu, upto - w, k);
+                    u.t0 = 0;
+                    u.t1 = fill_part<kUnitRows>(a, of, s0 + src, head, qt0 + k, u);
+                    return at;
+                }
+                at += __shfl_sync(0xffffffffu, upto, 31);
+            }
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    u.live = 0;
+    return 0;
 }
 
 template <int D>
 __global__ void __launch_bounds__(Tile<D>::kThreads, 1)
-kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int items) {
+kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int items) {
     using T = Tile<D>;
     constexpr int kQt = T::kQt;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -619,8 +705,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
                 fence_after();
             }
             if (live_tile) {
-                const bool whole = u.parts == 1;
-                float* part = a.partials + ((static_cast<size_t>(u.unit) * splits + u.index) * kQt + qi) * T::kPart;
+                const bool whole = u.slot < 0;
+                float* part = a.partials + (static_cast<size_t>(max(u.slot, 0)) * kQt + qi) * T::kPart;
                 const float inv = 1.0f / l;
 #pragma unroll 1
                 for (int c = 0; has_rows && c < D; c += 16) {
@@ -698,7 +784,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             // (The page id asked for here serves the next call: nothing waits for it.)
             constexpr int kLines = kToks * D / 128;
             const int far = i + kFar, tf = token_of(far);
-            if (splits == 1) return;                     // many units: what one reads others have read
+            if (!split) return;                          // many units: what one reads others have read
             if (i > 0 && far < tiles && tf < u.hi && lane < kLines) {
                 const size_t at = ((static_cast<size_t>(kv_page_of_id(a.l, page_far)) * a.l.kv_heads + u.head) * a.l.page_size +
                                    (tf & (a.l.page_size - 1))) * D + lane * 128;
@@ -899,19 +985,37 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
         (void)bar_wait(bar(T::kDone), 0);
     } else {
         // ---------------------------------------------------------------------- plan
-        int least = 0;
+        long long at = 0, end = 0;                       // of this CTA's share
+        if (split) {
+            long long all;
+            const long long each = share_places<kQt * kRows>(a, gridDim.x, &all);
+            at = min(all, blockIdx.x * each);
+            end = min(all, at + each);
+        }
         for (int k = 0;; ++k) {
             // every role has the item before, and the loaders are nearly done with it
             if (k >= 1 && !__all_sync(0xffffffffu, bar_wait(bar(T::kPartFree + ((k - 1) & 1)), ((k - 1) >> 1) & 1))) break;
             Part u = {};
             bool found = false, last = false;
             while (!found) {
-                unsigned int item = 0;
-                if (lane == 0) item = atomicAdd(a.counters, 1u);
-                if (least == 0) least = splits > 1 ? least_chunk<kQt * kRows>(a, gridDim.x) : kMinChunk;
-                item = __shfl_sync(0xffffffffu, item, 0);
-                if (item >= items) { last = true; break; }
-                found = find_part<kQt * kRows>(a, item, splits, least, u);
+                if (split) {
+                    if (at >= end) { last = true; break; }
+                    const long long first = find_place<kQt * kRows>(a, at, u) + kLead;    // place of tile 0
+                    const int tiles = u.t1, full = max(1, tiles);
+                    const int t0 = static_cast<int>(max(0ll, at - first)), t1 = static_cast<int>(min(static_cast<long long>(full), end - first));
+                    if (u.live == 0) { last = true; break; }
+                    u.t0 = t0;
+                    u.t1 = min(t1, tiles);
+                    if (t0 > 0 || t1 < full) u.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
+                    at = first + full;
+                    found = t1 > t0;
+                } else {
+                    unsigned int item = 0;
+                    if (lane == 0) item = atomicAdd(a.counters, 1u);
+                    item = __shfl_sync(0xffffffffu, item, 0);
+                    if (item >= items) { last = true; break; }
+                    found = find_unit<kQt * kRows>(a, item, u);
+                }
             }
             if (last) u.live = 0;
             if (lane == 0) {
@@ -921,7 +1025,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
             if (last) break;
         }
         // the CTA that leaves last puts the counters back
-        if (lane == 0 && atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
+        if (!split && lane == 0 && atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
             a.counters[0] = 0u;
             a.counters[1] = 0u;
         }
@@ -940,24 +1044,34 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, int splits, unsigned int it
 // rows, after the kernel above (whose last CTA would else add a long unit's parts alone).
 constexpr int kJoinThreads = 128, kJoinCols = 32;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ AttendArgs a, int splits, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ AttendArgs a, int ctas) {
     using T = Tile<D>;
     __shared__ Part shared_part;
-    __shared__ int shared_ok;
+    __shared__ int shared_parts;
     griddep_wait();
+    // the unit that CTA blockIdx.x / kQt began last, if others went on with it
     const int qi = blockIdx.x % T::kQt;
+    const long long cta = blockIdx.x / T::kQt;
     if (threadIdx.x < 32) {
+        long long all;
         Part p = {};
-        const int least = least_chunk<T::kQt * kRows>(a, ctas);
-        const bool ok = find_part<T::kQt * kRows>(a, static_cast<unsigned>(blockIdx.x / T::kQt) * splits, splits, least, p);
-        if (threadIdx.x == 0) { shared_part = p; shared_ok = ok && p.parts > 1 && qi < p.live; }
+        const long long each = share_places<T::kQt * kRows>(a, ctas, &all);
+        const long long begin = min(all, cta * each), end = min(all, begin + each);
+        int parts = 0;
+        if (end > begin) {
+            const long long first = find_place<T::kQt * kRows>(a, end - 1, p) + kLead, past = first + max(1, p.t1);
+            if (p.live > qi && first >= begin && first < end && past > end) parts = static_cast<int>((past - 1) / each - cta) + 1;
+        }
+        if (threadIdx.x == 0) { shared_part = p; shared_parts = parts; }
     }
     __syncthreads();
-    if (shared_ok) {
+    const int parts = shared_parts;
+    if (parts > 1) {
         const Part& u = shared_part;
-        const int row0 = (u.qt * T::kQt + qi) * kRows, rows = min(kRows, u.n * a.group - row0), parts = u.parts;
-        const size_t step = T::kQt * T::kPart;
-        const float* base = a.partials + (static_cast<size_t>(u.unit) * splits * T::kQt + qi) * T::kPart;
+        const int row0 = (u.qt * T::kQt + qi) * kRows, rows = min(kRows, u.n * a.group - row0);
+        // the first part stands in the second slot of its CTA, the others in the first of theirs
+        const size_t step = 2 * T::kQt * T::kPart;
+        const float* base = a.partials + (static_cast<size_t>(2 * cta) * T::kQt + qi) * T::kPart;
         const int d = blockIdx.y * kJoinCols + threadIdx.x % 8 * 4;
         for (int row = threadIdx.x / 8; row < rows; row += kJoinThreads / 8) {
             float top = -INFINITY, l = 0.0f;
@@ -968,7 +1082,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
                 float4 v[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const float* from = base + min(p0 + q, parts - 1) * step;
+                    const int part = min(p0 + q, parts - 1);
+                    const float* from = base + part * step + (part == 0 ? T::kQt * T::kPart : 0);
                     pm[q] = __ldcg(from + D * kRows + row);
                     pl[q] = __ldcg(from + D * kRows + kRows + row);
                     v[q] = __ldcg(reinterpret_cast<const float4*>(from + row * D + d));
@@ -1009,44 +1124,37 @@ long long unit_bound(int tokens, int seqs, int group, int kv_heads, int head_dim
     return (t < rows ? t : rows) * kv_heads;
 }
 
-// Parts that a unit's tokens are cut into: one where the units fill the SMs four
-// times, else enough for that.
-int split_count(long long units, int sms) {
-    const long long want = 4ll * sms;
-    return units >= want ? 1 : static_cast<int>((want + units - 1) / units);
-}
+// Units are split among the CTAs where they would fill the SMs less than four times.
+bool is_split(long long units, int sms) { return units < 4ll * sms; }
 
 template <int D>
-int launch(const AttendArgs& a, long long units, int splits, int sms, cudaStream_t stream) {
+int launch(const AttendArgs& a, long long units, int sms, cudaStream_t stream) {
     using T = Tile<D>;
     static std::atomic<unsigned long long> opted{0};
     if (!smem_opt_in(kv_tile_kernel<D>, T::kSmem, opted)) return TRELLIS_ERR_CUDA;
-    const unsigned items = static_cast<unsigned>(units * splits);
-    const cudaError_t e = launch_programmatic(kv_tile_kernel<D>, items < static_cast<unsigned>(sms) ? items : static_cast<unsigned>(sms),
-                                              static_cast<unsigned>(T::kThreads), T::kSmem, stream, a, splits, items);
+    const bool split = is_split(units, sms);
+    const cudaError_t e = launch_programmatic(kv_tile_kernel<D>, static_cast<unsigned>(sms), static_cast<unsigned>(T::kThreads),
+                                              T::kSmem, stream, a, split, static_cast<unsigned>(units));
     if (e != cudaSuccess) return TRELLIS_ERR_CUDA;
-    if (splits == 1) return TRELLIS_OK;
-    const int ctas = items < static_cast<unsigned>(sms) ? static_cast<int>(items) : sms;
-    return launch_programmatic_grid(kv_join_kernel<D>, dim3(static_cast<unsigned>(units) * T::kQt, D / kJoinCols), kJoinThreads, 0,
-                                    stream, a, splits, ctas) == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
+    if (!split) return TRELLIS_OK;
+    return launch_programmatic_grid(kv_join_kernel<D>, dim3(static_cast<unsigned>(sms) * T::kQt, D / kJoinCols), kJoinThreads, 0,
+                                    stream, a, sms) == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
 }
 
 }  // namespace
 
 size_t kv_tile_workspace_bytes(int tokens, int seqs, int q_heads, int kv_heads, int head_dim, const DeviceInfo& dev) {
     const long long units = unit_bound(tokens > 0 ? tokens : 1, seqs, q_heads / kv_heads, kv_heads, head_dim);
-    const int splits = split_count(units, dev.num_sms);
-    if (splits == 1) return kKvCounterBytes;
-    return kKvCounterBytes + static_cast<size_t>(units) * splits * unit_rows(head_dim) * (static_cast<size_t>(head_dim) + 2) * 4;
+    if (!is_split(units, dev.num_sms)) return kKvCounterBytes;
+    return kKvCounterBytes + static_cast<size_t>(2 * dev.num_sms) * unit_rows(head_dim) * (static_cast<size_t>(head_dim) + 2) * 4;
 }
 
 int launch_kv_tile(const AttendArgs& a, int head_dim, const DeviceInfo& dev, cudaStream_t stream) {
     const long long units = unit_bound(a.l.tokens, a.l.seqs, a.group, a.l.kv_heads, head_dim);
-    const int splits = split_count(units, dev.num_sms);
-    if (units * splits >= (1ll << 31)) return TRELLIS_ERR_SHAPE;
-    return head_dim == 64 ? launch<64>(a, units, splits, dev.num_sms, stream)
-           : head_dim == 128 ? launch<128>(a, units, splits, dev.num_sms, stream)
-                             : launch<256>(a, units, splits, dev.num_sms, stream);
+    if (units >= (1ll << 31)) return TRELLIS_ERR_SHAPE;
+    return head_dim == 64 ? launch<64>(a, units, dev.num_sms, stream)
+           : head_dim == 128 ? launch<128>(a, units, dev.num_sms, stream)
+                             : launch<256>(a, units, dev.num_sms, stream);
 }
 
 int kv_take_device_error(unsigned int* flags) {
