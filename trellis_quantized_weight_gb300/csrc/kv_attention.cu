@@ -1,7 +1,4 @@
 // trellis_kv_attention: argument checks and the choice of kernel.
-#ifndef TCR
-#define TCR 16
-#endif
 #include <cmath>
 
 #include "kv_attention.cuh"
@@ -20,9 +17,15 @@ int rows_of(int tokens, int max_q, int q_heads, int kv_heads) {
     return r > (1 << 30) ? 1 << 30 : static_cast<int>(r < 1 ? 1 : r);
 }
 
-// The tensor-core kernel where a sequence has more rows to a key head than one unit
-// of the streaming kernel.
-bool on_tensor_cores(int head_dim, int rows) { return rows > TCR; }
+// The tensor-core kernel where a sequence has more rows to a key head than one unit of the
+// streaming kernel, whose time grows with every 8 or 16 rows while the other's does not.
+// Measured, us streaming / tensor cores, 16 sequences of 300 to 9000 tokens and 8 key heads
+// (4 at D = 256): D = 128, 16 rows 59 / 77, 18 to 24 98 / 78, 32 104 / 79, 64 197 / 83;
+// D = 256, 8 rows 41 / 65, 16 72 / 67, 24 95 / 68, 40 154 / 71.  One sequence of 100000:
+// D = 128, 16 rows 58 / 90, 24 93 / 94, 40 128 / 97; D = 256, 16 rows 79 / 74, 24 107 / 81.
+// At D = 64 two units still take less: 16 sequences, 24 rows 69 / 68, 32 70 / 69, 40 98 / 70;
+// one, 32 rows 64 / 83, 40 87 / 86.
+bool on_tensor_cores(int head_dim, int rows) { return rows > (head_dim == 64 ? 32 : 16); }
 
 size_t workspace_bytes_of(int tokens, int seqs, int rows, int q_heads, int kv_heads, int head_dim,
                           const DeviceInfo& dev) {

@@ -308,45 +308,60 @@ __device__ bool find_unit(const AttendArgs& a, unsigned int item, Part& u) {
 // Few units: their tiles in a row, and kLead places before each unit's for what an item
 // costs a CTA beside its tiles (its queries, its result), are cut into equal shares, one a
 // CTA.  So a CTA holds at most one part that began before it and one that goes on
-// after it: its two slots of partial results.
+// after it: its two slots of partial results.  Where the longest unit has few tiles the
+// units are taken whole instead: of 40-row drafts at D = 128 with contexts of 5 to 100 per
+// cent of the most, 320 units of up to 600 tokens take 53 us in shares and 37 whole, up to
+// 2000 tokens (32 tiles) 68 and 67, up to 4500 105 and 126, up to 12000 217 and 301.
 constexpr int kLead = 10;
+constexpr int kWhole = 32;
 template <int kUnitRows>
 __device__ __forceinline__ int unit_places(const AttendArgs& a, const Seq& q, int qt) {
     int lo, hi;
     return kLead + max(1, unit_tiles<kUnitRows>(a, q, qt, &lo, &hi));    // an empty unit still writes its zeros
 }
-// Places of a head of each lane's sequence.  The warp shares those of many units.
+// Places of a head of each lane's sequence; `longest` is raised to its longest unit's.  The
+// warp shares the sequences of many units.
 template <int kUnitRows>
-__device__ long long head_places(const AttendArgs& a, const Seq& q) {
+__device__ long long head_places(const AttendArgs& a, const Seq& q, int& longest) {
     const int lane = threadIdx.x & 31, qts = unit_count<kUnitRows>(a, q);
     long long sum = 0;
     if (qts <= 4)
-        for (int qt = 0; qt < qts; ++qt) sum += unit_places<kUnitRows>(a, q, qt);
+        for (int qt = 0; qt < qts; ++qt) {
+            const int n = unit_places<kUnitRows>(a, q, qt);
+            sum += n;
+            longest = max(longest, n);
+        }
     for (unsigned many = __ballot_sync(0xffffffffu, qts > 4); many != 0u; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const Seq of = seq_of_lane(q, src);
         const int n = __shfl_sync(0xffffffffu, qts, src);
         long long part = 0;
-        for (int qt = lane; qt < n; qt += 32) part += unit_places<kUnitRows>(a, of, qt);
+        for (int qt = lane; qt < n; qt += 32) {
+            const int w = unit_places<kUnitRows>(a, of, qt);
+            part += w;
+            longest = max(longest, w);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
         if (lane == src) sum = part;
     }
     return sum;
 }
-// Places of a CTA's share.  One warp calls it, as the next.
+// Places of a CTA's share, 0: units are taken whole.  One warp calls it, as the next.
 template <int kUnitRows>
 __device__ long long share_places(const AttendArgs& a, int ctas, long long* all) {
     const int lane = threadIdx.x & 31;
     long long sum = 0;
+    int longest = 0;
     for (int s0 = 0; s0 < a.l.seqs; s0 += 32) {
         Seq q = {};
         if (s0 + lane < a.l.seqs) q = load_seq(a.l, s0 + lane);
-        sum += head_places<kUnitRows>(a, q);
+        sum += head_places<kUnitRows>(a, q, longest);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     *all = sum * a.l.kv_heads;
+    if (!__any_sync(0xffffffffu, longest > kLead + kWhole)) return 0;
     return max(static_cast<long long>(kLead + kMinChunk), (*all + ctas - 1) / ctas);
 }
 // The unit that holds a place (of [0, all)), as a part with all of its tiles, and its first place.
@@ -354,10 +369,11 @@ template <int kUnitRows>
 __device__ long long find_place(const AttendArgs& a, long long place, Part& u) {
     const int lane = threadIdx.x & 31;
     long long before = 0;
+    int longest = 0;
     for (int s0 = 0; s0 < a.l.seqs; s0 += 32) {
         Seq q = {};
         if (s0 + lane < a.l.seqs) q = load_seq(a.l, s0 + lane);
-        const long long each = head_places<kUnitRows>(a, q), mine = each * a.l.kv_heads;
+        const long long each = head_places<kUnitRows>(a, q, longest), mine = each * a.l.kv_heads;
         long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -986,9 +1002,11 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
     } else {
         // ---------------------------------------------------------------------- plan
         long long at = 0, end = 0;                       // of this CTA's share
+        bool shares = false;
         if (split) {
             long long all;
             const long long each = share_places<kQt * kRows>(a, gridDim.x, &all);
+            shares = each > 0;
             at = min(all, blockIdx.x * each);
             end = min(all, at + each);
         }
@@ -998,7 +1016,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
             Part u = {};
             bool found = false, last = false;
             while (!found) {
-                if (split) {
+                if (shares) {
                     if (at >= end) { last = true; break; }
                     const long long first = find_place<kQt * kRows>(a, at, u) + kLead;    // place of tile 0
                     const int tiles = u.t1, full = max(1, tiles);
@@ -1025,7 +1043,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
             if (last) break;
         }
         // the CTA that leaves last puts the counters back
-        if (!split && lane == 0 && atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
+        if (!shares && lane == 0 && atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
             a.counters[0] = 0u;
             a.counters[1] = 0u;
         }
@@ -1124,7 +1142,9 @@ long long unit_bound(int tokens, int seqs, int group, int kv_heads, int head_dim
     return (t < rows ? t : rows) * kv_heads;
 }
 
-// Units are split among the CTAs where they would fill the SMs less than four times.
+// Units may be split among the CTAs where they would fill the SMs less than four times.  (Past
+// that the second launch and the parts' results cost prompts more than the evenness
+// saves: chunks of 4 x 2k tokens, 1024 units, 737 us split and 702 whole.)
 bool is_split(long long units, int sms) { return units < 4ll * sms; }
 
 template <int D>
