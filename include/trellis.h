@@ -178,9 +178,10 @@ TRELLIS_API int trellis_gemm_ws(const uint16_t *x, const uint32_t *codes, const 
 
 /*
  * trellis_device_status — synchronise `stream`, then report whether a bounded
- * device-side wait of the tensor-core product gave up since the last query
- * (TRELLIS_ERR_TIMEOUT; the affected outputs are undefined) or not
- * (TRELLIS_OK).  Clears the flag.  A wait gives up after 2 s of wall-clock
+ * device-side wait of the tensor-core product, or of trellis_kv_attention,
+ * gave up since the last query (TRELLIS_ERR_TIMEOUT; the affected outputs are
+ * undefined, and the workspace of the call is zero-filled again before its next
+ * use) or not (TRELLIS_OK).  Clears the flag.  A wait gives up after 2 s of wall-clock
  * time; the kernel then waits (bounded the same way) for its own copies and
  * tensor-core operations still in flight, releases its tensor memory and
  * returns, so the context stays usable.  The flag is one word per device,
@@ -397,7 +398,10 @@ TRELLIS_API int trellis_kv_append(const uint16_t *q, long long q_stride, const u
  *           use, at least trellis_kv_attention_workspace_size bytes; one buffer
  *           may serve the products too.
  * The scales of the cache must be powers of two (trellis_kv_append writes no others).
- * The order of all sums is fixed by the sizes, so equal calls give equal bits.
+ * The order of all sums is fixed by the sizes and lengths, so equal calls give
+ * equal bits.  Few rows to a key head run on a streaming kernel, many on the tensor
+ * cores, whose waits are bounded (see trellis_device_status); one or two kernels are
+ * enqueued.
  */
 TRELLIS_API int trellis_kv_attention(const uint16_t *q, long long q_stride, const int *starts, const int *kv_len,
                                      const int *pages, int tokens, int seqs, int max_q, int page_cols, int num_pages,
@@ -426,7 +430,7 @@ TRELLIS_API int trellis_kv_attention_workspace_size(int tokens, int seqs, int ma
  *   workspace  256-byte aligned, at least trellis_lora_add_workspace_size bytes;
  *           its first 1 MiB is not touched, so a product's workspace will do.
  * M <= 65536 (0: nothing is enqueued), segments <= 65536.  Sums are fp32, with one
- * rounding of the result.
+ * rounding of the result, in an order that the sizes fix.  Two kernels are enqueued.
  */
 TRELLIS_API int trellis_lora_add(const uint16_t *y, const uint16_t *x, const uint16_t *a, const uint16_t *b,
                                  const float *scales, const int *starts, const int *which, int M, int K, int N, int R,

@@ -12,8 +12,10 @@
 //   codes      e4m3(x / s), nearest even.  When a block's scale grows, the codes from
 //              before are multiplied by the (power of two) ratio and rounded again.
 //
-// What bounds it: at prompts the bytes (2 in and 1 or 2 out a value); for a step of
-// single tokens the latency of lengths -> page -> values.  A CTA takes one block of 16
+// What bounds it: at prompts the bytes (2 in and 1 or 2 out a value) and the rotation's
+// single operations; for a step of single tokens the latency of lengths -> page -> values.
+// Measured (GPU time; the least bytes at 6.69 TB/s): prompts of 8k tokens 45.5 us (26.5),
+// 128 single tokens 6.8 us (0.4), one 3.1 to 3.7 us.  A CTA takes one block of 16
 // positions of a sequence and some of its heads ("tasks": a key head, a value head
 // or a query head), a warp a task at a time.  The block's rows of the table are read once a
 // CTA into shared memory.  A lane takes 8 consecutive values a token (16 bytes in, 8 of

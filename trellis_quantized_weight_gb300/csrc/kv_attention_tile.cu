@@ -10,31 +10,39 @@
 //                          q = hi + lo in two e4m3 numbers, exactly (down to 2^-17 of the
 //                          row's largest value, the row being scaled by a power of
 //                          two): two 8-bit products at twice the rate of one 16-bit
-//                          product, and keys need no conversion.  Q lies in tensor memory.
+//                          product, and keys need no conversion.
 //   O[row, d]  += P V      P [128, 64] f16 in tensor memory over the columns that S had,
 //                          V converted to f16 in shared memory as the cache has it
 //                          (tokens x D: "MN-major" for this product, nothing is transposed).
 //                          Weights need more than e4m3's bits; f16 keeps 11.
 //
 // A CTA an SM works through items: (sequence, QT x 128 query rows of one key head's
-// group, key head), or a part of its tokens where there are too few units for the SMs.
+// group, key head), or where there are too few units for the SMs an equal share of all
+// units' tiles, cut where it falls (kv_join_kernel adds the parts up).
 // QT = 2 query tiles share every loaded tile of keys and values (1 at D = 256, whose sums
 // fill tensor memory), and one's softmax runs beside the other's products.  Roles:
 //
-// * 1 warp plans: takes the next item from a counter and finds its rows, shortly before
-//   the one at hand ends.
+// * 1 warp plans: finds the next item's rows, shortly before the one at hand ends.
 // * 4 warps load (8 at D = 256): warp w the codes of tokens 16w .. 16w+15 of each 64-token
-//   tile (one block of the cache, so one page and one pair of scales), a tile ahead in registers;
-//   K goes to shared memory as it is, V as f16, both in the 128-byte-swizzled layout:
-//   row = token, 128 bytes a row (a panel), 16-byte chunk c of row r at c ^ (r % 8).
+//   tile (one block of the cache, so one page and one pair of scales; half of one at D = 256),
+//   a tile ahead in registers, keys one further; K goes to shared memory as it is, V as f16,
+//   both in the 128-byte-swizzled layout: row = token, 128 bytes a row (a panel), 16-byte
+//   chunk c of row r at c ^ (r % 8).
 // * 1 warp issues the products.
 // * 4 warps a query tile do the softmax, a row a thread: scores from tensor memory,
 //   p' = 2^(x - m), sums in registers.  O is rescaled in tensor memory only when a row's
 //   reference moves.  They also store the result and bring in the next item's queries.
 //
-// What bounds it: per 64-key tile and 128 rows at D = 128 the products take 512 clocks,
-// the exponentials 256 (32 a clock and SM), and the softmax warps' instructions come near
-// the products' time; the tile's shared-memory traffic is 384 clocks.
+// What bounds it: per 64-key tile and 128 rows at D = 128 the products take 512 clocks of the
+// tensor pipe; but a row's softmax is one thread's chain of some 1000
+// to 1400 clocks (scores out of tensor memory, maximum, exponentials, P back), two warps a
+// scheduler, and an item costs 10 to 14 thousand clocks of its own (queries, first and last
+// products, result).  Measured (GPU time; the least bytes or operations at 6.69 TB/s and
+// 1951 TFLOP/s): chunks of 4 x 2048 tokens on contexts of 4100 to 9001, 32 / 8 heads of 128:
+// 702 us (351), 0.97 PFLOP/s; 6 prompts of 130 to 4099 tokens, window 1024, 24 / 8 heads of 64:
+// 166 us (31), where a row-tile has half of the products to the same softmax; 16 x 5 drafts on
+// contexts of 300 to 9000, 32 / 4 heads of 256: 71 us (23), one query tile of 40 rows, so that
+// nothing runs beside its chain.
 //
 // Waits are bounded as in gemm_tc_kernel.cu: one that gives up sets the device error
 // word and its role leaves; the issuing warp always waits for its last products
@@ -58,7 +66,6 @@ constexpr int kMinChunk = 4;             // fewest tiles of a split unit's part
 template <int D>
 struct Tile {
     static constexpr int kQt = D <= 128 ? 2 : 1;         // query tiles of a CTA
-    static constexpr int kSBufs = 2;                     // score buffers of a query tile
     static constexpr int kSoftWarps = 4 * kQt;
     // loading warps: 16 tokens of a tile each, or 8 where the one query tile leaves room for more warps
     static constexpr int kLoadWarps = D == 256 ? 8 : 4;
@@ -87,9 +94,9 @@ struct Tile {
                          kDone = kPartFree + 2, kBars = kDone + 1;
     static constexpr int kOffTaddr = kOffBar + kBars * 8;
     static constexpr int kSmem = kOffTaddr + 32 + 1024;  // + rounding of the base to 1 KB
-    // tensor memory: scores (P over them) and sums of each query tile
+    // tensor memory: two tiles of scores (P over them) and the sums of each query tile
     static constexpr int kSCol = 0;
-    static constexpr int kOCol = kSCol + kQt * kSBufs * kKeys;
+    static constexpr int kOCol = kSCol + kQt * 2 * kKeys;
     static constexpr int kCols = 512;
     // fp32 sums; N in bits 17-22, M in 24-28; formats 0 are e4m3 and f16; bit 16: B is MN-major
     static constexpr uint32_t kIdescS = (1u << 4) | (static_cast<uint32_t>(kKeys >> 3) << 17) |
