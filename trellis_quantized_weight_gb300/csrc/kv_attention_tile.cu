@@ -56,7 +56,7 @@ __device__ unsigned int g_kv_error = 0u;
 
 namespace {
 
-constexpr float kMoveBy = 8.0f;
+constexpr float kMoveBy = 14.0f;         // a weight is at most 2^14 then, f16 holds 2^15
 constexpr int kRows = 128;               // query rows of a tile (lanes of tensor memory)
 constexpr int kKeys = 64;                // cached tokens of a tile
 constexpr int kScaleSlots = 8;           // tiles whose scales are held
