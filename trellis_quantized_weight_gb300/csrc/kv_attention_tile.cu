@@ -39,8 +39,8 @@
 // scheduler, and an item costs 10 to 14 thousand clocks of its own (queries, first and last
 // products, result).  Measured (GPU time; the least bytes or operations at 6.69 TB/s and
 // 1951 TFLOP/s): chunks of 4 x 2048 tokens on contexts of 4100 to 9001, 32 / 8 heads of 128:
-// 702 us (351), 0.97 PFLOP/s; 6 prompts of 130 to 4099 tokens, window 1024, 24 / 8 heads of 64:
-// 166 us (31), where a row-tile has half of the products to the same softmax; 16 x 5 drafts on
+// 664 us (351), 1.03 PFLOP/s; 6 prompts of 130 to 4099 tokens, window 1024, 24 / 8 heads of 64:
+// 157 us (31), where a row-tile has half of the products to the same softmax; 16 x 5 drafts on
 // contexts of 300 to 9000, 32 / 4 heads of 256: 71 us (23), one query tile of 40 rows, so that
 // nothing runs beside its chain.
 //
@@ -56,7 +56,10 @@ __device__ unsigned int g_kv_error = 0u;
 
 namespace {
 
-constexpr float kMoveBy = 14.0f;         // a weight is at most 2^14 then, f16 holds 2^15
+// The reference moves when exceeded by 2^14: weights are at most that (f16 holds 2^15), and the
+// move, a pass over O of some 1500 to 3800 clocks, is rare (at 2^8 the chunks below took
+// 702 us for 664, the windowed prompts 166 for 157).
+constexpr float kMoveBy = 14.0f;
 constexpr int kRows = 128;               // query rows of a tile (lanes of tensor memory)
 constexpr int kKeys = 64;                // cached tokens of a tile
 constexpr int kScaleSlots = 8;           // tiles whose scales are held
