@@ -53,3 +53,12 @@ def test_equal_calls_give_equal_bits(lens):
     first = tq.kv_attention(q, cache, step.starts, step.kv_len, step.pages, max_q=6)
     for _ in range(5):
         assert torch.equal(tq.kv_attention(q, cache, step.starts, step.kv_len, step.pages, max_q=6), first)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_units_of_one_tile(d):
+    from trellis_quantized_weight_gb300 import binding
+    lens = [20 + (i * 7) % 45 for i in range(90)]
+    step = R.Step(d, [20] * 90, lens, 32, 4, d, 64)
+    check(step)
+    assert binding.load().trellis_device_status(None) == 0

@@ -893,8 +893,9 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
                     scales[slot * 4 + kToks * w / kKvBlock] =
                         valid > 0 ? make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
                 slot = (slot + 1) % kScaleSlots;
-                // the last tile of the item before frees its stage at that item's own barrier
-                ok = !(i == 1 && q_before >= 0) || item_done();
+                // the last tile of the item before frees its stage at that item's own barrier, which
+                // cannot pass again before this wait: that takes the values of the item's last tile
+                ok = !(i == min(1, tiles - 1) && q_before >= 0) || item_done();
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
                 if (valid < kToks) {
 #pragma unroll
@@ -923,7 +924,6 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
                 load_values();                           // of tile i + 1
                 load_keys(i + 2, tiles);
             }
-            if (tiles == 1 && q_before >= 0 && !__all_sync(0xffffffffu, item_done())) break;
             if (tiles > 0) {
 #pragma unroll
                 for (int q = 0; q < kQt; ++q)
