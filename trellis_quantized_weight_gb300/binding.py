@@ -322,22 +322,30 @@ def _raw_stream(index, stream):
     return _torch()._C._cuda_getCurrentRawStream(index)
 
 
-def _with_workspace(call, size, device, index, handle, stream):
-    """call(pointer, bytes) on this stream's workspace; grown to size() bytes if it is too small."""
+def _cached_workspace(index, handle):
+    """Pointer and bytes of this stream's workspace; none before its first use (the call asks for it then)."""
     buf = _ws_cache.get((index, handle))
-    rc = -7 if buf is None else call(buf.data_ptr(), buf.numel())
-    if rc == -7:
-        buf = _workspace(device, size(), stream)
-        rc = call(buf.data_ptr(), buf.numel())
-    return rc
+    return (None, 0) if buf is None else (buf.data_ptr(), buf.numel())
+
+
+_types = None
+
+
+def _torch_types():
+    """Tensor, bfloat16, float32, int32, float8_e4m3fn."""
+    global _types
+    if _types is None:
+        torch = _torch()
+        _types = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn)
+    return _types
 
 
 def _require_rows(t, name, index):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+    Tensor, bf16, _, _, _ = _types or _torch_types()
+    if not isinstance(t, Tensor) or t.get_device() != index:
         raise ValueError(f"{name} must be a tensor on cuda:{index}")
     shape = t.shape
-    if t.dtype != torch.bfloat16 or len(shape) != 3:
+    if t.dtype != bf16 or len(shape) != 3:
         raise ValueError(f"{name} must be a bfloat16 [tokens, heads, head_dim] tensor")
     row, head, one = t.stride()
     if t.numel() and (one != 1 or (shape[1] > 1 and head != shape[2])):
@@ -346,23 +354,24 @@ def _require_rows(t, name, index):
     return shape, row if shape[0] > 1 else shape[1] * shape[2]
 
 
+def _require_on(t, name, dtype, ndim, index):
+    if not isinstance(t, _types[0]) or index < 0 or t.get_device() != index or t.dtype != dtype \
+            or not t.is_contiguous() or len(shape := t.shape) != ndim:
+        raise ValueError(f"{name} must be a contiguous {ndim}-d {dtype} tensor on one CUDA device")
+    return shape
+
+
 def _require_ints(t, name, index, ndim):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.int32 or t.dim() != ndim \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {ndim}-d int32 tensor on cuda:{index}")
-    return t.shape
+    return _require_on(t, name, (_types or _torch_types())[3], ndim, index)
 
 
 def _require_cache(cache, starts, kv_len, pages):
     """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns, device index)."""
-    torch = _torch()
+    Tensor, _, f32, _, f8 = _types or _torch_types()
     k, v, ks, vs = cache
-    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+    if not isinstance(k, Tensor) or (index := k.get_device()) < 0:
         raise ValueError("the cache must be CUDA tensors")
-    index = k.get_device()
     shape = k.shape
-    f8, f32 = torch.float8_e4m3fn, torch.float32
     if len(shape) != 4 or v.shape != shape or k.dtype != f8 or v.dtype != f8:
         raise ValueError("cache codes must be float8_e4m3fn [pages, kv_heads, page_size, head_dim]")
     want = (shape[0], shape[1], shape[2] // 16)
@@ -381,11 +390,11 @@ def _require_cache(cache, starts, kv_len, pages):
 
 
 def _output(out, name, shape, index, device):
-    torch = _torch()
+    Tensor, bf16, _, _, _ = _types or _torch_types()
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    if not isinstance(out, torch.Tensor) or out.shape != shape or out.dtype != torch.bfloat16 \
-            or out.get_device() != index or not out.is_contiguous():
+        return _torch().empty(shape, dtype=bf16, device=device)
+    if not isinstance(out, Tensor) or out.shape != shape or out.dtype != bf16 or out.get_device() != index \
+            or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bfloat16 {tuple(shape)} tensor on cuda:{index}")
     return out
 
@@ -460,9 +469,11 @@ def kv_attention(q, cache, starts, kv_len, pages, scale=None, window: int = 0, m
     args = (q.data_ptr(), q_stride, starts.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, most, cols,
             num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
             cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr())
-    _check(_with_workspace(lambda ptr, size: fn(*args, ptr, size, handle),
-                           lambda: kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), dev, index, handle,
-                           stream), "trellis_kv_attention")
+    rc = fn(*args, *_cached_workspace(index, handle), handle)
+    if rc == -7:
+        buf = _workspace(dev, kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), stream)
+        rc = fn(*args, buf.data_ptr(), buf.numel(), handle)
+    _check(rc, "trellis_kv_attention")
     return out
 
 
@@ -480,32 +491,31 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
     input; a: bf16 [adapters, R, K]; b: bf16 [adapters, N, R]; scales: float32 [adapters].
     starts int32 [S + 1]: the rows of each request; which int32 [S]: its adapter, -1 for none.
     out may be y."""
-    torch = _torch()
-    bf16 = (torch.bfloat16,)
-    _require(y, "y", bf16, 2)
-    _require(x, "x", bf16, 2)
-    _require(a, "a", bf16, 3)
-    _require(b, "b", bf16, 3)
-    _require(scales, "scales", (torch.float32,), 1)
+    Tensor, bf16, f32, _, _ = _types or _torch_types()
+    if not isinstance(y, Tensor):
+        raise ValueError("y must be a CUDA tensor")
     dev, index = y.device, y.get_device()
+    shape = _require_on(y, "y", bf16, 2, index)
+    x_rows, K = _require_on(x, "x", bf16, 2, index)
+    n_ad, R, k_a = _require_on(a, "a", bf16, 3, index)
+    b_shape = _require_on(b, "b", bf16, 3, index)
+    n_scales, = _require_on(scales, "scales", f32, 1, index)
     n, = _require_ints(starts, "starts", index, 1)
     segments, = _require_ints(which, "which", index, 1)
-    shape, x_shape = y.shape, x.shape
-    (M, N), K = shape, x_shape[1]
-    n_ad, R, k_a = a.shape
-    if x_shape[0] != M or k_a != K or b.shape != (n_ad, N, R) or scales.shape[0] != n_ad:
+    M, N = shape
+    if x_rows != M or k_a != K or b_shape != (n_ad, N, R) or n_scales != n_ad:
         raise ValueError("y must be [M, N], x [M, K], a [adapters, R, K], b [adapters, N, R] and scales [adapters]")
     if n != segments + 1:
         raise ValueError("starts must be [S + 1] with which [S]")
-    if x.get_device() != index or a.get_device() != index or b.get_device() != index or scales.get_device() != index:
-        raise ValueError("all tensors must be on one device")
     out = _output(out, "out", shape, index, dev)
     if M == 0:
         return out
     fn, handle = load().trellis_lora_add, _raw_stream(index, stream)
     args = (y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), starts.data_ptr(),
             which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr())
-    _check(_with_workspace(lambda ptr, size: fn(*args, ptr, size, handle),
-                           lambda: lora_add_workspace_bytes(M, K, N, R, n_ad, segments), dev, index, handle, stream),
-           "trellis_lora_add")
+    rc = fn(*args, *_cached_workspace(index, handle), handle)
+    if rc == -7:
+        buf = _workspace(dev, lora_add_workspace_bytes(M, K, N, R, n_ad, segments), stream)
+        rc = fn(*args, buf.data_ptr(), buf.numel(), handle)
+    _check(rc, "trellis_lora_add")
     return out
