@@ -319,7 +319,7 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, stretch: float =
 def _raw_stream(index, stream):
     if stream is not None:
         return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(index)
+    return (_types or _torch_types())[6](index)
 
 
 def _cached_workspace(index, handle):
@@ -332,23 +332,24 @@ _types = None
 
 
 def _torch_types():
-    """Tensor, bfloat16, float32, int32, float8_e4m3fn."""
+    """Tensor, bfloat16, float32, int32, float8_e4m3fn, empty, the current stream's handle."""
     global _types
     if _types is None:
         torch = _torch()
-        _types = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn)
+        _types = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.empty,
+                  torch._C._cuda_getCurrentRawStream)
     return _types
 
 
 def _require_rows(t, name, index):
-    Tensor, bf16, _, _, _ = _types or _torch_types()
-    if not isinstance(t, Tensor) or t.get_device() != index:
+    types = _types or _torch_types()
+    if not isinstance(t, types[0]) or t.get_device() != index:
         raise ValueError(f"{name} must be a tensor on cuda:{index}")
     shape = t.shape
-    if t.dtype != bf16 or len(shape) != 3:
+    if t.dtype != types[1] or len(shape) != 3:
         raise ValueError(f"{name} must be a bfloat16 [tokens, heads, head_dim] tensor")
     row, head, one = t.stride()
-    if t.numel() and (one != 1 or (shape[1] > 1 and head != shape[2])):
+    if (one != 1 or (shape[1] > 1 and head != shape[2])) and t.numel():
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     # the stride of a single row is arbitrary: the row's own length then
     return shape, row if shape[0] > 1 else shape[1] * shape[2]
@@ -361,13 +362,9 @@ def _require_on(t, name, dtype, ndim, index):
     return shape
 
 
-def _require_ints(t, name, index, ndim):
-    return _require_on(t, name, (_types or _torch_types())[3], ndim, index)
-
-
 def _require_cache(cache, starts, kv_len, pages):
     """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns, device index)."""
-    Tensor, _, f32, _, f8 = _types or _torch_types()
+    Tensor, _, f32, i32, f8, _, _ = _types or _torch_types()
     k, v, ks, vs = cache
     if not isinstance(k, Tensor) or (index := k.get_device()) < 0:
         raise ValueError("the cache must be CUDA tensors")
@@ -381,19 +378,19 @@ def _require_cache(cache, starts, kv_len, pages):
         raise ValueError("the cache must be on one device")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("the cache must be contiguous")
-    n, = _require_ints(starts, "starts", index, 1)
-    seqs, = _require_ints(kv_len, "kv_len", index, 1)
-    rows, cols = _require_ints(pages, "pages", index, 2)
+    n, = _require_on(starts, "starts", i32, 1, index)
+    seqs, = _require_on(kv_len, "kv_len", i32, 1, index)
+    rows, cols = _require_on(pages, "pages", i32, 2, index)
     if n != seqs + 1 or rows != seqs:
         raise ValueError("starts must be [S + 1], kv_len [S] and pages [S, columns]")
     return shape, seqs, cols, index
 
 
 def _output(out, name, shape, index, device):
-    Tensor, bf16, _, _, _ = _types or _torch_types()
+    types = _types or _torch_types()
     if out is None:
-        return _torch().empty(shape, dtype=bf16, device=device)
-    if not isinstance(out, Tensor) or out.shape != shape or out.dtype != bf16 or out.get_device() != index \
+        return types[5](shape, dtype=types[1], device=device)
+    if not isinstance(out, types[0]) or out.shape != shape or out.dtype != types[1] or out.get_device() != index \
             or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bfloat16 {tuple(shape)} tensor on cuda:{index}")
     return out
@@ -409,7 +406,6 @@ def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved
     sequence; kv_len int32 [S]: its tokens with these; pages int32 [S, columns]: its pages.
     rope: float32 [positions, rot] from rope_table, or None.  max_q: rows of the sequence that
     has most (a hint).  The cache is updated in place."""
-    torch = _torch()
     (num_pages, hk, page, d), seqs, cols, index = _require_cache(cache, starts, kv_len, pages)
     k_shape, k_stride = _require_rows(k, "k", index)
     v_shape, v_stride = _require_rows(v, "v", index)
@@ -428,13 +424,11 @@ def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved
         raise ValueError("q_out without q")
     rope_ptr, rows, rot = None, 0, 0
     if rope is not None:
-        if not isinstance(rope, torch.Tensor) or rope.get_device() != index or rope.dtype != torch.float32 \
-                or rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be a contiguous float32 [positions, rot] tensor")
-        rope_ptr, (rows, rot) = rope.data_ptr(), rope.shape
+        rows, rot = _require_on(rope, "rope", _types[2], 2, index)
+        rope_ptr = rope.data_ptr()
     if seqs == 0 or tokens == 0:
         return q_out
-    _check(load().trellis_kv_append(
+    _check((_lib or load()).trellis_kv_append(
         q_ptr, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, starts.data_ptr(), kv_len.data_ptr(),
         pages.data_ptr(), tokens, seqs, tokens if max_q is None else max_q, cols, num_pages, hq, hk, d, page, rope_ptr, rows,
         rot, 1 if interleaved else 0, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
@@ -465,7 +459,7 @@ def kv_attention(q, cache, starts, kv_len, pages, scale=None, window: int = 0, m
     if seqs == 0 or tokens == 0:
         return out
     most = tokens if max_q is None else max_q
-    fn, handle = load().trellis_kv_attention, _raw_stream(index, stream)
+    fn, handle = (_lib or load()).trellis_kv_attention, _raw_stream(index, stream)
     args = (q.data_ptr(), q_stride, starts.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, most, cols,
             num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
             cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr())
@@ -491,7 +485,7 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
     input; a: bf16 [adapters, R, K]; b: bf16 [adapters, N, R]; scales: float32 [adapters].
     starts int32 [S + 1]: the rows of each request; which int32 [S]: its adapter, -1 for none.
     out may be y."""
-    Tensor, bf16, f32, _, _ = _types or _torch_types()
+    Tensor, bf16, f32, i32, _, _, _ = _types or _torch_types()
     if not isinstance(y, Tensor):
         raise ValueError("y must be a CUDA tensor")
     dev, index = y.device, y.get_device()
@@ -500,8 +494,8 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
     n_ad, R, k_a = _require_on(a, "a", bf16, 3, index)
     b_shape = _require_on(b, "b", bf16, 3, index)
     n_scales, = _require_on(scales, "scales", f32, 1, index)
-    n, = _require_ints(starts, "starts", index, 1)
-    segments, = _require_ints(which, "which", index, 1)
+    n, = _require_on(starts, "starts", i32, 1, index)
+    segments, = _require_on(which, "which", i32, 1, index)
     M, N = shape
     if x_rows != M or k_a != K or b_shape != (n_ad, N, R) or n_scales != n_ad:
         raise ValueError("y must be [M, N], x [M, K], a [adapters, R, K], b [adapters, N, R] and scales [adapters]")
@@ -510,7 +504,7 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
     out = _output(out, "out", shape, index, dev)
     if M == 0:
         return out
-    fn, handle = load().trellis_lora_add, _raw_stream(index, stream)
+    fn, handle = (_lib or load()).trellis_lora_add, _raw_stream(index, stream)
     args = (y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), starts.data_ptr(),
             which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr())
     rc = fn(*args, *_cached_workspace(index, handle), handle)
