@@ -6,15 +6,15 @@
 // Two launches: h = x A^T (sums over K, the long axis), then out = y + s h B^T (over
 // the rank).  Both are skinny: at few rows they read A and B (2 R (K + N) bytes an
 // adapter), at many rows x, y and out.  The tensor work is 2 M R (K + 2 N) multiply-adds
-// (h counts twice, see below); m16n8k16 issues one in 8 cycles a quarter of an SM, which
-// stays below the time of the bytes up to a rank of 64 and is no further step from it at 128.
+// (h counts twice, see below): at m16n8k16's 8 cycles each 32 us of the second kernel's 43
+// for its bytes in the largest case below, and about twice that at rank 128 (120 us in all).
 //
 // Measured (GPU time of both launches; the least bytes at 6.69 TB/s): 1 row, K 5120, N 17408,
-// rank 16: 4.6 us, two launches in a row; 64 requests of one row on 24 adapters, K 17408,
+// rank 16: 4.6 to 5.1 us, two launches in a row; 64 requests of one row on 24 adapters, K 17408,
 // N 5120, rank 32: 17 us (5.7), half of it start and the reads of 64 tiles, which do not
 // share an adapter; 4068 rows of 4 requests, K 5120, N 17408, rank 64: 78 us (53), of which
 // the first kernel 20 (chain of copy, shared memory and mma of 4 warps an SM) and the second
-// 58 at 4.9 TB/s.  Rows without an adapter are copied at 6.2 TB/s by the same loop.
+// 58 at 4.9 TB/s.  Rows without an adapter are copied at 6 TB/s by the same loop.
 //
 // * The order of a sum's terms is free, so a lane's 8 consecutive elements (16 bytes) serve
 //   as its operands of two products, in both factors alike: fragments need no
