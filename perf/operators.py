@@ -11,7 +11,7 @@ The cache.  keys and values: float8_e4m3fn [pages, kv_heads, page_size, head_dim
 page_size / 16], a power of two for each block of 16 tokens of a page and head.  A stored value is code * scale.  Token t
 of sequence s lies in page table[s, t // page_size], at t % page_size.  `starts` [S + 1] says which rows of the step's
 packed tokens are sequence s's, `kv_len` [S] how many tokens it has with them, so that its last row is token kv_len - 1.
-The scale of a block of values with largest magnitude a is the smallest power of two s >= 2^-60 with a <= 448 s; a block
+The scale of a block of values with largest magnitude a is the smallest power of two s >= 2^-100 with a <= 448 s; a block
 that had tokens before keeps its scale unless the new tokens need a larger one, and then its old codes are rounded again.
 
 `own` false: the operators in elementary torch operations, in 32 bits; true: the package's calls.
@@ -234,10 +234,10 @@ def _rotate(x, table, rot, inter):
 
 
 def _power(a):
-    """The smallest power of two s >= 2^-60 with a <= 448 s, from a's own bits."""
+    """The smallest power of two s >= 2^-100 with a <= 448 s, from a's own bits."""
     m, e = torch.frexp(a)
-    e = (e - 9 + (m > 0.875).int()).clamp(min=-60)
-    e = torch.where(a > 0, e, -60)
+    e = (e - 9 + (m > 0.875).int()).clamp(min=-100)
+    e = torch.where(a > 0, e, -100)
     s = ((e + 127) << 23).view(torch.float32)
     return torch.where(torch.isfinite(a), s, torch.nan)
 
@@ -410,7 +410,7 @@ def _exact_append(s, c, new, total, start):
                 y = x[lo - (t - n):hi - (t - n)].transpose(0, 1)                        # [heads, tokens, dim]
                 most = y.abs().amax((1, 2))
                 m, e = torch.frexp(most / E4M3_MAX)                                     # most = 448 m 2^e, 0.5 <= m < 1
-                want = torch.ldexp(torch.ones_like(m), (e - (m == 0.5).int()).clamp(min=-60))
+                want = torch.ldexp(torch.ones_like(m), (e - (m == 0.5).int()).clamp(min=-100))
                 had = scale[ph, :, off // BLOCK].clone()
                 kept = lo - b * BLOCK
                 now = torch.maximum(want, had) if kept else want
