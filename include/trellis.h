@@ -393,7 +393,9 @@ TRELLIS_API int trellis_kv_append(const uint16_t *q, long long q_stride, const u
  *   scale   factor of the scores (1 / sqrt(head_dim) for most models).
  *   window  0: a row at position p sees the tokens 0 .. p; w > 0: the last w of them.
  *   out     device, bf16 [tokens, q_heads, head_dim], rounded once from fp32 sums;
- *           a row that sees no token is zero.
+ *           a row that sees no token is zero.  A block with a NaN scale makes the rows
+ *           that see a token of it NaN, and no other row.  (NaN codes in used slots are
+ *           expected under a NaN scale only, as trellis_kv_append leaves them.)
  *   workspace  as trellis_gemm_ws: 256-byte aligned, zero-filled before its first
  *           use, at least trellis_kv_attention_workspace_size bytes; one buffer
  *           may serve the products too.

@@ -427,8 +427,11 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                         mma_f16(sc[nt][w & 1], a0, a1, a2, a3, qf[nt][4 * j + w][0], qf[nt][4 * j + w][1]);
                 }
             }
-            const float lv = pow2_log2(vs), iv = pow2_recip(vs);
+            const float lv = pow2_log2(vs), iv = pow2_recip_finite(vs);
             const bool edge = tok0 + kKvBlock > all_hi || tok0 < all_lo;
+            // A NaN value scale makes the weights of the rows that see its block NaN (lv is).  Its values
+            // must not reach rows that do not see it, whose weights are 0
+            const int values_end = edge && vs != vs ? tok0 : u.hi;
             bool over = false;
             float x[NT][4];
 #pragma unroll
@@ -472,8 +475,9 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                 pf[nt][0] = movmatrix_trans(f32_to_f16x2(p0, p1));
                 pf[nt][1] = movmatrix_trans(f32_to_f16x2(p2, p3));
             }
-            // slots past the last token may hold anything, NaN too: their values count as 0
-            const bool tail = tok0 + kKvBlock > u.hi;
+            // slots past the last token may hold anything, NaN too: their values count as 0, as those of a
+            // block with a NaN scale do (0 times NaN is not 0)
+            const bool tail = tok0 + kKvBlock > values_end;
             const uint32_t vsrc = src + kKvBlock * D;
             auto products = [&](int q, const uint32_t (&w)[4]) {       // 4 values of 4 tokens: tiles 2q, 2q + 1
 #pragma unroll
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             };
             bool keep[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) keep[r] = !tail || tok0 + 2 * t + (r & 1) + (r >> 1) * 8 < u.hi;
+            for (int r = 0; r < 4; ++r) keep[r] = !tail || tok0 + 2 * t + (r & 1) + (r >> 1) * 8 < values_end;
             if constexpr (D == 64) {
                 uint32_t w[2][4];
 #pragma unroll

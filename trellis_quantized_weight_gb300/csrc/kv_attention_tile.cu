@@ -889,20 +889,23 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
                 // tokens of the block that count: what lies past them may be anything, NaN
                 // codes too, and 0 times NaN is not 0.  (Scores of such keys are masked.)
                 const int valid = u.hi - token_of(i);
+                // A block with a NaN scale makes the weights of the rows that see it NaN; its values
+                // must not reach the others, whose weights are 0
+                const int finite = vs == vs ? valid : 0;
                 if (lane == 0 && kToks * w % kKvBlock == 0)
                     scales[slot * 4 + kToks * w / kKvBlock] =
-                        valid > 0 ? make_float4(ks, pow2_log2(vs), pow2_recip(vs), 0.0f) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+                        valid > 0 ? make_float4(ks, pow2_log2(vs), pow2_recip_finite(vs), 0.0f) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
                 slot = (slot + 1) % kScaleSlots;
                 // the last tile of the item before frees its stage at that item's own barrier, which
                 // cannot pass again before this wait: that takes the values of the item's last tile
                 ok = !(i == min(1, tiles - 1) && q_before >= 0) || item_done();
                 if (!__all_sync(0xffffffffu, ok)) { run = false; break; }
-                if (valid < kToks) {
+                if (finite < kToks) {
 #pragma unroll
                     for (int h = 0; h < kH; ++h)
 #pragma unroll
                         for (int p = 0; p < P; ++p)
-                            if (r8 + 8 * h >= valid) vraw[h][p] = make_uint4(0u, 0u, 0u, 0u);
+                            if (r8 + 8 * h >= finite) vraw[h][p] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 const uint32_t vdst = sbase + T::kOffV + vst * T::kVPanels * T::kPanel;
 #pragma unroll

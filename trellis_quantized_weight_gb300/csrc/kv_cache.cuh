@@ -103,6 +103,12 @@ __device__ __forceinline__ float pow2_recip(float s) {
     return e < 254u ? __uint_as_float((254u - e) << 23) : s;
 }
 
+// The same where the factor goes with weights: finite for a NaN scale (whose logarithm makes the
+// weights that count NaN), so that a weight of 0 stays 0.
+__device__ __forceinline__ float pow2_recip_finite(float s) {
+    return __uint_as_float((254u - min(__float_as_uint(s) >> 23, 253u)) << 23);
+}
+
 // ---- asynchronous copies and small matrix products ----------------------------------
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
