@@ -399,6 +399,8 @@ TRELLIS_API int trellis_kv_append(const uint16_t *q, long long q_stride, const u
  *   workspace  as trellis_gemm_ws: 256-byte aligned, zero-filled before its first
  *           use, at least trellis_kv_attention_workspace_size bytes; one buffer
  *           may serve the products too.
+ * Weights are held in f16 against fp32 denominators: 2^-11 of itself for each, and the smallest
+ * lose at most 2^-14 of the largest weight in all, up to 2^18 tokens.
  * The scales of the cache must be powers of two (trellis_kv_append writes no others).
  * The order of all sums is fixed by the sizes and lengths, so equal calls give
  * equal bits.  Few rows to a key head run on a streaming kernel, many on the tensor

@@ -33,10 +33,12 @@
 //   p' = p * v_scale comes out of the exponential and no further multiplication
 //   is needed; the denominators add p' / v_scale.
 // * Running maximum: p' is taken against a reference that is only moved when a score
-//   exceeds it by 2^8, so a step has one vote instead of reductions.  p' <= 2^8 in
-//   f16 (11 significant bits, relative to the largest) is the one rounding
-//   between q, k, v and the fp32 sums; queries enter as f16 times a power of
-//   two per row, which is exact for bf16 down to 2^-24 of the row's largest.
+//   exceeds it by 2^15.5, so a step has one vote instead of reductions.  p' in f16 (11
+//   significant bits down to 2^-14, 2^-25 of error below) is the one rounding between q, k, v and
+//   the fp32 sums.  A weight that rounds to 0 still counts in the denominators, so the
+//   reference is set 2^7 below the largest score: 2^17 tokens lose under 2^-15 of the
+//   largest weight (2^-8 with the reference at the largest score).  Queries enter as f16 times a
+//   power of two per row: bf16's 8 bits down to 2^-17 of the row's largest, 2^-25 of it below.
 #include <cfloat>
 
 #include "kv_attention.cuh"
@@ -46,7 +48,10 @@ namespace trellis {
 
 namespace {
 
-constexpr float kMoveBy = 8.0f;          // the reference moves when exceeded by 2^8
+// The reference moves when exceeded by 2^15.5 (f16 ends at 65504), to the largest score over 2^7: the
+// weights that vanish in f16, under 2^-25, are under 2^-32 of the largest then.
+constexpr float kMoveBy = 15.5f;
+constexpr float kBelow = 7.0f;
 constexpr int kJoin = 16;                // pieces of a unit that one CTA joins
 
 // Warps of a CTA and ring steps by head width and rows: 128 to 160 KB of codes in
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        top = fmaxf(top, m[nt][h]);
+                        top = fmaxf(top - kBelow, m[nt][h]);
                         const float f = m[nt][h] == -INFINITY ? 0.0f : exp2_approx(m[nt][h] - top);
                         m[nt][h] = top;
                         sum[nt][h] *= f;

@@ -7,10 +7,11 @@
 //
 //   S[row, key] = Q K^T    K: the cache's e4m3 codes as they are, [64 keys, D] in shared
 //                          memory.  A bf16 query has 8 significant bits and e4m3 4, so
-//                          q = hi + lo in two e4m3 numbers, exactly (down to 2^-17 of the
-//                          row's largest value, the row being scaled by a power of
-//                          two): two 8-bit products at twice the rate of one 16-bit
-//                          product, and keys need no conversion.
+//                          q = hi + lo in two e4m3 numbers, the row being scaled by a
+//                          power of two: exactly down to 2^-9 of the row's largest
+//                          value, within 2^-17 of that value below.  Two 8-bit products
+//                          at twice the rate of one 16-bit product, and keys need no
+//                          conversion.
 //   O[row, d]  += P V      P [128, 64] f16 in tensor memory over the columns that S had,
 //                          V converted to f16 in shared memory as the cache has it
 //                          (tokens x D: "MN-major" for this product, nothing is transposed).
@@ -56,10 +57,15 @@ __device__ unsigned int g_kv_error = 0u;
 
 namespace {
 
-// The reference moves when exceeded by 2^14: weights are at most that (f16 holds 2^15), and the
-// move, a pass over O of some 1500 to 3800 clocks, is rare (at 2^8 the chunks below took
-// 702 us for 664, the windowed prompts 166 for 157).
-constexpr float kMoveBy = 14.0f;
+// The reference moves when exceeded by 2^15.9: weights are at most that (f16 ends at 65504), and the
+// move, a pass over O of some 1500 to 3800 clocks, is rare (at 2^8 the chunks above took 702 us
+// for 664, the windowed prompts 166 for 157).  It moves to the largest score over 2^below, because
+// weights under 2^-25 vanish in f16 but count in the denominators: N tokens then lose at most
+// N 2^-(25 + below) of the largest weight, and below = log2(N) - kNear, rounded up, keeps that
+// under 2^-14 up to 2^21 tokens.  Units of up to 2^11 tokens need none.  (Chunks 663 us without it,
+// 670 so; 677, 683, 690, 699 with 4 to 7 at every length.)
+constexpr float kMoveBy = 15.9f;
+constexpr int kNear = 11, kFarBelow = 10;
 constexpr int kRows = 128;               // query rows of a tile (lanes of tensor memory)
 constexpr int kKeys = 64;                // cached tokens of a tile
 constexpr int kScaleSlots = 8;           // tiles whose scales are held
@@ -607,6 +613,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
             const int all_hi = min(u.hi, u.p0 + row0 / a.group + 1);
             const int all_lo = a.window > 0 ? u.p0 + min(u.n - 1, (row0 + kRows - 1) / a.group) + 1 - a.window : 0;
             const bool has_rows = row0 + w0 < u.n * a.group;
+            // how far the reference stays below the largest score: by the tokens of the unit, not of the part
+            const float below = static_cast<float>(min(max(0, 32 - __clz(max(u.hi - u.lo - 1, 0)) - kNear), kFarBelow));
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int i = 0; live_tile && i < tiles; ++i) {
@@ -661,7 +669,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
                 };
                 block_top(s0, 0); block_top(s0 + 16, 1); block_top(s1, 2); block_top(s1 + 16, 3);
                 if (__any_sync(0xffffffffu, top > m + kMoveBy)) {
-                    const float to = fmaxf(m, top);
+                    const float to = fmaxf(m, top - below);
                     const float f = m == -INFINITY ? 0.0f : exp2_approx(m - to);
                     m = to;
                     l *= f;
