@@ -396,6 +396,7 @@ TRELLIS_API int trellis_kv_append(const uint16_t *q, long long q_stride, const u
  *           a row that sees no token is zero.  A block with a NaN scale makes the rows
  *           that see a token of it NaN, and no other row.  (NaN codes in used slots are
  *           expected under a NaN scale only, as trellis_kv_append leaves them.)
+ *           A query row that holds a NaN or an infinity is NaN if it sees a token.
  *   workspace  as trellis_gemm_ws: 256-byte aligned, zero-filled before its first
  *           use, at least trellis_kv_attention_workspace_size bytes; one buffer
  *           may serve the products too.

@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
                         qf[nt][4 * j + 2 * h + (i >> 1)][i & 1] = f32_to_f16x2(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
                 }
             // the column's factor, from the lane that holds its row
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
+            // (a row with an infinity or a NaN has no softmax: it is NaN, whatever signs its scores would get)
+            const float up = most >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                             : __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 qmul[nt][h] = __shfl_sync(0xffffffffu, up, (2 * t + h) * 4);
