@@ -167,7 +167,8 @@ TRELLIS_API int trellis_gemm_workspace_size(int M, int K, int N, int k, int L, i
  * reused, for any geometry that fits it, without clearing.  Geometries with
  * more than 2^18 row tiles (tiles are 64 rows) are rejected with
  * TRELLIS_ERR_SHAPE.  Two calls that may overlap on the GPU must not
- * share a workspace.  A workspace sized for one geometry serves any geometry
+ * share a workspace, and host threads that share one (on one stream) take turns
+ * call by call: a call may enqueue several kernels that hand data on in it.  A workspace sized for one geometry serves any geometry
  * whose reported size is not larger.
  * Errors: as trellis_gemm, plus TRELLIS_ERR_WORKSPACE when the workspace is
  * NULL or too small, TRELLIS_ERR_ALIGN when it is misaligned.

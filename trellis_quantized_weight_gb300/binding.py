@@ -150,27 +150,49 @@ def _require(t, name, dtypes, ndim):
         raise ValueError(f"{name} must be a contiguous {ndim}-d tensor")
 
 
+class _Workspace:
+    """The zero-filled workspace of a device and stream, reused across calls and grown as needed.
+
+    It is allocated and zero-filled on the stream the calls run on, so stream order alone makes the
+    fill land first and lets torch's caching allocator recycle an outgrown buffer once the calls
+    enqueued before it are done: no host synchronisation.  One buffer per stream also keeps calls on
+    different streams off each other's counters and partial sums.  Calls of several host threads on
+    one stream take turns: a call may enqueue two kernels that hand data on in the workspace, and
+    the buffer must not be replaced between the look at it and the launch."""
+    __slots__ = ("lock", "buf", "ptr", "size")
+
+    def __init__(self):
+        self.lock = threading.Lock()
+        self.buf, self.ptr, self.size = None, None, 0
+
+    def grow(self, nbytes, index, stream):
+        buf = _zeros(max(nbytes, 256), index, stream)
+        self.buf, self.ptr, self.size = buf, buf.data_ptr(), buf.numel()
+
+
 _ws_cache: dict = {}
-_ws_lock = threading.Lock()
 
 
-def _workspace(device, nbytes: int, stream=None):
-    """A zero-filled torch buffer per (device, stream), reused across calls and grown
-    as needed.  It is allocated and zero-filled on the stream the calls run on, so
-    stream order alone makes the fill land first and lets torch's caching allocator
-    recycle an outgrown buffer once the calls enqueued before it are done: no host
-    synchronisation.  One buffer per stream also keeps calls on different streams
-    off each other's split-K counters."""
+def _zeros(nbytes, index, stream):
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (torch.device(device).index, s.cuda_stream)
-    with _ws_lock:
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            with torch.cuda.stream(s):
-                buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-            _ws_cache[key] = buf
-    return buf
+    with torch.cuda.stream(stream):             # None: the current stream
+        return torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
+
+
+def _launch(fn, args, index, stream, need, ask=True):
+    """fn(*args, workspace, its bytes, stream) with the stream's workspace.  need() is the size of it; with ask=False
+    it is not looked up unless the call refuses the workspace at hand."""
+    handle = _raw_stream(index, stream)
+    ws = _ws_cache.get((index, handle)) or _ws_cache.setdefault((index, handle), _Workspace())
+    least = max(need(), 256) if ask else 0
+    with ws.lock:
+        if ws.size < least:
+            ws.grow(least, index, stream)
+        rc = fn(*args, ws.ptr, ws.size, handle)
+        if rc == -7 and not ask:
+            ws.grow(need(), index, stream)
+            rc = fn(*args, ws.ptr, ws.size, handle)
+    _check(rc, fn.__name__)
 
 
 def decode(codes, scales, K: int, k: int, L: int = 12, T: int = 256, out=None, stream=None):
@@ -207,11 +229,8 @@ def gemm(x, codes, scales, k: int, L: int = 12, T: int = 256, out=None, stream=N
     _require(out, "out", (torch.bfloat16,), 2)
     if tuple(out.shape) != (M, N):
         raise ValueError("out must be [M, N]")
-    nbytes = gemm_workspace_bytes(M, K, N, k, L, T)
-    ws = _workspace(x.device, max(nbytes, 256), stream)
-    rc = abi_gemm_ws(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, K, N, k, L, T,
-                     out.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(x.device, stream))
-    _check(rc, "trellis_gemm_ws")
+    _launch(load().trellis_gemm_ws, (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, K, N, k, L, T, out.data_ptr()),
+            x.get_device(), stream, lambda: gemm_workspace_bytes(M, K, N, k, L, T))
     return out
 
 
@@ -233,13 +252,10 @@ def gemm_gateup(x, codes_gate, scales_gate, codes_up, scales_up, k: int, act: bo
     g = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     u = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     a = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if act else None
-    nbytes = gemm_gateup_workspace_bytes(M, K, N, k, L, T)
-    ws = _workspace(x.device, max(nbytes, 256), stream)
-    rc = load().trellis_gemm_gateup(x.data_ptr(), codes_gate.data_ptr(), scales_gate.data_ptr(),
-                                    codes_up.data_ptr(), scales_up.data_ptr(), M, K, N, k, L, T,
-                                    g.data_ptr(), u.data_ptr(), a.data_ptr() if act else None,
-                                    ws.data_ptr(), ws.numel(), _stream_handle(x.device, stream))
-    _check(rc, "trellis_gemm_gateup")
+    _launch(load().trellis_gemm_gateup, (x.data_ptr(), codes_gate.data_ptr(), scales_gate.data_ptr(), codes_up.data_ptr(),
+                                         scales_up.data_ptr(), M, K, N, k, L, T, g.data_ptr(), u.data_ptr(),
+                                         a.data_ptr() if act else None),
+            x.get_device(), stream, lambda: gemm_gateup_workspace_bytes(M, K, N, k, L, T))
     return g, u, a
 
 
@@ -266,14 +282,11 @@ def gemm_packed(xs, codes, scales, k: int, L: int = 12, T: int = 256, outs=None,
         _require(o, f"outs[{i}]", (torch.bfloat16,), 2)
         if tuple(o.shape) != (r, N):
             raise ValueError(f"outs[{i}] must be [{r}, {N}]")
-    nbytes = gemm_packed_workspace_bytes(rows, K, N, k, L, T)
-    ws = _workspace(xs[0].device, max(nbytes, 256), stream)
     xp = (ctypes.c_void_p * len(xs))(*[x.data_ptr() for x in xs])
     op = (ctypes.c_void_p * len(outs))(*[o.data_ptr() for o in outs])
     rp = (ctypes.c_int * len(rows))(*rows)
-    rc = load().trellis_gemm_packed(xp, rp, len(rows), codes.data_ptr(), scales.data_ptr(), K, N, k, L, T, op,
-                                    ws.data_ptr(), ws.numel(), _stream_handle(xs[0].device, stream))
-    _check(rc, "trellis_gemm_packed")
+    _launch(load().trellis_gemm_packed, (xp, rp, len(rows), codes.data_ptr(), scales.data_ptr(), K, N, k, L, T, op),
+            xs[0].get_device(), stream, lambda: gemm_packed_workspace_bytes(rows, K, N, k, L, T))
     return outs
 
 
@@ -320,12 +333,6 @@ def _raw_stream(index, stream):
     if stream is not None:
         return stream.cuda_stream
     return (_types or _torch_types())[6](index)
-
-
-def _cached_workspace(index, handle):
-    """Pointer and bytes of this stream's workspace; none before its first use (the call asks for it then)."""
-    buf = _ws_cache.get((index, handle))
-    return (None, 0) if buf is None else (buf.data_ptr(), buf.numel())
 
 
 _types = None
@@ -459,15 +466,11 @@ def kv_attention(q, cache, starts, kv_len, pages, scale=None, window: int = 0, m
     if seqs == 0 or tokens == 0:
         return out
     most = tokens if max_q is None else max_q
-    fn, handle = (_lib or load()).trellis_kv_attention, _raw_stream(index, stream)
-    args = (q.data_ptr(), q_stride, starts.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, most, cols,
-            num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
-            cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr())
-    rc = fn(*args, *_cached_workspace(index, handle), handle)
-    if rc == -7:
-        buf = _workspace(dev, kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), stream)
-        rc = fn(*args, buf.data_ptr(), buf.numel(), handle)
-    _check(rc, "trellis_kv_attention")
+    _launch((_lib or load()).trellis_kv_attention,
+            (q.data_ptr(), q_stride, starts.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), tokens, seqs, most, cols,
+             num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
+             cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr()),
+            index, stream, lambda: kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), ask=False)
     return out
 
 
@@ -504,12 +507,8 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
     out = _output(out, "out", shape, index, dev)
     if M == 0:
         return out
-    fn, handle = (_lib or load()).trellis_lora_add, _raw_stream(index, stream)
-    args = (y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), starts.data_ptr(),
-            which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr())
-    rc = fn(*args, *_cached_workspace(index, handle), handle)
-    if rc == -7:
-        buf = _workspace(dev, lora_add_workspace_bytes(M, K, N, R, n_ad, segments), stream)
-        rc = fn(*args, buf.data_ptr(), buf.numel(), handle)
-    _check(rc, "trellis_lora_add")
+    _launch((_lib or load()).trellis_lora_add,
+            (y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), starts.data_ptr(),
+             which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr()),
+            index, stream, lambda: lora_add_workspace_bytes(M, K, N, R, n_ad, segments), ask=False)
     return out
