@@ -1,5 +1,4 @@
 """The binding's workspaces on the host: a fake of the library's call and CPU buffers, no GPU."""
-import contextlib
 import gc
 import threading
 import time
@@ -13,13 +12,14 @@ from trellis_quantized_weight_gb300 import binding  # noqa: E402
 
 class Stream:
     def __init__(self, handle):
-        self.cuda_stream = handle
+        self.cuda_stream, self.capturing = handle, False
 
 
 @pytest.fixture(autouse=True)
 def host(monkeypatch):
     monkeypatch.setattr(binding, "_ws_cache", {})
     monkeypatch.setattr(binding, "_zeros", lambda nbytes, index, stream: torch.zeros(nbytes, dtype=torch.uint8))
+    monkeypatch.setattr(binding, "_is_capturing", lambda stream: stream.capturing)
 
 
 def call(needs, body=None):
@@ -33,8 +33,10 @@ def call(needs, body=None):
     return trellis_fake
 
 
-def launch(fn, needs, handle=1, ask=False):
-    binding._launch(fn, (), 0, Stream(handle), lambda: needs, ask=ask)
+def launch(fn, needs, handle=1, ask=False, capturing=False):
+    stream = Stream(handle)
+    stream.capturing = capturing
+    binding._launch(fn, (), 0, stream, lambda: needs, ask=ask)
     return fn.taken[-1]
 
 
@@ -93,3 +95,32 @@ def test_a_buffer_in_use_is_not_replaced():
     launch(call(100, body), 100)
     t.join()
     assert alive == [True] and binding._ws_cache[(0, 1)].size >= 9000
+
+
+@pytest.mark.parametrize("ask", [False, True])
+def test_a_captured_buffer_outlives_its_growth(ask):
+    """What a graph was captured with stays allocated when a later call needs more; what none was, does not."""
+    launch(call(100), 100, ask=ask)
+    plain = weakref.ref(binding._ws_cache[(0, 1)].buf)
+    launch(call(1000), 1000, ask=ask)
+    gc.collect()
+    assert plain() is None
+    ws = binding._ws_cache[(0, 1)]
+    captured, taken = weakref.ref(ws.buf), ws.ptr
+    assert launch(call(1000), 1000, ask=ask, capturing=True)[0] == taken
+    for n in (5000, 20000):                                # the second one outgrows a buffer that no graph has
+        assert launch(call(n), n, ask=ask)[0] != taken
+    gc.collect()
+    assert captured() is not None and captured().data_ptr() == taken and len(ws.kept) == 1
+
+
+@pytest.mark.parametrize("ask", [False, True])
+def test_a_buffer_made_during_a_capture_is_the_graphs_alone(ask):
+    """Its zero-fill runs in replays only, so no call outside the graph may get it."""
+    inside = launch(call(1000), 1000, ask=ask, capturing=True)
+    ws = binding._ws_cache[(0, 1)]
+    assert inside[1] >= 1000 and ws.buf is None and ws.size == 0 and not ws.in_graph
+    launch(call(1000), 1000, ask=ask)
+    before = ws.ptr
+    launch(call(9000), 9000, ask=ask, capturing=True)
+    assert ws.ptr == before and ws.size < 9000

@@ -158,16 +158,26 @@ class _Workspace:
     enqueued before it are done: no host synchronisation.  One buffer per stream also keeps calls on
     different streams off each other's counters and partial sums.  Calls of several host threads on
     one stream take turns: a call may enqueue two kernels that hand data on in the workspace, and
-    the buffer must not be replaced between the look at it and the launch."""
-    __slots__ = ("lock", "buf", "ptr", "size")
+    the buffer must not be replaced between the look at it and the launch.
+
+    A captured call's replays use the buffer that it was captured with, so one that is in a graph is
+    kept for good when it is outgrown.  A call that needs a new buffer while it is captured takes one
+    of the graph's own memory, zero-filled by every replay, which no other call gets."""
+    __slots__ = ("lock", "buf", "ptr", "size", "in_graph", "kept")
 
     def __init__(self):
         self.lock = threading.Lock()
         self.buf, self.ptr, self.size = None, None, 0
+        self.in_graph, self.kept = False, []
 
-    def grow(self, nbytes, index, stream):
+    def grow(self, nbytes, index, stream, capturing):
+        """A buffer of at least nbytes; the caller holds it until its launch."""
         buf = _zeros(max(nbytes, 256), index, stream)
-        self.buf, self.ptr, self.size = buf, buf.data_ptr(), buf.numel()
+        if not capturing:
+            if self.in_graph:
+                self.kept.append(self.buf)
+            self.buf, self.ptr, self.size, self.in_graph = buf, buf.data_ptr(), buf.numel(), False
+        return buf
 
 
 _ws_cache: dict = {}
@@ -179,6 +189,14 @@ def _zeros(nbytes, index, stream):
         return torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
 
 
+def _is_capturing(stream):
+    is_capturing = (_types or _torch_types())[7]
+    if stream is None:
+        return is_capturing()
+    with _torch().cuda.stream(stream):
+        return is_capturing()
+
+
 def _launch(fn, args, index, stream, need, ask=True):
     """fn(*args, workspace, its bytes, stream) with the stream's workspace.  need() is the size of it; with ask=False
     it is not looked up unless the call refuses the workspace at hand."""
@@ -186,12 +204,15 @@ def _launch(fn, args, index, stream, need, ask=True):
     ws = _ws_cache.get((index, handle)) or _ws_cache.setdefault((index, handle), _Workspace())
     least = max(need(), 256) if ask else 0
     with ws.lock:
-        if ws.size < least:
-            ws.grow(least, index, stream)
-        rc = fn(*args, ws.ptr, ws.size, handle)
-        if rc == -7 and not ask:
-            ws.grow(need(), index, stream)
+        capturing = _is_capturing(stream)
+        rc = -7
+        if ws.size >= least:
+            if capturing and ws.buf is not None:
+                ws.in_graph = True
             rc = fn(*args, ws.ptr, ws.size, handle)
+        if rc == -7:
+            buf = ws.grow(least or need(), index, stream, capturing)
+            rc = fn(*args, buf.data_ptr(), buf.numel(), handle)
     _check(rc, fn.__name__)
 
 
@@ -339,12 +360,12 @@ _types = None
 
 
 def _torch_types():
-    """Tensor, bfloat16, float32, int32, float8_e4m3fn, empty, the current stream's handle."""
+    """Tensor, bfloat16, float32, int32, float8_e4m3fn, empty, the current stream's handle and whether it is capturing."""
     global _types
     if _types is None:
         torch = _torch()
         _types = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.empty,
-                  torch._C._cuda_getCurrentRawStream)
+                  torch._C._cuda_getCurrentRawStream, torch.cuda.is_current_stream_capturing)
     return _types
 
 
@@ -371,7 +392,7 @@ def _require_on(t, name, dtype, ndim, index):
 
 def _require_cache(cache, starts, kv_len, pages):
     """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns, device index)."""
-    Tensor, _, f32, i32, f8, _, _ = _types or _torch_types()
+    Tensor, _, f32, i32, f8 = (_types or _torch_types())[:5]
     k, v, ks, vs = cache
     if not isinstance(k, Tensor) or (index := k.get_device()) < 0:
         raise ValueError("the cache must be CUDA tensors")
@@ -488,7 +509,7 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
     input; a: bf16 [adapters, R, K]; b: bf16 [adapters, N, R]; scales: float32 [adapters].
     starts int32 [S + 1]: the rows of each request; which int32 [S]: its adapter, -1 for none.
     out may be y."""
-    Tensor, bf16, f32, i32, _, _, _ = _types or _torch_types()
+    Tensor, bf16, f32, i32 = (_types or _torch_types())[:4]
     if not isinstance(y, Tensor):
         raise ValueError("y must be a CUDA tensor")
     dev, index = y.device, y.get_device()
