@@ -216,6 +216,27 @@ def _launch(fn, args, index, stream, need, ask=True):
     _check(rc, fn.__name__)
 
 
+def _empty(shape, dtype, index, stream):
+    """A result for a call on `stream` (None: the current one).  Memory that the current stream may still be using
+    is not given to a call on another, and what it gets is not handed on before the current stream is done with it."""
+    torch = _torch()
+    device = f"cuda:{index}"
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(index))
+    return out
+
+
+def _used_on(stream, *tensors):
+    """What the tensors hold is not given to others before the work that `stream` has by then is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def decode(codes, scales, K: int, k: int, L: int = 12, T: int = 256, out=None, stream=None):
     """Dense bf16 weights [N, K] from packed codes [N, K*k/32] and bf16 scales [N]."""
     torch = _torch()
@@ -225,13 +246,14 @@ def decode(codes, scales, K: int, k: int, L: int = 12, T: int = 256, out=None, s
     if codes.shape[1] * 32 != K * k or scales.numel() != N:
         raise ValueError("codes must be [N, K*k/32] and scales [N]")
     if out is None:
-        out = torch.empty((N, K), dtype=torch.bfloat16, device=codes.device)
+        out = _empty((N, K), torch.bfloat16, codes.get_device(), stream)
     _require(out, "out", (torch.bfloat16,), 2)
     if tuple(out.shape) != (N, K):
         raise ValueError("out must be [N, K]")
     rc = abi_decode(codes.data_ptr(), scales.data_ptr(), K, N, k, L, T, out.data_ptr(),
                     _stream_handle(codes.device, stream))
     _check(rc, "trellis_decode")
+    _used_on(stream, codes, scales, out)
     return out
 
 
@@ -246,12 +268,13 @@ def gemm(x, codes, scales, k: int, L: int = 12, T: int = 256, out=None, stream=N
     if codes.shape[1] * 32 != K * k or scales.numel() != N:
         raise ValueError("codes must be [N, K*k/32] and scales [N]")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, N), torch.bfloat16, x.get_device(), stream)
     _require(out, "out", (torch.bfloat16,), 2)
     if tuple(out.shape) != (M, N):
         raise ValueError("out must be [M, N]")
     _launch(load().trellis_gemm_ws, (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, K, N, k, L, T, out.data_ptr()),
             x.get_device(), stream, lambda: gemm_workspace_bytes(M, K, N, k, L, T))
+    _used_on(stream, x, codes, scales, out)
     return out
 
 
@@ -270,15 +293,13 @@ def gemm_gateup(x, codes_gate, scales_gate, codes_up, scales_up, k: int, act: bo
         raise ValueError("codes_gate and codes_up must both be [N, K*k/32]")
     if scales_gate.numel() != N or scales_up.numel() != N:
         raise ValueError("scales must be [N]")
-    g = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    u = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    a = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if act else None
+    g, u, a = (_empty((M, N), torch.bfloat16, x.get_device(), stream) if wanted else None for wanted in (True, True, act))
     _launch(load().trellis_gemm_gateup, (x.data_ptr(), codes_gate.data_ptr(), scales_gate.data_ptr(), codes_up.data_ptr(),
                                          scales_up.data_ptr(), M, K, N, k, L, T, g.data_ptr(), u.data_ptr(),
                                          a.data_ptr() if act else None),
             x.get_device(), stream, lambda: gemm_gateup_workspace_bytes(M, K, N, k, L, T))
+    _used_on(stream, x, codes_gate, scales_gate, codes_up, scales_up, g, u, a)
     return g, u, a
-
 
 
 def gemm_packed(xs, codes, scales, k: int, L: int = 12, T: int = 256, outs=None, stream=None):
@@ -298,7 +319,7 @@ def gemm_packed(xs, codes, scales, k: int, L: int = 12, T: int = 256, outs=None,
         raise ValueError("every x must be [rows, K] with codes [N, K*k/32] and scales [N]")
     rows = [int(x.shape[0]) for x in xs]
     if outs is None:
-        outs = [torch.empty((r, N), dtype=torch.bfloat16, device=xs[0].device) for r in rows]
+        outs = [_empty((r, N), torch.bfloat16, xs[0].get_device(), stream) for r in rows]
     for i, (o, r) in enumerate(zip(outs, rows)):
         _require(o, f"outs[{i}]", (torch.bfloat16,), 2)
         if tuple(o.shape) != (r, N):
@@ -308,6 +329,7 @@ def gemm_packed(xs, codes, scales, k: int, L: int = 12, T: int = 256, outs=None,
     rp = (ctypes.c_int * len(rows))(*rows)
     _launch(load().trellis_gemm_packed, (xp, rp, len(rows), codes.data_ptr(), scales.data_ptr(), K, N, k, L, T, op),
             xs[0].get_device(), stream, lambda: gemm_packed_workspace_bytes(rows, K, N, k, L, T))
+    _used_on(stream, *xs, codes, scales, *outs)
     return outs
 
 
@@ -339,11 +361,14 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, stretch: float =
     torch = _torch()
     if not isinstance(positions, int) or positions < 1 or not isinstance(rot, int) or rot < 1:
         raise ValueError("positions and rot must be positive ints")
-    table = torch.empty((positions, rot), dtype=torch.float32, device=device)
-    if not table.is_cuda:
+    device = torch.device(device)
+    if device.type != "cuda":
         raise ValueError("device must be a CUDA device")
+    index = torch.cuda.current_device() if device.index is None else device.index
+    table = _empty((positions, rot), torch.float32, index, stream)
     _check(load().trellis_rope_table(table.data_ptr(), positions, rot, base, stretch, float(original), low, high, gain,
-                                     _stream_handle(table.device, stream)), "trellis_rope_table")
+                                     _raw_stream(index, stream)), "trellis_rope_table")
+    _used_on(stream, table)
     return table
 
 
@@ -414,10 +439,10 @@ def _require_cache(cache, starts, kv_len, pages):
     return shape, seqs, cols, index
 
 
-def _output(out, name, shape, index, device):
+def _output(out, name, shape, index, device, stream):
     types = _types or _torch_types()
     if out is None:
-        return types[5](shape, dtype=types[1], device=device)
+        return types[5](shape, dtype=types[1], device=device) if stream is None else _empty(shape, types[1], index, stream)
     if not isinstance(out, types[0]) or out.shape != shape or out.dtype != types[1] or out.get_device() != index \
             or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bfloat16 {tuple(shape)} tensor on cuda:{index}")
@@ -446,7 +471,7 @@ def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved
         hq = q_shape[1]
         if q_shape[0] != tokens or q_shape[2] != d:
             raise ValueError(f"q must be [{tokens}, heads, {d}]")
-        q_out = _output(q_out, "q_out", q_shape, index, k.device)
+        q_out = _output(q_out, "q_out", q_shape, index, k.device, stream)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -461,6 +486,8 @@ def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved
         pages.data_ptr(), tokens, seqs, tokens if max_q is None else max_q, cols, num_pages, hq, hk, d, page, rope_ptr, rows,
         rot, 1 if interleaved else 0, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
         out_ptr, _raw_stream(index, stream)), "trellis_kv_append")
+    if stream is not None:
+        _used_on(stream, *cache, k, v, q, starts, kv_len, pages, rope, q_out)
     return q_out
 
 
@@ -483,7 +510,7 @@ def kv_attention(q, cache, starts, kv_len, pages, scale=None, window: int = 0, m
     if shape[2] != d:
         raise ValueError(f"q must be [tokens, heads, {d}]")
     dev = q.device
-    out = _output(out, "out", shape, index, dev)
+    out = _output(out, "out", shape, index, dev, stream)
     if seqs == 0 or tokens == 0:
         return out
     most = tokens if max_q is None else max_q
@@ -492,6 +519,8 @@ def kv_attention(q, cache, starts, kv_len, pages, scale=None, window: int = 0, m
              num_pages, hq, hk, d, page, d ** -0.5 if scale is None else scale, window, cache[0].data_ptr(),
              cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), out.data_ptr()),
             index, stream, lambda: kv_attention_workspace_bytes(tokens, seqs, most, hq, hk, d), ask=False)
+    if stream is not None:
+        _used_on(stream, q, *cache, starts, kv_len, pages, out)
     return out
 
 
@@ -525,11 +554,13 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
         raise ValueError("y must be [M, N], x [M, K], a [adapters, R, K], b [adapters, N, R] and scales [adapters]")
     if n != segments + 1:
         raise ValueError("starts must be [S + 1] with which [S]")
-    out = _output(out, "out", shape, index, dev)
+    out = _output(out, "out", shape, index, dev, stream)
     if M == 0:
         return out
     _launch((_lib or load()).trellis_lora_add,
             (y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), starts.data_ptr(),
              which.data_ptr(), M, K, N, R, n_ad, segments, out.data_ptr()),
             index, stream, lambda: lora_add_workspace_bytes(M, K, N, R, n_ad, segments), ask=False)
+    if stream is not None:
+        _used_on(stream, y, x, a, b, scales, starts, which, out)
     return out
