@@ -1,4 +1,5 @@
 """The binding's workspaces on the host: a fake of the library's call and CPU buffers, no GPU."""
+import contextlib
 import gc
 import threading
 import time
@@ -15,10 +16,24 @@ class Stream:
         self.cuda_stream, self.capturing = handle, False
 
 
+device = [0]                                               # of the thread
+
+
+@contextlib.contextmanager
+def on_device(index):
+    device.append(index)
+    try:
+        yield
+    finally:
+        device.pop()
+
+
 @pytest.fixture(autouse=True)
 def host(monkeypatch):
     monkeypatch.setattr(binding, "_ws_cache", {})
     monkeypatch.setattr(binding, "_zeros", lambda nbytes, index, stream: torch.zeros(nbytes, dtype=torch.uint8))
+    monkeypatch.setattr(binding, "_current_device", lambda: device[-1])
+    monkeypatch.setattr(binding, "_on_device", on_device)
     monkeypatch.setattr(binding, "_is_capturing", lambda stream: stream.capturing)
 
 
@@ -124,3 +139,31 @@ def test_a_buffer_made_during_a_capture_is_the_graphs_alone(ask):
     before = ws.ptr
     launch(call(9000), 9000, ask=ask, capturing=True)
     assert ws.ptr == before and ws.size < 9000
+
+
+def test_calls_run_on_the_tensors_device():
+    """The library launches on the thread's current device: a call whose tensors are elsewhere changes it meanwhile."""
+    seen = []
+
+    def trellis_fake(ptr, size, handle):
+        seen.append(device[-1])
+        return 0 if size >= 1000 else -7
+
+    def trellis_plain(a, handle):
+        seen.append((device[-1], a, handle))
+        return 0
+    sizes = []
+    for index in (1, 0, 3):
+        for ask in (False, True):
+            binding._launch(trellis_fake, (), index, Stream(5), lambda: sizes.append(device[-1]) or 1000, ask=ask)
+        binding._enqueue(trellis_plain, (7,), index, Stream(5))
+        assert [s if isinstance(s, int) else s[0] for s in seen] == [index] * len(seen) and (index, 7, 5) in seen
+        assert sizes == [index] * len(sizes) and device == [0]
+        seen.clear()
+        sizes.clear()
+    assert sorted(k[0] for k in binding._ws_cache) == [0, 1, 3]
+    with pytest.raises(binding.TrellisError, match="trellis_plain"):
+        def trellis_plain(handle):
+            return -5
+        binding._enqueue(trellis_plain, (), 1, Stream(5))
+    assert device == [0]

@@ -134,12 +134,6 @@ def _torch():
     return torch
 
 
-def _stream_handle(device, stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
-
-
 def _require(t, name, dtypes, ndim):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -189,6 +183,22 @@ def _zeros(nbytes, index, stream):
         return torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
 
 
+def _current_device():
+    return (_types or _torch_types())[8]()
+
+
+def _on_device(index):
+    return _torch().cuda.device(index)
+
+
+def _enqueue(fn, args, index, stream):
+    """fn(*args, stream) on the tensors' device, as _launch: the library launches on the thread's current device."""
+    if _current_device() != index:
+        with _on_device(index):
+            return _enqueue(fn, args, index, stream)
+    _check(fn(*args, _raw_stream(index, stream)), fn.__name__)
+
+
 def _is_capturing(stream):
     is_capturing = (_types or _torch_types())[7]
     if stream is None:
@@ -200,6 +210,9 @@ def _is_capturing(stream):
 def _launch(fn, args, index, stream, need, ask=True):
     """fn(*args, workspace, its bytes, stream) with the stream's workspace.  need() is the size of it; with ask=False
     it is not looked up unless the call refuses the workspace at hand."""
+    if _current_device() != index:
+        with _on_device(index):
+            return _launch(fn, args, index, stream, need, ask)
     handle = _raw_stream(index, stream)
     ws = _ws_cache.get((index, handle)) or _ws_cache.setdefault((index, handle), _Workspace())
     least = max(need(), 256) if ask else 0
@@ -250,9 +263,8 @@ def decode(codes, scales, K: int, k: int, L: int = 12, T: int = 256, out=None, s
     _require(out, "out", (torch.bfloat16,), 2)
     if tuple(out.shape) != (N, K):
         raise ValueError("out must be [N, K]")
-    rc = abi_decode(codes.data_ptr(), scales.data_ptr(), K, N, k, L, T, out.data_ptr(),
-                    _stream_handle(codes.device, stream))
-    _check(rc, "trellis_decode")
+    _enqueue(load().trellis_decode, (codes.data_ptr(), scales.data_ptr(), K, N, k, L, T, out.data_ptr()), codes.get_device(),
+             stream)
     _used_on(stream, codes, scales, out)
     return out
 
@@ -366,8 +378,8 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, stretch: float =
         raise ValueError("device must be a CUDA device")
     index = torch.cuda.current_device() if device.index is None else device.index
     table = _empty((positions, rot), torch.float32, index, stream)
-    _check(load().trellis_rope_table(table.data_ptr(), positions, rot, base, stretch, float(original), low, high, gain,
-                                     _raw_stream(index, stream)), "trellis_rope_table")
+    _enqueue(load().trellis_rope_table, (table.data_ptr(), positions, rot, base, stretch, float(original), low, high, gain),
+             index, stream)
     _used_on(stream, table)
     return table
 
@@ -385,12 +397,13 @@ _types = None
 
 
 def _torch_types():
-    """Tensor, bfloat16, float32, int32, float8_e4m3fn, empty, the current stream's handle and whether it is capturing."""
+    """Tensor, bfloat16, float32, int32, float8_e4m3fn, empty, the current stream's handle, whether it is capturing,
+    and the current device."""
     global _types
     if _types is None:
         torch = _torch()
         _types = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.empty,
-                  torch._C._cuda_getCurrentRawStream, torch.cuda.is_current_stream_capturing)
+                  torch._C._cuda_getCurrentRawStream, torch._C._cuda_isCurrentStreamCapturing, torch._C._cuda_getDevice)
     return _types
 
 
@@ -481,11 +494,11 @@ def kv_append(cache, k, v, starts, kv_len, pages, q=None, rope=None, interleaved
         rope_ptr = rope.data_ptr()
     if seqs == 0 or tokens == 0:
         return q_out
-    _check((_lib or load()).trellis_kv_append(
-        q_ptr, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, starts.data_ptr(), kv_len.data_ptr(),
-        pages.data_ptr(), tokens, seqs, tokens if max_q is None else max_q, cols, num_pages, hq, hk, d, page, rope_ptr, rows,
-        rot, 1 if interleaved else 0, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
-        out_ptr, _raw_stream(index, stream)), "trellis_kv_append")
+    _enqueue((_lib or load()).trellis_kv_append,
+             (q_ptr, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, starts.data_ptr(), kv_len.data_ptr(),
+              pages.data_ptr(), tokens, seqs, tokens if max_q is None else max_q, cols, num_pages, hq, hk, d, page, rope_ptr,
+              rows, rot, 1 if interleaved else 0, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+              cache[3].data_ptr(), out_ptr), index, stream)
     if stream is not None:
         _used_on(stream, *cache, k, v, q, starts, kv_len, pages, rope, q_out)
     return q_out
