@@ -1063,7 +1063,7 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
             }
             if (last) break;
         }
-        // the CTA that leaves last puts the counters back
+        // the CTA that leaves last puts the counters back; every planner comes here, by a wait that gave up too
         if (!shares && lane == 0 && atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
             a.counters[0] = 0u;
             a.counters[1] = 0u;
