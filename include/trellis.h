@@ -182,7 +182,8 @@ TRELLIS_API int trellis_gemm_ws(const uint16_t *x, const uint32_t *codes, const 
  * device-side wait of the tensor-core product, or of trellis_kv_attention,
  * gave up since the last query (TRELLIS_ERR_TIMEOUT; the affected outputs are
  * undefined, workspaces are as ready for their next call as after any other) or
- * not (TRELLIS_OK).  Clears the flag.  A wait gives up after 2 s of wall-clock time; the kernel then waits (bounded the same way) for its own copies and
+ * not (TRELLIS_OK).  Clears the flag.  A wait gives up after 2 s of wall-clock
+ * time; the kernel then waits (bounded the same way) for its own copies and
  * tensor-core operations still in flight, releases its tensor memory and
  * returns, so the context stays usable.  The flag is one word per device,
  * shared by every stream and every caller on that device: a timeout on any

@@ -43,7 +43,8 @@ class Packed(NamedTuple):
 
 
 class AttentionBlock:
-    """q_heads and kv_heads of head_dim over hidden features; k bits a weight."""
+    """q_heads and kv_heads of head_dim over hidden features; k bits a weight; contexts of up to `positions` tokens
+    (later ones would be rotated as the last)."""
 
     def __init__(self, hidden, q_heads, kv_heads, head_dim, k=4, adapters=4, rank=16, positions=32768, device="cuda",
                  seed=0):
@@ -92,9 +93,10 @@ def main(argv=None):
     args = ap.parse_args(argv)
 
     dev, S = "cuda", args.requests
-    block = AttentionBlock(args.hidden, args.q_heads, args.kv_heads, args.head_dim)
     new = [max(1, args.prompt * (s + 1) // S) for s in range(S)]
-    cols = (max(new) + args.steps + 4 + args.page - 1) // args.page
+    longest = max(new) + args.steps + 1                                   # one step runs before the capture
+    block = AttentionBlock(args.hidden, args.q_heads, args.kv_heads, args.head_dim, positions=longest)
+    cols = -(-longest // args.page)
     pages = torch.randperm(S * cols, device=dev).int().view(S, cols)
     cache = kv_cache(S * cols, args.kv_heads, args.page, args.head_dim)
     which = torch.arange(S, device=dev).remainder(5).int() - 1            # every fifth request has none
