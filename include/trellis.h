@@ -416,7 +416,8 @@ TRELLIS_API int trellis_kv_attention(const uint16_t *q, long long q_stride, cons
                                      const float *v_scales, uint16_t *out, void *workspace, size_t workspace_bytes,
                                      cudaStream_t stream);
 
-/* Bytes of workspace trellis_kv_attention needs on the current device. */
+/* Bytes of workspace trellis_kv_attention needs on the current device.  It may be larger for a
+ * smaller call (few units are cut into parts, many are not): ask for each kind of step. */
 TRELLIS_API int trellis_kv_attention_workspace_size(int tokens, int seqs, int max_q, int q_heads, int kv_heads,
                                                     int head_dim, size_t *bytes);
 
@@ -435,6 +436,8 @@ TRELLIS_API int trellis_kv_attention_workspace_size(int tokens, int seqs, int ma
  *           the rows of y pass unchanged.
  *   workspace  256-byte aligned, at least trellis_lora_add_workspace_size bytes;
  *           its first 1 MiB is not touched, so a product's workspace will do.
+ * h = s x A^T enters the second product as two bf16 terms (16 significant bits), so an
+ * infinite entry of b gives NaN; infinities of x and y come out as the formula has them.
  * M <= 65536 (0: nothing is enqueued), segments <= 65536.  Sums are fp32, with one
  * rounding of the result, in an order that the sizes fix.  Two kernels are enqueued.
  */

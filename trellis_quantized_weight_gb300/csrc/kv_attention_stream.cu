@@ -6,8 +6,8 @@
 //
 // What bounds it: 2 D bytes of codes a cached token and key head, each read once
 // and used by the head group's few rows, so HBM.  Measured at D = 128, 8 key heads (GPU time;
-// the least bytes at 6.69 TB/s): one sequence of 131071 tokens 54 us (40); 64 of 1 to 16384
-// 170 us (153), 6.0 TB/s, at about 7.5 TB/s between the start (5 us of dependent first loads)
+// the least bytes at 6.69 TB/s): one sequence of 131071 tokens 55 us (40); 64 of 1 to 16384
+// 172 us (153), 6.0 TB/s, at about 7.5 TB/s between the start (5 us of dependent first loads)
 // and the joins; one of 777 tokens 8.5 us (0.2), which is start and joins alone.  With 9
 // to 16 rows a unit the products' instructions take over: 16 x 300 to 9000 tokens, 8 rows
 // 43 us, 16 rows 59.  Everything else is arranged around a long stream of 16-byte loads:

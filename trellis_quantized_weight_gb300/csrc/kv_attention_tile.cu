@@ -40,9 +40,9 @@
 // scheduler, and an item costs 10 to 14 thousand clocks of its own (queries, first and last
 // products, result).  Measured (GPU time; the least bytes or operations at 6.69 TB/s and
 // 1951 TFLOP/s): chunks of 4 x 2048 tokens on contexts of 4100 to 9001, 32 / 8 heads of 128:
-// 664 us (351), 1.03 PFLOP/s; 6 prompts of 130 to 4099 tokens, window 1024, 24 / 8 heads of 64:
+// 672 us (351), 1.02 PFLOP/s; 6 prompts of 130 to 4099 tokens, window 1024, 24 / 8 heads of 64:
 // 157 us (31), where a row-tile has half of the products to the same softmax; 16 x 5 drafts on
-// contexts of 300 to 9000, 32 / 4 heads of 256: 71 us (23), one query tile of 40 rows, so that
+// contexts of 300 to 9000, 32 / 4 heads of 256: 70 us (23), one query tile of 40 rows, so that
 // nothing runs beside its chain.
 //
 // Waits are bounded as in gemm_tc_kernel.cu: one that gives up sets the device error
@@ -63,7 +63,7 @@ namespace {
 // weights under 2^-25 vanish in f16 but count in the denominators: N tokens then lose at most
 // N 2^-(25 + below) of the largest weight, and below = log2(N) - kNear, rounded up, keeps that
 // under 2^-14 up to 2^21 tokens.  Units of up to 2^11 tokens need none.  (Chunks 663 us without it,
-// 670 so; 677, 683, 690, 699 with 4 to 7 at every length.)
+// 670 to 672 so; 677, 683, 690, 699 with 4 to 7 at every length.)
 constexpr float kMoveBy = 15.9f;
 constexpr int kNear = 11, kFarBelow = 10;
 constexpr int kRows = 128;               // query rows of a tile (lanes of tensor memory)

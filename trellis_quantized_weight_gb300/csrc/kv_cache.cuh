@@ -16,7 +16,6 @@
 namespace trellis {
 
 constexpr int kKvBlock = 16;             // tokens that share a scale
-constexpr float kE4m3Max = 448.0f;
 
 // What both cache operators read on the device to find their tokens.
 struct KvLayout {
@@ -112,9 +111,6 @@ __device__ __forceinline__ float pow2_recip_finite(float s) {
 // ---- asynchronous copies and small matrix products ----------------------------------
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");

@@ -27,7 +27,7 @@
 //   rounding of the result.
 // * Rows are cut into tiles inside each request's rows.  A warp of the first kernel takes
 //   a tile's 16, 32 or 64 rows by all of the rank and a share of K of its own, so that no
-//   two warps read the same.  In the second kernel's tiles of 128 rows the warps, 16 rows
+//   two warps read the same.  In the second kernel's tiles of 64 rows the warps, 16 rows
 //   each, share B's columns.
 // * The first kernel lets the second start once all of its blocks run, after its own wait
 //   for what came before: so the second may find its tile and fetch y and B while the
