@@ -449,6 +449,114 @@ TRELLIS_API int trellis_lora_add(const uint16_t *y, const uint16_t *x, const uin
 /* Bytes of workspace trellis_lora_add needs on the current device. */
 TRELLIS_API int trellis_lora_add_workspace_size(int M, int K, int N, int R, int adapters, int segments, size_t *bytes);
 
+/* ---- pages handed out on the device ---------------------------------------------------
+ *
+ *   refs    device, int32 [num_pages]: how many places of the table name each page; 0 is free.
+ *           A new pool is all zeros.  A page that something else holds is kept from these calls
+ *           by counting it once more.
+ *   kv_len, pages  as above; the table names a sequence's pages in its first
+ *           ceil(kv_len / page_size) columns, the other columns mean nothing.
+ * Free pages are handed out lowest first, to sequences in their order; those that a call gives
+ * back are free from the next call on.  So the results are one function of the arrays, and the
+ * calls can be captured and replayed.  Table entries outside the pool are not counted.
+ * Accepted: 1 <= seqs <= 16384; num_pages and page_cols up to 2^24; page_size 16, 32, 64 or 128.
+ *   ok      device, uint8 [seqs]: 1 where the sequence got what it asked for.
+ *   workspace  256-byte aligned, at least trellis_kv_pages_workspace_size bytes; its first 1 MiB
+ *           is not touched, so a product's workspace will do.
+ * The three return TRELLIS_ERR_NULL, _SHAPE, _UNSUPPORTED, _ALIGN and _WORKSPACE as the other
+ * cache operators do.
+ */
+
+/*
+ * trellis_kv_grow - sequence s gets grow[s] more tokens (kv_len += grow), and the pages that they
+ * need; a negative count drops its last tokens (all of them if there are not so many) and gives
+ * back the pages that hold nothing then.
+ * Not served, with everything of it left as it was: a sequence that would need more columns than
+ * the table has, or 2^31 tokens; one whose pages, after those of the sequences before it (served
+ * or not), are more than the free ones; one that would be cut inside a page that is counted more
+ * than once (its next token would be written for the others too).  A sequence that needs no page
+ * is always served.  One kernel is enqueued.
+ */
+TRELLIS_API int trellis_kv_grow(int *refs, int *kv_len, int *pages, const int *grow, int seqs, int page_cols,
+                                int num_pages, int page_size, uint8_t *ok, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/*
+ * trellis_kv_fork - sequence s goes on as a continuation of sequence parents[s] as it was, for all s
+ * at once: samples of one prompt, beams in a new order, ended requests.
+ *   parents[s] == s    it stays as it is.
+ *   parents[s] < 0     it ends: kv_len 0, its pages given back.
+ *   otherwise          it takes the parent's length and pages.  Whole pages are shared; a last page that
+ *                      is not full stays with the parent itself, or else with the first of its
+ *                      continuations, and the others get a copy (of the blocks of 16 that hold tokens) in
+ *                      a free page.
+ * The pages that s had before are given back.  Not served: a sequence for which no free page is left,
+ * or whose parents[s] is past the last sequence; it ends.  Two kernels are enqueued.
+ */
+TRELLIS_API int trellis_kv_fork(int *refs, int *kv_len, int *pages, const int *parents, int seqs, int page_cols,
+                                int num_pages, int page_size, int kv_heads, int head_dim, uint8_t *k_codes,
+                                uint8_t *v_codes, float *k_scales, float *v_scales, uint8_t *ok, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * trellis_kv_compact - the pages in use, in their order, become pages 0, 1, 2, .. of another cache of
+ * num_pages_out pages, and the counts, lengths and table go with them.
+ *   refs_out   int32 [num_pages_out]; kv_len_out int32 [seqs]; pages_out int32 [seqs, page_cols], 0 past a
+ *              sequence's pages.
+ * Pages that the other cache has no room for are left behind; the sequences that name one come out with
+ * kv_len 0, no longer counted.  Pages past the last one in use are left as they were.  No output may
+ * overlap an input or another output (TRELLIS_ERR_SHAPE).  Two kernels are enqueued.
+ */
+TRELLIS_API int trellis_kv_compact(const int *refs, const int *kv_len, const int *pages, int seqs, int page_cols,
+                                   int num_pages, int page_size, int kv_heads, int head_dim, const uint8_t *k_codes,
+                                   const uint8_t *v_codes, const float *k_scales, const float *v_scales,
+                                   int num_pages_out, uint8_t *k_codes_out, uint8_t *v_codes_out, float *k_scales_out,
+                                   float *v_scales_out, int *refs_out, int *kv_len_out, int *pages_out, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace that each of the three takes at most. */
+TRELLIS_API int trellis_kv_pages_workspace_size(int seqs, int page_cols, int num_pages, size_t *bytes);
+
+/* ---- from one projection to the next ---------------------------------------------------- */
+
+/*
+ * trellis_rms_norm - h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, a row at a time.
+ *
+ *   x       device, bf16; `rows` tokens `x_stride` elements apart, each of `heads` rows of `width`
+ *           values side by side (heads of a projection's output; heads = 1 for plain rows).
+ *   residual      bf16 [rows * heads, width], or NULL (then residual_out is NULL too).
+ *   weight        bf16 [width].
+ *   out           bf16 [rows * heads, width], or NULL with
+ *   codes, scales e4m3 bytes [rows * heads, width] and float [rows * heads]: y = code * scale, with the
+ *                 scale max(max|y| / 448, 2^-100) of each row.  A row of y that is not finite has a NaN scale.
+ *   residual_out  bf16 [rows * heads, width]: h, rounded once.
+ * y is computed from h before its rounding, sums are fp32.  out or residual_out may be x (where that is
+ * contiguous) or residual, but not each other; other overlaps are not allowed.  Any width up to 2^20;
+ * widths and strides that are multiples of 8, with 16-byte aligned arrays, take wide accesses.
+ * rows == 0 enqueues nothing.  One kernel is enqueued.
+ */
+TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const uint16_t *residual,
+                                 const uint16_t *weight, int rows, int heads, int width, float eps, uint16_t *out,
+                                 uint8_t *codes, float *scales, uint16_t *residual_out, cudaStream_t stream);
+
+/*
+ * trellis_gemm_q4 - out[m, n] = sum_k x[m, k] w[n, k] with 4-bit weights in groups of `group` along k.
+ *
+ *   codes   device, uint32 [N, K / 8], 16-byte aligned: eight codes c a word, the first in the lowest bits.
+ *   scales  device, bf16 [N, K / group]; biases the same, or NULL.
+ *           w = scale * c + bias, or scale * (c - 8) without biases.
+ *   x       device, 16-byte aligned: bf16 [M, K] (x_scales NULL), or e4m3 bytes [M, K] with
+ *   x_scales  float [M]: x = code * x_scale, as trellis_rms_norm writes them.
+ *   out     device, bf16 [M, N], rounded once from fp32 sums.
+ * No weight is rounded: c - 8 and x meet exactly, scales and biases are applied to the sums of each group in
+ * fp32.  A row of x that holds an infinity or a NaN has no finite output.
+ * group: 32, 64 or 128; K a multiple of it, K and N up to 2^20, M up to 65536 (0: nothing is enqueued).
+ * The order of all sums is fixed by the sizes.
+ */
+TRELLIS_API int trellis_gemm_q4(const void *x, const float *x_scales, const uint32_t *codes, const uint16_t *scales,
+                                const uint16_t *biases, int M, int K, int N, int group, uint16_t *out,
+                                cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,156 @@
+"""trellis_gemm_q4 against a plain 64-bit implementation on a GB300.
+
+Tolerance, element by element: 2^-8 |ref| + size (1.1 G 2^-23 + (2 groups + 32) 2^-24), with
+size = s_m sum_k |x| (8 |scale| + |bias + 8 scale|).  The first term is the result's rounding.  Products of codes and
+activations are exact; a group's sum takes at most 17 additions for each 16 of its G values, each within 2^-23 of the
+sum of magnitudes; then a multiply-add (two with biases) for each group, and the joins of at most 8 warps and 16 CTAs.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(N, K, group, bias, g):
+    codes = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=g, dtype=torch.int64).int().cuda()
+    scales = ((torch.rand(N, K // group, generator=g) + 0.5) * 0.05).bfloat16().cuda()
+    biases = (-scales.float() * (6 + 3 * torch.rand(N, K // group, generator=g).cuda())).bfloat16() if bias else None
+    return codes, scales, biases
+
+
+def reference(x, codes, scales, biases, x_scales=None):
+    """(the product, the sum of magnitudes) in 64 bits."""
+    N, K = codes.shape[0], codes.shape[1] * 8
+    groups = scales.shape[1]
+    q = torch.stack([(codes.long() >> (4 * i)) & 15 for i in range(8)], -1).view(N, groups, -1).double()
+    s = scales.double()[..., None]
+    b = biases.double()[..., None] if biases is not None else -8 * s
+    w = (s * q + b).view(N, K)
+    x = x.float().double()
+    ref = x @ w.T
+    size = x.abs() @ (8 * s.abs() + (b + 8 * s).abs()).expand(N, groups, K // groups).reshape(N, K).T
+    if x_scales is not None:
+        ref, size = ref * x_scales.double()[:, None], size * x_scales.double().abs()[:, None]
+    return ref, size
+
+
+def check(got, ref, size, group, groups):
+    tol = ref.abs() * 2.0 ** -8 + size * (1.1 * group * 2.0 ** -23 + (2 * groups + 32) * 2.0 ** -24)
+    err = (got.double() - ref).abs()
+    assert got.dtype == torch.bfloat16 and torch.all(err <= tol), ((err - tol).max(), err.max())
+
+
+def run(M, K, N, group, bias, eight, seed=0, offset=0.0):
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(seed)
+    codes, scales, biases = weights(N, K, group, bias, g)
+    x = torch.randn(M, K, generator=g) + offset
+    x_scales = None
+    if eight:
+        x = (x * 100).clamp(-448, 448).to(torch.float8_e4m3fn).cuda()
+        x_scales = (torch.rand(M, generator=g) * 0.02 + 0.001).cuda()
+    else:
+        x = x.bfloat16().cuda()
+    got = tq.gemm_q4(x, codes, scales, biases, x_scales=x_scales)
+    ref, size = reference(x, codes, scales, biases, x_scales)
+    check(got, ref, size, group, K // group)
+    return got
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 31, 33, 64, 65, 130])
+def test_rows(M, group, bias):
+    run(M, 1280, 200, group, bias, M % 2 == 0, seed=M)
+
+
+@pytest.mark.parametrize("K,group", [(32, 32), (64, 64), (96, 32), (128, 128), (160, 32), (192, 64), (384, 128), (4064, 32), (4160, 64), (8320, 128),
+                                     (17408, 64)])
+@pytest.mark.parametrize("M", [1, 12, 40, 200])
+def test_depths(M, K, group):
+    for bias in (False, True):
+        run(M, K, 77, group, bias, bias, seed=K)
+
+
+@pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 127, 129, 1000, 5121])
+@pytest.mark.parametrize("M", [1, 11, 64, 129])
+def test_widths(M, N):
+    run(M, 512, N, 64, True, False, seed=N)
+
+
+@pytest.mark.parametrize("M", [3, 16, 50, 300])
+def test_activations_with_a_mean(M):
+    # the sums of a group are large against its centred part
+    run(M, 2560, 300, 128, True, False, offset=8.0)
+    run(M, 2560, 300, 32, False, True, offset=1.0)
+
+
+@pytest.mark.parametrize("M,K,N,group", [(1, 5120, 17408, 64), (2000, 1024, 1000, 128), (257, 5120, 640, 64)])
+def test_larger(M, K, N, group):
+    run(M, K, N, group, True, False)
+    run(M, K, N, group, False, True)
+
+
+@pytest.mark.parametrize("M", [1, 12, 100])
+def test_every_code(M):
+    """Each code at each place of a word, by one-hot activations: exact but for the result's rounding."""
+    import trellis_quantized_weight_gb300 as tq
+    K, N = 128, 16
+    q = (torch.arange(K)[None] + torch.arange(N)[:, None]) % 16
+    codes = (q.view(N, -1, 8) << (4 * torch.arange(8))).sum(-1)
+    codes = torch.where(codes >= 2 ** 31, codes - 2 ** 32, codes).int().cuda()
+    x = torch.eye(K).bfloat16().cuda()
+    for group in (32, 64, 128):
+        s = torch.full((N, K // group), 0.5).bfloat16().cuda()
+        for k0 in range(0, K, M):
+            rows = x[k0:k0 + M].contiguous()
+            want = 0.5 * (q.T[k0:k0 + M].float() - 8)
+            assert torch.equal(tq.gemm_q4(rows, codes, s).float().cpu(), want)
+            assert torch.equal(tq.gemm_q4(rows, codes, s, s).float().cpu(), want + 4.5)
+
+
+@pytest.mark.parametrize("M", [1, 9, 64, 200])
+def test_rows_that_are_not_finite_stay_alone(M):
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(1)
+    codes, scales, biases = weights(100, 640, 64, True, g)
+    x = torch.randn(M, 640, generator=g).bfloat16().cuda()
+    want = tq.gemm_q4(x, codes, scales, biases)
+    y = x.clone()
+    y[M // 2, 333] = float("inf")
+    y[0, 5] = float("nan")
+    got = tq.gemm_q4(y, codes, scales, biases)
+    for m in range(M):
+        if m in (0, M // 2):
+            assert not got[m].isfinite().any()
+        else:
+            assert torch.equal(got[m], want[m])
+
+
+@pytest.mark.parametrize("M", [1, 11, 64, 300])
+def test_equal_calls_give_equal_bits(M):
+    a, b = run(M, 5120, 1111, 64, True, False, seed=4), run(M, 5120, 1111, 64, True, False, seed=4)
+    assert torch.equal(a, b)
+
+
+def test_no_rows_out_and_refusals():
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(1)
+    codes, scales, biases = weights(48, 256, 64, True, g)
+    x = torch.randn(3, 256).bfloat16().cuda()
+    assert tq.gemm_q4(x[:0], codes, scales).shape == (0, 48)
+    out = torch.empty(3, 48).bfloat16().cuda()
+    assert tq.gemm_q4(x, codes, scales, biases, out=out) is out
+    assert torch.equal(out, tq.gemm_q4(x, codes.view(torch.uint32), scales, biases))
+    x8, xs = tq.rms_norm_q8(x, torch.ones(256).bfloat16().cuda())
+    for bad in (lambda: tq.gemm_q4(x8, codes, scales), lambda: tq.gemm_q4(x, codes, scales, x_scales=xs),
+                lambda: tq.gemm_q4(x8, codes, scales, x_scales=xs[:2]), lambda: tq.gemm_q4(x[:, :128], codes, scales),
+                lambda: tq.gemm_q4(x, codes[:, :16], scales), lambda: tq.gemm_q4(x, codes, scales[:40]),
+                lambda: tq.gemm_q4(x, codes, scales, biases[:, :2]), lambda: tq.gemm_q4(x, codes, scales.float()),
+                lambda: tq.gemm_q4(x.cpu(), codes, scales), lambda: tq.gemm_q4(x, codes.long(), scales),
+                lambda: tq.gemm_q4(x, codes, scales, out=out[:2])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(tq.TrellisError):
+        tq.gemm_q4(x, codes, torch.ones(48, 16).bfloat16().cuda())

@@ -48,6 +48,12 @@ SIGNATURES = {
     "trellis_kv_attention_workspace_size": (_I, [*[_I] * 6, ctypes.POINTER(_SZ)]),
     "trellis_lora_add": (_I, [*[_P] * 7, *[_I] * 6, _P, _P, _SZ, _P]),
     "trellis_lora_add_workspace_size": (_I, [*[_I] * 6, ctypes.POINTER(_SZ)]),
+    "trellis_kv_grow": (_I, [_P, _P, _P, _P, *[_I] * 4, _P, _P, _SZ, _P]),
+    "trellis_kv_fork": (_I, [_P, _P, _P, _P, *[_I] * 6, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "trellis_kv_compact": (_I, [_P, _P, _P, *[_I] * 6, _P, _P, _P, _P, _I, *[_P] * 7, _P, _SZ, _P]),
+    "trellis_kv_pages_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
+    "trellis_rms_norm": (_I, [_P, _LL, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "trellis_gemm_q4": (_I, [_P, _P, _P, _P, _P, *[_I] * 4, _P, _P]),
 }
 
 
@@ -580,4 +586,194 @@ def lora_add(y, x, a, b, scales, starts, which, out=None, stream=None):
             index, stream, lambda: lora_add_workspace_bytes(M, K, N, R, n_ad, segments), ask=False)
     if stream is not None:
         _used_on(stream, y, x, a, b, scales, starts, which, out)
+    return out
+
+
+# ---- pages handed out on the device ------------------------------------------
+def kv_pool(pages: int, device="cuda"):
+    """The counts of a cache's pages, int32 [pages], all free: how many places of the table name each page."""
+    return _torch().zeros(pages, dtype=_torch().int32, device=device)
+
+
+def kv_pages_workspace_bytes(seqs, columns, pages) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().trellis_kv_pages_workspace_size(seqs, columns, pages, ctypes.byref(n)), "trellis_kv_pages_workspace_size")
+    return int(n.value)
+
+
+def _require_codes(cache, name):
+    """Checks a cache's four tensors; returns (codes' shape, device index)."""
+    Tensor, _, f32, _, f8 = (_types or _torch_types())[:5]
+    k, v, ks, vs = cache
+    if not isinstance(k, Tensor) or (index := k.get_device()) < 0:
+        raise ValueError(f"{name} must be CUDA tensors")
+    shape = _require_on(k, f"{name}'s codes", f8, 4, index)
+    want = (shape[0], shape[1], shape[2] // 16)
+    if _require_on(v, f"{name}'s codes", f8, 4, index) != shape or _require_on(ks, f"{name}'s scales", f32, 3, index) != want \
+            or _require_on(vs, f"{name}'s scales", f32, 3, index) != want:
+        raise ValueError(f"{name} must be codes [pages, kv_heads, page_size, head_dim] and scales [pages, kv_heads, page_size / 16]")
+    return shape, index
+
+
+def _require_pool(cache, refs, kv_len, pages):
+    shape, index = _require_codes(cache, "the cache")
+    i32 = _types[3]
+    n, = _require_on(refs, "refs", i32, 1, index)
+    seqs, = _require_on(kv_len, "kv_len", i32, 1, index)
+    rows, cols = _require_on(pages, "pages", i32, 2, index)
+    if n != shape[0] or rows != seqs:
+        raise ValueError(f"refs must be [{shape[0]}], kv_len [S] and pages [S, columns]")
+    return shape, seqs, cols, index
+
+
+def _flags(seqs, index, stream):
+    return _empty((seqs,), _torch().bool, index, stream)
+
+
+def kv_grow(cache, refs, kv_len, pages, grow, stream=None):
+    """Give the sequences grow[s] more tokens (int32 [S]) and the pages they need, or with negative
+    counts drop their last tokens and the pages that hold nothing then.  kv_len, pages and refs are
+    updated in place; call it before kv_append, which takes the new lengths.
+
+    Returns bool [S]: False where a sequence was left as it was, because the free pages (lowest first,
+    to sequences in their order) or the table's columns do not reach, or because it would be cut inside a
+    page that it shares."""
+    (num_pages, _, page, _), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
+    if _require_on(grow, "grow", _types[3], 1, index) != (seqs,):
+        raise ValueError("grow must be [S]")
+    ok = _flags(seqs, index, stream)
+    if seqs == 0:
+        return ok
+    _launch((_lib or load()).trellis_kv_grow,
+            (refs.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), grow.data_ptr(), seqs, cols, num_pages, page, ok.data_ptr()),
+            index, stream, lambda: kv_pages_workspace_bytes(seqs, cols, num_pages), ask=False)
+    if stream is not None:
+        _used_on(stream, refs, kv_len, pages, grow, ok)
+    return ok
+
+
+def kv_fork(cache, refs, kv_len, pages, parents, stream=None):
+    """Every sequence s goes on as a continuation of sequence parents[s] (int32 [S]) as it was before the
+    call: itself for one that stays, -1 for one that ends.  Whole pages are shared and counted; a last page
+    that is not full is copied for all but one of its continuations.  The cache, kv_len, pages and refs are
+    updated in place.
+
+    Returns bool [S]: False where a sequence ended because no free page was left for its copy, or its parent
+    is past the last sequence."""
+    (num_pages, hk, page, d), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
+    if _require_on(parents, "parents", _types[3], 1, index) != (seqs,):
+        raise ValueError("parents must be [S]")
+    ok = _flags(seqs, index, stream)
+    if seqs == 0:
+        return ok
+    _launch((_lib or load()).trellis_kv_fork,
+            (refs.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), parents.data_ptr(), seqs, cols, num_pages, page, hk, d,
+             *(t.data_ptr() for t in cache), ok.data_ptr()),
+            index, stream, lambda: kv_pages_workspace_bytes(seqs, cols, num_pages), ask=False)
+    if stream is not None:
+        _used_on(stream, *cache, refs, kv_len, pages, parents, ok)
+    return ok
+
+
+def kv_compact(cache, refs, kv_len, pages, into, stream=None):
+    """Copy the pages in use, in their order, to the first pages of another cache (of the same heads, page
+    size and head width).  Returns its (refs, kv_len, pages); the first cache and its arrays stay as they are.
+    Sequences that name a page which `into` has no room for come out with kv_len 0."""
+    (num_pages, hk, page, d), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
+    shape, where = _require_codes(into, "into")
+    if shape[1:] != (hk, page, d) or where != index:
+        raise ValueError(f"into must be a cache of pages [{hk}, {page}, {d}] on cuda:{index}")
+    i32 = _types[3]
+    out = [_empty(s, i32, index, stream) for s in ((shape[0],), (seqs,), (seqs, cols))]
+    if seqs == 0:
+        raise ValueError("the table must hold at least one sequence")
+    _launch((_lib or load()).trellis_kv_compact,
+            (refs.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), seqs, cols, num_pages, page, hk, d,
+             *(t.data_ptr() for t in cache), shape[0], *(t.data_ptr() for t in into), *(t.data_ptr() for t in out)),
+            index, stream, lambda: kv_pages_workspace_bytes(seqs, cols, num_pages), ask=False)
+    if stream is not None:
+        _used_on(stream, *cache, *into, refs, kv_len, pages, *out)
+    return tuple(out)
+
+
+# ---- from one projection to the next -----------------------------------------
+def _norm(x, weight, eps, residual, residual_out, out, eight, stream):
+    Tensor, bf16, f32 = (_types or _torch_types())[:3]
+    if not isinstance(x, Tensor) or (index := x.get_device()) < 0 or x.dtype != bf16 or len(shape := x.shape) not in (2, 3):
+        raise ValueError("x must be a bfloat16 CUDA tensor [rows, width] or [tokens, heads, width]")
+    stride = x.stride()
+    rows, heads, width = shape[0], shape[1] if len(shape) == 3 else 1, shape[-1]
+    if x.numel() and ((width > 1 and stride[-1] != 1) or (heads > 1 and stride[1] != width)):
+        raise ValueError("x: the values of a row must be contiguous")
+    if _require_on(weight, "weight", bf16, 1, index) != (width,):
+        raise ValueError(f"weight must be [{width}]")
+    if residual is not None:
+        if _require_on(residual, "residual", bf16, len(shape), index) != shape:
+            raise ValueError(f"residual must be {tuple(shape)}")
+        residual_out = _output(residual_out, "residual_out", shape, index, x.device, stream)
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    codes = scales = None
+    if eight:
+        codes = _empty(shape, _types[4], index, stream)
+        scales = _empty(shape[:-1], f32, index, stream)
+    else:
+        out = _output(out, "out", shape, index, x.device, stream)
+        if residual is not None and out.numel() and out.data_ptr() == residual_out.data_ptr():
+            raise ValueError("out and residual_out must not be the same tensor")
+    if x.numel():
+        ptr = [None if t is None else t.data_ptr() for t in (residual, out, codes, scales, residual_out)]
+        _enqueue((_lib or load()).trellis_rms_norm,
+                 (x.data_ptr(), stride[0] if rows > 1 else heads * width, ptr[0], weight.data_ptr(), rows, heads, width, eps,
+                  *ptr[1:]), index, stream)
+        if stream is not None:
+            _used_on(stream, x, weight, residual, residual_out, out, codes, scales)
+    return out, codes, scales, residual_out
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None, out=None, stream=None):
+    """h / sqrt(mean(h^2) + eps) * weight in bf16, with h = x, or h = x + residual.
+
+    x: bf16 [rows, width] or [tokens, heads, width], rows (tokens) may be strided; weight: bf16 [width];
+    residual: bf16 of x's shape.  Returns the norm, or with a residual (norm, h).  residual_out may be
+    residual, out may be x (where that is contiguous)."""
+    y, _, _, h = _norm(x, weight, eps, residual, residual_out, out, False, stream)
+    return y if residual is None else (y, h)
+
+
+def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, residual_out=None, stream=None):
+    """rms_norm to 8 bits: codes float8_e4m3fn of x's shape and float32 scales, one a row, as gemm_q4 takes them.
+    Returns (codes, scales), or with a residual (codes, scales, h)."""
+    _, codes, scales, h = _norm(x, weight, eps, residual, residual_out, None, True, stream)
+    return (codes, scales) if residual is None else (codes, scales, h)
+
+
+def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None):
+    """out [M, N] bf16 = x [M, K] times 4-bit weights [N, K] transposed.
+
+    codes: int32 [N, K / 8], eight codes a word, the first in the lowest bits; scales (and biases): bf16
+    [N, K / group], group 32, 64 or 128.  A weight is scale * code + bias, or scale * (code - 8) without biases.
+    x: bf16, or float8_e4m3fn with x_scales float32 [M], as rms_norm_q8 returns them."""
+    torch = _torch()
+    Tensor, bf16, f32, i32, f8 = (_types or _torch_types())[:5]
+    if not isinstance(x, Tensor):
+        raise ValueError("x must be a CUDA tensor")
+    index = x.get_device()
+    M, K = _require_on(x, "x", f8 if x_scales is not None else bf16, 2, index)
+    N, words = _require_on(codes, "codes", torch.uint32 if getattr(codes, "dtype", None) == torch.uint32 else i32, 2, index)
+    shape = _require_on(scales, "scales", bf16, 2, index)
+    if words * 8 != K or shape[0] != N or shape[1] == 0 or K % shape[1] != 0:
+        raise ValueError("codes must be [N, K / 8] and scales [N, K / group]")
+    if biases is not None and _require_on(biases, "biases", bf16, 2, index) != shape:
+        raise ValueError("biases must be as scales")
+    if x_scales is not None and _require_on(x_scales, "x_scales", f32, 1, index) != (M,):
+        raise ValueError("x_scales must be [M]")
+    out = _output(out, "out", (M, N), index, x.device, stream)
+    if M == 0:
+        return out
+    _enqueue((_lib or load()).trellis_gemm_q4,
+             (x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+              None if biases is None else biases.data_ptr(), M, K, N, K // shape[1], out.data_ptr()), index, stream)
+    if stream is not None:
+        _used_on(stream, x, x_scales, codes, scales, biases, out)
     return out

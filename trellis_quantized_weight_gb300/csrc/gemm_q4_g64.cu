@@ -1,0 +1,8 @@
+// Products with 4-bit weights, groups of 64: the kernels of gemm_q4_mma.cuh.
+#include "gemm_q4_mma.cuh"
+
+namespace trellis {
+
+template cudaError_t launch_q4_mma<64>(const Q4Args&, const DeviceInfo&, cudaStream_t);
+
+}  // namespace trellis

@@ -142,6 +142,10 @@ struct KvLayout;
 KvLayout kv_layout(const int* starts, const int* kv_len, const int* pages, int tokens, int seqs, int page_cols,
                    int num_pages, int q_heads, int kv_heads, int page_size);
 
+// Widest row of trellis_rms_norm, and most pages of a pool.
+constexpr int kNormMaxWidth = 1 << 20;
+constexpr int kKvMaxPages = 1 << 24;
+
 // Launches one thread whose bounded wait on an mbarrier runs out (nothing
 // arrives), which sets the device error word exactly as a product wait that
 // gives up would.  Returns 0 or a trellis_status.
