@@ -179,7 +179,7 @@ TRELLIS_API int trellis_gemm_ws(const uint16_t *x, const uint32_t *codes, const 
 
 /*
  * trellis_device_status — synchronise `stream`, then report whether a bounded
- * device-side wait of the tensor-core product, or of trellis_kv_attention,
+ * device-side wait of a tensor-core product, or of trellis_kv_attention,
  * gave up since the last query (TRELLIS_ERR_TIMEOUT; the affected outputs are
  * undefined, workspaces are as ready for their next call as after any other) or
  * not (TRELLIS_OK).  Clears the flag.  A wait gives up after 2 s of wall-clock
@@ -551,11 +551,18 @@ TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const ui
  * No weight is rounded: c - 8 and x meet exactly, scales and biases are applied to the sums of each group in
  * fp32.  A row of x that holds an infinity or a NaN has no finite output.
  * group: 32, 64 or 128; K a multiple of it, K and N up to 2^20, M up to 65536 (0: nothing is enqueued).
- * The order of all sums is fixed by the sizes.
+ *   workspace  256-byte aligned, at least trellis_gemm_q4_workspace_size bytes (NULL where that is 0: for
+ *           few rows, and for bf16 activations without biases); its first 1 MiB is not touched, so a product's
+ *           workspace will do.
+ * The order of all sums is fixed by the sizes.  M > 16 runs on the tensor cores, whose waits are bounded (see
+ * trellis_device_status).  One or two kernels are enqueued.
  */
 TRELLIS_API int trellis_gemm_q4(const void *x, const float *x_scales, const uint32_t *codes, const uint16_t *scales,
                                 const uint16_t *biases, int M, int K, int N, int group, uint16_t *out,
-                                cudaStream_t stream);
+                                void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace trellis_gemm_q4 needs; eight and bias: whether it gets x_scales and biases. */
+TRELLIS_API int trellis_gemm_q4_workspace_size(int M, int K, int N, int group, int eight, int bias, size_t *bytes);
 
 #ifdef __cplusplus
 }

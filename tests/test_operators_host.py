@@ -23,7 +23,7 @@ FORK = dict(POOL, parents=P, **SIZES, **CACHE, ok=P, **WORK)
 COMPACT = dict(POOL, **SIZES, **CACHE, num_pages_out=9, k_codes_out=Q, v_codes_out=Q + (1 << 20), k_scales_out=Q + (2 << 20),
                v_scales_out=Q + (3 << 20), refs_out=Q + (4 << 20), kv_len_out=Q + (5 << 20), pages_out=Q + (6 << 20), **WORK)
 NORM = dict(x=P, x_stride=256, residual=P, weight=P, rows=4, heads=2, width=128, eps=1e-6, out=P, codes=0, scales=0, residual_out=Q, stream=None)
-Q4 = dict(x=P, x_scales=0, codes=P, scales=P, biases=P, M=3, K=256, N=50, group=64, out=P, stream=None)
+Q4 = dict(x=P, x_scales=0, codes=P, scales=P, biases=P, M=3, K=256, N=50, group=64, out=P, workspace=P, workspace_bytes=1 << 30, stream=None)
 
 SHARED = [(dict(refs=0), -1), (dict(kv_len=0), -1), (dict(pages=0), -1), (dict(seqs=0), -2), (dict(page_cols=0), -2), (dict(num_pages=0), -2),
           (dict(seqs=16385), -3), (dict(num_pages=(1 << 24) + 1), -3), (dict(page_cols=(1 << 24) + 1), -3), (dict(page_size=8), -3),
@@ -74,7 +74,8 @@ def test_norm_refuses(lib, change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(x=0), -1), (dict(codes=0), -1), (dict(scales=0), -1), (dict(out=0), -1), (dict(M=-1), -2), (dict(K=0), -2), (dict(N=0), -2),
     (dict(group=16), -3), (dict(group=256), -3), (dict(K=224), -2), (dict(M=65537), -3), (dict(K=(1 << 20) + 64), -3), (dict(N=(1 << 20) + 1), -3),
-    (dict(x=P + 8), -4), (dict(codes=P + 8), -4), (dict(scales=P + 1), -4), (dict(biases=P + 1), -4), (dict(x_scales=P + 2), -4), (dict(out=P + 1), -4)])
+    (dict(x=P + 8), -4), (dict(codes=P + 8), -4), (dict(scales=P + 1), -4), (dict(biases=P + 1), -4), (dict(x_scales=P + 2), -4), (dict(out=P + 1), -4),
+    (dict(M=17, workspace=0), -7), (dict(M=17, workspace_bytes=1 << 20), -7), (dict(M=17, workspace=P + 64), -4)])
 def test_gemm_q4_refuses(lib, change, want):
     assert lib.trellis_gemm_q4(*{**Q4, **change}.values()) == want
 
@@ -82,3 +83,14 @@ def test_gemm_q4_refuses(lib, change, want):
 def test_nothing_to_do(lib):
     assert lib.trellis_rms_norm(*{**NORM, "rows": 0}.values()) == 0
     assert lib.trellis_gemm_q4(*{**Q4, "M": 0}.values()) == 0
+
+
+@pytest.mark.parametrize("args,want", [((-1, 256, 5, 64, 0, 0), -2), ((1, 0, 5, 64, 0, 0), -2), ((1, 256, 0, 64, 0, 0), -2),
+                                       ((1, 256, 5, 48, 0, 0), -3), ((1, 96, 5, 64, 0, 0), -2), ((65537, 256, 5, 64, 0, 0), -3)])
+def test_gemm_q4_workspace_size(lib, args, want):
+    n = ctypes.c_size_t(7)
+    assert lib.trellis_gemm_q4_workspace_size(*args, ctypes.byref(n)) == want
+    assert lib.trellis_gemm_q4_workspace_size(1, 256, 5, 64, 0, 0, None) == -1
+    for M, eight, bias in ((1, 1, 1), (300, 0, 0)):
+        assert lib.trellis_gemm_q4_workspace_size(M, 256, 5, 64, eight, bias, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.trellis_gemm_q4_workspace_size(300, 256, 5, 64, 1, 0, ctypes.byref(n)) == 0 and n.value >= 300 * 512

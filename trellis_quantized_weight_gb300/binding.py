@@ -53,7 +53,8 @@ SIGNATURES = {
     "trellis_kv_compact": (_I, [_P, _P, _P, *[_I] * 6, _P, _P, _P, _P, _I, *[_P] * 7, _P, _SZ, _P]),
     "trellis_kv_pages_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
     "trellis_rms_norm": (_I, [_P, _LL, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P]),
-    "trellis_gemm_q4": (_I, [_P, _P, _P, _P, _P, *[_I] * 4, _P, _P]),
+    "trellis_gemm_q4": (_I, [_P, _P, _P, _P, _P, *[_I] * 4, _P, _P, _SZ, _P]),
+    "trellis_gemm_q4_workspace_size": (_I, [*[_I] * 6, ctypes.POINTER(_SZ)]),
 }
 
 
@@ -748,6 +749,13 @@ def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, residual_out=None, 
     return (codes, scales) if residual is None else (codes, scales, h)
 
 
+def gemm_q4_workspace_bytes(M, K, N, group, eight=False, bias=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().trellis_gemm_q4_workspace_size(M, K, N, group, int(eight), int(bias), ctypes.byref(n)),
+           "trellis_gemm_q4_workspace_size")
+    return int(n.value)
+
+
 def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None):
     """out [M, N] bf16 = x [M, K] times 4-bit weights [N, K] transposed.
 
@@ -771,9 +779,11 @@ def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None)
     out = _output(out, "out", (M, N), index, x.device, stream)
     if M == 0:
         return out
-    _enqueue((_lib or load()).trellis_gemm_q4,
-             (x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-              None if biases is None else biases.data_ptr(), M, K, N, K // shape[1], out.data_ptr()), index, stream)
+    group = K // shape[1]
+    _launch((_lib or load()).trellis_gemm_q4,
+            (x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+             None if biases is None else biases.data_ptr(), M, K, N, group, out.data_ptr()), index, stream,
+            lambda: gemm_q4_workspace_bytes(M, K, N, group, x_scales is not None, biases is not None), ask=False)
     if stream is not None:
         _used_on(stream, x, x_scales, codes, scales, biases, out)
     return out

@@ -57,4 +57,8 @@ __device__ __forceinline__ uint4 q4_load_x(const void* x, bool eight, size_t at)
 template <int G>
 cudaError_t launch_q4_mma(const Q4Args& a, const DeviceInfo& dev, cudaStream_t stream);
 
+// On the tensor cores, for more rows; workspace bytes: 0 where it takes none.
+size_t q4_tc_workspace_bytes(int M, int K, int groups, bool eight, bool bias);
+cudaError_t launch_q4_tc(const Q4Args& a, int group, void* workspace, const DeviceInfo& dev, cudaStream_t stream);
+
 }  // namespace trellis

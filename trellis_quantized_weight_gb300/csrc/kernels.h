@@ -155,5 +155,7 @@ int launch_wait_selftest(cudaStream_t stream);
 int tc_take_device_error(unsigned int* flags);
 // The same for the attention kernel on the tensor cores.
 int kv_take_device_error(unsigned int* flags);
+// The same for the products with 4-bit weights on the tensor cores.
+int q4_take_device_error(unsigned int* flags);
 
 }  // namespace trellis

@@ -236,10 +236,11 @@ int trellis_selftest_wait_timeout(cudaStream_t stream) { return trellis::launch_
 
 int trellis_device_status(cudaStream_t stream) {
     if (cudaStreamSynchronize(stream) != cudaSuccess) return TRELLIS_ERR_CUDA;
-    unsigned int flags = 0u, kv_flags = 0u;
-    if (trellis::tc_take_device_error(&flags) != 0 || trellis::kv_take_device_error(&kv_flags) != 0)
+    unsigned int flags = 0u, kv_flags = 0u, q4_flags = 0u;
+    if (trellis::tc_take_device_error(&flags) != 0 || trellis::kv_take_device_error(&kv_flags) != 0 ||
+        trellis::q4_take_device_error(&q4_flags) != 0)
         return TRELLIS_ERR_CUDA;
-    return (flags | kv_flags) != 0u ? TRELLIS_ERR_TIMEOUT : TRELLIS_OK;
+    return (flags | kv_flags | q4_flags) != 0u ? TRELLIS_ERR_TIMEOUT : TRELLIS_OK;
 }
 
 }  // extern "C"
