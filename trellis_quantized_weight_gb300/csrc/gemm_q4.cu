@@ -12,7 +12,7 @@ namespace {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // More rows than the register tiles' kernel takes at once go to the tensor cores' tiles.
-bool on_tensor_cores(int M) { return M > 16; }
+bool on_tensor_cores(int M) { return M > 0; }
 
 int check_sizes(int M, int K, int N, int group) {
     if (M < 0 || K < 1 || N < 1) return TRELLIS_ERR_SHAPE;
@@ -33,7 +33,8 @@ int trellis_gemm_q4_workspace_size(int M, int K, int N, int group, int eight, in
     if (bytes == nullptr) return TRELLIS_ERR_NULL;
     const int rc = check_sizes(M, K, N, group);
     if (rc != TRELLIS_OK) return rc;
-    *bytes = on_tensor_cores(M) ? q4_tc_workspace_bytes(M, K, K / group, eight != 0, bias != 0) : 0;
+    *bytes = on_tensor_cores(M) ? q4_tc_workspace_bytes(M, K, eight != 0) : 0;
+    (void)bias;
     return TRELLIS_OK;
 }
 
@@ -46,7 +47,7 @@ int trellis_gemm_q4(const void* x, const float* x_scales, const uint32_t* codes,
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(biases, 2) || !aligned(x_scales, 4) || !aligned(out, 2))
         return TRELLIS_ERR_ALIGN;
     if (M == 0) return TRELLIS_OK;
-    const size_t need = on_tensor_cores(M) ? q4_tc_workspace_bytes(M, K, K / group, x_scales != nullptr, biases != nullptr) : 0;
+    const size_t need = on_tensor_cores(M) ? q4_tc_workspace_bytes(M, K, x_scales != nullptr) : 0;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return TRELLIS_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
     DeviceInfo dev;

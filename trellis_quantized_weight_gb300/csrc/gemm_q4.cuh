@@ -28,14 +28,21 @@ struct Q4Args {
     int M, K, N, groups;
 };
 
-// Codes 0 and 4, 1 and 5, 2 and 6, 3 and 7 of a word as bf16 pairs of c - 8: a code in the low bits
-// of 128's significand is 128 + c, and 136 comes off exactly.
+// The codes in the low bits of a word's halves as a bf16 pair of c - 8: a code in the low bits of 128's significand is
+// 128 + c, and 136 comes off exactly.  (One logical instruction: left to itself the compiler takes one for the mask and
+// one for the exponent.)
+template <int kMinus>
+__device__ __forceinline__ uint32_t code_pair(uint32_t v) {
+    uint32_t c, r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(c) : "r"(v), "r"(0x000f000fu), "r"(0x43004300u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(kMinus == 136 ? 0x43084308u : 0x43004300u));
+    return r;
+}
+
+// Codes 0 and 4, 1 and 5, 2 and 6, 3 and 7 of a word as such pairs.
 __device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t (&p)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(v), "r"(0x43084308u));
-    }
+    for (int i = 0; i < 4; ++i) p[i] = code_pair<136>(w >> (4 * i));
 }
 
 // Eight activations, bf16 or e4m3, as bf16 pairs.
@@ -58,7 +65,7 @@ template <int G>
 cudaError_t launch_q4_mma(const Q4Args& a, const DeviceInfo& dev, cudaStream_t stream);
 
 // On the tensor cores, for more rows; workspace bytes: 0 where it takes none.
-size_t q4_tc_workspace_bytes(int M, int K, int groups, bool eight, bool bias);
+size_t q4_tc_workspace_bytes(int M, int K, bool eight);
 cudaError_t launch_q4_tc(const Q4Args& a, int group, void* workspace, const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace trellis

@@ -1,21 +1,18 @@
-// Products with 4-bit weights for many activation rows, on the 5th-generation tensor cores.
+// Products with 4-bit weights in groups, on the 5th-generation tensor cores.
 //
-//   D[n, m] (tensor memory, fp32) = sum over a group's k of (c[n, k] - 8) x[m, k]     128 weight rows, NB activation rows
-//   o[n, m] (registers, fp32)    += scale[n, g] D[n, m] + (bias + 8 scale)[n, g] sum_k x[m, k]
+//   D[n, m] (tensor memory, fp32) = sum_k w[n, k] x[m, k],   w = bf16(scale c + bias), or bf16(scale (c - 8))
 //
-// The codes minus 8 and the activations are exact in bf16, so no weight is rounded; a group's sum leaves the
-// accumulators after its own products and is scaled in fp32.  That costs a read of tensor memory and a multiply-add for
-// each output and group, by warps that have nothing else to do: it stays behind the tensor cores as long as a group is
-// long enough.
+// Each weight is rounded once to bf16, the type of its scale and of the activations (as the weights of the packed
+// codes are): a code is a whole number of 4 bits, exact in bf16, and one multiply-add of bf16 pairs rounds the
+// weight.  (Kept exact instead, with each group's sum scaled in fp32 on its way out of tensor memory, the
+// product took 328 us at 2000 rows of K = 5120, N = 17408 in groups of 128, 1426 us in groups of 32 with
+// biases; the group sums, not the products, were what it waited for.)
 //
-// A CTA has 20 warps: one loads code tiles, one activation tiles, one issues the products, one keeps tensor
-// memory, 8 turn codes into bf16 pairs in tensor memory (the products' first operand), 8 take the
-// groups' sums.  Tiles are 128 rows x NB; a CTA takes tile after tile (those of one weight row block next to
-// each other, so that codes come from L2), and where there are few tiles a cluster of CTAs shares the k of
-// one and adds its parts in shared memory in their order.
-//
-// The sums of x over each group, for weights with biases, and activations in 8 bits as bf16, are made by a
-// small kernel before.
+// A CTA's warps: one loads code tiles, one activation tiles, one issues the products, one keeps tensor
+// memory, 16 turn codes into weights in tensor memory (the products' first operand), 4 store results.
+// Tiles are 128 weight rows x NB activation rows; a CTA takes tile after tile (those of one block of weight rows
+// next to each other, so that their codes come from L2), its results leaving while the next tile is under way.
+// Where there are few tiles, a cluster of CTAs shares the k of one and adds its parts in shared memory, in order.
 #include <cuda.h>
 #include <cooperative_groups.h>
 #include <mutex>
@@ -33,37 +30,32 @@ namespace cg = cooperative_groups;
 constexpr int kTcRows = 128;                 // weight rows of a tile
 constexpr int kTcStageK = 128;               // k of a stage
 constexpr int kCodeBytes = kTcRows * 128;    // a code tile: 256 k (two stages) of 128 rows
-constexpr int kDecodeWarps = 8, kSumWarps = 8;
-constexpr int kTcThreads = 32 * (4 + kDecodeWarps + kSumWarps);
 
-// Slots: D buffers of NB columns and A slots of 64 columns fill the 512 of tensor memory.
-template <int G, int NB>
+// Of tensor memory's 512 columns 256 are A slots of 64, the others two D buffers.
+template <int NB>
 struct TcShape {
-    static constexpr int kPer = kTcStageK / G;                      // groups of a stage
-    static constexpr int kD = NB == 32 ? 8 : NB == 64 ? 4 : 2;
-    static constexpr int kA = (512 - kD * NB) / 64 < 4 ? (512 - kD * NB) / 64 : 4;
-    static constexpr int kXTile = NB * kTcStageK * 2;               // two boxes of 64 k
-    static constexpr int kXBytes = kXTile + (kPer * NB * 4 + 1023) / 1024 * 1024;      // and the sums of its groups
-    static constexpr int kX = NB == 192 ? 3 : NB == 128 ? 4 : NB == 64 ? 6 : 8;
-    static constexpr int kCode = NB >= 128 ? 2 : 5;
-    static constexpr int kOffX = 0, kOffCode = kX * kXBytes, kOffBar = kOffCode + kCode * kCodeBytes;
-    static constexpr int kBarX = 0, kBarXEmpty = kX, kBarCode = 2 * kX, kBarCodeEmpty = 2 * kX + kCode;
-    static constexpr int kBarA = 2 * (kX + kCode), kBarAEmpty = kBarA + kA, kBarD = kBarA + 2 * kA, kBarDEmpty = kBarD + kD;
-    static constexpr int kBarSums = kBarDEmpty + kD, kBars = kBarSums + 1;
+    static constexpr int kA = 4;                                    // stages under way: a slot of weights and one of activations each
+    static constexpr int kXBytes = NB * kTcStageK * 2;              // two boxes of 64 k
+    static constexpr int kCode = NB == 128 ? 4 : 8;                 // code tiles under way
+    static constexpr int kOffX = 0, kOffCode = kA * kXBytes, kOffBar = kOffCode + kCode * kCodeBytes;
+    static constexpr int kBarFull = 0, kBarEmpty = kA, kBarCode = 2 * kA, kBarCodeEmpty = kBarCode + kCode;
+    static constexpr int kBarD = kBarCodeEmpty + kCode, kBarDEmpty = kBarD + 2, kBars = kBarDEmpty + 2;
     static constexpr int kOffTaddr = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffTaddr + 16 + 1024;             // the base is rounded up to 1 KB
     static constexpr uint32_t kInstr = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NB >> 3) << 17) |
                                        (static_cast<uint32_t>(kTcRows >> 4) << 24);
     static_assert(kSmem <= 232448, "shared memory of a CTA");
-    static_assert(kD * NB + kA * 64 <= 512 && kA >= 2, "tensor memory");
-    static_assert(kTcRows * NB * 4 <= kX * kXBytes, "a part of the sums fits where activations were");
+    static_assert(kTcRows * NB * 4 <= kOffBar, "a part of the sums fits where operands were");
 };
+constexpr int kDecodeWarps = 16, kStageWarps = 8;    // those of even stages and those of odd ones
+constexpr int kStoreWarps = 4;
+constexpr int kTcThreads = 32 * (4 + kDecodeWarps + kStoreWarps);
 
 struct TcArgs {
     const uint16_t *scales, *biases;
-    const float *x_scales, *sums;       // sums [groups, m_pad]
+    const float* x_scales;
     uint16_t* out;
-    int M, K, N, groups, m_pad;
+    int M, K, N, groups;
     int m_tiles, tiles, parts;
 };
 
@@ -105,35 +97,38 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
 }
 
-// A place in a ring of kSlots and the parity of its turn.
-template <int kSlots>
-struct Ring {
-    int slot = 0;
-    uint32_t turn = 0u;
-    __device__ __forceinline__ void next() {
-        if (++slot == kSlots) { slot = 0; turn ^= 1u; }
-    }
-};
-
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 // K-major, 128-byte swizzle: 1 KB between atoms of 8 rows, version 1, swizzle mode 2.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) |
            (2ull << 61);
 }
-__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, uint32_t accumulate) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(instr), "r"(accumulate) : "memory");
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+// One product of 16 k, its operands a base and an immediate (a shared-memory offset only reaches the address field).
+template <int kOffA, int kOffB>
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, uint32_t accumulate, uint32_t elected) {
+    asm volatile("{\n .reg .pred p, e;\n .reg .b64 y;\n .reg .b32 x;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %7, 0;\n"
+                 " add.s32 x, %1, %5;\n add.s64 y, %2, %6;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(instr), "r"(accumulate), "n"(kOffA), "n"(kOffB >> 4), "r"(elected) : "memory");
+}
+// A stage's eight products, added to the sum or (the first one of a tile) begun anew.
+template <int NB, int k = 0>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, uint32_t accumulate, uint32_t elected) {
+    mma_step<8 * k, (k >> 2) * (NB * 128) + (k & 3) * 32>(d, a, b, instr, k > 0 ? 1u : accumulate, elected);
+    if constexpr (k + 1 < kTcStageK / 16) mma_stage<NB, k + 1>(d, a, b, instr, accumulate, elected);
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t elected) {
+    asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+                 " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+                 :: "r"(bar), "r"(elected) : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -161,24 +156,27 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     return v;
 }
 
-// Codes 2i and 2i + 1 of a word as a bf16 pair of c - 8, i = 0 .. 3: a byte goes to both halves, the upper one's from
-// the word shifted by a code.
-__device__ __forceinline__ void pairs_in_order(uint32_t w, uint32_t* p) {
+// Codes 2i and 2i + 1 of a word as a bf16 pair of the codes plus `minus` (-128 - 8 or -128 as bf16 pairs), i = 0 .. 3: a
+// byte goes to both halves, the upper one's from the word shifted by a code.  Then the weights.
+template <bool kBias>
+__device__ __forceinline__ void weights_of(uint32_t w, uint32_t scale, uint32_t bias, uint32_t* p) {
     const uint32_t u = w >> 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t both = __byte_perm(w, u, static_cast<uint32_t>(i) | (static_cast<uint32_t>(i) << 4) |
                                                     (static_cast<uint32_t>(4 + i) << 8) | (static_cast<uint32_t>(4 + i) << 12));
-        const uint32_t c = (both & 0x000f000fu) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(c), "r"(0x43084308u));
+        const uint32_t c = code_pair<kBias ? 128 : 136>(both);
+        if constexpr (kBias)
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(p[i]) : "r"(c), "r"(scale), "r"(bias));
+        else
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(c), "r"(scale));
     }
 }
 
 template <int G, int NB, bool kBias>
 __global__ void __launch_bounds__(kTcThreads, 1)
 q4_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap code_map, const __grid_constant__ CUtensorMap x_map) {
-    using S = TcShape<G, NB>;
-    constexpr int kPer = S::kPer, kCols = NB / 2;
+    using S = TcShape<NB>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sraw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
@@ -187,23 +185,18 @@ q4_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorM
     auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kX; ++i) {
-            mbar_init(bar(S::kBarX + i), 1);
-            mbar_init(bar(S::kBarXEmpty + i), 1 + (kBias ? kSumWarps : 0));
+        for (int i = 0; i < S::kA; ++i) {
+            mbar_init(bar(S::kBarFull + i), kStageWarps + 1);         // weights by the warps that made them, activations by their bytes
+            mbar_init(bar(S::kBarEmpty + i), 1);
         }
         for (int i = 0; i < S::kCode; ++i) {
             mbar_init(bar(S::kBarCode + i), 1);
             mbar_init(bar(S::kBarCodeEmpty + i), kDecodeWarps);
         }
-        for (int i = 0; i < S::kA; ++i) {
-            mbar_init(bar(S::kBarA + i), kDecodeWarps);
-            mbar_init(bar(S::kBarAEmpty + i), 1);
-        }
-        for (int i = 0; i < S::kD; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(S::kBarD + i), 1);
-            mbar_init(bar(S::kBarDEmpty + i), kSumWarps);
+            mbar_init(bar(S::kBarDEmpty + i), kStoreWarps);
         }
-        mbar_init(bar(S::kBarSums), kSumWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -215,7 +208,7 @@ q4_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorM
     __syncthreads();
     fence_after();
     const uint32_t taddr = *reinterpret_cast<volatile uint32_t*>(smem + S::kOffTaddr);
-    const uint32_t t_a = taddr + S::kD * NB;
+    const uint32_t t_a = taddr + 256;
 
     // this CTA's share of k, in blocks of two stages, and its first tile
     const int part = a.parts > 1 ? static_cast<int>(blockIdx.x) % a.parts : 0;
@@ -233,230 +226,181 @@ q4_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorM
     }
     griddep_wait();
 
+    // Slots are taken in turn: use number i of a ring of n (a power of two) is slot i % n, its phase's parity (i / n) & 1.
     bool alive = true;
-    if (warp < 4) {
-        if constexpr (NB >= 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 0 && lane == 0) {
-            // ------------------------------------------------------------ code tiles
-            Ring<S::kCode> r;
-            int issued = 0;
+    if (warp == 0) {
+        // ---------------------------------------------------------------- code tiles
+        if (lane == 0) {
+            uint32_t i = 0;
             for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
                 const int n0 = tile / a.m_tiles * kTcRows;
-                for (int b = b0; b < b1; ++b) {
-                    alive = mbar_wait(bar(S::kBarCodeEmpty + r.slot), r.turn ^ 1u);
+                for (int b = b0; b < b1; ++b, ++i) {
+                    const uint32_t slot = i % S::kCode;
+                    alive = mbar_wait(bar(S::kBarCodeEmpty + slot), ((i / S::kCode) & 1u) ^ 1u);
                     if (!alive) break;
-                    mbar_expect(bar(S::kBarCode + r.slot), kCodeBytes);
-                    tma_load_2d(sbase + S::kOffCode + r.slot * kCodeBytes, &code_map, b * 32, n0, bar(S::kBarCode + r.slot));
-                    r.next();
-                    ++issued;
+                    mbar_expect(bar(S::kBarCode + slot), kCodeBytes);
+                    tma_load_2d(sbase + S::kOffCode + slot * kCodeBytes, &code_map, b * 32, n0, bar(S::kBarCode + slot));
                 }
             }
             // what was asked for has landed before the CTA ends
-            for (int i = max(issued - S::kCode, 0); i < issued; ++i) (void)mbar_wait(bar(S::kBarCode + i % S::kCode), (i / S::kCode) & 1);
-        } else if (warp == 1 && lane == 0) {
-            // ------------------------------------------------------------ activation tiles
-            Ring<S::kX> r;
-            int issued = 0;
+            for (uint32_t j = i > S::kCode ? i - S::kCode : 0u; j < i; ++j) (void)mbar_wait(bar(S::kBarCode + j % S::kCode), (j / S::kCode) & 1u);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- activation tiles
+        if (lane == 0) {
+            uint32_t i = 0;
             for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
                 const int m0 = tile % a.m_tiles * NB;
-                for (int s = s0; s < s1; ++s) {
-                    alive = mbar_wait(bar(S::kBarXEmpty + r.slot), r.turn ^ 1u);
+                for (int s = s0; s < s1; ++s, ++i) {
+                    const uint32_t slot = i % S::kA, full = bar(S::kBarFull + slot), dst = sbase + S::kOffX + slot * S::kXBytes;
+                    alive = mbar_wait(bar(S::kBarEmpty + slot), ((i / S::kA) & 1u) ^ 1u);
                     if (!alive) break;
-                    const uint32_t full = bar(S::kBarX + r.slot), dst = sbase + S::kOffX + r.slot * S::kXBytes;
-                    const int sums = kBias ? min(kPer, a.groups - s * kPer) : 0;
-                    mbar_expect(full, static_cast<uint32_t>(S::kXTile + sums * NB * 4));
+                    mbar_expect(full, S::kXBytes);
                     tma_load_2d(dst, &x_map, s * kTcStageK, m0, full);
                     tma_load_2d(dst + NB * 128, &x_map, s * kTcStageK + 64, m0, full);
-                    for (int q = 0; q < sums; ++q)
-                        bulk_load(dst + S::kXTile + q * NB * 4, a.sums + static_cast<size_t>(s * kPer + q) * a.m_pad + m0, NB * 4, full);
-                    r.next();
-                    ++issued;
                 }
             }
-            for (int i = max(issued - S::kX, 0); i < issued; ++i) (void)mbar_wait(bar(S::kBarX + i % S::kX), (i / S::kX) & 1);
-        } else if (warp == 2 && lane == 0) {
-            // ------------------------------------------------------------ products
-            Ring<S::kX> x;
-            Ring<S::kA> c;
-            Ring<S::kD> d;
-            const uint64_t desc0 = smem_desc(sbase + S::kOffX);
-            const uint32_t desc_hi = static_cast<uint32_t>(desc0 >> 32);
-            int last = -1;
-            uint32_t last_turn = 0u;
-            for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
-                for (int s = s0; s < s1 && alive; ++s) {
-                    alive = mbar_wait(bar(S::kBarX + x.slot), x.turn) && mbar_wait(bar(S::kBarA + c.slot), c.turn);
-                    if (!alive) break;
-                    fence_after();
-                    const uint32_t desc = static_cast<uint32_t>(desc0) + static_cast<uint32_t>(x.slot * (S::kXBytes >> 4));
-#pragma unroll
-                    for (int q = 0; q < kPer; ++q) {
-                        if (s * kPer + q >= a.groups) break;
-                        alive = mbar_wait(bar(S::kBarDEmpty + d.slot), d.turn ^ 1u);
-                        if (!alive) break;
-                        fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < G / 16; ++kk) {
-                            const int k = q * (G / 16) + kk;                      // step of 16 in the stage
-                            const uint32_t lo = desc + static_cast<uint32_t>(((k >> 2) * (NB * 128) + (k & 3) * 32) >> 4);
-                            mma_ta(taddr + d.slot * NB, t_a + c.slot * 64 + 8 * k, (static_cast<uint64_t>(desc_hi) << 32) | lo, S::kInstr,
-                                   kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit(bar(S::kBarD + d.slot));
-                        last = d.slot;
-                        last_turn = d.turn;
-                        d.next();
-                    }
-                    if (!alive) break;
-                    mma_commit(bar(S::kBarAEmpty + c.slot));
-                    mma_commit(bar(S::kBarXEmpty + x.slot));
-                    x.next();
-                    c.next();
-                }
-            }
-            // the last products are done before tensor memory is given back
-            if (last >= 0) (void)mbar_wait(bar(S::kBarD + last), last_turn);
+            // (a stage whose weights were never made keeps its barrier: that wait gives up)
+            for (uint32_t j = i > S::kA ? i - S::kA : 0u; j < i; ++j) (void)mbar_wait(bar(S::kBarFull + j % S::kA), (j / S::kA) & 1u);
         }
-        __syncwarp();
-    } else if (warp < 4 + kDecodeWarps) {
-        if constexpr (NB >= 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        // ---------------------------------------------------------------- codes to bf16
-        const int quarter = warp & 3, half = (warp - 4) >> 2;           // 32 rows; 64 k of each stage
-        const int row = 32 * quarter + lane;
-        const uint32_t t_row = t_a + (static_cast<uint32_t>(32 * quarter) << 16) + 32 * half;
-        const uint32_t row_at = sbase + S::kOffCode + row * 128, r7 = row & 7;
-        Ring<S::kCode> r;
-        Ring<S::kA> c;
-        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
-            for (int s = s0; s < s1; ++s) {
-                if ((s & 1) == 0) alive = mbar_wait(bar(S::kBarCode + r.slot), r.turn);
-                if (!alive) break;
-                const uint32_t at = row_at + r.slot * kCodeBytes;
-                const uint32_t chunk = 4 * (s & 1) + 2 * half;
-                const uint4 lo = lds128(at + ((chunk ^ r7) << 4)), hi = lds128(at + (((chunk + 1) ^ r7) << 4));
-                uint32_t p[16], u[16];
-                pairs_in_order(lo.x, p); pairs_in_order(lo.y, p + 4); pairs_in_order(lo.z, p + 8); pairs_in_order(lo.w, p + 12);
-                pairs_in_order(hi.x, u); pairs_in_order(hi.y, u + 4); pairs_in_order(hi.z, u + 8); pairs_in_order(hi.w, u + 12);
-                if ((s & 1) == 1 || s + 1 == s1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::kBarCodeEmpty + r.slot));
-                    r.next();
-                }
-                alive = mbar_wait(bar(S::kBarAEmpty + c.slot), c.turn ^ 1u);
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- products
+        // All lanes walk the same path and one issues, so that the operands live in uniform registers.
+        const uint32_t elected = elect_lane();
+        const uint64_t desc0 = smem_desc(sbase + S::kOffX);
+        uint32_t i = 0, d = 0;
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
+            const uint32_t td = taddr + (d & 1u) * NB;
+            alive = mbar_wait(bar(S::kBarDEmpty + (d & 1u)), ((d >> 1) & 1u) ^ 1u);
+            for (int s = s0; s < s1 && alive; ++s, ++i) {
+                const uint32_t slot = i % S::kA;
+                alive = mbar_wait(bar(S::kBarFull + slot), (i / S::kA) & 1u);
                 if (!alive) break;
                 fence_after();
-                tmem_st16(t_row + c.slot * 64, p);
-                tmem_st16(t_row + c.slot * 64 + 16, u);
+                mma_stage<NB>(td, t_a + slot * 64, desc0 + static_cast<uint64_t>(slot * (S::kXBytes >> 4)), S::kInstr, s > s0 ? 1u : 0u, elected);
+                mma_commit(bar(S::kBarEmpty + slot), elected);
+            }
+            // also where a wait gave up: what was issued is done before tensor memory is given back
+            mma_commit(bar(S::kBarD + (d & 1u)), elected);
+        }
+        if (d > 0) (void)mbar_wait(bar(S::kBarD + ((d - 1) & 1u)), ((d - 1) >> 1) & 1u);
+    } else if (warp >= 4 && warp < 4 + kDecodeWarps) {
+        // ---------------------------------------------------------------- codes to weights
+        // 32 rows (a lane's row is its lane of tensor memory), 64 k of each even or odd stage
+        const int quarter = warp & 3, half = ((warp - 4) >> 2) & 1, odd = (warp - 4) >> 3;
+        const int row = 32 * quarter + lane;
+        const uint32_t t_row = t_a + (static_cast<uint32_t>(32 * quarter) << 16) + 32 * half;
+        const uint32_t row_at = sbase + S::kOffCode + row * 128;
+        const uint32_t chunk0 = ((4 * odd + 2 * half) ^ (row & 7)) << 4, chunk1 = ((4 * odd + 2 * half + 1) ^ (row & 7)) << 4;
+        constexpr int kPer = G == 32 ? 2 : 1;                        // groups of 64 k (a part of one where G = 128)
+        uint32_t i0 = 0, b_i0 = 0;                                   // stages and blocks of the tiles before
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, i0 += s1 - s0, b_i0 += b1 - b0) {
+            const int n = min(tile / a.m_tiles * kTcRows + row, a.N - 1);
+            const uint16_t* scales = a.scales + static_cast<size_t>(n) * a.groups;
+            const uint16_t* biases = kBias ? a.biases + static_cast<size_t>(n) * a.groups : nullptr;
+            // the groups of a stage's 64 k: those past the last read as zero
+            auto load = [&](int s, uint32_t (&sc)[kPer], uint32_t (&bi)[kPer]) {
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    const int g = (s * kTcStageK + 64 * half) / G + q;
+                    const bool has = s < s1 && g < a.groups;
+                    sc[q] = has ? __ldg(scales + g) : 0u;
+                    if constexpr (kBias) bi[q] = has ? __ldg(biases + g) : 0u;
+                }
+            };
+            uint32_t sc[kPer], bi[kPer], sc_next[kPer], bi_next[kPer];
+            load(s0 + odd, sc, bi);
+            for (int s = s0 + odd; s < s1; s += 2) {
+                const uint32_t i = i0 + (s - s0), b_i = b_i0 + ((s - s0) >> 1), slot = i % S::kA, code = b_i % S::kCode;
+                load(s + 2, sc_next, bi_next);
+                alive = mbar_wait(bar(S::kBarCode + code), (b_i / S::kCode) & 1u);
+                if (!alive) break;
+                const uint32_t at = row_at + code * kCodeBytes;
+                const uint4 w0 = lds128(at + chunk0), w1 = lds128(at + chunk1);
+                alive = mbar_wait(bar(S::kBarEmpty + slot), ((i / S::kA) & 1u) ^ 1u);
+                if (!alive) break;
+                fence_after();
+                uint32_t p[16];
+                uint32_t s_pair = sc[0] | (sc[0] << 16), b_pair = kBias ? bi[0] | (bi[0] << 16) : 0u;
+                weights_of<kBias>(w0.x, s_pair, b_pair, p); weights_of<kBias>(w0.y, s_pair, b_pair, p + 4);
+                weights_of<kBias>(w0.z, s_pair, b_pair, p + 8); weights_of<kBias>(w0.w, s_pair, b_pair, p + 12);
+                tmem_st16(t_row + slot * 64, p);
+                uint32_t u[16];
+                if constexpr (kPer == 2) { s_pair = sc[1] | (sc[1] << 16); b_pair = kBias ? bi[1] | (bi[1] << 16) : 0u; }
+                weights_of<kBias>(w1.x, s_pair, b_pair, u); weights_of<kBias>(w1.y, s_pair, b_pair, u + 4);
+                weights_of<kBias>(w1.z, s_pair, b_pair, u + 8); weights_of<kBias>(w1.w, s_pair, b_pair, u + 12);
+                tmem_st16(t_row + slot * 64 + 16, u);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::kBarA + c.slot));
-                c.next();
+                if (lane == 0) {
+                    mbar_arrive(bar(S::kBarFull + slot));
+                    mbar_arrive(bar(S::kBarCodeEmpty + code));
+                }
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) { sc[q] = sc_next[q]; bi[q] = kBias ? bi_next[q] : 0u; }
+            }
+            // a block whose odd stage is not there is released all the same
+            if (alive && odd == 1 && ((s1 - s0) & 1) != 0) {
+                const uint32_t b_i = b_i0 + ((s1 - s0) >> 1), code = b_i % S::kCode;
+                alive = mbar_wait(bar(S::kBarCode + code), (b_i / S::kCode) & 1u);
+                if (lane == 0) mbar_arrive(bar(S::kBarCodeEmpty + code));
             }
         }
-    } else {
-        if constexpr (NB >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-        // ---------------------------------------------------------------- sums of the groups
-        const int quarter = warp & 3, half = (warp - 4 - kDecodeWarps) >> 2;
-        const uint32_t t_row = taddr + (static_cast<uint32_t>(32 * quarter) << 16) + kCols * half;
-        Ring<S::kX> x;
-        Ring<S::kD> d;
-        float2 o[kCols / 2];
-        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
-            const int m0 = tile % a.m_tiles * NB + kCols * half;
-            const int n = tile / a.m_tiles * kTcRows + 32 * quarter + lane;
-            const size_t row = static_cast<size_t>(min(n, a.N - 1)) * a.groups;
-            const uint16_t* scales = a.scales + row;
-            const uint16_t* biases = kBias ? a.biases + row : nullptr;
-            const int g0 = s0 * kPer, g1 = min(s1 * kPer, a.groups);
-#pragma unroll
-            for (int j = 0; j < kCols / 2; ++j) o[j] = make_float2(0.0f, 0.0f);
-            uint32_t s_next = g0 < g1 ? __ldg(scales + g0) : 0u, b_next = kBias && g0 < g1 ? __ldg(biases + g0) : 0u;
-            for (int g = g0; g < g1; ++g) {
-                const float scale = __uint_as_float(s_next << 16);
-                const float bias = kBias ? fmaf(8.0f, scale, __uint_as_float(b_next << 16)) : 0.0f;
-                if (g + 1 < g1) {
-                    s_next = __ldg(scales + g + 1);
-                    if constexpr (kBias) b_next = __ldg(biases + g + 1);
-                }
-                const int q = g % kPer;
-                alive = mbar_wait(bar(S::kBarD + d.slot), d.turn);
-                if (alive && kBias && q == 0) alive = mbar_wait(bar(S::kBarX + x.slot), x.turn);
-                if (!alive) break;
-                fence_after();
-                const float4* sums = reinterpret_cast<const float4*>(smem + S::kOffX + x.slot * S::kXBytes + S::kXTile + q * NB * 4) + kCols / 4 * half;
-                constexpr int kBufs = NB == 192 ? 1 : 2;         // 192: there are no registers for a second one
-                uint32_t v[kBufs][16];
-                if (kBufs == 2) tmem_ld16(v[0], t_row + d.slot * NB);
-#pragma unroll
-                for (int i = 0; i < kCols / 16; ++i) {
-                    uint32_t(&now)[16] = v[i % kBufs];
-                    if (kBufs == 1) tmem_ld16(now, t_row + d.slot * NB + 16 * i);
-                    tmem_wait_ld(now);
-                    if (i + 1 < kCols / 16) {
-                        if (kBufs == 2) tmem_ld16(v[(i + 1) % kBufs], t_row + d.slot * NB + 16 * (i + 1));
-                    } else {
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(S::kBarDEmpty + d.slot));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float2& y = o[8 * i + j];
-                        y = __ffma2_rn(make_float2(scale, scale), make_float2(__uint_as_float(now[2 * j]), __uint_as_float(now[2 * j + 1])), y);
-                    }
-                    if constexpr (kBias) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 u = sums[4 * i + j];
-                            o[8 * i + 2 * j] = __ffma2_rn(make_float2(bias, bias), make_float2(u.x, u.y), o[8 * i + 2 * j]);
-                            o[8 * i + 2 * j + 1] = __ffma2_rn(make_float2(bias, bias), make_float2(u.z, u.w), o[8 * i + 2 * j + 1]);
-                        }
-                    }
-                }
-                d.next();
-                if (kBias && (q == kPer - 1 || g + 1 == g1)) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(S::kBarXEmpty + x.slot));
-                    x.next();
-                }
-            }
+    } else if (warp >= 4 + kDecodeWarps) {
+        // ---------------------------------------------------------------- results
+        const int quarter = warp & 3;
+        constexpr int kStep = NB < 32 ? 16 : 32;
+        uint32_t d = 0;
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
+            const int m0 = tile % a.m_tiles * NB, n = tile / a.m_tiles * kTcRows + 32 * quarter + lane;
+            const uint32_t t_row = taddr + (static_cast<uint32_t>(32 * quarter) << 16) + (d & 1u) * NB;
+            alive = mbar_wait(bar(S::kBarD + (d & 1u)), (d >> 1) & 1u);
             if (!alive) break;
-            if (a.parts > 1) {
-                // [column][row], where the activations and their sums were, once all warps have taken the last ones
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::kBarSums));
-                alive = mbar_wait(bar(S::kBarSums), 0u);
-                if (!alive) break;
-                float* part_sums = reinterpret_cast<float*>(smem + S::kOffX) + 32 * quarter + lane;
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NB; c += kStep) {
+                uint32_t v[kStep / 16][16];
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) part_sums[(kCols * half + j) * kTcRows] = j & 1 ? o[j / 2].y : o[j / 2].x;
-            } else if (n < a.N) {
+                for (int i = 0; i < kStep / 16; ++i) tmem_ld16(v[i], t_row + c + 16 * i);
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    if (m0 + j < a.M) {
-                        float y = j & 1 ? o[j / 2].y : o[j / 2].x;
-                        if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m0 + j);
-                        a.out[static_cast<size_t>(m0 + j) * a.N + n] = bf16_bits_rn(y);
+                for (int i = 0; i < kStep / 16; ++i) tmem_wait_ld(v[i]);
+                if (c + kStep == NB) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::kBarDEmpty + (d & 1u)));
+                }
+                if (a.parts > 1) {
+                    // [column][row], where the operands were: all of the products are done
+                    float* part_sums = reinterpret_cast<float*>(smem) + c * kTcRows + 32 * quarter + lane;
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) part_sums[j * kTcRows] = __uint_as_float(v[j / 16][j % 16]);
+                } else if (n < a.N) {
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) {
+                        const int m = m0 + c + j;
+                        if (m >= a.M) break;
+                        float y = __uint_as_float(v[j / 16][j % 16]);
+                        if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m);
+                        a.out[static_cast<size_t>(m) * a.N + n] = bf16_bits_rn(y);
                     }
                 }
             }
         }
     }
+    __syncwarp();
     if (a.parts > 1) {
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
-        if (warp >= 4 + kDecodeWarps) {
-            const int m0 = tile0 % a.m_tiles * NB, n0 = tile0 / a.m_tiles * kTcRows;
-            const int t = threadIdx.x - 32 * (4 + kDecodeWarps);
-            const int row = t % kTcRows;
-            float* mine = reinterpret_cast<float*>(smem + S::kOffX);
-            for (int col = part * 2 + t / kTcRows; col < NB && m0 + col < a.M; col += 2 * a.parts) {
-                float y = 0.0f;
-                for (int r = 0; r < a.parts; ++r) y += cluster.map_shared_rank(mine, r)[col * kTcRows + row];
-                if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m0 + col);
-                if (n0 + row < a.N) a.out[static_cast<size_t>(m0 + col) * a.N + n0 + row] = bf16_bits_rn(y);
-            }
+        const int m0 = tile0 % a.m_tiles * NB, n0 = tile0 / a.m_tiles * kTcRows;
+        const int row = threadIdx.x % kTcRows;
+        constexpr int kStride = kTcThreads / kTcRows;
+        float* mine = reinterpret_cast<float*>(smem);
+        for (int col = part * kStride + threadIdx.x / kTcRows; col < NB && m0 + col < a.M; col += kStride * a.parts) {
+            float y = 0.0f;
+            for (int r = 0; r < a.parts; ++r) y += cluster.map_shared_rank(mine, r)[col * kTcRows + row];
+            if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m0 + col);
+            if (n0 + row < a.N) a.out[static_cast<size_t>(m0 + col) * a.N + n0 + row] = bf16_bits_rn(y);
         }
         cluster.sync();                 // the others may still be reading this CTA's part
     }
@@ -469,26 +413,11 @@ q4_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorM
     }
 }
 
-// Before the product: the sums of x over each group, [groups, m_pad], and 8-bit activations as bf16.
-template <int G>
-__global__ void __launch_bounds__(256) q4_prepare_kernel(const void* x, int eight, int M, int K, int m_pad, float* sums, uint16_t* x16) {
-    constexpr int kLanes = G / 8;                 // of a group
+// Before the product: 8-bit activations as bf16.
+__global__ void __launch_bounds__(256) q4_widen_kernel(const uint8_t* x, long long count, uint16_t* x16) {
     griddep_wait();
-    const int blocks = K / 8;                     // of eight values, in a row
-    const long long all = static_cast<long long>(M) * blocks, step = static_cast<long long>(gridDim.x) * 256;
-    for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e - (threadIdx.x & 31) < all; e += step) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (e < all) v = q4_load_x(x, eight != 0, static_cast<size_t>(e) * 8);
-        if (x16 != nullptr && e < all) *reinterpret_cast<uint4*>(x16 + static_cast<size_t>(e) * 8) = v;
-        if (sums != nullptr) {
-            float s = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
-                      ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
-#pragma unroll
-            for (int d = kLanes / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            const int m = static_cast<int>(e / blocks), b = static_cast<int>(e - static_cast<long long>(m) * blocks);
-            if (e < all && b % kLanes == 0) sums[static_cast<size_t>(b / kLanes) * m_pad + m] = s;
-        }
-    }
+    for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < count; e += static_cast<long long>(gridDim.x) * 256)
+        *reinterpret_cast<uint4*>(x16 + e * 8) = q4_load_x(x, true, static_cast<size_t>(e) * 8);
     griddep_launch_dependents();
 }
 
@@ -522,21 +451,23 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void*
 }
 
 template <int G, int NB, bool kBias>
-cudaError_t launch_as(const TcArgs& args, const Q4Args& q, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
-    using S = TcShape<G, NB>;
+cudaError_t launch_as(const Q4Args& q, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
+    using S = TcShape<NB>;
     static std::atomic<unsigned long long> done{0};
     if (!smem_opt_in(q4_tc_kernel<G, NB, kBias>, S::kSmem, done)) return cudaErrorInvalidValue;
     CUtensorMap codes, xs;
     if (!make_map(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, q.codes, q.K / 8, q.N, kTcRows) ||
         !make_map(&xs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, q.K, q.M, NB))
         return cudaErrorInvalidValue;
-    TcArgs a = args;
+    TcArgs a;
+    a.scales = q.scales; a.biases = q.biases; a.x_scales = q.x_scales; a.out = q.out;
+    a.M = q.M; a.K = q.K; a.N = q.N; a.groups = q.groups;
     a.m_tiles = (q.M + NB - 1) / NB;
     a.tiles = (q.N + kTcRows - 1) / kTcRows * a.m_tiles;
     // parts of k for clusters of CTAs, while all CTAs still run at once and each has two blocks of k or more
     const int blocks = (q.K + 2 * kTcStageK - 1) / (2 * kTcStageK);
     a.parts = 1;
-    while (a.parts < 4 && 2 * a.parts * static_cast<long long>(a.tiles) <= dev.num_sms && blocks >= 4 * a.parts) a.parts *= 2;
+    while (a.parts < 8 && (a.parts + 1ll) * a.tiles <= (a.parts < 4 ? dev.num_sms : dev.num_sms / 2) && blocks >= 2 * (a.parts + 1)) ++a.parts;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.parts > 1 ? a.tiles * a.parts : (a.tiles < dev.num_sms ? a.tiles : dev.num_sms));
     cfg.blockDim = dim3(kTcThreads);
@@ -548,72 +479,40 @@ cudaError_t launch_as(const TcArgs& args, const Q4Args& q, const void* x, const 
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = a.parts; attr[1].val.clusterDim.y = 1; attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = a.parts > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, q4_tc_kernel<G, NB, kBias>, a, codes, xs);
 }
 
 template <int G, int NB>
-cudaError_t launch_rows(const TcArgs& a, const Q4Args& q, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
-    return q.biases != nullptr ? launch_as<G, NB, true>(a, q, x, dev, stream) : launch_as<G, NB, false>(a, q, x, dev, stream);
-}
-
-// Activation rows of a tile: the one that leaves the fewest of them empty, the larger of two alike.
-int tile_rows(int M) {
-    if (M <= 32) return 32;
-    if (M <= 64) return 64;
-    const long long by128 = (M + 127ll) / 128 * 128, by192 = (M + 191ll) / 192 * 192;
-    return by128 < by192 ? 128 : 192;
-}
-
-struct Workspace {
-    size_t sums = 0, x16 = 0, total = 0;
-    int m_pad = 0;
-};
-Workspace workspace_of(int M, int K, int groups, bool eight, bool bias) {
-    constexpr size_t kCounters = size_t(1) << 20;      // the products' counters in front of a workspace stay zero
-    Workspace w;
-    w.m_pad = (M + tile_rows(M) - 1) / tile_rows(M) * tile_rows(M);
-    size_t at = kCounters;
-    w.sums = at;
-    if (bias) at += (static_cast<size_t>(groups) * w.m_pad * 4 + 255) / 256 * 256;
-    w.x16 = at;
-    if (eight) at += static_cast<size_t>(M) * K * 2;
-    w.total = bias || eight ? at : 0;
-    return w;
+cudaError_t launch_rows(const Q4Args& q, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
+    return q.biases != nullptr ? launch_as<G, NB, true>(q, x, dev, stream) : launch_as<G, NB, false>(q, x, dev, stream);
 }
 
 template <int G>
-cudaError_t launch_group(const Q4Args& q, char* workspace, const DeviceInfo& dev, cudaStream_t stream) {
-    const bool eight = q.x_scales != nullptr, bias = q.biases != nullptr;
-    const Workspace w = workspace_of(q.M, q.K, q.groups, eight, bias);
-    float* sums = bias ? reinterpret_cast<float*>(workspace + w.sums) : nullptr;
-    uint16_t* x16 = eight ? reinterpret_cast<uint16_t*>(workspace + w.x16) : nullptr;
-    if (eight || bias) {
-        const long long ctas = (static_cast<long long>(q.M) * (q.K / 8) + 255) / 256, most = 8ll * dev.num_sms;
-        const cudaError_t e = launch_programmatic(q4_prepare_kernel<G>, static_cast<unsigned>(ctas < most ? ctas : most), 256u, 0, stream,
-                                                  q.x, eight ? 1 : 0, q.M, q.K, w.m_pad, sums, x16);
-        if (e != cudaSuccess) return e;
-    }
-    TcArgs a = {};
-    a.scales = q.scales; a.biases = q.biases; a.x_scales = q.x_scales; a.sums = sums; a.out = q.out;
-    a.M = q.M; a.K = q.K; a.N = q.N; a.groups = q.groups; a.m_pad = w.m_pad;
-    const void* x = eight ? static_cast<const void*>(x16) : q.x;
-    switch (tile_rows(q.M)) {
-        case 32: return launch_rows<G, 32>(a, q, x, dev, stream);
-        case 64: return launch_rows<G, 64>(a, q, x, dev, stream);
-        case 128: return launch_rows<G, 128>(a, q, x, dev, stream);
-        default: return launch_rows<G, 192>(a, q, x, dev, stream);
-    }
+cudaError_t launch_group(const Q4Args& q, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
+    if (q.M <= 16) return launch_rows<G, 16>(q, x, dev, stream);
+    if (q.M <= 32) return launch_rows<G, 32>(q, x, dev, stream);
+    return q.M <= 64 ? launch_rows<G, 64>(q, x, dev, stream) : launch_rows<G, 128>(q, x, dev, stream);
 }
+
+constexpr size_t kCounters = size_t(1) << 20;      // the products' counters in front of a workspace stay zero
 
 }  // namespace
 
-size_t q4_tc_workspace_bytes(int M, int K, int groups, bool eight, bool bias) { return workspace_of(M, K, groups, eight, bias).total; }
+size_t q4_tc_workspace_bytes(int M, int K, bool eight) { return eight ? kCounters + static_cast<size_t>(M) * K * 2 : 0; }
 
 cudaError_t launch_q4_tc(const Q4Args& q, int group, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
-    char* ws = static_cast<char*>(workspace);
-    return group == 32 ? launch_group<32>(q, ws, dev, stream)
-                       : group == 64 ? launch_group<64>(q, ws, dev, stream) : launch_group<128>(q, ws, dev, stream);
+    const void* x = q.x;
+    if (q.x_scales != nullptr) {
+        uint16_t* x16 = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kCounters);
+        const long long count = static_cast<long long>(q.M) * (q.K / 8), ctas = (count + 255) / 256, most = 8ll * dev.num_sms;
+        const cudaError_t e = launch_programmatic(q4_widen_kernel, static_cast<unsigned>(ctas < most ? ctas : most), 256u, 0, stream,
+                                                  static_cast<const uint8_t*>(q.x), count, x16);
+        if (e != cudaSuccess) return e;
+        x = x16;
+    }
+    return group == 32 ? launch_group<32>(q, x, dev, stream)
+                       : group == 64 ? launch_group<64>(q, x, dev, stream) : launch_group<128>(q, x, dev, stream);
 }
 
 int q4_take_device_error(unsigned int* flags) {
