@@ -544,25 +544,24 @@ TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const ui
  *
  *   codes   device, uint32 [N, K / 8], 16-byte aligned: eight codes c a word, the first in the lowest bits.
  *   scales  device, bf16 [N, K / group]; biases the same, or NULL.
- *           w = scale * c + bias, or scale * (c - 8) without biases.
+ *           w = bf16(scale * c + bias), or bf16(scale * (c - 8)) without biases: one rounding of each weight.
  *   x       device, 16-byte aligned: bf16 [M, K] (x_scales NULL), or e4m3 bytes [M, K] with
  *   x_scales  float [M]: x = code * x_scale, as trellis_rms_norm writes them.
  *   out     device, bf16 [M, N], rounded once from fp32 sums.
- * No weight is rounded: c - 8 and x meet exactly, scales and biases are applied to the sums of each group in
- * fp32.  A row of x that holds an infinity or a NaN has no finite output.
+ * Products are exact, sums fp32.  A row of x that holds an infinity or a NaN has no finite output, and no other row
+ * feels it.
  * group: 32, 64 or 128; K a multiple of it, K and N up to 2^20, M up to 65536 (0: nothing is enqueued).
- *   workspace  256-byte aligned, at least trellis_gemm_q4_workspace_size bytes (NULL where that is 0: for
- *           few rows, and for bf16 activations without biases); its first 1 MiB is not touched, so a product's
- *           workspace will do.
- * The order of all sums is fixed by the sizes.  M > 16 runs on the tensor cores, whose waits are bounded (see
- * trellis_device_status).  One or two kernels are enqueued.
+ *   workspace  256-byte aligned, at least trellis_gemm_q4_workspace_size bytes (NULL where that is 0: for bf16
+ *           activations); its first 1 MiB is not touched, so a product's workspace will do.
+ * The order of all sums is fixed by the sizes.  It runs on the tensor cores (tcgen05), whose waits are bounded (see
+ * trellis_device_status).  One kernel is enqueued, two for 8-bit activations.
  */
 TRELLIS_API int trellis_gemm_q4(const void *x, const float *x_scales, const uint32_t *codes, const uint16_t *scales,
                                 const uint16_t *biases, int M, int K, int N, int group, uint16_t *out,
                                 void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of workspace trellis_gemm_q4 needs; eight and bias: whether it gets x_scales and biases. */
-TRELLIS_API int trellis_gemm_q4_workspace_size(int M, int K, int N, int group, int eight, int bias, size_t *bytes);
+/* Bytes of workspace trellis_gemm_q4 needs; eight: whether it gets x_scales. */
+TRELLIS_API int trellis_gemm_q4_workspace_size(int M, int K, int N, int group, int eight, size_t *bytes);
 
 #ifdef __cplusplus
 }

@@ -75,7 +75,7 @@ def test_norm_refuses(lib, change, want):
     (dict(x=0), -1), (dict(codes=0), -1), (dict(scales=0), -1), (dict(out=0), -1), (dict(M=-1), -2), (dict(K=0), -2), (dict(N=0), -2),
     (dict(group=16), -3), (dict(group=256), -3), (dict(K=224), -2), (dict(M=65537), -3), (dict(K=(1 << 20) + 64), -3), (dict(N=(1 << 20) + 1), -3),
     (dict(x=P + 8), -4), (dict(codes=P + 8), -4), (dict(scales=P + 1), -4), (dict(biases=P + 1), -4), (dict(x_scales=P + 2), -4), (dict(out=P + 1), -4),
-    (dict(M=17, workspace=0), -7), (dict(M=17, workspace_bytes=1 << 20), -7), (dict(M=17, workspace=P + 64), -4)])
+    (dict(x_scales=P, workspace=0), -7), (dict(x_scales=P, workspace_bytes=1 << 20), -7), (dict(x_scales=P, workspace=P + 64), -4)])
 def test_gemm_q4_refuses(lib, change, want):
     assert lib.trellis_gemm_q4(*{**Q4, **change}.values()) == want
 
@@ -85,12 +85,11 @@ def test_nothing_to_do(lib):
     assert lib.trellis_gemm_q4(*{**Q4, "M": 0}.values()) == 0
 
 
-@pytest.mark.parametrize("args,want", [((-1, 256, 5, 64, 0, 0), -2), ((1, 0, 5, 64, 0, 0), -2), ((1, 256, 0, 64, 0, 0), -2),
-                                       ((1, 256, 5, 48, 0, 0), -3), ((1, 96, 5, 64, 0, 0), -2), ((65537, 256, 5, 64, 0, 0), -3)])
+@pytest.mark.parametrize("args,want", [((-1, 256, 5, 64, 0), -2), ((1, 0, 5, 64, 0), -2), ((1, 256, 0, 64, 0), -2),
+                                       ((1, 256, 5, 48, 0), -3), ((1, 96, 5, 64, 0), -2), ((65537, 256, 5, 64, 0), -3)])
 def test_gemm_q4_workspace_size(lib, args, want):
     n = ctypes.c_size_t(7)
     assert lib.trellis_gemm_q4_workspace_size(*args, ctypes.byref(n)) == want
-    assert lib.trellis_gemm_q4_workspace_size(1, 256, 5, 64, 0, 0, None) == -1
-    for M, eight, bias in ((1, 1, 1), (300, 0, 0)):
-        assert lib.trellis_gemm_q4_workspace_size(M, 256, 5, 64, eight, bias, ctypes.byref(n)) == 0 and n.value == 0
-    assert lib.trellis_gemm_q4_workspace_size(300, 256, 5, 64, 1, 0, ctypes.byref(n)) == 0 and n.value >= 300 * 512
+    assert lib.trellis_gemm_q4_workspace_size(1, 256, 5, 64, 0, None) == -1
+    assert lib.trellis_gemm_q4_workspace_size(300, 256, 5, 64, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.trellis_gemm_q4_workspace_size(300, 256, 5, 64, 1, ctypes.byref(n)) == 0 and n.value >= 300 * 512

@@ -54,7 +54,7 @@ SIGNATURES = {
     "trellis_kv_pages_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
     "trellis_rms_norm": (_I, [_P, _LL, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P]),
     "trellis_gemm_q4": (_I, [_P, _P, _P, _P, _P, *[_I] * 4, _P, _P, _SZ, _P]),
-    "trellis_gemm_q4_workspace_size": (_I, [*[_I] * 6, ctypes.POINTER(_SZ)]),
+    "trellis_gemm_q4_workspace_size": (_I, [*[_I] * 5, ctypes.POINTER(_SZ)]),
 }
 
 
@@ -749,9 +749,9 @@ def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, residual_out=None, 
     return (codes, scales) if residual is None else (codes, scales, h)
 
 
-def gemm_q4_workspace_bytes(M, K, N, group, eight=False, bias=False) -> int:
+def gemm_q4_workspace_bytes(M, K, N, group, eight=False) -> int:
     n = ctypes.c_size_t(0)
-    _check(load().trellis_gemm_q4_workspace_size(M, K, N, group, int(eight), int(bias), ctypes.byref(n)),
+    _check(load().trellis_gemm_q4_workspace_size(M, K, N, group, int(eight), ctypes.byref(n)),
            "trellis_gemm_q4_workspace_size")
     return int(n.value)
 
@@ -760,7 +760,8 @@ def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None)
     """out [M, N] bf16 = x [M, K] times 4-bit weights [N, K] transposed.
 
     codes: int32 [N, K / 8], eight codes a word, the first in the lowest bits; scales (and biases): bf16
-    [N, K / group], group 32, 64 or 128.  A weight is scale * code + bias, or scale * (code - 8) without biases.
+    [N, K / group], group 32, 64 or 128.  A weight is scale * code + bias, or scale * (code - 8) without biases,
+    rounded once to bf16.
     x: bf16, or float8_e4m3fn with x_scales float32 [M], as rms_norm_q8 returns them."""
     torch = _torch()
     Tensor, bf16, f32, i32, f8 = (_types or _torch_types())[:5]
@@ -783,7 +784,7 @@ def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None)
     _launch((_lib or load()).trellis_gemm_q4,
             (x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
              None if biases is None else biases.data_ptr(), M, K, N, group, out.data_ptr()), index, stream,
-            lambda: gemm_q4_workspace_bytes(M, K, N, group, x_scales is not None, biases is not None), ask=False)
+            lambda: gemm_q4_workspace_bytes(M, K, N, group, x_scales is not None), ask=False)
     if stream is not None:
         _used_on(stream, x, x_scales, codes, scales, biases, out)
     return out

@@ -1,18 +1,570 @@
-// trellis_gemm_q4: the entry point of the products with 4-bit weights in groups.
-#include "gemm_q4.cuh"
+// Products with 4-bit weights in groups, on the 5th-generation tensor cores.
+//
+//   D[n, m] (tensor memory, fp32) = sum_k w[n, k] x[m, k],   w = bf16(scale c + bias), or bf16(scale (c - 8))
+//
+// Each weight is rounded once to bf16, the type of its scale and of the activations (as the weights of the packed
+// codes are): a code is a whole number of 4 bits, exact in bf16, and one multiply-add of bf16 pairs rounds the
+// weight.  (Kept exact instead, with each group's sum scaled in fp32 on its way out of tensor memory, the
+// product took 328 us at 2000 rows of K = 5120, N = 17408 in groups of 128, 1426 us in groups of 32 with
+// biases; the group sums, not the products, were what it waited for.)
+//
+// A CTA's warps: one loads code tiles, one activation tiles, one issues the products, one keeps tensor
+// memory, 4 load scales and biases, 16 turn codes into weights in tensor memory (the products' first operand), 4 store results.
+// Tiles are 128 weight rows x NB activation rows; a CTA takes tile after tile (those of one block of weight rows
+// next to each other, so that their codes come from L2), its results leaving while the next tile is under way.
+// Where there are few tiles, a cluster of CTAs shares the k of one and adds its parts in shared memory, in order.
+#include <cuda.h>
+#include <cooperative_groups.h>
+#include <mutex>
+
+#include "kernels.h"
+#include "kv_cache.cuh"
+#include "trellis.h"
+#include "trellis_device.cuh"
 
 namespace trellis {
 
-template <> cudaError_t launch_q4_mma<32>(const Q4Args&, const DeviceInfo&, cudaStream_t);
-template <> cudaError_t launch_q4_mma<64>(const Q4Args&, const DeviceInfo&, cudaStream_t);
-template <> cudaError_t launch_q4_mma<128>(const Q4Args&, const DeviceInfo&, cudaStream_t);
+__device__ unsigned int g_q4_error = 0u;
 
 namespace {
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+namespace cg = cooperative_groups;
 
-// More rows than the register tiles' kernel takes at once go to the tensor cores' tiles.
-bool on_tensor_cores(int M) { return M > 0; }
+constexpr int kRows = 128;                 // weight rows of a tile
+constexpr int kStageK = 128;               // k of a stage
+constexpr int kCodeBytes = kRows * 128;    // a code tile: 256 k (two stages) of 128 rows
+
+// Of tensor memory's 512 columns two D buffers take 2 NB, A slots of 64 the others.
+template <int G, int NB>
+struct Q4Shape {
+    static constexpr int kA = NB == 128 ? 4 : 6;                    // stages under way: a slot of weights and one of activations each
+    static constexpr int kXBytes = NB * kStageK * 2;              // two boxes of 64 k
+    static constexpr int kCode = NB == 128 ? 4 : 6;                 // code tiles under way, each with its rows' scales and biases
+    static constexpr int kGroups = 2 * kStageK / G;               // groups of a code tile
+    static constexpr int kScaleBytes = kRows * kGroups * 4;
+    static constexpr int kOffX = 0, kOffCode = kA * kXBytes, kOffScale = kOffCode + kCode * kCodeBytes;
+    static constexpr int kOffBar = kOffScale + kCode * kScaleBytes;
+    static constexpr int kBarFull = 0, kBarEmpty = kA, kBarCode = 2 * kA, kBarCodeEmpty = kBarCode + kCode;
+    static constexpr int kBarD = kBarCodeEmpty + kCode, kBarDEmpty = kBarD + 2, kBars = kBarDEmpty + 2;
+    static constexpr int kOffTaddr = kOffBar + 8 * kBars;
+    static constexpr int kSmem = kOffTaddr + 16 + 1024;             // the base is rounded up to 1 KB
+    static constexpr uint32_t kInstr = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NB >> 3) << 17) |
+                                       (static_cast<uint32_t>(kRows >> 4) << 24);
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
+    static constexpr int kAColumn = 512 - 64 * kA;
+    static_assert(2 * NB <= kAColumn, "tensor memory");
+    static_assert(kRows * NB * 4 <= kOffBar, "a part of the sums fits where operands were");
+};
+constexpr int kDecodeWarps = 16, kStageWarps = 4;    // a stage's weights are made by four warps
+constexpr int kScaleWarps = 4;
+constexpr int kStoreWarps = 4;
+constexpr int kThreads = 32 * (4 + kDecodeWarps + kScaleWarps + kStoreWarps);
+
+struct Q4Args {
+    const uint32_t* codes;          // [N, K / 8]
+    const uint16_t *scales, *biases;  // bf16 [N, groups]; biases may be NULL
+    const float* x_scales;          // [M], or NULL
+    uint16_t* out;                  // bf16 [M, N]
+    int M, K, N, groups;
+    int m_tiles, tiles, parts;
+};
+
+// ---- waits --------------------------------------------------------------------------
+// Every wait is bounded, as the other tensor-core kernels' are: one that runs out sets the error word and its
+// warp leaves its loops; copies in flight are waited for, tensor memory is given back.
+constexpr unsigned long long kWaitNs = 2000000000ull;   // 2 s
+constexpr uint32_t kWaitPollCap = 1u << 26, kPollNs = 1000000u;
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0u;
+}
+// A poll may sleep for as long as its hint: without one a waiting warp comes back often, and the polls of those that wait
+// for most of a tile took issue slots from those that make its weights.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (uint32_t i = 0; i < kWaitPollCap; ++i) {
+        uint32_t ok;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.b32 %0, 1, 0, p;\n}"
+                     : "=r"(ok) : "r"(bar), "r"(parity), "r"(kPollNs) : "memory");
+        if (ok != 0u) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t - t0 > kWaitNs) break;
+    }
+    atomicOr(&g_q4_error, 1u);
+    return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+// K-major, 128-byte swizzle: 1 KB between atoms of 8 rows, version 1, swizzle mode 2.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
+}
+// One product of 16 k, its operands a base and an immediate (a shared-memory offset only reaches the address field).
+template <int kOffA, int kOffB>
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, uint32_t accumulate, uint32_t elected) {
+    asm volatile("{\n .reg .pred p, e;\n .reg .b64 y;\n .reg .b32 x;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %7, 0;\n"
+                 " add.s32 x, %1, %5;\n add.s64 y, %2, %6;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(instr), "r"(accumulate), "n"(kOffA), "n"(kOffB >> 4), "r"(elected) : "memory");
+}
+// A stage's eight products, added to the sum or (the first one of a tile) begun anew.
+template <int NB, int k = 0>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, uint32_t accumulate, uint32_t elected) {
+    mma_step<8 * k, (k >> 2) * (NB * 128) + (k & 3) * 32>(d, a, b, instr, k > 0 ? 1u : accumulate, elected);
+    if constexpr (k + 1 < kStageK / 16) mma_stage<NB, k + 1>(d, a, b, instr, accumulate, elected);
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t elected) {
+    asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+                 " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+                 :: "r"(bar), "r"(elected) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
+// The registers are operands, so that nothing takes them before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+                 :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// The weights of a word's codes 2i and 2i + 1 as bf16 pairs, i = 0 .. 3.  Even and odd codes are masked into the bytes of
+// two words, and one byte permutation a pair puts a code into the low byte of each half (the upper bytes are copies of the
+// sign of a byte that has none).  Such a half is the bf16 number c 2^-133, below the normal ones: multiplied by 2^127 it
+// is c 2^-6, exactly, less 8 2^-6 without biases; and 64 times the scale makes the weight in one rounding.
+template <bool kBias>
+__device__ __forceinline__ void weights_of(uint32_t w, uint32_t scale64, uint32_t bias, uint32_t* p) {
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t c;
+        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(c) : "r"(even), "r"(odd), "r"(0xc480u + 0x1111u * static_cast<uint32_t>(i)));
+        if constexpr (kBias) {
+            uint32_t v;
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(c), "r"(0x7f007f00u));
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(p[i]) : "r"(v), "r"(scale64), "r"(bias));
+        } else {
+            uint32_t v;
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(c), "r"(0x7f007f00u), "r"(0xbe00be00u));
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(v), "r"(scale64));
+        }
+    }
+}
+// 64 times the bf16 number in the low half, in both halves.
+__device__ __forceinline__ uint32_t scale64_of(uint32_t v) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(v, 0u, 0x1010)), "r"(0x42804280u));
+    return r;
+}
+
+template <int G, int NB, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap code_map, const __grid_constant__ CUtensorMap x_map) {
+    using S = Q4Shape<G, NB>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sraw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+    const uint32_t sbase = (sraw + 1023u) & ~1023u;
+    unsigned char* const smem = smem_raw + (sbase - sraw);
+    auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kA; ++i) {
+            mbar_init(bar(S::kBarFull + i), kStageWarps + 1);         // weights by the warps that made them, activations by their bytes
+            mbar_init(bar(S::kBarEmpty + i), 1);
+        }
+        for (int i = 0; i < S::kCode; ++i) {
+            mbar_init(bar(S::kBarCode + i), 1 + kScaleWarps);               // codes by their bytes, scales by the warps that load them
+            mbar_init(bar(S::kBarCodeEmpty + i), 2 * kStageWarps);       // two stages
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(S::kBarD + i), 1);
+            mbar_init(bar(S::kBarDEmpty + i), kStoreWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 3) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(sbase + S::kOffTaddr), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t taddr = *reinterpret_cast<volatile uint32_t*>(smem + S::kOffTaddr);
+    const uint32_t t_a = taddr + S::kAColumn;
+
+    // this CTA's share of k, in blocks of two stages, and its first tile
+    const int part = a.parts > 1 ? static_cast<int>(blockIdx.x) % a.parts : 0;
+    const int blocks = (a.K + 2 * kStageK - 1) / (2 * kStageK), stages = (a.K + kStageK - 1) / kStageK;
+    const int b0 = static_cast<int>(static_cast<long long>(blocks) * part / a.parts);
+    const int b1 = static_cast<int>(static_cast<long long>(blocks) * (part + 1) / a.parts);
+    const int s0 = 2 * b0, s1 = min(2 * b1, stages);
+    const int tile0 = a.parts > 1 ? static_cast<int>(blockIdx.x) / a.parts : static_cast<int>(blockIdx.x);
+    const int tile_step = a.parts > 1 ? a.tiles : static_cast<int>(gridDim.x);
+    if (warp == 0 && lane == 0) {
+        // L2 prefetches only: nothing reaches the CTA before the wait for the previous grid
+        for (int b = b0; b < b1 && b < b0 + S::kCode; ++b)
+            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+                         :: "l"(reinterpret_cast<uint64_t>(&code_map)), "r"(b * 32), "r"(tile0 / a.m_tiles * kRows) : "memory");
+    }
+    griddep_wait();
+    griddep_launch_dependents();        // the next grid may set itself up meanwhile; it waits for this one's end before it reads
+
+    // Slots are taken in turn: use number i of a ring of n is slot i % n, its phase's parity (i / n) & 1.
+    bool alive = true;
+    if (warp == 0) {
+        // ---------------------------------------------------------------- code tiles
+        if (lane == 0) {
+            uint32_t i = 0;
+            for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
+                const int n0 = tile / a.m_tiles * kRows;
+                for (int b = b0; b < b1; ++b, ++i) {
+                    const uint32_t slot = i % S::kCode;
+                    alive = mbar_wait(bar(S::kBarCodeEmpty + slot), ((i / S::kCode) & 1u) ^ 1u);
+                    if (!alive) break;
+                    mbar_expect(bar(S::kBarCode + slot), kCodeBytes);
+                    tma_load_2d(sbase + S::kOffCode + slot * kCodeBytes, &code_map, b * 32, n0, bar(S::kBarCode + slot));
+                }
+            }
+            // what was asked for has landed before the CTA ends
+            // (a tile whose scales were never loaded keeps its barrier: that wait gives up)
+            for (uint32_t j = i > S::kCode ? i - S::kCode : 0u; j < i; ++j) (void)mbar_wait(bar(S::kBarCode + j % S::kCode), (j / S::kCode) & 1u);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- activation tiles
+        if (lane == 0) {
+            uint32_t i = 0;
+            for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
+                const int m0 = tile % a.m_tiles * NB;
+                for (int s = s0; s < s1; ++s, ++i) {
+                    const uint32_t slot = i % S::kA, full = bar(S::kBarFull + slot), dst = sbase + S::kOffX + slot * S::kXBytes;
+                    alive = mbar_wait(bar(S::kBarEmpty + slot), ((i / S::kA) & 1u) ^ 1u);
+                    if (!alive) break;
+                    mbar_expect(full, S::kXBytes);
+                    tma_load_2d(dst, &x_map, s * kStageK, m0, full);
+                    tma_load_2d(dst + NB * 128, &x_map, s * kStageK + 64, m0, full);
+                }
+            }
+            // (a stage whose weights were never made keeps its barrier: that wait gives up)
+            for (uint32_t j = i > S::kA ? i - S::kA : 0u; j < i; ++j) (void)mbar_wait(bar(S::kBarFull + j % S::kA), (j / S::kA) & 1u);
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- products
+        // All lanes walk the same path and one issues, so that the operands live in uniform registers.
+        const uint32_t elected = elect_lane();
+        const uint64_t desc0 = smem_desc(sbase + S::kOffX);
+        uint32_t slot = 0, turn = 0, d = 0;
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
+            const uint32_t td = taddr + (d & 1u) * NB;
+            alive = mbar_wait(bar(S::kBarDEmpty + (d & 1u)), ((d >> 1) & 1u) ^ 1u);
+            for (int s = s0; s < s1 && alive; ++s) {
+                alive = mbar_wait(bar(S::kBarFull + slot), turn);
+                if (!alive) break;
+                fence_after();
+                mma_stage<NB>(td, t_a + slot * 64, desc0 + static_cast<uint64_t>(slot * (S::kXBytes >> 4)), S::kInstr, s > s0 ? 1u : 0u, elected);
+                mma_commit(bar(S::kBarEmpty + slot), elected);
+                if (++slot == S::kA) { slot = 0; turn ^= 1u; }
+            }
+            // also where a wait gave up: what was issued is done before tensor memory is given back
+            mma_commit(bar(S::kBarD + (d & 1u)), elected);
+        }
+        if (d > 0) (void)mbar_wait(bar(S::kBarD + ((d - 1) & 1u)), ((d - 1) >> 1) & 1u);
+    } else if (warp >= 4 && warp < 4 + kDecodeWarps) {
+        // ---------------------------------------------------------------- codes to weights
+        // 32 rows (a lane's row is its lane of tensor memory) of every fourth stage
+        constexpr int kGroups = kDecodeWarps / kStageWarps;
+        static_assert(S::kA >= kGroups, "a slot for each four warps");
+        const int quarter = warp & 3, group = (warp - 4) >> 2;
+        const int row = 32 * quarter + lane;
+        const uint32_t t_row = t_a + (static_cast<uint32_t>(32 * quarter) << 16);
+        const uint32_t row_at = sbase + S::kOffCode + row * 128, turned = static_cast<uint32_t>(row & 7) << 4;
+        constexpr int kPer = kStageK / G;
+        uint32_t slot = group, parity = 1u;                          // of its next stage
+        int ahead = group;                                           // stages from this tile's first to it
+        uint32_t blocks_before = 0;
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ahead -= s1 - s0, blocks_before += b1 - b0) {
+            int s = s0 + ahead;
+            for (; s < s1; s += kGroups) {
+                const uint32_t b_i = blocks_before + static_cast<uint32_t>((s - s0) >> 1), code = b_i % S::kCode;
+                alive = mbar_wait(bar(S::kBarCode + code), (b_i / S::kCode) & 1u);
+                if (!alive) break;
+                // scale, and bias above it, of each of the stage's groups
+                uint32_t now[kPer];
+                const unsigned char* scale_at = smem + S::kOffScale + code * S::kScaleBytes + (2 * row + (s & 1)) * (kPer * 4);
+                if constexpr (kPer == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(scale_at);
+                    now[0] = v.x; now[1] = v.y; now[2] = v.z; now[3] = v.w;
+                } else if constexpr (kPer == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(scale_at);
+                    now[0] = v.x; now[1] = v.y;
+                } else {
+                    now[0] = *reinterpret_cast<const uint32_t*>(scale_at);
+                }
+                const uint32_t at = row_at + code * kCodeBytes + ((s & 1) << 6);
+                uint4 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = lds128(at ^ (turned ^ (16 * j)));
+                alive = mbar_wait(bar(S::kBarEmpty + slot), parity);
+                if (!alive) break;
+                fence_after();
+                const uint32_t to = t_row + slot * 64;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t v = now[j * kPer / 4];
+                    const uint32_t scale = scale64_of(v), bias = kBias ? __byte_perm(v, 0u, 0x3232) : 0u;
+                    uint32_t p[16];
+                    weights_of<kBias>(w[j].x, scale, bias, p); weights_of<kBias>(w[j].y, scale, bias, p + 4);
+                    weights_of<kBias>(w[j].z, scale, bias, p + 8); weights_of<kBias>(w[j].w, scale, bias, p + 12);
+                    tmem_st16(to + 16 * j, p);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(S::kBarFull + slot));
+                    mbar_arrive(bar(S::kBarCodeEmpty + code));
+                    if (s + 1 == s1 && (s & 1) == 0) mbar_arrive(bar(S::kBarCodeEmpty + code));      // for the block's odd stage, which is not there
+                }
+                slot += kGroups;
+                if (slot >= S::kA) { slot -= S::kA; parity ^= 1u; }
+            }
+            ahead = s - s0;
+        }
+    } else if (warp >= 4 + kDecodeWarps && warp < 4 + kDecodeWarps + kScaleWarps) {
+        // ---------------------------------------------------------------- scales and biases
+        // A code tile's rows have 2 to 8 groups each: a load takes as many lanes a row (a lane a row, as the codes are taken,
+        // would look up 32 lines for 64 bytes each time).  A tile's loads are under way while those of the one before land.
+        constexpr int kG = S::kGroups, kLoadRows = 32 / kG;
+        const int first_row = 32 * (warp - 4 - kDecodeWarps) + lane / kG, of = lane % kG;
+        uint32_t i = 0, v[2][kG];
+        auto load = [&](int tile, int b, uint32_t (&r)[kG]) {
+            const int g = b * kG + of;
+#pragma unroll
+            for (int j = 0; j < kG; ++j) {
+                const int n = min(tile / a.m_tiles * kRows + first_row + j * kLoadRows, a.N - 1);
+                const size_t at = static_cast<size_t>(n) * a.groups + g;
+                r[j] = g < a.groups ? __ldg(a.scales + at) : 0u;
+                if constexpr (kBias) r[j] |= g < a.groups ? static_cast<uint32_t>(__ldg(a.biases + at)) << 16 : 0u;
+            }
+        };
+        if (tile0 < a.tiles) load(tile0, b0, v[0]);
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
+            for (int b = b0; b < b1; ++b, ++i) {
+                const int tile_next = b + 1 < b1 ? tile : tile + tile_step;
+                if (tile_next < a.tiles) load(tile_next, b + 1 < b1 ? b + 1 : b0, v[1]);
+                const uint32_t slot = i % S::kCode;
+                alive = mbar_wait(bar(S::kBarCodeEmpty + slot), ((i / S::kCode) & 1u) ^ 1u);
+                if (!alive) break;
+                uint32_t* to = reinterpret_cast<uint32_t*>(smem + S::kOffScale + slot * S::kScaleBytes) + first_row * kG + of;
+#pragma unroll
+                for (int j = 0; j < kG; ++j) to[j * 32] = v[0][j];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::kBarCode + slot));
+#pragma unroll
+                for (int j = 0; j < kG; ++j) v[0][j] = v[1][j];
+            }
+        }
+    } else if (warp >= 4 + kDecodeWarps + kScaleWarps) {
+        // ---------------------------------------------------------------- results
+        const int quarter = warp & 3;
+        constexpr int kStep = NB < 32 ? 16 : 32;
+        uint32_t d = 0;
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
+            const int m0 = tile % a.m_tiles * NB, n = tile / a.m_tiles * kRows + 32 * quarter + lane;
+            const uint32_t t_row = taddr + (static_cast<uint32_t>(32 * quarter) << 16) + (d & 1u) * NB;
+            alive = mbar_wait(bar(S::kBarD + (d & 1u)), (d >> 1) & 1u);
+            if (!alive) break;
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NB; c += kStep) {
+                uint32_t v[kStep / 16][16];
+#pragma unroll
+                for (int i = 0; i < kStep / 16; ++i) tmem_ld16(v[i], t_row + c + 16 * i);
+#pragma unroll
+                for (int i = 0; i < kStep / 16; ++i) tmem_wait_ld(v[i]);
+                if (c + kStep == NB) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(S::kBarDEmpty + (d & 1u)));
+                }
+                if (a.parts > 1) {
+                    // [column][row], where the operands were: all of the products are done
+                    float* part_sums = reinterpret_cast<float*>(smem) + c * kRows + 32 * quarter + lane;
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) part_sums[j * kRows] = __uint_as_float(v[j / 16][j % 16]);
+                } else if (n < a.N) {
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) {
+                        const int m = m0 + c + j;
+                        if (m >= a.M) break;
+                        float y = __uint_as_float(v[j / 16][j % 16]);
+                        if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m);
+                        a.out[static_cast<size_t>(m) * a.N + n] = bf16_bits_rn(y);
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (a.parts > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        const int m0 = tile0 % a.m_tiles * NB, n0 = tile0 / a.m_tiles * kRows;
+        const int row = threadIdx.x % kRows;
+        constexpr int kStride = kThreads / kRows;
+        float* mine = reinterpret_cast<float*>(smem);
+        for (int col = part * kStride + threadIdx.x / kRows; col < NB && m0 + col < a.M; col += kStride * a.parts) {
+            float y = 0.0f;
+            for (int r = 0; r < a.parts; ++r) y += cluster.map_shared_rank(mine, r)[col * kRows + row];
+            if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m0 + col);
+            if (n0 + row < a.N) a.out[static_cast<size_t>(m0 + col) * a.N + n0 + row] = bf16_bits_rn(y);
+        }
+        cluster.sync();                 // the others may still be reading this CTA's part
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(512) : "memory");
+    }
+}
+
+// Before the product: 8-bit activations as bf16, exactly.
+__device__ __forceinline__ uint4 widened(uint2 v) {
+    uint32_t f[4], r[4];
+    e4m3x4_to_f16x2(v.x, f[0], f[1]);
+    e4m3x4_to_f16x2(v.y, f[2], f[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 d = f16x2_to_f32(f[i]);
+        r[i] = pack_bf16x2(d.x, d.y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__global__ void __launch_bounds__(256) q4_widen_kernel(const uint8_t* x, long long count, uint16_t* x16) {
+    griddep_wait();
+    for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < count; e += static_cast<long long>(gridDim.x) * 256)
+        *reinterpret_cast<uint4*>(x16 + e * 8) = widened(__ldg(reinterpret_cast<const uint2*>(x) + e));
+    griddep_launch_dependents();
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// Rows of `width` elements as boxes of 128 bytes x `rows`, swizzled; what lies outside is zero.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void* p, int width, int height, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(height)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * bytes};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / bytes), static_cast<cuuint32_t>(rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int G, int NB, bool kBias>
+cudaError_t launch_as(Q4Args a, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
+    using S = Q4Shape<G, NB>;
+    static std::atomic<unsigned long long> done{0};
+    if (!smem_opt_in(q4_kernel<G, NB, kBias>, S::kSmem, done)) return cudaErrorInvalidValue;
+    CUtensorMap codes, xs;
+    if (!make_map(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.codes, a.K / 8, a.N, kRows) ||
+        !make_map(&xs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, a.K, a.M, NB))
+        return cudaErrorInvalidValue;
+    a.m_tiles = (a.M + NB - 1) / NB;
+    a.tiles = (a.N + kRows - 1) / kRows * a.m_tiles;
+    // parts of k for clusters of CTAs, while all CTAs still run at once and each has two blocks of k or more
+    const int blocks = (a.K + 2 * kStageK - 1) / (2 * kStageK);
+    a.parts = 1;
+    while (a.parts < 8 && (a.parts + 1ll) * a.tiles <= (a.parts < 4 ? dev.num_sms : dev.num_sms / 2) && blocks >= 2 * (a.parts + 1)) ++a.parts;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.parts > 1 ? a.tiles * a.parts : (a.tiles < dev.num_sms ? a.tiles : dev.num_sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.parts; attr[1].val.clusterDim.y = 1; attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.parts > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, q4_kernel<G, NB, kBias>, a, codes, xs);
+}
+
+template <int G, int NB>
+cudaError_t launch_rows(const Q4Args& a, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
+    return a.biases != nullptr ? launch_as<G, NB, true>(a, x, dev, stream) : launch_as<G, NB, false>(a, x, dev, stream);
+}
+
+template <int G>
+cudaError_t launch_group(const Q4Args& a, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
+    if (a.M <= 16) return launch_rows<G, 16>(a, x, dev, stream);
+    if (a.M <= 32) return launch_rows<G, 32>(a, x, dev, stream);
+    return a.M <= 64 ? launch_rows<G, 64>(a, x, dev, stream) : launch_rows<G, 128>(a, x, dev, stream);
+}
+
+constexpr size_t kCounters = size_t(1) << 20;      // the products' counters in front of a workspace stay zero
+size_t workspace_bytes_of(int M, int K, bool eight) { return eight ? kCounters + static_cast<size_t>(M) * K * 2 : 0; }
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 int check_sizes(int M, int K, int N, int group) {
     if (M < 0 || K < 1 || N < 1) return TRELLIS_ERR_SHAPE;
@@ -24,17 +576,27 @@ int check_sizes(int M, int K, int N, int group) {
 
 }  // namespace
 
+int q4_take_device_error(unsigned int* flags) {
+    unsigned int v = 0u;
+    if (cudaMemcpyFromSymbol(&v, g_q4_error, sizeof(v)) != cudaSuccess) return -5;
+    if (v != 0u) {
+        const unsigned int zero = 0u;
+        if (cudaMemcpyToSymbol(g_q4_error, &zero, sizeof(zero)) != cudaSuccess) return -5;
+    }
+    *flags = v;
+    return 0;
+}
+
 }  // namespace trellis
 
 extern "C" {
 
-int trellis_gemm_q4_workspace_size(int M, int K, int N, int group, int eight, int bias, size_t* bytes) {
+int trellis_gemm_q4_workspace_size(int M, int K, int N, int group, int eight, size_t* bytes) {
     using namespace trellis;
     if (bytes == nullptr) return TRELLIS_ERR_NULL;
     const int rc = check_sizes(M, K, N, group);
     if (rc != TRELLIS_OK) return rc;
-    *bytes = on_tensor_cores(M) ? q4_tc_workspace_bytes(M, K, eight != 0) : 0;
-    (void)bias;
+    *bytes = workspace_bytes_of(M, K, eight != 0);
     return TRELLIS_OK;
 }
 
@@ -47,18 +609,25 @@ int trellis_gemm_q4(const void* x, const float* x_scales, const uint32_t* codes,
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(biases, 2) || !aligned(x_scales, 4) || !aligned(out, 2))
         return TRELLIS_ERR_ALIGN;
     if (M == 0) return TRELLIS_OK;
-    const size_t need = on_tensor_cores(M) ? q4_tc_workspace_bytes(M, K, x_scales != nullptr) : 0;
-    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return TRELLIS_ERR_WORKSPACE;
-    if (need > 0 && !aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
+    const bool eight = x_scales != nullptr;
+    if (eight && (workspace == nullptr || workspace_bytes < workspace_bytes_of(M, K, true))) return TRELLIS_ERR_WORKSPACE;
+    if (eight && !aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
     DeviceInfo dev;
     rc = device_info(dev);
     if (rc != TRELLIS_OK) return rc;
-    Q4Args a;
-    a.x = x; a.codes = codes; a.scales = scales; a.biases = biases; a.x_scales = x_scales; a.out = out;
+    if (eight) {
+        uint16_t* x16 = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kCounters);
+        const long long count = static_cast<long long>(M) * (K / 8), ctas = (count + 255) / 256, most = 8ll * dev.num_sms;
+        if (launch_programmatic(q4_widen_kernel, static_cast<unsigned>(ctas < most ? ctas : most), 256u, 0, stream,
+                                static_cast<const uint8_t*>(x), count, x16) != cudaSuccess)
+            return TRELLIS_ERR_CUDA;
+        x = x16;
+    }
+    Q4Args a = {};
+    a.codes = codes; a.scales = scales; a.biases = biases; a.x_scales = x_scales; a.out = out;
     a.M = M; a.K = K; a.N = N; a.groups = K / group;
-    const cudaError_t e = on_tensor_cores(M) ? launch_q4_tc(a, group, workspace, dev, stream)
-                          : group == 32 ? launch_q4_mma<32>(a, dev, stream)
-                          : group == 64 ? launch_q4_mma<64>(a, dev, stream) : launch_q4_mma<128>(a, dev, stream);
+    const cudaError_t e = group == 32 ? launch_group<32>(a, x, dev, stream)
+                          : group == 64 ? launch_group<64>(a, x, dev, stream) : launch_group<128>(a, x, dev, stream);
     return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
 }
 
