@@ -105,6 +105,20 @@ __device__ __forceinline__ Growth growth(const GrowArgs& a, int s) {
     return r;
 }
 
+// A warp's way through `count` page ids: eight loads a lane before the first use (one at a time, 64 prompts of up to 16384
+// tokens in pages of 32 took 14.5 us).
+template <class Load, class Use>
+__device__ __forceinline__ void eight_at_once(long long count, int lane, Load load, Use use) {
+    for (long long i0 = lane; i0 < count; i0 += 256) {
+        int id[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) id[j] = i0 + 32 * j < count ? load(i0 + 32 * j) : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i0 + 32 * j < count) use(i0 + 32 * j, id[j]);
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) kv_grow_kernel(const __grid_constant__ GrowArgs a) {
     __shared__ int part[kWarps];
     __shared__ long long part64[kWarps];
@@ -144,16 +158,14 @@ __global__ void __launch_bounds__(kThreads) kv_grow_kernel(const __grid_constant
             const long long need = r.want - r.have, at = a.upto[s];
             ok = need == 0 || at + need <= found;
             if (ok)
-                for (long long i = lane; i < need; i += 32) {
-                    const int id = a.list[at + i];
+                eight_at_once(need, lane, [&](long long i) { return a.list[at + i]; }, [&](long long i, int id) {
                     row[r.have + i] = id;
                     a.refs[id] = 1;
-                }
+                });
         } else if (ok && r.g < 0) {
-            for (long long i = r.want + lane; i < r.have; i += 32) {
-                const int id = row[i];
+            eight_at_once(r.have - r.want, lane, [&](long long i) { return row[r.want + i]; }, [&](long long, int id) {
                 if (id >= 0 && id < a.num_pages) atomicSub(a.refs + id, 1);
-            }
+            });
         }
         if (lane == 0) {
             if (ok && r.g != 0) a.kv_len[s] = static_cast<int>(r.now);

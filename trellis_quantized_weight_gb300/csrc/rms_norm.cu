@@ -67,8 +67,8 @@ __device__ __forceinline__ void reduce(float& sum, uint32_t& most, float2* part)
 
 // kVec: 8 values by one 16-byte access; otherwise single values, a thread apart.
 // kPer: units of 8 values that a thread holds.
-template <int kPer, bool kVec, bool kWarpRow, bool kEight>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) rms_norm_kernel(const __grid_constant__ NormArgs a) {
+template <int kPer, bool kVec, bool kWarpRow, bool kEight, int kThreads>
+__global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float2 part[2][32];
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
     const long long step = static_cast<long long>(gridDim.x) * (kWarpRow ? 8 : 1);
@@ -219,32 +219,31 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
 
 constexpr int kMostThreads = 1024, kMostPer = 4;
 
-template <int kPer, bool kVec, bool kEight>
-cudaError_t launch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-    const int units = (a.width + 7) / 8;
-    if (units <= 32 * kPer) {
-        const long long ctas = (a.rows + 7) / 8, most = 8ll * dev.num_sms;
-        return launch_programmatic(rms_norm_kernel<kPer, kVec, true, kEight>, static_cast<unsigned>(ctas < most ? ctas : most), 256u,
-                                   0, stream, a);
-    }
-    const int threads = ((units + kPer - 1) / kPer + 31) / 32 * 32;
-    const long long most = static_cast<long long>(2048 / threads) * dev.num_sms;
-    return launch_programmatic(rms_norm_kernel<kPer, kVec, false, kEight>, static_cast<unsigned>(a.rows < most ? a.rows : most),
-                               static_cast<unsigned>(threads), 0, stream, a);
+template <int kPer, bool kVec, bool kEight, bool kWarpRow, int kThreads>
+cudaError_t launch(const NormArgs& a, int threads, const DeviceInfo& dev, cudaStream_t stream) {
+    // as many CTAs as run at once, each with its weights in registers: the next row's CTA would load them again
+    auto* kernel = rms_norm_kernel<kPer, kVec, kWarpRow, kEight, kThreads>;
+    const int per_sm = 2048 / threads;
+    const long long ctas = kWarpRow ? (a.rows + 7) / 8 : a.rows, most = static_cast<long long>(per_sm) * dev.num_sms;
+    return launch_programmatic(kernel, static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(threads), 0, stream, a);
 }
 
 template <bool kVec, bool kEight>
 cudaError_t launch_rows(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
     const int units = (a.width + 7) / 8;
+    auto threads = [&](int per) { return ((units + per - 1) / per + 31) / 32 * 32; };
     if (units > kMostThreads * kMostPer) {
         const long long most = 2ll * dev.num_sms;
         return launch_programmatic(rms_norm_wide_kernel<kEight>, static_cast<unsigned>(a.rows < most ? a.rows : most), 1024u, 0, stream, a);
     }
-    if (units <= 32) return launch<1, kVec, kEight>(a, dev, stream);
-    if (units <= 64 || units > 2 * kMostThreads) return units <= 64 ? launch<2, kVec, kEight>(a, dev, stream) : launch<4, kVec, kEight>(a, dev, stream);
+    if (units <= 32) return launch<1, kVec, kEight, true, 256>(a, 256, dev, stream);
+    if (units <= 64) return launch<2, kVec, kEight, true, 256>(a, 256, dev, stream);
     // few rows: one unit a thread where that fits, for the shortest chain
-    if (a.rows < dev.num_sms && units <= kMostThreads) return launch<1, kVec, kEight>(a, dev, stream);
-    return units <= 512 || units > 1024 ? launch<2, kVec, kEight>(a, dev, stream) : launch<4, kVec, kEight>(a, dev, stream);
+    if (a.rows < dev.num_sms && units <= kMostThreads) return launch<1, kVec, kEight, false, 1024>(a, threads(1), dev, stream);
+    // two units a thread: 8165 rows of 5120 with residual to 8 bits take 50 us, with one 64 to 68, four 59, five 54
+    if (units <= 1024) return launch<2, kVec, kEight, false, 512>(a, threads(2), dev, stream);
+    if (units <= 2048) return launch<2, kVec, kEight, false, 1024>(a, threads(2), dev, stream);
+    return launch<4, kVec, kEight, false, 1024>(a, threads(4), dev, stream);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
