@@ -154,3 +154,22 @@ def test_no_rows_out_and_refusals():
             bad()
     with pytest.raises(tq.TrellisError):
         tq.gemm_q4(x, codes, torch.ones(48, 16).bfloat16().cuda())
+
+
+@pytest.mark.parametrize("M,K,N,group,bias,eight", [(300, 5120, 1111, 32, True, False), (300, 5120, 1111, 64, True, False),
+                                                    (16, 5120, 1111, 32, True, False), (64, 1152, 3001, 128, False, True),
+                                                    (2000, 1024, 1000, 128, True, False)])
+def test_many_calls_give_equal_bits(M, K, N, group, bias, eight):
+    """Operands that a slow reader still needs are not overwritten: a few calls in a hundred differed where they could be."""
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(4)
+    codes, scales, biases = weights(N, K, group, bias, g)
+    x = torch.randn(M, K, generator=g).bfloat16().cuda()
+    x_scales = None
+    if eight:
+        x, x_scales = tq.rms_norm_q8(x, torch.ones(K).bfloat16().cuda())
+    first = tq.gemm_q4(x, codes, scales, biases, x_scales=x_scales)
+    check(first, *reference(x, codes, scales, biases, x_scales), K)
+    differ = sum(not torch.equal(tq.gemm_q4(x, codes, scales, biases, x_scales=x_scales), first) for _ in range(300))
+    assert differ == 0
+    assert tq.load().trellis_device_status(None) == 0

@@ -34,18 +34,25 @@ constexpr int kRows = 128;                 // weight rows of a tile
 constexpr int kStageK = 128;               // k of a stage
 constexpr int kCodeBytes = kRows * 128;    // a code tile: 256 k (two stages) of 128 rows
 
+constexpr int kDecodeWarps = 16, kStageWarps = 4;    // a stage's weights are made by four warps
+constexpr int kScaleWarps = 4, kScaleGroups = 16;    // 32 bytes of a row's scales (and of its biases) are loaded at once
+constexpr int kStoreWarps = 4;
+constexpr int kThreads = 32 * (4 + kDecodeWarps + kScaleWarps + kStoreWarps);
+
 // Of tensor memory's 512 columns two D buffers take 2 NB, A slots of 64 the others.
 template <int G, int NB>
 struct Q4Shape {
     static constexpr int kA = NB == 128 ? 4 : 6;                    // stages under way: a slot of weights and one of activations each
     static constexpr int kXBytes = NB * kStageK * 2;              // two boxes of 64 k
-    static constexpr int kCode = NB == 128 ? 4 : 6;                 // code tiles under way, each with its rows' scales and biases
-    static constexpr int kGroups = 2 * kStageK / G;               // groups of a code tile
-    static constexpr int kScaleBytes = kRows * kGroups * 4;
-    static constexpr int kOffX = 0, kOffCode = kA * kXBytes, kOffScale = kOffCode + kCode * kCodeBytes;
-    static constexpr int kOffBar = kOffScale + kCode * kScaleBytes;
+    static constexpr int kPer = kStageK / G;                        // groups of a stage
+    static constexpr int kScaleStages = kScaleGroups / kPer;        // stages of a run of scales
+    static constexpr int kScaleBytes = kRows * kScaleGroups * 4, kScale = 2;
+    static constexpr int kOffX = 0, kOffScale = kA * kXBytes, kOffCode = kOffScale + kScale * kScaleBytes;
+    static constexpr int kCode = 4;                                 // code tiles under way (6 and 8 take 0.3 to 0.7 us more: the first ones come later)
+    static constexpr int kOffBar = kOffCode + kCode * kCodeBytes;
     static constexpr int kBarFull = 0, kBarEmpty = kA, kBarCode = 2 * kA, kBarCodeEmpty = kBarCode + kCode;
-    static constexpr int kBarD = kBarCodeEmpty + kCode, kBarDEmpty = kBarD + 2, kBars = kBarDEmpty + 2;
+    static constexpr int kBarD = kBarCodeEmpty + kCode, kBarDEmpty = kBarD + 2;
+    static constexpr int kBarScale = kBarDEmpty + 2, kBarScaleEmpty = kBarScale + kScale, kBars = kBarScaleEmpty + kScale;
     static constexpr int kOffTaddr = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffTaddr + 16 + 1024;             // the base is rounded up to 1 KB
     static constexpr uint32_t kInstr = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NB >> 3) << 17) |
@@ -55,10 +62,6 @@ struct Q4Shape {
     static_assert(2 * NB <= kAColumn, "tensor memory");
     static_assert(kRows * NB * 4 <= kOffBar, "a part of the sums fits where operands were");
 };
-constexpr int kDecodeWarps = 16, kStageWarps = 4;    // a stage's weights are made by four warps
-constexpr int kScaleWarps = 4;
-constexpr int kStoreWarps = 4;
-constexpr int kThreads = 32 * (4 + kDecodeWarps + kScaleWarps + kStoreWarps);
 
 struct Q4Args {
     const uint32_t* codes;          // [N, K / 8]
@@ -80,6 +83,9 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_many(uint32_t bar, int count) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(count) : "memory");
 }
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
@@ -165,7 +171,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
 
@@ -198,6 +204,9 @@ __device__ __forceinline__ uint32_t scale64_of(uint32_t v) {
     return r;
 }
 
+// Where group g of a row's sixteen stands: fours of them are turned by the row.
+__device__ __forceinline__ int scale_column(int row, int g) { return g ^ (((row >> 1) & 3) << 2); }
+
 template <int G, int NB, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
 q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap code_map, const __grid_constant__ CUtensorMap x_map) {
@@ -215,12 +224,16 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
             mbar_init(bar(S::kBarEmpty + i), 1);
         }
         for (int i = 0; i < S::kCode; ++i) {
-            mbar_init(bar(S::kBarCode + i), 1 + kScaleWarps);               // codes by their bytes, scales by the warps that load them
+            mbar_init(bar(S::kBarCode + i), 1);
             mbar_init(bar(S::kBarCodeEmpty + i), 2 * kStageWarps);       // two stages
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(S::kBarD + i), 1);
             mbar_init(bar(S::kBarDEmpty + i), kStoreWarps);
+        }
+        for (int i = 0; i < S::kScale; ++i) {
+            mbar_init(bar(S::kBarScale + i), kScaleWarps);
+            mbar_init(bar(S::kBarScaleEmpty + i), kStageWarps * S::kScaleStages);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -269,7 +282,6 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 }
             }
             // what was asked for has landed before the CTA ends
-            // (a tile whose scales were never loaded keeps its barrier: that wait gives up)
             for (uint32_t j = i > S::kCode ? i - S::kCode : 0u; j < i; ++j) (void)mbar_wait(bar(S::kBarCode + j % S::kCode), (j / S::kCode) & 1u);
         }
     } else if (warp == 1) {
@@ -320,27 +332,30 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         const int row = 32 * quarter + lane;
         const uint32_t t_row = t_a + (static_cast<uint32_t>(32 * quarter) << 16);
         const uint32_t row_at = sbase + S::kOffCode + row * 128, turned = static_cast<uint32_t>(row & 7) << 4;
-        constexpr int kPer = kStageK / G;
+        constexpr int kPer = S::kPer;
         uint32_t slot = group, parity = 1u;                          // of its next stage
         int ahead = group;                                           // stages from this tile's first to it
-        uint32_t blocks_before = 0;
-        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ahead -= s1 - s0, blocks_before += b1 - b0) {
+        uint32_t blocks_before = 0, runs_before = 0;
+        const uint32_t runs = (s1 - s0 + S::kScaleStages - 1) / S::kScaleStages;
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ahead -= s1 - s0, blocks_before += b1 - b0, runs_before += runs) {
             int s = s0 + ahead;
             for (; s < s1; s += kGroups) {
                 const uint32_t b_i = blocks_before + static_cast<uint32_t>((s - s0) >> 1), code = b_i % S::kCode;
-                alive = mbar_wait(bar(S::kBarCode + code), (b_i / S::kCode) & 1u);
+                const uint32_t run = runs_before + static_cast<uint32_t>(s - s0) / S::kScaleStages, run_slot = run % S::kScale;
+                alive = mbar_wait(bar(S::kBarCode + code), (b_i / S::kCode) & 1u) && mbar_wait(bar(S::kBarScale + run_slot), (run / S::kScale) & 1u);
                 if (!alive) break;
-                // scale, and bias above it, of each of the stage's groups
-                uint32_t now[kPer];
-                const unsigned char* scale_at = smem + S::kOffScale + code * S::kScaleBytes + (2 * row + (s & 1)) * (kPer * 4);
+                // scale, and bias above it, of each of the stage's groups; a row's are turned so that the rows of a quarter
+                // warp lie in different banks
+                uint32_t v[kPer];
+                const uint32_t scale_at = sbase + S::kOffScale + run_slot * S::kScaleBytes + row * (kScaleGroups * 4) +
+                                          scale_column(row, static_cast<int>(static_cast<uint32_t>(s - s0) % S::kScaleStages * kPer)) * 4;
                 if constexpr (kPer == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(scale_at);
-                    now[0] = v.x; now[1] = v.y; now[2] = v.z; now[3] = v.w;
+                    const uint4 u = lds128(scale_at);
+                    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
                 } else if constexpr (kPer == 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(scale_at);
-                    now[0] = v.x; now[1] = v.y;
+                    asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(scale_at));
                 } else {
-                    now[0] = *reinterpret_cast<const uint32_t*>(scale_at);
+                    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(scale_at));
                 }
                 const uint32_t at = row_at + code * kCodeBytes + ((s & 1) << 6);
                 uint4 w[4];
@@ -352,8 +367,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 const uint32_t to = t_row + slot * 64;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t v = now[j * kPer / 4];
-                    const uint32_t scale = scale64_of(v), bias = kBias ? __byte_perm(v, 0u, 0x3232) : 0u;
+                    const uint32_t scale = scale64_of(v[j * kPer / 4]), bias = kBias ? __byte_perm(v[j * kPer / 4], 0u, 0x3232) : 0u;
                     uint32_t p[16];
                     weights_of<kBias>(w[j].x, scale, bias, p); weights_of<kBias>(w[j].y, scale, bias, p + 4);
                     weights_of<kBias>(w[j].z, scale, bias, p + 8); weights_of<kBias>(w[j].w, scale, bias, p + 12);
@@ -362,8 +376,11 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 fence_before();
                 __syncwarp();
+                // Codes and scales make room only now that the weights made of them are stored, so that their loads are known to
+                // be over: given back right after the loads were issued, now and then they were those of the next tile in the slot.
                 if (lane == 0) {
                     mbar_arrive(bar(S::kBarFull + slot));
+                    mbar_arrive(bar(S::kBarScaleEmpty + run_slot));
                     mbar_arrive(bar(S::kBarCodeEmpty + code));
                     if (s + 1 == s1 && (s & 1) == 0) mbar_arrive(bar(S::kBarCodeEmpty + code));      // for the block's odd stage, which is not there
                 }
@@ -374,36 +391,44 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         }
     } else if (warp >= 4 + kDecodeWarps && warp < 4 + kDecodeWarps + kScaleWarps) {
         // ---------------------------------------------------------------- scales and biases
-        // A code tile's rows have 2 to 8 groups each: a load takes as many lanes a row (a lane a row, as the codes are taken,
-        // would look up 32 lines for 64 bytes each time).  A tile's loads are under way while those of the one before land.
-        constexpr int kG = S::kGroups, kLoadRows = 32 / kG;
-        const int first_row = 32 * (warp - 4 - kDecodeWarps) + lane / kG, of = lane % kG;
-        uint32_t i = 0, v[2][kG];
-        auto load = [&](int tile, int b, uint32_t (&r)[kG]) {
-            const int g = b * kG + of;
+        // Sixteen lanes a row, 32 bytes (a lane a row, stage by stage as the codes are taken, looks up 32 lines for 64 bytes and
+        // fetches each sector again and again).  A run's loads are under way while those of the one before are used.
+        constexpr int kLoads = 16;                                   // of two rows each
+        const int first_row = 32 * (warp - 4 - kDecodeWarps) + (lane >> 4), of = lane & 15;
+        const int runs = (s1 - s0 + S::kScaleStages - 1) / S::kScaleStages;
+        uint32_t i = 0, v[kLoads];
+        auto load = [&](int tile, int run) {
+            const int g = s0 * S::kPer + run * kScaleGroups + of;
+            const bool has = g < a.groups;
 #pragma unroll
-            for (int j = 0; j < kG; ++j) {
-                const int n = min(tile / a.m_tiles * kRows + first_row + j * kLoadRows, a.N - 1);
+            for (int j = 0; j < kLoads; ++j) {
+                const int n = min(tile / a.m_tiles * kRows + first_row + 2 * j, a.N - 1);
                 const size_t at = static_cast<size_t>(n) * a.groups + g;
-                r[j] = g < a.groups ? __ldg(a.scales + at) : 0u;
-                if constexpr (kBias) r[j] |= g < a.groups ? static_cast<uint32_t>(__ldg(a.biases + at)) << 16 : 0u;
+                v[j] = has ? __ldg(a.scales + at) : 0u;
+                if constexpr (kBias) v[j] |= has ? static_cast<uint32_t>(__ldg(a.biases + at)) << 16 : 0u;
             }
         };
-        if (tile0 < a.tiles) load(tile0, b0, v[0]);
+        if (tile0 < a.tiles) load(tile0, 0);
         for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
-            for (int b = b0; b < b1; ++b, ++i) {
-                const int tile_next = b + 1 < b1 ? tile : tile + tile_step;
-                if (tile_next < a.tiles) load(tile_next, b + 1 < b1 ? b + 1 : b0, v[1]);
-                const uint32_t slot = i % S::kCode;
-                alive = mbar_wait(bar(S::kBarCodeEmpty + slot), ((i / S::kCode) & 1u) ^ 1u);
+            for (int run = 0; run < runs; ++run, ++i) {
+                const uint32_t slot = i % S::kScale;
+                alive = mbar_wait(bar(S::kBarScaleEmpty + slot), ((i / S::kScale) & 1u) ^ 1u);
                 if (!alive) break;
-                uint32_t* to = reinterpret_cast<uint32_t*>(smem + S::kOffScale + slot * S::kScaleBytes) + first_row * kG + of;
+                uint32_t* to = reinterpret_cast<uint32_t*>(smem + S::kOffScale + slot * S::kScaleBytes);
 #pragma unroll
-                for (int j = 0; j < kG; ++j) to[j * 32] = v[0][j];
+                for (int j = 0; j < kLoads; ++j) {
+                    const int r = first_row + 2 * j;
+                    to[r * kScaleGroups + scale_column(r, of)] = v[j];
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::kBarCode + slot));
-#pragma unroll
-                for (int j = 0; j < kG; ++j) v[0][j] = v[1][j];
+                if (lane == 0) {
+                    mbar_arrive(bar(S::kBarScale + slot));
+                    // for the stages that a tile's last run does not have
+                    const int missing = (run + 1) * S::kScaleStages - (s1 - s0);
+                    if (missing > 0 && warp == 4 + kDecodeWarps) mbar_arrive_many(bar(S::kBarScaleEmpty + slot), kStageWarps * missing);
+                }
+                const bool more = run + 1 < runs;
+                if (more || tile + tile_step < a.tiles) load(more ? tile : tile + tile_step, more ? run + 1 : 0);
             }
         }
     } else if (warp >= 4 + kDecodeWarps + kScaleWarps) {
