@@ -405,12 +405,12 @@ _types = None
 
 def _torch_types():
     """Tensor, bfloat16, float32, int32, float8_e4m3fn, empty, the current stream's handle, whether it is capturing,
-    and the current device."""
+    the current device, and bool."""
     global _types
     if _types is None:
         torch = _torch()
         _types = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.empty,
-                  torch._C._cuda_getCurrentRawStream, torch._C._cuda_isCurrentStreamCapturing, torch._C._cuda_getDevice)
+                  torch._C._cuda_getCurrentRawStream, torch._C._cuda_isCurrentStreamCapturing, torch._C._cuda_getDevice, torch.bool)
     return _types
 
 
@@ -435,9 +435,9 @@ def _require_on(t, name, dtype, ndim, index):
     return shape
 
 
-def _require_cache(cache, starts, kv_len, pages):
-    """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns, device index)."""
-    Tensor, _, f32, i32, f8 = (_types or _torch_types())[:5]
+def _require_codes(cache):
+    """Checks a cache's four tensors; returns (codes' shape, device index)."""
+    Tensor, _, f32, _, f8 = (_types or _torch_types())[:5]
     k, v, ks, vs = cache
     if not isinstance(k, Tensor) or (index := k.get_device()) < 0:
         raise ValueError("the cache must be CUDA tensors")
@@ -451,6 +451,13 @@ def _require_cache(cache, starts, kv_len, pages):
         raise ValueError("the cache must be on one device")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("the cache must be contiguous")
+    return shape, index
+
+
+def _require_cache(cache, starts, kv_len, pages):
+    """Checks a cache and its sequences' arrays; returns (codes' shape, sequences, table columns, device index)."""
+    shape, index = _require_codes(cache)
+    i32 = _types[3]
     n, = _require_on(starts, "starts", i32, 1, index)
     seqs, = _require_on(kv_len, "kv_len", i32, 1, index)
     rows, cols = _require_on(pages, "pages", i32, 2, index)
@@ -602,22 +609,8 @@ def kv_pages_workspace_bytes(seqs, columns, pages) -> int:
     return int(n.value)
 
 
-def _require_codes(cache, name):
-    """Checks a cache's four tensors; returns (codes' shape, device index)."""
-    Tensor, _, f32, _, f8 = (_types or _torch_types())[:5]
-    k, v, ks, vs = cache
-    if not isinstance(k, Tensor) or (index := k.get_device()) < 0:
-        raise ValueError(f"{name} must be CUDA tensors")
-    shape = _require_on(k, f"{name}'s codes", f8, 4, index)
-    want = (shape[0], shape[1], shape[2] // 16)
-    if _require_on(v, f"{name}'s codes", f8, 4, index) != shape or _require_on(ks, f"{name}'s scales", f32, 3, index) != want \
-            or _require_on(vs, f"{name}'s scales", f32, 3, index) != want:
-        raise ValueError(f"{name} must be codes [pages, kv_heads, page_size, head_dim] and scales [pages, kv_heads, page_size / 16]")
-    return shape, index
-
-
 def _require_pool(cache, refs, kv_len, pages):
-    shape, index = _require_codes(cache, "the cache")
+    shape, index = _require_codes(cache)
     i32 = _types[3]
     n, = _require_on(refs, "refs", i32, 1, index)
     seqs, = _require_on(kv_len, "kv_len", i32, 1, index)
@@ -627,8 +620,8 @@ def _require_pool(cache, refs, kv_len, pages):
     return shape, seqs, cols, index
 
 
-def _flags(seqs, index, stream):
-    return _empty((seqs,), _torch().bool, index, stream)
+def _new(shape, dtype, index, device, stream):
+    return _types[5](shape, dtype=dtype, device=device) if stream is None else _empty(shape, dtype, index, stream)
 
 
 def kv_grow(cache, refs, kv_len, pages, grow, stream=None):
@@ -642,7 +635,7 @@ def kv_grow(cache, refs, kv_len, pages, grow, stream=None):
     (num_pages, _, page, _), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
     if _require_on(grow, "grow", _types[3], 1, index) != (seqs,):
         raise ValueError("grow must be [S]")
-    ok = _flags(seqs, index, stream)
+    ok = _new((seqs,), _types[9], index, kv_len.device, stream)
     if seqs == 0:
         return ok
     _launch((_lib or load()).trellis_kv_grow,
@@ -664,7 +657,7 @@ def kv_fork(cache, refs, kv_len, pages, parents, stream=None):
     (num_pages, hk, page, d), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
     if _require_on(parents, "parents", _types[3], 1, index) != (seqs,):
         raise ValueError("parents must be [S]")
-    ok = _flags(seqs, index, stream)
+    ok = _new((seqs,), _types[9], index, kv_len.device, stream)
     if seqs == 0:
         return ok
     _launch((_lib or load()).trellis_kv_fork,
@@ -681,13 +674,14 @@ def kv_compact(cache, refs, kv_len, pages, into, stream=None):
     size and head width).  Returns its (refs, kv_len, pages); the first cache and its arrays stay as they are.
     Sequences that name a page which `into` has no room for come out with kv_len 0."""
     (num_pages, hk, page, d), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
-    shape, where = _require_codes(into, "into")
+    shape, where = _require_codes(into)
     if shape[1:] != (hk, page, d) or where != index:
         raise ValueError(f"into must be a cache of pages [{hk}, {page}, {d}] on cuda:{index}")
     i32 = _types[3]
-    out = [_empty(s, i32, index, stream) for s in ((shape[0],), (seqs,), (seqs, cols))]
     if seqs == 0:
         raise ValueError("the table must hold at least one sequence")
+    dev = kv_len.device
+    out = [_new(s, i32, index, dev, stream) for s in ((shape[0],), (seqs,), (seqs, cols))]
     _launch((_lib or load()).trellis_kv_compact,
             (refs.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), seqs, cols, num_pages, page, hk, d,
              *(t.data_ptr() for t in cache), shape[0], *(t.data_ptr() for t in into), *(t.data_ptr() for t in out)),
@@ -716,8 +710,8 @@ def _norm(x, weight, eps, residual, residual_out, out, eight, stream):
         raise ValueError("residual_out without residual")
     codes = scales = None
     if eight:
-        codes = _empty(shape, _types[4], index, stream)
-        scales = _empty(shape[:-1], f32, index, stream)
+        codes = _new(shape, _types[4], index, x.device, stream)
+        scales = _new(shape[:-1], f32, index, x.device, stream)
     else:
         out = _output(out, "out", shape, index, x.device, stream)
         if residual is not None and out.numel() and out.data_ptr() == residual_out.data_ptr():
@@ -763,13 +757,12 @@ def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None)
     [N, K / group], group 32, 64 or 128.  A weight is scale * code + bias, or scale * (code - 8) without biases,
     rounded once to bf16.
     x: bf16, or float8_e4m3fn with x_scales float32 [M], as rms_norm_q8 returns them."""
-    torch = _torch()
     Tensor, bf16, f32, i32, f8 = (_types or _torch_types())[:5]
     if not isinstance(x, Tensor):
         raise ValueError("x must be a CUDA tensor")
     index = x.get_device()
     M, K = _require_on(x, "x", f8 if x_scales is not None else bf16, 2, index)
-    N, words = _require_on(codes, "codes", torch.uint32 if getattr(codes, "dtype", None) == torch.uint32 else i32, 2, index)
+    N, words = _require_on(codes, "codes", i32 if getattr(codes, "dtype", None) == i32 else _torch().uint32, 2, index)
     shape = _require_on(scales, "scales", bf16, 2, index)
     if words * 8 != K or shape[0] != N or shape[1] == 0 or K % shape[1] != 0:
         raise ValueError("codes must be [N, K / 8] and scales [N, K / group]")

@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) kv_grow_kernel(const __grid_constant
     __shared__ int part[kWarps];
     __shared__ long long part64[kWarps];
     griddep_wait();
+    griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
     // needs, and the sequences that are not served whatever the pool holds
     long long before = 0;
     for (int s0 = 0; s0 < a.seqs; s0 += kThreads) {
@@ -172,7 +173,6 @@ __global__ void __launch_bounds__(kThreads) kv_grow_kernel(const __grid_constant
             a.ok[s] = ok;
         }
     }
-    griddep_launch_dependents();
 }
 
 // ---- fork -----------------------------------------------------------------------------
@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const __grid_con
     extern __shared__ int first[];                  // [seqs] the sequence that keeps a parent's last page
     __shared__ int part[kWarps];
     griddep_wait();
+    griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
     if (blockIdx.x > 0) {
         for (int s = blockIdx.x - 1; s < a.seqs; s += gridDim.x - 1) {
             if (a.parents[s] == s) continue;
@@ -198,8 +199,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const __grid_con
             const size_t row = static_cast<size_t>(s) * a.cols;
             for (int c = threadIdx.x; c < have; c += kThreads) a.rows[row + c] = a.pages[row + c];
         }
-        griddep_launch_dependents();
-        return;
+            return;
     }
     for (int s = threadIdx.x; s < a.seqs; s += kThreads) first[s] = 0x7fffffff;
     __syncthreads();
@@ -235,12 +235,12 @@ __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const __grid_con
         if (lost) a.now[s] = 0;
         a.ok[s] = !lost && a.parents[s] < a.seqs;
     }
-    griddep_launch_dependents();
 }
 
 // Column y = 0: a sequence's row and its pages' counts.  The others: a head's keys or values of the page that it copies.
 __global__ void __launch_bounds__(256) kv_fork_apply_kernel(const __grid_constant__ ForkArgs a) {
     griddep_wait();
+    griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
     const int s = blockIdx.x, p = a.parents[s];
     if (p == s) return;
     const int now = a.now[s], fresh = a.fresh[s], whole = now >> a.shift;
@@ -297,6 +297,7 @@ struct CompactArgs {
 __global__ void __launch_bounds__(kThreads) kv_rank_kernel(const __grid_constant__ CompactArgs a) {
     __shared__ int part[kWarps];
     griddep_wait();
+    griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
     int before = 0;
     for (int i = 0; i < kRankChunk; i += kThreads) {
         const long long p = static_cast<long long>(blockIdx.x) * kRankChunk + i + threadIdx.x;
@@ -309,13 +310,13 @@ __global__ void __launch_bounds__(kThreads) kv_rank_kernel(const __grid_constant
     if (threadIdx.x == 0) a.chunks[blockIdx.x] = before;
     for (long long p = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; p < a.room; p += static_cast<long long>(gridDim.x) * kThreads)
         a.refs_out[p] = 0;
-    griddep_launch_dependents();
 }
 
 __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__ CompactArgs a, int chunks) {
     extern __shared__ int base[];       // used pages before each chunk
     __shared__ int warp_sum[8];
     griddep_wait();
+    griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
     // prefix sums of the chunks: a thread takes a run of them
     const int run = (chunks + 255) / 256, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int sum = 0;
@@ -375,7 +376,6 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
         }
         if (threadIdx.x == 0) atomicAdd(a.refs_out + to, a.refs[p]);
     }
-    griddep_launch_dependents();
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

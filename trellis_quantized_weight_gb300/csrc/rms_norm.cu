@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
     // position of value j of unit i, and whether the row has it
     auto at = [&](int i, int j) { return kVec ? 8 * (t + i * threads) + j : t + (8 * i + j) * threads; };
     griddep_wait();
+    griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
     uint4 w[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -177,7 +178,6 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
             }
         }
     }
-    griddep_launch_dependents();
 }
 
 // Rows that do not fit a CTA's registers: read twice, the second time from L2.
@@ -185,6 +185,7 @@ template <bool kEight>
 __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float2 part[2][32];
     griddep_wait();
+    griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
     int turn = 0;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const long long token = row / a.heads, base = row * a.width;
@@ -214,7 +215,6 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
         }
         if (kEight && threadIdx.x == 0) a.scales[row] = s;
     }
-    griddep_launch_dependents();
 }
 
 constexpr int kMostThreads = 1024, kMostPer = 4;
