@@ -230,7 +230,7 @@ def test_captured_steps_and_another_stream():
     import trellis_quantized_weight_gb300 as tq
     p = Pool([20, 0, 0, 33], 16, 10, spare=30, seed=4)
     one, parents = ints([3, 0, 0, 5]), ints([0, 0, 3, 3])
-    stream = torch.cuda.Stream()
+    stream = torch.cuda.Stream(priority=-1)          # not of the pool whose streams other tests look into
     stream.wait_stream(torch.cuda.current_stream())
     p.grow([3, 0, 0, 5])
     p.fork([0, 0, 3, 3])

@@ -118,7 +118,7 @@ def test_captured_steps_hand_out_pages_as_eager_ones():
         prompt(layer, cache, refs, kv_len, pages, [30, 1, 16])
         rows, row, residual, step = decode(layer, cache, refs, kv_len, pages, 25)
         if captured:
-            stream = torch.cuda.Stream()
+            stream = torch.cuda.Stream(priority=-1)          # not of the pool whose streams other tests look into
             stream.wait_stream(torch.cuda.current_stream())
             with torch.cuda.stream(stream):
                 graph = torch.cuda.CUDAGraph()
@@ -163,8 +163,13 @@ def test_a_moved_cache_goes_on():
         assert torch.equal(a, b)
 
 
-def test_the_command(capsys):
+def test_the_command(capsys, monkeypatch):
     from trellis_quantized_weight_gb300 import attention_block
+
+    class Stream(torch.cuda.Stream):                # of the other pool
+        def __new__(cls, *a, **kw):
+            return super().__new__(cls, *a, **{**kw, "priority": -1})
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
     attention_block.main(["--requests", "3", "--prompt", "70", "--samples", "2", "--steps", "20", "--hidden", "512", "--inner", "768",
                           "--q-heads", "4", "--kv-heads", "1", "--head-dim", "64", "--page", "16"])
     out = capsys.readouterr().out
