@@ -203,7 +203,9 @@ def _enqueue(fn, args, index, stream):
     if _current_device() != index:
         with _on_device(index):
             return _enqueue(fn, args, index, stream)
-    _check(fn(*args, _raw_stream(index, stream)), fn.__name__)
+    rc = fn(*args, _raw_stream(index, stream))
+    if rc != 0:
+        _check(rc, fn.__name__)
 
 
 def _is_capturing(stream):
@@ -233,7 +235,8 @@ def _launch(fn, args, index, stream, need, ask=True):
         if rc == -7:
             buf = ws.grow(least or need(), index, stream, capturing)
             rc = fn(*args, buf.data_ptr(), buf.numel(), handle)
-    _check(rc, fn.__name__)
+    if rc != 0:
+        _check(rc, fn.__name__)
 
 
 def _empty(shape, dtype, index, stream):
@@ -429,10 +432,12 @@ def _require_rows(t, name, index):
 
 
 def _require_on(t, name, dtype, ndim, index):
-    if not isinstance(t, _types[0]) or index < 0 or t.get_device() != index or t.dtype != dtype \
-            or not t.is_contiguous() or len(shape := t.shape) != ndim:
-        raise ValueError(f"{name} must be a contiguous {ndim}-d {dtype} tensor on one CUDA device")
-    return shape
+    try:
+        if t.dtype is dtype and t.get_device() == index >= 0 and t.is_contiguous() and len(shape := t.shape) == ndim:
+            return shape
+    except AttributeError:                          # not a tensor
+        pass
+    raise ValueError(f"{name} must be a contiguous {ndim}-d {dtype} tensor on one CUDA device")
 
 
 def _require_codes(cache):
@@ -662,7 +667,7 @@ def kv_fork(cache, refs, kv_len, pages, parents, stream=None):
         return ok
     _launch((_lib or load()).trellis_kv_fork,
             (refs.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), parents.data_ptr(), seqs, cols, num_pages, page, hk, d,
-             *(t.data_ptr() for t in cache), ok.data_ptr()),
+             cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), ok.data_ptr()),
             index, stream, lambda: kv_pages_workspace_bytes(seqs, cols, num_pages), ask=False)
     if stream is not None:
         _used_on(stream, *cache, refs, kv_len, pages, parents, ok)
@@ -684,7 +689,8 @@ def kv_compact(cache, refs, kv_len, pages, into, stream=None):
     out = [_new(s, i32, index, dev, stream) for s in ((shape[0],), (seqs,), (seqs, cols))]
     _launch((_lib or load()).trellis_kv_compact,
             (refs.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), seqs, cols, num_pages, page, hk, d,
-             *(t.data_ptr() for t in cache), shape[0], *(t.data_ptr() for t in into), *(t.data_ptr() for t in out)),
+             cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), shape[0], into[0].data_ptr(),
+             into[1].data_ptr(), into[2].data_ptr(), into[3].data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()),
             index, stream, lambda: kv_pages_workspace_bytes(seqs, cols, num_pages), ask=False)
     if stream is not None:
         _used_on(stream, *cache, *into, refs, kv_len, pages, *out)
@@ -694,33 +700,40 @@ def kv_compact(cache, refs, kv_len, pages, into, stream=None):
 # ---- from one projection to the next -----------------------------------------
 def _norm(x, weight, eps, residual, residual_out, out, eight, stream):
     Tensor, bf16, f32 = (_types or _torch_types())[:3]
-    if not isinstance(x, Tensor) or (index := x.get_device()) < 0 or x.dtype != bf16 or len(shape := x.shape) not in (2, 3):
+    if not isinstance(x, Tensor) or (index := x.get_device()) < 0 or x.dtype is not bf16 or (ndim := len(shape := x.shape)) not in (2, 3):
         raise ValueError("x must be a bfloat16 CUDA tensor [rows, width] or [tokens, heads, width]")
-    stride = x.stride()
-    rows, heads, width = shape[0], shape[1] if len(shape) == 3 else 1, shape[-1]
-    if x.numel() and ((width > 1 and stride[-1] != 1) or (heads > 1 and stride[1] != width)):
-        raise ValueError("x: the values of a row must be contiguous")
-    if _require_on(weight, "weight", bf16, 1, index) != (width,):
+    rows, heads, width = shape[0], shape[1] if ndim == 3 else 1, shape[-1]
+    step = heads * width
+    some = rows > 0 and step > 0
+    if some and not x.is_contiguous():
+        stride = x.stride()
+        if (width > 1 and stride[-1] != 1) or (heads > 1 and stride[1] != width):
+            raise ValueError("x: the values of a row must be contiguous")
+        if rows > 1:                                # the stride of a single row is arbitrary
+            step = stride[0]
+    if _require_on(weight, "weight", bf16, 1, index)[0] != width:
         raise ValueError(f"weight must be [{width}]")
+    dev = x.device
+    r_ptr = h_ptr = y_ptr = c_ptr = s_ptr = codes = scales = None
     if residual is not None:
-        if _require_on(residual, "residual", bf16, len(shape), index) != shape:
+        if _require_on(residual, "residual", bf16, ndim, index) != shape:
             raise ValueError(f"residual must be {tuple(shape)}")
-        residual_out = _output(residual_out, "residual_out", shape, index, x.device, stream)
+        residual_out = _output(residual_out, "residual_out", shape, index, dev, stream)
+        r_ptr, h_ptr = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
-    codes = scales = None
     if eight:
-        codes = _new(shape, _types[4], index, x.device, stream)
-        scales = _new(shape[:-1], f32, index, x.device, stream)
+        codes = _new(shape, _types[4], index, dev, stream)
+        scales = _new(shape[:-1], f32, index, dev, stream)
+        c_ptr, s_ptr = codes.data_ptr(), scales.data_ptr()
     else:
-        out = _output(out, "out", shape, index, x.device, stream)
-        if residual is not None and out.numel() and out.data_ptr() == residual_out.data_ptr():
+        out = _output(out, "out", shape, index, dev, stream)
+        y_ptr = out.data_ptr()
+        if some and y_ptr == h_ptr:
             raise ValueError("out and residual_out must not be the same tensor")
-    if x.numel():
-        ptr = [None if t is None else t.data_ptr() for t in (residual, out, codes, scales, residual_out)]
+    if some:
         _enqueue((_lib or load()).trellis_rms_norm,
-                 (x.data_ptr(), stride[0] if rows > 1 else heads * width, ptr[0], weight.data_ptr(), rows, heads, width, eps,
-                  *ptr[1:]), index, stream)
+                 (x.data_ptr(), step, r_ptr, weight.data_ptr(), rows, heads, width, eps, y_ptr, c_ptr, s_ptr, h_ptr), index, stream)
         if stream is not None:
             _used_on(stream, x, weight, residual, residual_out, out, codes, scales)
     return out, codes, scales, residual_out
