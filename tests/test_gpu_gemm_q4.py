@@ -173,3 +173,73 @@ def test_many_calls_give_equal_bits(M, K, N, group, bias, eight):
     differ = sum(not torch.equal(tq.gemm_q4(x, codes, scales, biases, x_scales=x_scales), first) for _ in range(300))
     assert differ == 0
     assert tq.load().trellis_device_status(None) == 0
+
+
+@pytest.mark.parametrize("M,K,N,group,eight", [(3, 5120, 1111, 64, False), (3, 5120, 1111, 64, True), (200, 1280, 700, 32, True)])
+def test_captured_and_replayed(M, K, N, group, eight):
+    """Clusters of CTAs and the widened rows' workspace in a graph; inputs change between replays."""
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(2)
+    codes, scales, biases = weights(N, K, group, True, g)
+    xs = [torch.randn(M, K, generator=g).bfloat16().cuda() for _ in range(3)]
+    x_scales = None
+    if eight:
+        one = torch.ones(K).bfloat16().cuda()
+        xs, rows = zip(*(tq.rms_norm_q8(x, one) for x in xs))
+        x_scales = rows[0].clone()
+    want = [tq.gemm_q4(x, codes, scales, biases, x_scales=rows[i] if eight else None) for i, x in enumerate(xs)]
+    x, out = xs[0].clone(), torch.empty_like(want[0])
+    stream = torch.cuda.Stream(priority=-1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        tq.gemm_q4(x, codes, scales, biases, x_scales=x_scales, out=out)
+    with torch.cuda.stream(stream):
+        for i in (1, 2, 0, 1):
+            x.copy_(xs[i])
+            if eight:
+                x_scales.copy_(rows[i])
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, want[i])
+    stream.synchronize()
+
+
+def test_on_two_streams_at_once():
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(2)
+    codes, scales, biases = weights(3000, 5120, 64, True, g)
+    one = torch.ones(5120).bfloat16().cuda()
+    streams = [torch.cuda.Stream(priority=-1) for _ in range(2)]
+    inputs = [tq.rms_norm_q8(torch.randn(M, 5120, generator=g).bfloat16().cuda(), one) for M in (9, 150)]
+    want = [tq.gemm_q4(x, codes, scales, biases, x_scales=s) for x, s in inputs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(tq.gemm_q4(inputs[i][0], codes, scales, biases, x_scales=inputs[i][1], stream=streams[i]))
+    for s in streams:
+        s.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -130, 2.0 ** -60, 2.0 ** 60])
+def test_small_and_large_scales(scale):
+    """Weights below the normal numbers round as they are stored: to multiples of 2^-133."""
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(5)
+    codes, _, _ = weights(40, 256, 32, False, g)
+    s = (torch.rand(40, 8, generator=g).cuda() + 0.5).bfloat16() * scale
+    q = torch.stack([(codes.long() >> (4 * i)) & 15 for i in range(8)], -1).view(40, 8, 32).double() - 8
+    w = s.double()[..., None] * q
+    w = (torch.round(w * 2.0 ** 133) * 2.0 ** -133 if scale < 2.0 ** -120 else w.float().bfloat16().double()).view(40, 256)
+    for bias in (None, torch.zeros_like(s)):
+        x = torch.zeros(256, 256).bfloat16().cuda()
+        x.fill_diagonal_(2.0 ** 20 if scale < 1 else 2.0 ** -20)
+        want = w.T * float(x[0, 0]) if bias is None else (s.double()[..., None] * (q + 8)).view(40, 256).T * float(x[0, 0])
+        if bias is not None:
+            v = (s.double()[..., None] * (q + 8)).view(40, 256)
+            v = torch.round(v * 2.0 ** 133) * 2.0 ** -133 if scale < 2.0 ** -120 else v.float().bfloat16().double()
+            want = v.T * float(x[0, 0])
+        assert torch.equal(tq.gemm_q4(x, codes, s, bias).double(), want.float().bfloat16().double())

@@ -151,3 +151,45 @@ def test_no_rows_and_refusals():
     for eps in (-1.0, float("nan"), float("inf")):
         with pytest.raises(tq.TrellisError):
             tq.rms_norm(x, w, eps)
+
+
+def test_on_a_given_stream_and_captured():
+    import trellis_quantized_weight_gb300 as tq
+    x, r, w = data(300, 5120, 1)
+    want, want_h = tq.rms_norm(x, w, residual=r)
+    codes, scales, _ = tq.rms_norm_q8(x, w, residual=r)
+    stream = torch.cuda.Stream(priority=-1)
+    torch.cuda.synchronize()
+    got, got_h = tq.rms_norm(x, w, residual=r, stream=stream)
+    eight = tq.rms_norm_q8(x, w, residual=r, stream=stream)
+    stream.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_h, want_h)
+    assert torch.equal(eight[0].view(torch.uint8), codes.view(torch.uint8)) and torch.equal(eight[1], scales) and torch.equal(eight[2], want_h)
+    stream_r = r.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        y, _ = tq.rms_norm(x, w, residual=stream_r, residual_out=stream_r)
+        y8, s8 = tq.rms_norm_q8(y, w)
+    with torch.cuda.stream(stream):
+        for _ in range(2):
+            stream_r.copy_(r)
+            graph.replay()
+            assert torch.equal(y, want) and torch.equal(stream_r, want_h)
+            again = tq.rms_norm_q8(want, w)
+            assert torch.equal(y8.view(torch.uint8), again[0].view(torch.uint8)) and torch.equal(s8, again[1])
+    stream.synchronize()
+
+
+def test_many_rows():
+    """More values than 32 bits count."""
+    import trellis_quantized_weight_gb300 as tq
+    rows = (1 << 31) // 8192 + 5
+    x = torch.zeros(rows, 8192, dtype=torch.bfloat16, device="cuda")
+    x[-1], x[0] = 3, -2
+    w = torch.ones(8192).bfloat16().cuda()
+    y = tq.rms_norm(x, w, 0.0625)
+    assert torch.all(y[0] == torch.tensor(-2 / 4.0625 ** 0.5).bfloat16().item()) and not y[1:-1:1009].any()
+    assert torch.all(y[-1] == torch.tensor(3 / 9.0625 ** 0.5).bfloat16().item())
+    del y
+    codes, scales = tq.rms_norm_q8(x, w, 0.0625)
+    assert torch.all(codes[-1].float() == 448) and torch.all(codes[0].float() == -448) and not codes[1:-1:1009].float().any()

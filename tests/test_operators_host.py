@@ -23,7 +23,7 @@ FORK = dict(POOL, parents=P, **SIZES, **CACHE, ok=P, **WORK)
 COMPACT = dict(POOL, **SIZES, **CACHE, num_pages_out=9, k_codes_out=Q, v_codes_out=Q + (1 << 20), k_scales_out=Q + (2 << 20),
                v_scales_out=Q + (3 << 20), refs_out=Q + (4 << 20), kv_len_out=Q + (5 << 20), pages_out=Q + (6 << 20), **WORK)
 NORM = dict(x=P, x_stride=256, residual=P, weight=P, rows=4, heads=2, width=128, eps=1e-6, out=P, codes=0, scales=0, residual_out=Q, stream=None)
-Q4 = dict(x=P, x_scales=0, codes=P, scales=P, biases=P, M=3, K=256, N=50, group=64, out=P, workspace=P, workspace_bytes=1 << 30, stream=None)
+Q4 = dict(x=P, x_scales=0, codes=P, scales=P, biases=P, M=3, K=256, N=50, group=64, out=Q, workspace=P, workspace_bytes=1 << 30, stream=None)
 
 SHARED = [(dict(refs=0), -1), (dict(kv_len=0), -1), (dict(pages=0), -1), (dict(seqs=0), -2), (dict(page_cols=0), -2), (dict(num_pages=0), -2),
           (dict(seqs=16385), -3), (dict(num_pages=(1 << 24) + 1), -3), (dict(page_cols=(1 << 24) + 1), -3), (dict(page_size=8), -3),
@@ -74,6 +74,7 @@ def test_norm_refuses(lib, change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(x=0), -1), (dict(codes=0), -1), (dict(scales=0), -1), (dict(out=0), -1), (dict(M=-1), -2), (dict(K=0), -2), (dict(N=0), -2),
     (dict(group=16), -3), (dict(group=256), -3), (dict(K=224), -2), (dict(M=65537), -3), (dict(K=(1 << 20) + 64), -3), (dict(N=(1 << 20) + 1), -3),
+    (dict(out=P), -2), (dict(out=P + 1534), -2), (dict(x_scales=P, out=P + 766), -2),
     (dict(x=P + 8), -4), (dict(codes=P + 8), -4), (dict(scales=P + 1), -4), (dict(biases=P + 1), -4), (dict(x_scales=P + 2), -4), (dict(out=P + 1), -4),
     (dict(x_scales=P, workspace=0), -7), (dict(x_scales=P, workspace_bytes=1 << 20), -7), (dict(x_scales=P, workspace=P + 64), -4)])
 def test_gemm_q4_refuses(lib, change, want):

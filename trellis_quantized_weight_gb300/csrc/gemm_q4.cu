@@ -591,6 +591,11 @@ size_t workspace_bytes_of(int M, int K, bool eight) { return eight ? kCounters +
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 int check_sizes(int M, int K, int N, int group) {
     if (M < 0 || K < 1 || N < 1) return TRELLIS_ERR_SHAPE;
     if (group != 32 && group != 64 && group != 128) return TRELLIS_ERR_UNSUPPORTED;
@@ -635,6 +640,8 @@ int trellis_gemm_q4(const void* x, const float* x_scales, const uint32_t* codes,
         return TRELLIS_ERR_ALIGN;
     if (M == 0) return TRELLIS_OK;
     const bool eight = x_scales != nullptr;
+    // tiles of x are read until the last result is stored
+    if (overlap(x, static_cast<size_t>(M) * K * (eight ? 1 : 2), out, static_cast<size_t>(M) * N * 2)) return TRELLIS_ERR_SHAPE;
     if (eight && (workspace == nullptr || workspace_bytes < workspace_bytes_of(M, K, true))) return TRELLIS_ERR_WORKSPACE;
     if (eight && !aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
     DeviceInfo dev;
