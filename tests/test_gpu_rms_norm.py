@@ -68,6 +68,31 @@ def test_norm(width, rows):
     check_q8(*tq.rms_norm_q8(x, w, 1e-3), y)
 
 
+@pytest.mark.parametrize("rows,width,pitch", [(9001, 520, 520), (10000, 1024, 1032), (2000, 5120, 5120), (3001, 4104, 4112), (1217, 8192, 8192),
+                                              (700, 16384, 16384), (305, 16384, 16392), (9729, 640, 640)])
+def test_rows_ahead(rows, width, pitch):
+    """Many rows a CTA: the next one is on its way while one is at work, in place too."""
+    import trellis_quantized_weight_gb300 as tq
+    x, r, w = data(rows, pitch, 7)
+    x, r, w = x[:, :width], r[:, :width].contiguous(), w[:width].contiguous()
+    h, y = reference(x, w, 1e-6, r)
+    got, got_h = tq.rms_norm(x, w, residual=r)
+    check_y(got, y)
+    assert torch.equal(got_h, (x.float() + r.float()).bfloat16())
+    codes, scales, _ = tq.rms_norm_q8(x, w, residual=r)
+    check_q8(codes, scales, y)
+    stream = r.clone()
+    again, _ = tq.rms_norm(x, w, residual=stream, residual_out=stream)
+    assert torch.equal(again, got) and torch.equal(stream, got_h)
+    if pitch == width:
+        out = x.clone()
+        tq.rms_norm(out, w, residual=r, out=out)
+        assert torch.equal(out, got)
+    _, y = reference(x, w, 1e-6)
+    check_y(tq.rms_norm(x, w), y)
+    check_q8(*tq.rms_norm_q8(x, w), y)
+
+
 @pytest.mark.parametrize("tokens,heads,width,extra", [(1, 8, 128, 0), (5, 40, 128, 16), (300, 3, 64, 1), (33, 2, 256, 4), (7, 5, 100, 3),
                                                       (2, 3, 1024, 1)])
 def test_heads_of_a_projection(tokens, heads, width, extra):

@@ -7,7 +7,9 @@
 //
 // A row stays in registers between its two reductions (sum of squares and, for the
 // 8-bit form, max|h w|, which are taken together: y's maximum is the product's times
-// rsqrt) and its stores, so each value is read and written once.
+// rsqrt) and its stores, so each value is read and written once.  Bound by HBM: with a
+// residual 6.3 TB/s of the 6.7 that a copy reaches, without one 4.5 to 5.1 (the chain load,
+// sum, store of a row, with as many rows in flight as there is room for).
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "trellis.h"
@@ -30,12 +32,19 @@ struct NormArgs {
 
 constexpr float kLeastScale = 7.888609052210118e-31f;    // 2^-100
 
-__device__ __forceinline__ void bf16x8_to_f32(uint4 v, float (&f)[8]) {
-    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+// Eight values as four pairs: sums, products and multiply-adds take two at a time.
+__device__ __forceinline__ void bf16x8_to_f32(uint4 v, float2 (&f)[4]) {
+    f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x)); f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z)); f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
 }
-__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 f32_to_bf16x8(const float2 (&f)[4]) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+}
+// The largest magnitude of a (already one) and two more values; NaN if one of them is.
+__device__ __forceinline__ float most_of(float a, float2 v) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(v.x), "f"(v.y));
+    return r;
 }
 
 // Magnitudes compare as their bits do, and NaN above all of them.
@@ -66,8 +75,8 @@ __device__ __forceinline__ void reduce(float& sum, uint32_t& most, float2* part)
 }
 
 // kVec: 8 values by one 16-byte access; otherwise single values, a thread apart.
-// kPer: units of 8 values that a thread holds.
-template <int kPer, bool kVec, bool kWarpRow, bool kEight, int kThreads>
+// kPer: units of 8 values that a thread holds.  kRing: rows under way, the one at work included (0: loaded when their turn comes).
+template <int kPer, bool kVec, bool kWarpRow, bool kEight, int kThreads, int kRing>
 __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float2 part[2][32];
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
@@ -104,48 +113,85 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
             }
         }
     };
-    auto store = [&](uint16_t* dst, int i, const float (&f)[8]) {
+    auto store = [&](uint16_t* dst, int i, const float2 (&f)[4]) {
         if constexpr (kVec) {
             if (at(i, 0) < a.width) *reinterpret_cast<uint4*>(dst + at(i, 0)) = f32_to_bf16x8(f);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (at(i, j) < a.width) dst[at(i, j)] = bf16_bits_rn(f[j]);
+                if (at(i, j) < a.width) dst[at(i, j)] = bf16_bits_rn(j & 1 ? f[j / 2].y : f[j / 2].x);
         }
     };
     auto source = [&](long long r) {
         const long long token = a.heads == 1 ? r : r / a.heads;
         return a.x + token * a.x_stride + (r - token * a.heads) * a.width;
     };
+    // With a ring, a thread's units of the rows to come are on their way to shared memory, where only it reads them: no
+    // thread waits for another's copies.
+    extern __shared__ __align__(16) unsigned char ring[];
+    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16 * threadIdx.x;
+    auto slot = [&](int stage, int which, int i) { return ring_at + ((stage * 2 + which) * kPer + i) * blockDim.x * 16; };
+    auto ahead = [&](long long of, int stage) {
+        if (of < a.rows) {
+            const uint16_t* src = source(of);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (at(i, 0) < a.width) {
+                    cp_async16(slot(stage, 0, i), src + at(i, 0));
+                    if (a.residual != nullptr) cp_async16(slot(stage, 1, i), a.residual + of * a.width + at(i, 0));
+                }
+        }
+        cp_async_commit();
+    };
+    if constexpr (kRing > 0) {
+#pragma unroll
+        for (int p = 0; p < kRing - 1; ++p) ahead(row + p * step, p);
+    }
+    int stage = 0;
     for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
         uint4 x[kPer], r[kPer];
-        load(source(row), x);
         const long long base = row * a.width;
-        if (a.residual != nullptr) load(a.residual + base, r);
-        float h[kPer][8];
-        float sum = 0.0f;
-        uint32_t most = 0u;
+        if constexpr (kRing > 0) {
+            cp_async_wait<kRing - 2>();
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                x[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (at(i, 0) < a.width) {
+                    x[i] = *reinterpret_cast<const uint4*>(ring + 16 * threadIdx.x + (stage * 2 * kPer + i) * blockDim.x * 16);
+                    if (a.residual != nullptr) r[i] = *reinterpret_cast<const uint4*>(ring + 16 * threadIdx.x + ((stage * 2 + 1) * kPer + i) * blockDim.x * 16);
+                }
+            }
+            ahead(row + (kRing - 1) * step, (stage + kRing - 1) % kRing);
+            stage = (stage + 1) % kRing;
+        } else {
+            load(source(row), x);
+            if (a.residual != nullptr) load(a.residual + base, r);
+        }
+        float2 h[kPer][4], sum2 = make_float2(0.0f, 0.0f);
+        float largest = 0.0f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             bf16x8_to_f32(x[i], h[i]);
             if (a.residual != nullptr) {
-                float f[8];
+                float2 f[4];
                 bf16x8_to_f32(r[i], f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] += f[j];
+                for (int j = 0; j < 4; ++j) h[i][j] = __fadd2_rn(h[i][j], f[j]);
                 store(a.residual_out + base, i, h[i]);
             }
-            float g[8];
-            bf16x8_to_f32(w[i], g);
+            float2 g[4];
+            if constexpr (kEight) bf16x8_to_f32(w[i], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sum = fmaf(h[i][j], h[i][j], sum);
+            for (int j = 0; j < 4; ++j) {
+                sum2 = __ffma2_rn(h[i][j], h[i][j], sum2);
                 if constexpr (kEight) {
-                    h[i][j] *= g[j];
-                    most = max(most, magnitude(h[i][j]));
+                    h[i][j] = __fmul2_rn(h[i][j], g[j]);
+                    largest = most_of(largest, h[i][j]);
                 }
             }
         }
+        float sum = sum2.x + sum2.y;
+        uint32_t most = magnitude(largest);
         reduce<kWarpRow>(sum, most, part[turn]);
         const float factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps);
         if constexpr (kEight) {
@@ -154,10 +200,13 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 uint32_t c[2];
+                float2 y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(h[i][j], make_float2(inv, inv));
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    c[q] = static_cast<uint32_t>(f32_to_e4m3x2(h[i][4 * q] * inv, h[i][4 * q + 1] * inv)) |
-                           (static_cast<uint32_t>(f32_to_e4m3x2(h[i][4 * q + 2] * inv, h[i][4 * q + 3] * inv)) << 16);
+                    c[q] = static_cast<uint32_t>(f32_to_e4m3x2(y[2 * q].x, y[2 * q].y)) |
+                           (static_cast<uint32_t>(f32_to_e4m3x2(y[2 * q + 1].x, y[2 * q + 1].y)) << 16);
                 if constexpr (kVec) {
                     if (at(i, 0) < a.width) *reinterpret_cast<uint2*>(a.codes + base + at(i, 0)) = make_uint2(c[0], c[1]);
                 } else {
@@ -170,10 +219,10 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                float g[8];
+                float2 g[4];
                 bf16x8_to_f32(w[i], g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = h[i][j] * factor * g[j];
+                for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(__fmul2_rn(h[i][j], make_float2(factor, factor)), g[j]);
                 store(a.out + base, i, g);
             }
         }
@@ -217,15 +266,17 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
     }
 }
 
-constexpr int kMostThreads = 1024, kMostPer = 4;
+constexpr int kMostThreads = 1024, kMostPer = 4, kAheadThreads = 1024;
 
-template <int kPer, bool kVec, bool kEight, bool kWarpRow, int kThreads>
+template <int kPer, bool kVec, bool kEight, bool kWarpRow, int kThreads, int kRing = 0>
 cudaError_t launch(const NormArgs& a, int threads, const DeviceInfo& dev, cudaStream_t stream) {
     // as many CTAs as run at once, each with its weights in registers: the next row's CTA would load them again
-    auto* kernel = rms_norm_kernel<kPer, kVec, kWarpRow, kEight, kThreads>;
-    const int per_sm = 2048 / threads;
+    auto* kernel = rms_norm_kernel<kPer, kVec, kWarpRow, kEight, kThreads, kRing>;
+    const int per_sm = (kRing > 0 ? kAheadThreads : 2048) / threads, smem = kRing * 2 * kPer * 16 * threads;
+    static std::atomic<unsigned long long> done{0};
+    if (kRing > 0 && !smem_opt_in(kernel, kRing * 2 * kPer * 16 * kThreads, done)) return cudaErrorInvalidValue;
     const long long ctas = kWarpRow ? (a.rows + 7) / 8 : a.rows, most = static_cast<long long>(per_sm) * dev.num_sms;
-    return launch_programmatic(kernel, static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(threads), 0, stream, a);
+    return launch_programmatic(kernel, static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(threads), smem, stream, a);
 }
 
 template <bool kVec, bool kEight>
@@ -240,7 +291,13 @@ cudaError_t launch_rows(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s
     if (units <= 64) return launch<2, kVec, kEight, true, 256>(a, 256, dev, stream);
     // few rows: one unit a thread where that fits, for the shortest chain
     if (a.rows < dev.num_sms && units <= kMostThreads) return launch<1, kVec, kEight, false, 1024>(a, threads(1), dev, stream);
-    // two units a thread: 8165 rows of 5120 with residual to 8 bits take 50 us, with one 64 to 68, four 59, five 54
+    // fewer: two units a thread (one: 64 to 68 us for those 8165 rows, five 54)
+    // Rows enough for a second one to be on its way while a CTA's first is at work: four units a thread, 1024 threads an SM.
+    // 8165 rows of 5120 with residual to 8 bits 45 us (50 without the second row, two units a thread; 59 with four); without
+    // a residual 27 against 34; two rows ahead 46 to 53.
+    if constexpr (kVec)
+        if (units <= 2048 && a.rows >= 2ll * (kAheadThreads / threads(4)) * dev.num_sms)
+            return launch<4, kVec, kEight, false, 512, 2>(a, threads(4), dev, stream);
     if (units <= 1024) return launch<2, kVec, kEight, false, 512>(a, threads(2), dev, stream);
     if (units <= 2048) return launch<2, kVec, kEight, false, 1024>(a, threads(2), dev, stream);
     return launch<4, kVec, kEight, false, 1024>(a, threads(4), dev, stream);
