@@ -552,9 +552,10 @@ TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const ui
  * feels it.
  * group: 32, 64 or 128; K a multiple of it, K and N up to 2^20, M up to 65536 (0: nothing is enqueued).
  *   workspace  256-byte aligned, at least trellis_gemm_q4_workspace_size bytes (NULL where that is 0: for bf16
- *           activations); its first 1 MiB is not touched, so a product's workspace will do.
+ *           activations, and up to 32 rows); its first 1 MiB is not touched, so a product's workspace will do.
  * The order of all sums is fixed by the sizes.  It runs on the tensor cores (tcgen05), whose waits are bounded (see
- * trellis_device_status).  One kernel is enqueued, two for 8-bit activations.
+ * trellis_device_status).  One kernel is enqueued, two for more
+ * than 32 rows of 8-bit activations.
  */
 TRELLIS_API int trellis_gemm_q4(const void *x, const float *x_scales, const uint32_t *codes, const uint16_t *scales,
                                 const uint16_t *biases, int M, int K, int N, int group, uint16_t *out,

@@ -76,7 +76,8 @@ def test_norm_refuses(lib, change, want):
     (dict(group=16), -3), (dict(group=256), -3), (dict(K=224), -2), (dict(M=65537), -3), (dict(K=(1 << 20) + 64), -3), (dict(N=(1 << 20) + 1), -3),
     (dict(out=P), -2), (dict(out=P + 1534), -2), (dict(x_scales=P, out=P + 766), -2),
     (dict(x=P + 8), -4), (dict(codes=P + 8), -4), (dict(scales=P + 1), -4), (dict(biases=P + 1), -4), (dict(x_scales=P + 2), -4), (dict(out=P + 1), -4),
-    (dict(x_scales=P, workspace=0), -7), (dict(x_scales=P, workspace_bytes=1 << 20), -7), (dict(x_scales=P, workspace=P + 64), -4)])
+    (dict(x_scales=P, M=33, out=Q, workspace=0), -7), (dict(x_scales=P, M=33, workspace_bytes=1 << 20), -7),
+    (dict(x_scales=P, M=33, workspace=P + 64), -4)])
 def test_gemm_q4_refuses(lib, change, want):
     assert lib.trellis_gemm_q4(*{**Q4, **change}.values()) == want
 
@@ -93,4 +94,5 @@ def test_gemm_q4_workspace_size(lib, args, want):
     assert lib.trellis_gemm_q4_workspace_size(*args, ctypes.byref(n)) == want
     assert lib.trellis_gemm_q4_workspace_size(1, 256, 5, 64, 0, None) == -1
     assert lib.trellis_gemm_q4_workspace_size(300, 256, 5, 64, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.trellis_gemm_q4_workspace_size(32, 256, 5, 64, 1, ctypes.byref(n)) == 0 and n.value == 0
     assert lib.trellis_gemm_q4_workspace_size(300, 256, 5, 64, 1, ctypes.byref(n)) == 0 and n.value >= 300 * 512

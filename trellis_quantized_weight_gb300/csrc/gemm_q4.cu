@@ -9,7 +9,8 @@
 // biases; the group sums, not the products, were what it waited for.)
 //
 // A CTA's warps: one loads code tiles, one activation tiles, one issues the products, one keeps tensor
-// memory, 4 load scales and biases, 16 turn codes into weights in tensor memory (the products' first operand), 4 store results.
+// memory, 4 load scales and biases, 16 turn codes into weights in tensor memory (the products' first operand), 4 store results
+// (and widen 8-bit activations, where they are few).
 // Tiles are 128 weight rows x NB activation rows; a CTA takes tile after tile (those of one block of weight rows
 // next to each other, so that their codes come from L2), its results leaving while the next tile is under way.
 // Where there are few tiles, a cluster of CTAs shares the k of one and adds its parts in shared memory, in order.
@@ -67,6 +68,7 @@ struct Q4Args {
     const uint32_t* codes;          // [N, K / 8]
     const uint16_t *scales, *biases;  // bf16 [N, groups]; biases may be NULL
     const float* x_scales;          // [M], or NULL
+    const uint8_t* x8;              // e4m3 [M, K], where they are widened on their way to shared memory
     uint16_t* out;                  // bf16 [M, N]
     int M, K, N, groups;
     int m_tiles, tiles, parts;
@@ -204,10 +206,26 @@ __device__ __forceinline__ uint32_t scale64_of(uint32_t v) {
     return r;
 }
 
+// Eight e4m3 codes as bf16, exactly.
+__device__ __forceinline__ uint4 widened(uint2 v) {
+    uint32_t f[4], r[4];
+    e4m3x4_to_f16x2(v.x, f[0], f[1]);
+    e4m3x4_to_f16x2(v.y, f[2], f[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 d = f16x2_to_f32(f[i]);
+        r[i] = pack_bf16x2(d.x, d.y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // Where group g of a row's sixteen stands: fours of them are turned by the row.
 __device__ __forceinline__ int scale_column(int row, int g) { return g ^ (((row >> 1) & 3) << 2); }
 
-template <int G, int NB, bool kBias>
+template <int G, int NB, bool kBias, bool kEight>
 __global__ void __launch_bounds__(kThreads, 1)
 q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap code_map, const __grid_constant__ CUtensorMap x_map) {
     using S = Q4Shape<G, NB>;
@@ -220,7 +238,8 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kA; ++i) {
-            mbar_init(bar(S::kBarFull + i), kStageWarps + 1);         // weights by the warps that made them, activations by their bytes
+            // weights by the warps that made them, activations by their bytes or by the warps that widened them
+            mbar_init(bar(S::kBarFull + i), kStageWarps + (kEight ? kStoreWarps : 1));
             mbar_init(bar(S::kBarEmpty + i), 1);
         }
         for (int i = 0; i < S::kCode; ++i) {
@@ -286,7 +305,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- activation tiles
-        if (lane == 0) {
+        if (!kEight && lane == 0) {
             uint32_t i = 0;
             for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
                 const int m0 = tile % a.m_tiles * NB;
@@ -432,12 +451,53 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
             }
         }
     } else if (warp >= 4 + kDecodeWarps + kScaleWarps) {
-        // ---------------------------------------------------------------- results
+        // ---------------------------------------------------------------- results, and before them 8-bit activations
         const int quarter = warp & 3;
         constexpr int kStep = NB < 32 ? 16 : 32;
         uint32_t d = 0;
+        // Sixteen codes a thread and 16 activation rows, some stages ahead.
+        constexpr int kPieces = kEight ? NB / 16 : 1, kFar = 3;
+        const int x_row = (32 * (warp - 4 - kDecodeWarps - kScaleWarps) + lane) >> 3, x_chunk = lane & 7;
+        uint4 x8[kFar][kPieces];
+        uint32_t x_slot = 0, x_turn = 1u;
+        auto load = [&](int s, uint4 (&v)[kPieces]) {
+            const int k = s * kStageK + 16 * x_chunk;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int m = x_row + 16 * i;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (s < s1 && k < a.K && m < a.M) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x8 + static_cast<size_t>(m) * a.K + k));
+            }
+        };
         for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
             const int m0 = tile % a.m_tiles * NB, n = tile / a.m_tiles * kRows + 32 * quarter + lane;
+            if constexpr (kEight) {
+#pragma unroll
+                for (int f = 0; f < kFar; ++f) load(s0 + f, x8[f]);
+                for (int s = s0; s < s1 && alive; s += kFar) {
+#pragma unroll
+                    for (int f = 0; f < kFar; ++f) {
+                        if (s + f >= s1) break;
+                        alive = mbar_wait(bar(S::kBarEmpty + x_slot), x_turn);
+                        if (!alive) break;
+                        // where the tensor copies put bf16 tiles: boxes of 64 k, rows of 128 bytes, their pieces of 16 turned by the row
+                        const uint32_t to = sbase + S::kOffX + x_slot * S::kXBytes + (x_chunk >> 2) * (NB * 128);
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            const int m = x_row + 16 * i;
+                            const uint4 lo = widened(make_uint2(x8[f][i].x, x8[f][i].y)), hi = widened(make_uint2(x8[f][i].z, x8[f][i].w));
+                            sts128(to + m * 128 + (((2 * (x_chunk & 3)) ^ (m & 7)) << 4), lo);
+                            sts128(to + m * 128 + (((2 * (x_chunk & 3) + 1) ^ (m & 7)) << 4), hi);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(S::kBarFull + x_slot));
+                        if (++x_slot == S::kA) { x_slot = 0; x_turn ^= 1u; }
+                        load(s + f + kFar, x8[f]);
+                    }
+                }
+                if (!alive) break;
+            }
             const uint32_t t_row = taddr + (static_cast<uint32_t>(32 * quarter) << 16) + (d & 1u) * NB;
             alive = mbar_wait(bar(S::kBarD + (d & 1u)), (d >> 1) & 1u);
             if (!alive) break;
@@ -496,18 +556,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
     }
 }
 
-// Before the product: 8-bit activations as bf16, exactly.
-__device__ __forceinline__ uint4 widened(uint2 v) {
-    uint32_t f[4], r[4];
-    e4m3x4_to_f16x2(v.x, f[0], f[1]);
-    e4m3x4_to_f16x2(v.y, f[2], f[3]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 d = f16x2_to_f32(f[i]);
-        r[i] = pack_bf16x2(d.x, d.y);
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
+// Before a product of more rows: 8-bit activations as bf16.
 __global__ void __launch_bounds__(256) q4_widen_kernel(const uint8_t* x, long long count, uint16_t* x16) {
     griddep_wait();
     for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < count; e += static_cast<long long>(gridDim.x) * 256)
@@ -544,14 +593,16 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void*
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int G, int NB, bool kBias>
+template <int G, int NB, bool kBias, bool kEight>
 cudaError_t launch_as(Q4Args a, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
     using S = Q4Shape<G, NB>;
     static std::atomic<unsigned long long> done{0};
-    if (!smem_opt_in(q4_kernel<G, NB, kBias>, S::kSmem, done)) return cudaErrorInvalidValue;
+    if (!smem_opt_in(q4_kernel<G, NB, kBias, kEight>, S::kSmem, done)) return cudaErrorInvalidValue;
     CUtensorMap codes, xs;
-    if (!make_map(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.codes, a.K / 8, a.N, kRows) ||
-        !make_map(&xs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, a.K, a.M, NB))
+    if (!make_map(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.codes, a.K / 8, a.N, kRows)) return cudaErrorInvalidValue;
+    if (kEight)
+        xs = codes;             // not used
+    else if (!make_map(&xs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, a.K, a.M, NB))
         return cudaErrorInvalidValue;
     a.m_tiles = (a.M + NB - 1) / NB;
     a.tiles = (a.N + kRows - 1) / kRows * a.m_tiles;
@@ -571,12 +622,20 @@ cudaError_t launch_as(Q4Args a, const void* x, const DeviceInfo& dev, cudaStream
     attr[1].val.clusterDim.x = a.parts; attr[1].val.clusterDim.y = 1; attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.parts > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q4_kernel<G, NB, kBias>, a, codes, xs);
+    return cudaLaunchKernelEx(&cfg, q4_kernel<G, NB, kBias, kEight>, a, codes, xs);
 }
+
+// 8-bit activations of up to 32 rows are widened in the product itself; of more, every tile of weight rows would widen them
+// again, so a kernel before it does (1 row, K = 5120, N = 17408 18.8 -> 17.8 us, N = 5120 12.0 -> 10.5; 11 rows, K = 17408,
+// N = 5120 21.9 -> 21.8; 32 rows in groups of 32 23.9 -> 23.4; and one launch less).
+constexpr int kWidenRows = 32;
 
 template <int G, int NB>
 cudaError_t launch_rows(const Q4Args& a, const void* x, const DeviceInfo& dev, cudaStream_t stream) {
-    return a.biases != nullptr ? launch_as<G, NB, true>(a, x, dev, stream) : launch_as<G, NB, false>(a, x, dev, stream);
+    if constexpr (NB <= kWidenRows)
+        if (a.x8 != nullptr)
+            return a.biases != nullptr ? launch_as<G, NB, true, true>(a, x, dev, stream) : launch_as<G, NB, false, true>(a, x, dev, stream);
+    return a.biases != nullptr ? launch_as<G, NB, true, false>(a, x, dev, stream) : launch_as<G, NB, false, false>(a, x, dev, stream);
 }
 
 template <int G>
@@ -587,7 +646,7 @@ cudaError_t launch_group(const Q4Args& a, const void* x, const DeviceInfo& dev, 
 }
 
 constexpr size_t kCounters = size_t(1) << 20;      // the products' counters in front of a workspace stay zero
-size_t workspace_bytes_of(int M, int K, bool eight) { return eight ? kCounters + static_cast<size_t>(M) * K * 2 : 0; }
+size_t workspace_bytes_of(int M, int K, bool eight) { return eight && M > kWidenRows ? kCounters + static_cast<size_t>(M) * K * 2 : 0; }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -642,12 +701,13 @@ int trellis_gemm_q4(const void* x, const float* x_scales, const uint32_t* codes,
     const bool eight = x_scales != nullptr;
     // tiles of x are read until the last result is stored
     if (overlap(x, static_cast<size_t>(M) * K * (eight ? 1 : 2), out, static_cast<size_t>(M) * N * 2)) return TRELLIS_ERR_SHAPE;
-    if (eight && (workspace == nullptr || workspace_bytes < workspace_bytes_of(M, K, true))) return TRELLIS_ERR_WORKSPACE;
-    if (eight && !aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
+    const size_t need = workspace_bytes_of(M, K, eight);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return TRELLIS_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
     DeviceInfo dev;
     rc = device_info(dev);
     if (rc != TRELLIS_OK) return rc;
-    if (eight) {
+    if (need > 0) {
         uint16_t* x16 = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kCounters);
         const long long count = static_cast<long long>(M) * (K / 8), ctas = (count + 255) / 256, most = 8ll * dev.num_sms;
         if (launch_programmatic(q4_widen_kernel, static_cast<unsigned>(ctas < most ? ctas : most), 256u, 0, stream,
@@ -658,6 +718,7 @@ int trellis_gemm_q4(const void* x, const float* x_scales, const uint32_t* codes,
     Q4Args a = {};
     a.codes = codes; a.scales = scales; a.biases = biases; a.x_scales = x_scales; a.out = out;
     a.M = M; a.K = K; a.N = N; a.groups = K / group;
+    if (eight && need == 0) a.x8 = static_cast<const uint8_t*>(x);
     const cudaError_t e = group == 32 ? launch_group<32>(a, x, dev, stream)
                           : group == 64 ? launch_group<64>(a, x, dev, stream) : launch_group<128>(a, x, dev, stream);
     return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
