@@ -92,6 +92,15 @@ def test_larger(M, K, N, group):
     run(M, K, N, group, False, True)
 
 
+@pytest.mark.parametrize("K,group", [(32, 32), (64, 64), (128, 128), (128, 32), (256, 128), (384, 128), (640, 32), (1152, 64)])
+@pytest.mark.parametrize("M", [40, 2049])
+def test_many_tiles_of_few_stages(M, K, group):
+    # each CTA takes ten tiles or five, one right after the other
+    N = 200_000 if M == 40 else 5121
+    for bias in (False, True):
+        run(M, K, N, group, bias, bias, seed=K)
+
+
 @pytest.mark.parametrize("M", [1, 12, 100])
 def test_every_code(M):
     """Each code at each place of a word, by one-hot activations: exact but for the result's rounding."""

@@ -269,10 +269,10 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
 
     // this CTA's share of k, in blocks of two stages, and its first tile
     const int part = a.parts > 1 ? static_cast<int>(blockIdx.x) % a.parts : 0;
-    const int blocks = (a.K + 2 * kStageK - 1) / (2 * kStageK), stages = (a.K + kStageK - 1) / kStageK;
+    const int blocks = (a.K + 2 * kStageK - 1) / (2 * kStageK);
     const int b0 = static_cast<int>(static_cast<long long>(blocks) * part / a.parts);
     const int b1 = static_cast<int>(static_cast<long long>(blocks) * (part + 1) / a.parts);
-    const int s0 = 2 * b0, s1 = min(2 * b1, stages);
+    const int s0 = 2 * b0, s1 = 2 * b1;         // past K: codes, scales and activations of zero
     const int tile0 = a.parts > 1 ? static_cast<int>(blockIdx.x) / a.parts : static_cast<int>(blockIdx.x);
     const int tile_step = a.parts > 1 ? a.tiles : static_cast<int>(gridDim.x);
     if (warp == 0 && lane == 0) {
@@ -284,7 +284,10 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
     griddep_wait();
     griddep_launch_dependents();        // the next grid may set itself up meanwhile; it waits for this one's end before it reads
 
-    // Slots are taken in turn: use number i of a ring of n is slot i % n, its phase's parity (i / n) & 1.
+    // Slots are taken in turn: use number i of a ring of n is slot i % n, its phase's parity (i / n) & 1.  A parity tells a
+    // phase only from its neighbours, so whoever waits for use i has to know that use i - n is over.  The decoding warps,
+    // which meet every fourth stage only, do because a tile has an even number of them: they meet every second code tile
+    // (of a ring of four), and go on by two runs of scales at most (of a ring of two, which is filled in order).
     bool alive = true;
     if (warp == 0) {
         // ---------------------------------------------------------------- code tiles
@@ -401,7 +404,6 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                     mbar_arrive(bar(S::kBarFull + slot));
                     mbar_arrive(bar(S::kBarScaleEmpty + run_slot));
                     mbar_arrive(bar(S::kBarCodeEmpty + code));
-                    if (s + 1 == s1 && (s & 1) == 0) mbar_arrive(bar(S::kBarCodeEmpty + code));      // for the block's odd stage, which is not there
                 }
                 slot += kGroups;
                 if (slot >= S::kA) { slot -= S::kA; parity ^= 1u; }
