@@ -152,6 +152,25 @@ def test_rows_of_zeros_and_not_finite(width):
     check_y(zero_eps[1:], reference(x[4:], w, 0.0)[1])
 
 
+@pytest.mark.parametrize("width", [96, 640, 5120, 40000])
+@pytest.mark.parametrize("rows", [2, 4000])
+def test_rows_next_to_nothing(width, rows):
+    """With a small eps the quotient of factor and scale is past fp32, the codes are not."""
+    import trellis_quantized_weight_gb300 as tq
+    if rows * width > 1 << 25:
+        rows = 320
+    g = torch.Generator().manual_seed(3)
+    x = (torch.rand(rows, width, generator=g) * 2.0 ** -120 + 2.0 ** -122).bfloat16().cuda()
+    x[::2] = 0
+    w = (torch.rand(width, generator=g) + 0.25).bfloat16().cuda()
+    for eps in (1e-20, 1e-30):
+        _, y = reference(x, w, eps)
+        check_y(tq.rms_norm(x, w, eps), y)
+        codes, scales = tq.rms_norm_q8(x, w, eps)
+        check_q8(codes, scales, y)
+        assert not codes[::2].float().any()
+
+
 def test_largest_value_becomes_448():
     import trellis_quantized_weight_gb300 as tq
     x = torch.zeros(1, 128).bfloat16().cuda()

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_plan_kernel(const __grid_con
             const size_t row = static_cast<size_t>(s) * a.cols;
             for (int c = threadIdx.x; c < have; c += kThreads) a.rows[row + c] = a.pages[row + c];
         }
-            return;
+        return;
     }
     for (int s = threadIdx.x; s < a.seqs; s += kThreads) first[s] = 0x7fffffff;
     __syncthreads();

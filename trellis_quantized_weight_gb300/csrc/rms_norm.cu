@@ -55,6 +55,9 @@ __device__ __forceinline__ float row_scale(uint32_t bits) {
     return bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(__fdiv_rn(__uint_as_float(bits), 448.0f), kLeastScale);
 }
 
+// factor / s of rows next to nothing and a small eps: taken in two steps there, since neither of them is.
+__device__ __forceinline__ bool too_large(float inv) { return __float_as_uint(inv) == 0x7f800000u; }
+
 // Sum and maximum over the `threads` threads of a row (a warp, or the whole CTA).  part: two buffers, taken in
 // turn from one row to the next, so that one barrier a row is enough.
 template <bool kWarpRow>
@@ -196,7 +199,14 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
         const float factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps);
         if constexpr (kEight) {
             const float s = row_scale(magnitude(__uint_as_float(most) * factor));
-            const float inv = factor / s;
+            float inv = factor / s;
+            if (too_large(inv)) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[i][j] = __fmul2_rn(h[i][j], make_float2(factor, factor));
+                inv = 1.0f / s;
+            }
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 uint32_t c[2];
@@ -253,14 +263,20 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
         reduce<false>(sum, most, part[turn]);
         const float factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps);
         const float s = kEight ? row_scale(magnitude(__uint_as_float(most) * factor)) : 1.0f;
-        const float inv = kEight ? factor / s : factor;
+        float first = factor, inv = kEight ? factor / s : 1.0f;
+        if (kEight) {
+            if (too_large(inv))
+                inv = 1.0f / s;
+            else
+                first = 1.0f;
+        }
         for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
-            const float h = value(c), y = h * bf16_bits_to_f32(__ldg(a.weight + c));
+            const float h = value(c), w = bf16_bits_to_f32(__ldg(a.weight + c)), y = kEight ? h * w * first : h * first * w;
             if (a.residual != nullptr) a.residual_out[base + c] = bf16_bits_rn(h);
             if constexpr (kEight)
                 a.codes[base + c] = static_cast<uint8_t>(f32_to_e4m3x2(y * inv, 0.0f));
             else
-                a.out[base + c] = bf16_bits_rn(y * inv);
+                a.out[base + c] = bf16_bits_rn(y);
         }
         if (kEight && threadIdx.x == 0) a.scales[row] = s;
     }
