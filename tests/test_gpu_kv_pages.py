@@ -275,3 +275,15 @@ def test_no_sequences_and_refusals():
         tq.kv_compact(cache, refs, lens, table, tuple(t[1:] for t in cache))
     with pytest.raises(tq.TrellisError):
         tq.kv_grow(cache, refs, lens, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), two)
+
+
+def test_growth_looks_at_the_shape_of_the_keys():
+    import trellis_quantized_weight_gb300 as tq
+    p = Pool([20, 5], 16, 4, spare=3)
+    cache, refs, lens, table = p.arrays()
+    two = ints([0, 1])
+    for bad in (cache[2], cache[0][0], cache[0].cpu(), cache[0].view(torch.uint8), cache[0][:, :, ::2], None):
+        with pytest.raises(ValueError):
+            tq.kv_grow((bad,) + tuple(cache[1:]), refs, lens, table, two)
+    with pytest.raises(ValueError):
+        tq.kv_grow((cache[0][1:],) + tuple(cache[1:]), refs, lens, table, two)

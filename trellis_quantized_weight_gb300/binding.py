@@ -614,8 +614,13 @@ def kv_pages_workspace_bytes(seqs, columns, pages) -> int:
     return int(n.value)
 
 
-def _require_pool(cache, refs, kv_len, pages):
-    shape, index = _require_codes(cache)
+def _require_pool(cache, refs, kv_len, pages, touched=True):
+    """touched: whether the call reads or writes the cache itself; if not, only the shape of its keys counts."""
+    if touched:
+        shape, index = _require_codes(cache)
+    else:
+        index = cache[0].get_device() if isinstance(cache[0], (_types or _torch_types())[0]) else -1
+        shape = _require_on(cache[0], "cache codes", _types[4], 4, index)
     i32 = _types[3]
     n, = _require_on(refs, "refs", i32, 1, index)
     seqs, = _require_on(kv_len, "kv_len", i32, 1, index)
@@ -637,7 +642,7 @@ def kv_grow(cache, refs, kv_len, pages, grow, stream=None):
     Returns bool [S]: False where a sequence was left as it was, because the free pages (lowest first,
     to sequences in their order) or the table's columns do not reach, or because it would be cut inside a
     page that it shares."""
-    (num_pages, _, page, _), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
+    (num_pages, _, page, _), seqs, cols, index = _require_pool(cache, refs, kv_len, pages, touched=False)
     if _require_on(grow, "grow", _types[3], 1, index) != (seqs,):
         raise ValueError("grow must be [S]")
     ok = _new((seqs,), _types[9], index, kv_len.device, stream)
