@@ -7,9 +7,10 @@
 //
 // A row stays in registers between its two reductions (sum of squares and, for the
 // 8-bit form, max|h w|, which are taken together: y's maximum is the product's times
-// rsqrt) and its stores, so each value is read and written once.  Bound by HBM: with a
-// residual 6.3 TB/s of the 6.7 that a copy reaches, without one 4.5 to 5.1 (the chain load,
-// sum, store of a row, with as many rows in flight as there is room for).
+// rsqrt) and its stores, so each value is read and written once.  Bound by HBM: 8165 rows of
+// 5120 with a residual to 8 bits 47 us, 6.2 TB/s of the 6.7 that a copy reaches; 7812 rows
+// without one 29 us (4.1 TB/s) to 8 bits and 31 (5.2) to bf16: the chain load, sum, store of a
+// row, with as many rows in flight as there is room for.  One row of 5120: 2.5 us.
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "trellis.h"
@@ -286,7 +287,8 @@ constexpr int kMostThreads = 1024, kMostPer = 4, kAheadThreads = 1024;
 
 template <int kPer, bool kVec, bool kEight, bool kWarpRow, int kThreads, int kRing = 0>
 cudaError_t launch(const NormArgs& a, int threads, const DeviceInfo& dev, cudaStream_t stream) {
-    // as many CTAs as run at once, each with its weights in registers: the next row's CTA would load them again
+    // as many CTAs as run at once (of the ring's, whose registers hold half as many, in two turns: 512 or 2048 threads an SM
+    // take the same 45 to 46 us), each with its weights in registers: the next row's CTA would load them again
     auto* kernel = rms_norm_kernel<kPer, kVec, kWarpRow, kEight, kThreads, kRing>;
     const int per_sm = (kRing > 0 ? kAheadThreads : 2048) / threads, smem = kRing * 2 * kPer * 16 * threads;
     static std::atomic<unsigned long long> done{0};
@@ -307,13 +309,13 @@ cudaError_t launch_rows(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s
     if (units <= 64) return launch<2, kVec, kEight, true, 256>(a, 256, dev, stream);
     // few rows: one unit a thread where that fits, for the shortest chain
     if (a.rows < dev.num_sms && units <= kMostThreads) return launch<1, kVec, kEight, false, 1024>(a, threads(1), dev, stream);
-    // fewer: two units a thread (one: 64 to 68 us for those 8165 rows, five 54)
     // Rows enough for a second one to be on its way while a CTA's first is at work: four units a thread, 1024 threads an SM.
     // 8165 rows of 5120 with residual to 8 bits 45 us (50 without the second row, two units a thread; 59 with four); without
     // a residual 27 against 34; two rows ahead 46 to 53.
     if constexpr (kVec)
         if (units <= 2048 && a.rows >= 2ll * (kAheadThreads / threads(4)) * dev.num_sms)
             return launch<4, kVec, kEight, false, 512, 2>(a, threads(4), dev, stream);
+    // fewer rows: two units a thread (8165 rows this way 50 us, with one unit 64 to 68, with five 54)
     if (units <= 1024) return launch<2, kVec, kEight, false, 512>(a, threads(2), dev, stream);
     if (units <= 2048) return launch<2, kVec, kEight, false, 1024>(a, threads(2), dev, stream);
     return launch<4, kVec, kEight, false, 1024>(a, threads(4), dev, stream);
