@@ -43,6 +43,7 @@ constexpr int kCodeBytes = kRows * 128;    // a code tile: 256 k (two stages) of
 constexpr int kDecodeWarps = 16, kStageWarps = 4;    // a stage's weights are made by four warps
 constexpr int kScaleWarps = 4, kScaleGroups = 16;    // 32 bytes of a row's scales (and of its biases) are loaded at once
 constexpr int kStoreWarps = 4;
+constexpr int kMostParts = 8;                       // of a tile's k, a CTA each
 constexpr int kThreads = 32 * (4 + kDecodeWarps + kScaleWarps + kStoreWarps);
 
 // Of tensor memory's 512 columns two D buffers take 2 NB, A slots of 64 the others.
@@ -538,15 +539,19 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                     float* part_sums = reinterpret_cast<float*>(smem) + c * kRows + 32 * quarter + lane;
 #pragma unroll
                     for (int j = 0; j < kStep; ++j) part_sums[j * kRows] = __uint_as_float(v[j / 16][j % 16]);
-                } else if (n < a.N) {
+                } else {
+                    if (a.x_scales != nullptr) {
+                        const float s = lane < kStep && m0 + c + lane < a.M ? __ldg(a.x_scales + m0 + c + lane) : 0.0f;
 #pragma unroll
-                    for (int j = 0; j < kStep; ++j) {
-                        const int m = m0 + c + j;
-                        if (m >= a.M) break;
-                        float y = __uint_as_float(v[j / 16][j % 16]);
-                        if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m);
-                        a.out[static_cast<size_t>(m) * a.N + n] = bf16_bits_rn(y);
+                        for (int j = 0; j < kStep; ++j)
+                            v[j / 16][j % 16] = __float_as_uint(__uint_as_float(v[j / 16][j % 16]) * __shfl_sync(0xffffffffu, s, j));
                     }
+                    // all of the rows that there are, without a branch between two stores
+                    const int rows = n < a.N ? a.M - m0 - c : 0;
+                    uint16_t* to = a.out + static_cast<size_t>(m0 + c) * a.N + n;
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j, to += a.N)
+                        if (j < rows) *to = bf16_bits_rn(__uint_as_float(v[j / 16][j % 16]));
                 }
             }
         }
@@ -556,14 +561,30 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
         const int m0 = tile0 % a.m_tiles * NB, n0 = tile0 / a.m_tiles * kRows;
-        const int row = threadIdx.x % kRows;
-        constexpr int kStride = kThreads / kRows;
-        float* mine = reinterpret_cast<float*>(smem);
-        for (int col = part * kStride + threadIdx.x / kRows; col < NB && m0 + col < a.M; col += kStride * a.parts) {
-            float y = 0.0f;
-            for (int r = 0; r < a.parts; ++r) y += cluster.map_shared_rank(mine, r)[col * kRows + row];
-            if (a.x_scales != nullptr) y *= __ldg(a.x_scales + m0 + col);
-            if (n0 + row < a.N) a.out[static_cast<size_t>(m0 + col) * a.N + n0 + row] = bf16_bits_rn(y);
+        // a warp a column, four rows a lane; all parts are on their way before the first is added
+        constexpr int kWarps = kThreads / 32;
+        const int row = 4 * lane;
+        const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
+        const float* mine = reinterpret_cast<const float*>(smem) + row;
+        for (int col = part * kWarps + warp; col < NB && m0 + col < a.M; col += kWarps * a.parts) {
+            float4 of[kMostParts];
+#pragma unroll
+            for (int r = 0; r < kMostParts; ++r)
+                if (r < a.parts) of[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(mine, r) + col * kRows);
+            const float s = a.x_scales != nullptr ? __ldg(a.x_scales + m0 + col) : 1.0f;
+            float4 y = of[0];
+#pragma unroll
+            for (int r = 1; r < kMostParts; ++r)
+                if (r < a.parts) y.x += of[r].x, y.y += of[r].y, y.z += of[r].z, y.w += of[r].w;
+            uint16_t* to = a.out + static_cast<size_t>(m0 + col) * a.N + n0 + row;
+            if (wide) {
+                if (n0 + row < a.N) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y.x * s, y.y * s), pack_bf16x2(y.z * s, y.w * s));
+            } else {
+                const float v[4] = {y.x * s, y.y * s, y.z * s, y.w * s};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n0 + row + i < a.N) to[i] = bf16_bits_rn(v[i]);
+            }
         }
         cluster.sync();                 // the others may still be reading this CTA's part
     }
@@ -628,7 +649,7 @@ cudaError_t launch_as(Q4Args a, const void* x, const DeviceInfo& dev, cudaStream
     // parts of k for clusters of CTAs, while all CTAs still run at once and each has two blocks of k or more
     const int blocks = (a.K + 2 * kStageK - 1) / (2 * kStageK);
     a.parts = 1;
-    while (a.parts < 8 && (a.parts + 1ll) * a.tiles <= (a.parts < 4 ? dev.num_sms : dev.num_sms / 2) && blocks >= 2 * (a.parts + 1)) ++a.parts;
+    while (a.parts < kMostParts && (a.parts + 1ll) * a.tiles <= (a.parts < 4 ? dev.num_sms : dev.num_sms / 2) && blocks >= 2 * (a.parts + 1)) ++a.parts;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.parts > 1 ? a.tiles * a.parts : (a.tiles < dev.num_sms ? a.tiles : dev.num_sms));
     cfg.blockDim = dim3(kThreads);
