@@ -646,10 +646,16 @@ cudaError_t launch_as(Q4Args a, const void* x, const DeviceInfo& dev, cudaStream
         return cudaErrorInvalidValue;
     a.m_tiles = (a.M + NB - 1) / NB;
     a.tiles = (a.N + kRows - 1) / kRows * a.m_tiles;
-    // parts of k for clusters of CTAs, while all CTAs still run at once and each has two blocks of k or more
-    const int blocks = (a.K + 2 * kStageK - 1) / (2 * kStageK);
+    // Parts of k for clusters of CTAs, while all CTAs still run at once.  The join takes about 2 us, of 128 rows more, so each part
+    // has two blocks of k or more (one row, K = 2048, N = 1024 in four parts 5.8 us, in one 7.8), of 128 rows five (512 rows, K = 2048,
+    // N = 1024 in two parts 10.6 us, in one 9.9; K = 5120 in four 13.0, in two 14.3), and K up to 1280 is not split (64 rows, K =
+    // N = 1024 in two parts 7.8 us, in one 6.1).  Clusters of more than four are placed less densely: half of the SMs (one row, K =
+    // 5120, N = 2560 in four parts 8.8 us, in seven 13.1).
+    const int blocks = (a.K + 2 * kStageK - 1) / (2 * kStageK), least = NB == 128 ? 5 : 2;
     a.parts = 1;
-    while (a.parts < kMostParts && (a.parts + 1ll) * a.tiles <= (a.parts < 4 ? dev.num_sms : dev.num_sms / 2) && blocks >= 2 * (a.parts + 1)) ++a.parts;
+    while (a.parts < kMostParts && (a.parts + 1ll) * a.tiles <= (a.parts < 4 ? dev.num_sms : dev.num_sms / 2) && blocks >= 6 &&
+           blocks >= least * (a.parts + 1))
+        ++a.parts;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.parts > 1 ? a.tiles * a.parts : (a.tiles < dev.num_sms ? a.tiles : dev.num_sms));
     cfg.blockDim = dim3(kThreads);
