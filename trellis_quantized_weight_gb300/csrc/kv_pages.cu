@@ -13,7 +13,7 @@
 //
 // All three are bound by latency but for the bytes that fork and compact copy: a growth of 5 tokens 4 us, of 64 prompts of
 // up to 16384 tokens 10.5 (one CTA: the scans need all needs and counts anyway, and more CTAs a barrier between them); a
-// fork of 24 x 4 beams 9.8 us with 27 MB of copies; compaction of 0.73 GB 249 us, 5.8 TB/s of the 6.7 that a copy reaches.
+// fork of 24 x 4 beams 9.8 us with 27 MB of copies; compaction of 0.73 GB 222 us, 6.6 TB/s of the 6.7 that a copy reaches.
 #include "kv_cache.cuh"
 #include "trellis.h"
 
@@ -527,7 +527,9 @@ int trellis_kv_compact(const int* refs, const int* kv_len, const int* pages, int
     const int chunks = rank_chunks(num_pages);
     cudaError_t e = launch_programmatic(kv_rank_kernel, static_cast<unsigned>(chunks), kThreads, 0, stream, a);
     if (e != cudaSuccess) return TRELLIS_ERR_CUDA;
-    const int most = num_pages > seqs ? num_pages : seqs, ctas = 8 * dev.num_sms;
+    // Many more CTAs than run at once (8 an SM): those that find free pages make room at once for others, and pages that are copied
+    // at the same time lie near each other.  0.73 GB with 8 CTAs an SM 250 us, 16 235, 32 226, 48 221.5, 96 the same.
+    const int most = num_pages > seqs ? num_pages : seqs, ctas = 48 * dev.num_sms;
     e = launch_programmatic(kv_compact_kernel, static_cast<unsigned>(most < ctas ? most : ctas), 256u, static_cast<size_t>(chunks) * 4,
                             stream, a, chunks);
     return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ERR_CUDA;
