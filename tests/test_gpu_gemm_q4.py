@@ -233,6 +233,27 @@ def test_on_two_streams_at_once():
         assert all(torch.equal(y, want[i]) for y in got[i])
 
 
+@pytest.mark.parametrize("M,group", [(1, 32), (3, 128), (40, 64), (200, 32)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_scales_around_a_quarter(M, group, bias):
+    """Weights are made in one of two ways, by the scales of 32 rows; both round the same number once."""
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(8)
+    codes, _, _ = weights(200, 1280, group, bias, g)
+    kinds = torch.tensor([0.0, 2.0 ** -20, 0.125, 0.2490234375, 0.25, -0.2490234375, -0.25, 0.375, 5.0]).bfloat16()
+    picked = torch.randint(0, 9, (200, 1280 // group), generator=g)
+    picked[32:64] = picked[32:64].clamp(max=3)                   # all of them below
+    picked[64:96] = picked[64:96].clamp(min=4)
+    scales = kinds[picked].cuda()
+    biases = (torch.randn(200, 1280 // group, generator=g) * scales.float().cpu() * 8).bfloat16().cuda() if bias else None
+    x = torch.randn(M, 1280, generator=g).bfloat16().cuda()
+    check(tq.gemm_q4(x, codes, scales, biases), *reference(x, codes, scales, biases), 1280)
+    one = torch.zeros(M, 1280).bfloat16().cuda()
+    one[:, 777] = 1                                              # a weight alone: exact
+    w = reference(torch.eye(1280)[777:778].bfloat16().cuda(), codes, scales, biases)[0]
+    assert torch.equal(tq.gemm_q4(one, codes, scales, biases).double(), w.expand(M, -1))
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -130, 2.0 ** -60, 2.0 ** 60])
 def test_small_and_large_scales(scale):
     """Weights below the normal numbers round as they are stored: to multiples of 2^-133."""
