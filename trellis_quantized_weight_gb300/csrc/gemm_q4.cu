@@ -402,7 +402,6 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 const uint32_t b_i = blocks_before + static_cast<uint32_t>((s - s0) >> 1), code = b_i % S::kCode;
                 const uint32_t run = runs_before + static_cast<uint32_t>(s - s0) / S::kScaleStages, run_slot = run % S::kScale;
                 alive = mbar_wait(bar(S::kBarCode + code), (b_i / S::kCode) & 1u) && mbar_wait(bar(S::kBarScale + run_slot), (run / S::kScale) & 1u);
-                if (!alive) break;
                 // scale, and bias above it, of each of the stage's groups; a row's are turned so that the rows of a quarter
                 // warp lie in different banks
                 uint32_t v[kPer];
@@ -420,7 +419,8 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 uint4 w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = lds128(at ^ (turned ^ (16 * j)));
-                alive = mbar_wait(bar(S::kBarEmpty + slot), parity);
+                // what follows needs all lanes: they go on, or none does
+                alive = __all_sync(0xffffffffu, alive && mbar_wait(bar(S::kBarEmpty + slot), parity));
                 if (!alive) break;
                 fence_after();
                 const uint32_t to = t_row + slot * 64;
@@ -547,10 +547,9 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                         load(s + f + kFar, x8[f]);
                     }
                 }
-                if (!alive) break;
             }
             const uint32_t t_row = taddr + (static_cast<uint32_t>(32 * quarter) << 16) + (d & 1u) * NB;
-            alive = mbar_wait(bar(S::kBarD + (d & 1u)), (d >> 1) & 1u);
+            alive = __all_sync(0xffffffffu, alive && mbar_wait(bar(S::kBarD + (d & 1u)), (d >> 1) & 1u));       // as the decoding warps
             if (!alive) break;
             fence_after();
 #pragma unroll 1
