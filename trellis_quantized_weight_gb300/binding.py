@@ -792,10 +792,12 @@ def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None)
     if M == 0:
         return out
     group = K // shape[1]
-    _launch((_lib or load()).trellis_gemm_q4,
-            (x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-             None if biases is None else biases.data_ptr(), M, K, N, group, out.data_ptr()), index, stream,
-            lambda: gemm_q4_workspace_bytes(M, K, N, group, x_scales is not None), ask=False)
+    fn, weights = (_lib or load()).trellis_gemm_q4, (codes.data_ptr(), scales.data_ptr(), None if biases is None else biases.data_ptr())
+    if x_scales is None:                            # no workspace
+        _enqueue(fn, (x.data_ptr(), None, *weights, M, K, N, group, out.data_ptr(), None, 0), index, stream)
+    else:
+        _launch(fn, (x.data_ptr(), x_scales.data_ptr(), *weights, M, K, N, group, out.data_ptr()), index, stream,
+                lambda: gemm_q4_workspace_bytes(M, K, N, group, True), ask=False)
     if stream is not None:
         _used_on(stream, x, x_scales, codes, scales, biases, out)
     return out

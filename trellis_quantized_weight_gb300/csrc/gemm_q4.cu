@@ -15,10 +15,10 @@
 // next to each other, so that their codes come from L2), its results leaving while the next tile is under way.
 // Where there are few tiles, a cluster of CTAs shares the k of one and adds its parts in shared memory, in order.
 //
-// Measured: 1999 rows, K = 5120, N = 17408 in groups of 128 202 to 206 us, 1.75 PFLOP/s, the tensor cores 89% busy; 64 rows in groups
-// of 32 with biases 18.8 us, one row in groups of 64 with biases 16.4 us (3.1 TB/s): start, first tile and end take 4.5 us of it, the decode
+// Measured: 1999 rows, K = 5120, N = 17408 in groups of 128 203 us, 1.75 PFLOP/s, the tensor cores 89% busy; 64 rows in groups
+// of 32 with biases 19.2 us, one row in groups of 64 with biases 16.2 us (3.1 TB/s): start, first tile and end take 4.5 us of it, the decode
 // 2 beyond what the copies hide, the rest is the codes' way from cold memory to 136 SMs.  Weights made in registers for mma.sync
-// instead, the k of a tile split over the warps of many small CTAs: 20 to 22 us at one row, 35 at 11 (here 21.1).
+// instead, the k of a tile split over the warps of many small CTAs: 20 to 22 us at one row, 35 at 11 (here 21.0).
 #include <cuda.h>
 #include <cooperative_groups.h>
 #include <mutex>
