@@ -123,6 +123,9 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
 }
+// For a whole warp whose lanes go on together, or none does: a wait may run out for some of them only, and those that were left
+// would meet another warp barrier, or arrive for the others.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -369,9 +372,9 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         uint32_t slot = 0, turn = 0, d = 0;
         for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
             const uint32_t td = taddr + (d & 1u) * NB;
-            alive = mbar_wait(bar(S::kBarDEmpty + (d & 1u)), ((d >> 1) & 1u) ^ 1u);
+            alive = mbar_wait_warp(bar(S::kBarDEmpty + (d & 1u)), ((d >> 1) & 1u) ^ 1u);
             for (int s = s0; s < s1 && alive; ++s) {
-                alive = mbar_wait(bar(S::kBarFull + slot), turn);
+                alive = mbar_wait_warp(bar(S::kBarFull + slot), turn);
                 if (!alive) break;
                 fence_after();
                 mma_stage<NB>(td, t_a + slot * 64, desc0 + static_cast<uint64_t>(slot * (S::kXBytes >> 4)), S::kInstr, s > s0 ? 1u : 0u, elected);
@@ -482,7 +485,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
             for (int run = 0; run < runs; ++run, ++i) {
                 const uint32_t slot = i % S::kScale;
-                alive = mbar_wait(bar(S::kBarScaleEmpty + slot), ((i / S::kScale) & 1u) ^ 1u);
+                alive = mbar_wait_warp(bar(S::kBarScaleEmpty + slot), ((i / S::kScale) & 1u) ^ 1u);
                 if (!alive) break;
                 uint32_t* to = reinterpret_cast<uint32_t*>(smem + S::kOffScale + slot * S::kScaleBytes);
 #pragma unroll
@@ -529,7 +532,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
 #pragma unroll
                     for (int f = 0; f < kFar; ++f) {
                         if (s + f >= s1) break;
-                        alive = mbar_wait(bar(S::kBarEmpty + x_slot), x_turn);
+                        alive = mbar_wait_warp(bar(S::kBarEmpty + x_slot), x_turn);
                         if (!alive) break;
                         // where the tensor copies put bf16 tiles: boxes of 64 k, rows of 128 bytes, their pieces of 16 turned by the row
                         const uint32_t to = sbase + S::kOffX + x_slot * S::kXBytes + (x_chunk >> 2) * (NB * 128);
