@@ -19,14 +19,16 @@ def test_waits_of_whole_warps_are_agreed_on():
     roles = re.split(r"\n    \} else if \(warp\b", kernel[kernel.index("bool alive = true;"):])
     assert len(roles) == 6
     for role in roles:
-        single = "lane == 0) {\n            uint32_t i = 0;" in role
-        open_wait = False
+        if "lane == 0) {\n            uint32_t i = 0;" in role:
+            continue
+        open_wait = stays = False
         for line in role.split("\n"):
-            if single:
-                break
             if "__all_sync(0xffffffffu, alive" in line or "mbar_wait_warp(" in line:
-                open_wait = False
+                open_wait = stays = False
+            elif "alive &= mbar_try(" in line:               # goes on with the others, whatever came of it
+                stays = True
             elif "mbar_wait(" in line and "(void)" not in line:
                 open_wait = True
             elif re.search(r"__syncwarp|_sync\(|tmem_|tcgen05|mbar_arrive|mma_|fence_", line):
                 assert not open_wait, line
+            assert not (stays and re.search(r"!alive|&& alive|break;\n", line)), line

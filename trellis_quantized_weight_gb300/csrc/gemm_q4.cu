@@ -528,12 +528,13 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
             if constexpr (kEight) {
 #pragma unroll
                 for (int f = 0; f < kFar; ++f) load(s0 + f, x8[f]);
-                for (int s = s0; s < s1 && alive; s += kFar) {
+                for (int s = s0; s < s1; s += kFar) {
 #pragma unroll
                     for (int f = 0; f < kFar; ++f) {
                         if (s + f >= s1) break;
-                        alive = mbar_wait_warp(bar(S::kBarEmpty + x_slot), x_turn);
-                        if (!alive) break;
+                        // No lane leaves before the vote below, so that all meet at the warp barrier; one whose wait ran out waits no
+                        // more (a vote here: 11 rows 21.2 -> 21.6 us).
+                        alive &= mbar_try(bar(S::kBarEmpty + x_slot), x_turn) || (alive && mbar_wait_long(bar(S::kBarEmpty + x_slot), x_turn));
                         // where the tensor copies put bf16 tiles: boxes of 64 k, rows of 128 bytes, their pieces of 16 turned by the row
                         const uint32_t to = sbase + S::kOffX + x_slot * S::kXBytes + (x_chunk >> 2) * (NB * 128);
 #pragma unroll
