@@ -544,11 +544,15 @@ TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const ui
  *
  *   codes   device, uint32 [N, K / 8], 16-byte aligned: eight codes c a word, the first in the lowest bits.
  *   scales  device, bf16 [N, K / group]; biases the same, or NULL.
- *           w = bf16(scale * c + bias), or bf16(scale * (c - 8)) without biases: one rounding of each weight.
+ *           w = bf16(scale * c + bias), or bf16(scale * (c - 8)) without biases: one rounding of each weight, by at most 2^-8
+ *           of it.  Groups that lie far from zero, |bias| > 32 |scale| (and |scale| >= 2^-126), keep what their codes say:
+ *           there w is the sum of o = bf16(bias + 8 scale) and bf16(scale * c + (bias - o)), which is within 2^-4 |scale| of
+ *           scale * c + bias.
  *   x       device, 16-byte aligned: bf16 [M, K] (x_scales NULL), or e4m3 bytes [M, K] with
  *   x_scales  float [M]: x = code * x_scale, as trellis_rms_norm writes them.
  *   out     device, bf16 [M, N], rounded once from fp32 sums; it must not overlap x (TRELLIS_ERR_SHAPE).
- * Products are exact, sums fp32.  |scale| below 2^120.  A row of x that holds an infinity or a NaN has no finite output, and no other row
+ * Products are exact, sums fp32.  |scale| below 2^120.  Stages of k with groups far from zero take two products (on a run of 16
+ * groups in 128 rows, if one of them is).  A row of x that holds an infinity or a NaN has no finite output, and no other row
  * feels it.
  * group: 32, 64 or 128; K a multiple of it, K and N up to 2^20, M up to 65536 (0: nothing is enqueued).
  *   workspace  256-byte aligned, at least trellis_gemm_q4_workspace_size bytes (NULL where that is 0: for bf16

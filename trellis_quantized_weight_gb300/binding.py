@@ -773,7 +773,8 @@ def gemm_q4(x, codes, scales, biases=None, x_scales=None, out=None, stream=None)
 
     codes: int32 [N, K / 8], eight codes a word, the first in the lowest bits; scales (and biases): bf16
     [N, K / group], group 32, 64 or 128.  A weight is scale * code + bias, or scale * (code - 8) without biases,
-    rounded once to bf16.
+    rounded once to bf16; where |bias| > 32 |scale| in two parts, so that the rounding is not of the bias' size but within
+    2^-4 |scale|.
     x: bf16, or float8_e4m3fn with x_scales float32 [M], as rms_norm_q8 returns them."""
     Tensor, bf16, f32, i32, f8 = (_types or _torch_types())[:5]
     if not isinstance(x, Tensor):

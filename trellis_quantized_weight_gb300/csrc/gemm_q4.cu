@@ -7,6 +7,11 @@
 // weight.  (Kept exact instead, with each group's sum scaled in fp32 on its way out of tensor memory, the
 // product took 328 us at 2000 rows of K = 5120, N = 17408 in groups of 128, 1426 us in groups of 32 with
 // biases; the group sums, not the products, were what it waited for.)
+// That rounding is one of 2^-8 of the weight.  Where |bias| > 32 |scale| it would be more than 1% of what the codes
+// say, and all of that in the end, so there a stage has two products: of
+//   bf16(scale c + r), r = bias - o, o = bf16(bias + 8 scale), and of o, the same for all of a group,
+// the second one's weights written when the first one is done.  |r| <= 16 |scale|, since bias is a bf16 number too, and r is one:
+// both numbers are multiples of the last bit of the smaller, which is above 2^-8 of that, and so 2^-4 of the scale.
 //
 // A CTA's warps: one loads code tiles, one activation tiles, one issues the products, one keeps tensor
 // memory, 4 load scales and biases, 16 turn codes into weights in tensor memory (the products' first operand), 4 store results
@@ -41,6 +46,7 @@ constexpr int kStageK = 128;               // k of a stage
 constexpr int kCodeBytes = kRows * 128;    // a code tile: 256 k (two stages) of 128 rows
 
 constexpr int kDecodeWarps = 16, kStageWarps = 4;    // a stage's weights are made by four warps
+constexpr int kStageGroups = kDecodeWarps / kStageWarps;
 constexpr int kScaleWarps = 4, kScaleGroups = 16;    // 32 bytes of a row's scales (and of its biases) are loaded at once
 constexpr int kStoreWarps = 4;
 constexpr int kMostParts = 8;                       // of a tile's k, a CTA each
@@ -56,11 +62,17 @@ struct Q4Shape {
     static constexpr int kScaleBytes = kRows * kScaleGroups * 4, kScale = 2;
     static constexpr int kOffX = 0, kOffScale = kA * kXBytes, kOffCode = kOffScale + kScale * kScaleBytes;
     static constexpr int kCode = 4;                                 // code tiles under way (6 and 8 take 0.3 to 0.7 us more: the first ones come later)
-    static constexpr int kOffBar = kOffCode + kCode * kCodeBytes;
+    static constexpr int kOffOffset = kOffCode + kCode * kCodeBytes;    // bf16, of groups far from zero
+    static constexpr int kOffBar = kOffOffset + kScale * kRows * kScaleGroups * 2;
     static constexpr int kBarFull = 0, kBarEmpty = kA, kBarCode = 2 * kA, kBarCodeEmpty = kBarCode + kCode;
     static constexpr int kBarD = kBarCodeEmpty + kCode, kBarDEmpty = kBarD + 2;
-    static constexpr int kBarScale = kBarDEmpty + 2, kBarScaleEmpty = kBarScale + kScale, kBars = kBarScaleEmpty + kScale;
-    static constexpr int kOffTaddr = kOffBar + 8 * kBars;
+    static constexpr int kBarScale = kBarDEmpty + 2, kBarScaleEmpty = kBarScale + kScale;
+    // a stage's second product: the first one is done, the second one's weights are there (one of each for the warps that made them)
+    static constexpr int kBarFirst = kBarScaleEmpty + kScale, kBarSecond = kBarFirst + kStageGroups, kBars = kBarSecond + kStageGroups;
+    // Of a run of scales: whether groups lie far from zero, a byte for 32 rows.  The products read it after the run's slot went to
+    // others, kA stages after the weights were made at most, which is up to three runs of two stages: with the two slots' five.
+    static constexpr int kFarRing = 8, kOffFar = kOffBar + 8 * kBars;
+    static constexpr int kOffTaddr = kOffFar + kFarRing * 4;
     static constexpr int kSmem = kOffTaddr + 16 + 1024;             // the base is rounded up to 1 KB
     static constexpr uint32_t kInstr = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NB >> 3) << 17) |
                                        (static_cast<uint32_t>(kRows >> 4) << 24);
@@ -180,6 +192,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
                  :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
                     "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -234,6 +251,28 @@ __device__ __forceinline__ uint32_t scale64_of(uint32_t v) {
     return r;
 }
 
+// A group's scale and, above it, its bias: whether the bias is far from zero, and its part that is left to the second product.
+// Groups of one value (scale 0) are exact as they are; next to the largest number, and where a bias is no number, nothing is parted.
+__device__ __forceinline__ bool is_far(uint32_t sb) {
+    const float s = fabsf(__uint_as_float(sb << 16)), b = fabsf(__uint_as_float(sb & 0xffff0000u));
+    return b > 32.0f * s && s > 0.0f && b < 8.507059173023462e37f;         // 2^126
+}
+// A bound that takes three instructions: |bias|'s bits less |scale|'s, above those of the scale.  Bits count as the logarithm does, 128 for
+// a factor of two, but for 0.086 of that at most, so a far one is never below 5 * 128 - 12.
+constexpr int kNearly = (5 * 128 - 12) << 16;
+__device__ __forceinline__ int distance_of(uint32_t sb) { return static_cast<int>((sb & 0x7fff7fffu) * (1u - 65536u)); }
+__device__ __forceinline__ uint32_t offset_of(uint32_t sb) {               // in both halves
+    uint32_t o;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o) : "r"(__byte_perm(sb, 0u, 0x1010)), "r"(0x41004100u), "r"(__byte_perm(sb, 0u, 0x3232)));
+    return is_far(sb) ? o : 0u;
+}
+// The group as the first product has it: its bias less that.
+__device__ __forceinline__ uint32_t without_offset(uint32_t sb, uint32_t offset) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(sb, 0u, 0x3232)), "r"(offset));
+    return __byte_perm(sb, r, 0x5410);
+}
+
 // Eight e4m3 codes as bf16, exactly.
 __device__ __forceinline__ uint4 widened(uint2 v) {
     uint32_t f[4], r[4];
@@ -281,6 +320,10 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         for (int i = 0; i < S::kScale; ++i) {
             mbar_init(bar(S::kBarScale + i), kScaleWarps);
             mbar_init(bar(S::kBarScaleEmpty + i), kStageWarps * S::kScaleStages);
+        }
+        for (int i = 0; i < kStageGroups; ++i) {
+            mbar_init(bar(S::kBarFirst + i), 1);
+            mbar_init(bar(S::kBarSecond + i), kStageWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -370,7 +413,10 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         const uint32_t elected = elect_lane();
         const uint64_t desc0 = smem_desc(sbase + S::kOffX);
         uint32_t slot = 0, turn = 0, d = 0;
-        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
+        uint32_t group = 0, seconds = 0;            // of the warps that made the stage, and their second products' parities
+        uint32_t runs_before = 0;
+        const uint32_t runs = (s1 - s0 + S::kScaleStages - 1) / S::kScaleStages;
+        for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d, runs_before += runs) {
             const uint32_t td = taddr + (d & 1u) * NB;
             alive = mbar_wait_warp(bar(S::kBarDEmpty + (d & 1u)), ((d >> 1) & 1u) ^ 1u);
             for (int s = s0; s < s1 && alive; ++s) {
@@ -378,6 +424,18 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 if (!alive) break;
                 fence_after();
                 mma_stage<NB>(td, t_a + slot * 64, desc0 + static_cast<uint64_t>(slot * (S::kXBytes >> 4)), S::kInstr, s > s0 ? 1u : 0u, elected);
+                if constexpr (kBias) {
+                    const uint32_t run = runs_before + static_cast<uint32_t>(s - s0) / S::kScaleStages;
+                    if (__any_sync(0xffffffffu, lds32(sbase + S::kOffFar + run % S::kFarRing * 4) != 0u)) {
+                        mma_commit(bar(S::kBarFirst + group), elected);
+                        alive = mbar_wait_warp(bar(S::kBarSecond + group), (seconds >> group) & 1u);
+                        if (!alive) break;
+                        seconds ^= 1u << group;
+                        fence_after();
+                        mma_stage<NB>(td, t_a + slot * 64, desc0 + static_cast<uint64_t>(slot * (S::kXBytes >> 4)), S::kInstr, 1u, elected);
+                    }
+                    group = (group + 1) % kStageGroups;
+                }
                 mma_commit(bar(S::kBarEmpty + slot), elected);
                 if (++slot == S::kA) { slot = 0; turn ^= 1u; }
             }
@@ -388,7 +446,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
     } else if (warp >= 4 && warp < 4 + kDecodeWarps) {
         // ---------------------------------------------------------------- codes to weights
         // 32 rows (a lane's row is its lane of tensor memory) of every fourth stage
-        constexpr int kGroups = kDecodeWarps / kStageWarps;
+        constexpr int kGroups = kStageGroups;
         static_assert(S::kA >= kGroups, "a slot for each four warps");
         const int quarter = warp & 3, group = (warp - 4) >> 2;
         const int row = 32 * quarter + lane;
@@ -396,6 +454,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         const uint32_t row_at = sbase + S::kOffCode + row * 128, turned = static_cast<uint32_t>(row & 7) << 4;
         constexpr int kPer = S::kPer;
         uint32_t slot = group, parity = 1u;                          // of its next stage
+        uint32_t firsts = 0;                                         // parity of its next stage with two products
         int ahead = group;                                           // stages from this tile's first to it
         uint32_t blocks_before = 0, runs_before = 0;
         const uint32_t runs = (s1 - s0 + S::kScaleStages - 1) / S::kScaleStages;
@@ -422,6 +481,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 uint4 w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = lds128(at ^ (turned ^ (16 * j)));
+                const uint32_t far = kBias ? lds32(sbase + S::kOffFar + run % S::kFarRing * 4) : 0u;
                 // what follows needs all lanes: they go on, or none does
                 alive = __all_sync(0xffffffffu, alive && mbar_wait(bar(S::kBarEmpty + slot), parity));
                 if (!alive) break;
@@ -450,10 +510,29 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 fence_before();
                 __syncwarp();
+                if (far != 0u) {                     // of any of the 128 rows
+                    if (lane == 0) mbar_arrive(bar(S::kBarFull + slot));
+                    alive = mbar_wait_warp(bar(S::kBarFirst + group), firsts);
+                    if (!alive) break;
+                    firsts ^= 1u;
+                    fence_after();
+                    // offsets stand only where some of these 32 rows have one
+                    const uint32_t mine = (far >> (8 * quarter)) & 1u ? 0x10001u : 0u;
+                    const volatile uint16_t* offsets = reinterpret_cast<const volatile uint16_t*>(smem + S::kOffOffset) + (run_slot * kRows + row) * kScaleGroups;
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t o = offsets[scale_column(row, static_cast<int>(static_cast<uint32_t>(s - s0) % S::kScaleStages * kPer) + j * kPer / 4)] * mine;
+                        const uint32_t p[16] = {o, o, o, o, o, o, o, o, o, o, o, o, o, o, o, o};
+                        tmem_st16(to + 16 * j, p);
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    fence_before();
+                    __syncwarp();
+                }
                 // Codes and scales make room only now that the weights made of them are stored, so that their loads are known to
                 // be over: given back right after the loads were issued, now and then they were those of the next tile in the slot.
                 if (lane == 0) {
-                    mbar_arrive(bar(S::kBarFull + slot));
+                    mbar_arrive(far != 0u ? bar(S::kBarSecond + group) : bar(S::kBarFull + slot));
                     mbar_arrive(bar(S::kBarScaleEmpty + run_slot));
                     mbar_arrive(bar(S::kBarCodeEmpty + code));
                 }
@@ -485,8 +564,28 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         for (int tile = tile0; tile < a.tiles && alive; tile += tile_step) {
             for (int run = 0; run < runs; ++run, ++i) {
                 const uint32_t slot = i % S::kScale;
+                bool far = false;
+                if constexpr (kBias) {
+                    int most[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < kLoads; ++j) most[j % 4] = max(most[j % 4], distance_of(v[j]));
+                    far = __any_sync(0xffffffffu, max(max(most[0], most[1]), max(most[2], most[3])) >= kNearly);
+                }
                 alive = mbar_wait_warp(bar(S::kBarScaleEmpty + slot), ((i / S::kScale) & 1u) ^ 1u);
                 if (!alive) break;
+                if constexpr (kBias) {
+                    if (far) {
+                        uint16_t* offsets = reinterpret_cast<uint16_t*>(smem + S::kOffOffset) + slot * kRows * kScaleGroups;
+#pragma unroll
+                        for (int j = 0; j < kLoads; ++j) {
+                            const int r = first_row + 2 * j;
+                            const uint32_t o = offset_of(v[j]);
+                            offsets[r * kScaleGroups + scale_column(r, of)] = static_cast<uint16_t>(o);
+                            v[j] = without_offset(v[j], o);
+                        }
+                    }
+                    if (lane == 0) smem[S::kOffFar + i % S::kFarRing * 4 + warp - 4 - kDecodeWarps] = far;
+                }
                 uint32_t* to = reinterpret_cast<uint32_t*>(smem + S::kOffScale + slot * S::kScaleBytes);
 #pragma unroll
                 for (int j = 0; j < kLoads; ++j) {
