@@ -2,12 +2,13 @@
 // rounding to bf16, or to e4m3 with a scale a row, in one pass.
 //
 //   h = x + residual                     fp32, exact to one rounding; residual_out = bf16(h)
-//   y = h * rsqrt(mean(h^2) + eps) * w   from the unrounded h, sums in fp32
+//   y = h * rsqrt(mean(h^2) + eps) * w   from the unrounded h of any size, sums in fp32
 //   out = bf16(y), or codes = e4m3(y / s) with s = max(max|y| / 448, 2^-100)
 //
 // A row stays in registers between its two reductions (sum of squares and, for the
 // 8-bit form, max|h w|, which are taken together: y's maximum is the product's times
-// rsqrt) and its stores, so each value is read and written once.  Bound by HBM: 8165 rows of
+// rsqrt) and its stores (the 8-bit form takes its products with w a second time there, so that h is at hand where a
+// row's squares are past fp32), so each value is read and written once.  Bound by HBM: 8165 rows of
 // 5120 with a residual to 8 bits 47 us, 6.2 TB/s of the 6.7 that a copy reaches; 7812 rows
 // without one 29 us (4.1 TB/s) to 8 bits and 31 (5.2) to bf16: the chain load, sum, store of a
 // row, with as many rows in flight as there is room for.  One row of 5120: 2.5 us.
@@ -78,10 +79,19 @@ __device__ __forceinline__ void reduce(float& sum, uint32_t& most, float2* part)
     }
 }
 
+// Squares of bf16 values reach from 2^-266 to 2^256, fp32 from 2^-149 to 2^128.  Where a row's sum is past that, or eps is next to
+// nothing and the sum too (least), the squares are added again of the values times 2^-80 or 2^80, and those are what the factor is for.
+constexpr float kDown = 8.271806125530277e-25f, kUp = 1.2089258196146292e24f;              // 2^-80, 2^80
+constexpr float kTinyEps = 7.523163845262640e-37f;      // 2^-120: beside a larger one, what a sum of squares drops below 2^-149 is nothing
+constexpr float kLeastSum = 7.888609052210118e-31f;     // 2^-100
+__device__ __forceinline__ float least_sum(float eps) { return eps < kTinyEps ? kLeastSum : 0.0f; }
+__device__ __forceinline__ bool fits(float sum, float least) { return sum >= least && sum <= 3.0e38f; }
+
 // kVec: 8 values by one 16-byte access; otherwise single values, a thread apart.
 // kPer: units of 8 values that a thread holds.  kRing: rows under way, the one at work included (0: loaded when their turn comes).
+// Rows of a warp: five CTAs an SM (2000 x 40 heads of 128 to 8 bits 20.9 -> 20.6 us).
 template <int kPer, bool kVec, bool kWarpRow, bool kEight, int kThreads, int kRing>
-__global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, kWarpRow && kPer == 1 ? 5 : 1) rms_norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float2 part[2][32];
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
     const long long step = static_cast<long long>(gridDim.x) * (kWarpRow ? 8 : 1);
@@ -90,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
     auto at = [&](int i, int j) { return kVec ? 8 * (t + i * threads) + j : t + (8 * i + j) * threads; };
     griddep_wait();
     griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
+    const float least = least_sum(a.eps);
     uint4 w[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -188,16 +199,37 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sum2 = __ffma2_rn(h[i][j], h[i][j], sum2);
-                if constexpr (kEight) {
-                    h[i][j] = __fmul2_rn(h[i][j], g[j]);
-                    largest = most_of(largest, h[i][j]);
-                }
+                if constexpr (kEight) largest = most_of(largest, __fmul2_rn(h[i][j], g[j]));
             }
         }
         float sum = sum2.x + sum2.y;
         uint32_t most = magnitude(largest);
         reduce<kWarpRow>(sum, most, part[turn]);
-        const float factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps);
+        // all threads of the row have the same sum
+        float factor;
+        if (__builtin_expect(fits(sum, least), 1)) {
+            factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps);
+        } else {
+            const float times = sum < least ? kUp : kDown;
+            float2 again = make_float2(0.0f, 0.0f);
+            largest = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                float2 g[4];
+                if constexpr (kEight) bf16x8_to_f32(w[i], g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[i][j] = __fmul2_rn(h[i][j], make_float2(times, times));
+                    again = __ffma2_rn(h[i][j], h[i][j], again);
+                    if constexpr (kEight) largest = most_of(largest, __fmul2_rn(h[i][j], g[j]));
+                }
+            }
+            sum = again.x + again.y;
+            most = magnitude(largest);
+            if constexpr (!kWarpRow) __syncthreads();           // others may still be reading their parts
+            reduce<kWarpRow>(sum, most, part[turn]);
+            factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps * times * times);
+        }
         if constexpr (kEight) {
             const float s = row_scale(magnitude(__uint_as_float(most) * factor));
             float inv = factor / s;
@@ -212,8 +244,9 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
             for (int i = 0; i < kPer; ++i) {
                 uint32_t c[2];
                 float2 y[4];
+                bf16x8_to_f32(w[i], y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(h[i][j], make_float2(inv, inv));
+                for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(__fmul2_rn(h[i][j], y[j]), make_float2(inv, inv));
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     c[q] = static_cast<uint32_t>(f32_to_e4m3x2(y[2 * q].x, y[2 * q].y)) |
@@ -246,6 +279,7 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
     __shared__ float2 part[2][32];
     griddep_wait();
     griddep_launch_dependents();        // the next grid's start beside this one; it waits for the end before it reads
+    const float least = least_sum(a.eps);
     int turn = 0;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const long long token = row / a.heads, base = row * a.width;
@@ -262,7 +296,22 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
             if constexpr (kEight) most = max(most, magnitude(h * bf16_bits_to_f32(__ldg(a.weight + c))));
         }
         reduce<false>(sum, most, part[turn]);
-        const float factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps);
+        float factor, times = 1.0f;
+        if (fits(sum, least)) {
+            factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps);
+        } else {
+            times = sum < least ? kUp : kDown;
+            sum = 0.0f;
+            most = 0u;
+            for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
+                const float h = value(c) * times;
+                sum = fmaf(h, h, sum);
+                if constexpr (kEight) most = max(most, magnitude(h * bf16_bits_to_f32(__ldg(a.weight + c))));
+            }
+            __syncthreads();                                    // others may still be reading their parts
+            reduce<false>(sum, most, part[turn]);
+            factor = rsqrtf(sum / static_cast<float>(a.width) + a.eps * times * times);
+        }
         const float s = kEight ? row_scale(magnitude(__uint_as_float(most) * factor)) : 1.0f;
         float first = factor, inv = kEight ? factor / s : 1.0f;
         if (kEight) {
@@ -272,7 +321,7 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(const __grid_consta
                 first = 1.0f;
         }
         for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
-            const float h = value(c), w = bf16_bits_to_f32(__ldg(a.weight + c)), y = kEight ? h * w * first : h * first * w;
+            const float h = value(c), t = h * times, w = bf16_bits_to_f32(__ldg(a.weight + c)), y = kEight ? t * w * first : t * first * w;
             if (a.residual != nullptr) a.residual_out[base + c] = bf16_bits_rn(h);
             if constexpr (kEight)
                 a.codes[base + c] = static_cast<uint8_t>(f32_to_e4m3x2(y * inv, 0.0f));
@@ -318,6 +367,9 @@ cudaError_t launch_rows(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s
     // fewer rows: two units a thread (8165 rows this way 50 us, with one unit 64 to 68, with five 54)
     if (units <= 1024) return launch<2, kVec, kEight, false, 512>(a, threads(2), dev, stream);
     if (units <= 2048) return launch<2, kVec, kEight, false, 1024>(a, threads(2), dev, stream);
+    // a bound of fewer threads where that does: with 64 registers each more of the four units' values spill (2000 rows of 17408
+    // to 8 bits 53 us, with 80 44; to bf16 46 and 41)
+    if (threads(4) <= 768) return launch<4, kVec, kEight, false, 768>(a, threads(4), dev, stream);
     return launch<4, kVec, kEight, false, 1024>(a, threads(4), dev, stream);
 }
 
