@@ -533,7 +533,7 @@ TRELLIS_API int trellis_kv_pages_workspace_size(int seqs, int page_cols, int num
  * y is computed from h before its rounding, sums are fp32 and hold the squares of any h that fp32 holds (an h past that is
  * infinite).  With eps = 0 a row of zeros is NaN.  In the 8-bit form a row counts as not finite where |h * weight| passes 2^128 with
  * |h| below 2^64.  out or residual_out may be x (where that is
- * contiguous) or residual, but not each other; other overlaps are not allowed.  Any width up to 2^20;
+ * contiguous) or residual, but not each other; other overlaps of an output are refused (TRELLIS_ERR_SHAPE).  Any width up to 2^20;
  * widths and strides that are multiples of 8, with 16-byte aligned arrays, take wide accesses.
  * rows == 0 enqueues nothing.  One kernel is enqueued.
  */

@@ -375,6 +375,23 @@ cudaError_t launch_rows(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Bytes of an array: `rows` pieces of `n`, `step` apart.
+struct Span {
+    uintptr_t at;
+    unsigned long long n, step, rows;
+    Span(const void* p, unsigned long long n_, unsigned long long step_ = 0, unsigned long long rows_ = 1)
+        : at(reinterpret_cast<uintptr_t>(p)), n(p == nullptr ? 0 : n_), step(step_), rows(rows_) {}
+};
+// Whether the piece `one` and a piece of `of` share a byte.
+bool overlap(const Span& one, const Span& of) {
+    if (one.n == 0 || of.n == 0 || one.at + one.n <= of.at) return false;
+    if (one.at < of.at + of.n) return true;
+    // the last piece that begins before the end of `one`
+    if (of.rows == 1 || of.step == 0) return false;
+    const unsigned long long last = (one.at + one.n - 1 - of.at) / of.step, row = last < of.rows ? last : of.rows - 1;
+    return one.at < of.at + row * of.step + of.n;
+}
+
 }  // namespace
 
 }  // namespace trellis
@@ -394,6 +411,19 @@ extern "C" int trellis_rms_norm(const uint16_t* x, long long x_stride, const uin
         !aligned(scales, 4))
         return TRELLIS_ERR_ALIGN;
     if (rows == 0) return TRELLIS_OK;
+    // Outputs lie apart from each other and from the inputs; those of h's size may be x or residual, row on row.
+    const unsigned long long count = static_cast<unsigned long long>(rows) * heads * width, token = 2ull * heads * width;
+    const Span in[] = {{x, token, 2ull * x_stride, static_cast<unsigned long long>(rows)}, {residual, 2 * count}, {weight, 2ull * width}};
+    const Span written[] = {{out, 2 * count}, {residual_out, 2 * count}, {codes, count}, {scales, 4ull * rows * heads}};
+    const bool whole = rows == 1 || 2ull * x_stride == token;
+    for (int i = 0; i < 4; ++i) {
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(written[i], written[j])) return TRELLIS_ERR_SHAPE;
+        for (int j = 0; j < 3; ++j) {
+            const bool in_place = i < 2 && written[i].at == in[j].at && (j == 0 ? whole : j == 1);
+            if (!in_place && overlap(written[i], in[j])) return TRELLIS_ERR_SHAPE;
+        }
+    }
     DeviceInfo dev;
     const int rc = device_info(dev);
     if (rc != TRELLIS_OK) return rc;
