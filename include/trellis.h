@@ -552,7 +552,7 @@ TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const ui
  *           scale * c + bias.
  *   x       device, 16-byte aligned: bf16 [M, K] (x_scales NULL), or e4m3 bytes [M, K] with
  *   x_scales  float [M]: x = code * x_scale, as trellis_rms_norm writes them.
- *   out     device, bf16 [M, N], rounded once from fp32 sums; it must not overlap x (TRELLIS_ERR_SHAPE).
+ *   out     device, bf16 [M, N], rounded once from fp32 sums; it must not overlap an input (TRELLIS_ERR_SHAPE).
  * Products are exact, sums fp32.  |scale| below 2^120.  Stages of k with groups far from zero take two products (on a run of 16
  * groups in 128 rows, if one of them is).  A row of x that holds an infinity or a NaN has no finite output, and no other row
  * feels it.

@@ -31,3 +31,15 @@ APART = dict(NORM, x_stride=1024)                                     # tokens 2
     (dict(EIGHT, x_stride=2048), dict(scales=X + 3 * 4096))])
 def test_norm_refuses(lib, base, change):
     assert lib.trellis_rms_norm(*{**base, **change}.values()) == SHAPE
+
+
+# 3 rows of 256 and 50: x 1536 bytes (768 in 8 bits), codes 6400, scales and biases 400 each, out 300
+Q4 = dict(x=X, x_scales=0, codes=C, scales=S, biases=Z, M=3, K=256, N=50, group=64, out=Y, workspace=W, workspace_bytes=1 << 27, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(out=C), dict(out=C + 6398), dict(out=C - 298), dict(out=S), dict(out=S + 398), dict(out=Z - 2), dict(out=Z + 200),
+    dict(x_scales=R, out=R), dict(x_scales=R, out=R + 10), dict(x_scales=R, out=X + 766), dict(out=X + 1534),
+    dict(x_scales=R, M=33, out=R + 130)])
+def test_gemm_q4_refuses(lib, change):
+    assert lib.trellis_gemm_q4(*{**Q4, **change}.values()) == SHAPE

@@ -878,8 +878,12 @@ int trellis_gemm_q4(const void* x, const float* x_scales, const uint32_t* codes,
         return TRELLIS_ERR_ALIGN;
     if (M == 0) return TRELLIS_OK;
     const bool eight = x_scales != nullptr;
-    // tiles of x are read until the last result is stored
-    if (overlap(x, static_cast<size_t>(M) * K * (eight ? 1 : 2), out, static_cast<size_t>(M) * N * 2)) return TRELLIS_ERR_SHAPE;
+    // all of them are read until the last result is stored
+    const size_t out_bytes = static_cast<size_t>(M) * N * 2, group_bytes = static_cast<size_t>(N) * (K / group) * 2;
+    if (overlap(x, static_cast<size_t>(M) * K * (eight ? 1 : 2), out, out_bytes) || overlap(codes, static_cast<size_t>(N) * K / 2, out, out_bytes) ||
+        overlap(scales, group_bytes, out, out_bytes) || (biases != nullptr && overlap(biases, group_bytes, out, out_bytes)) ||
+        (eight && overlap(x_scales, static_cast<size_t>(M) * 4, out, out_bytes)))
+        return TRELLIS_ERR_SHAPE;
     const size_t need = workspace_bytes_of(M, K, eight);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return TRELLIS_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return TRELLIS_ERR_ALIGN;
