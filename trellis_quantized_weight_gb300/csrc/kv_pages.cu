@@ -354,8 +354,9 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
         const int len = max(a.kv_len[s], 0);
         const int have = static_cast<int>(min(pages_of(len, a.shift), static_cast<long long>(a.cols)));
         const size_t row = static_cast<size_t>(s) * a.cols;
+        // an entry that is no page in use has no place either: as page 0 it would be another sequence's
         int left = 0;
-        for (int c = threadIdx.x; c < have; c += 256) left |= place(a.pages[row + c]) >= a.room;
+        for (int c = threadIdx.x; c < have; c += 256) left |= static_cast<unsigned>(place(a.pages[row + c])) >= static_cast<unsigned>(a.room);
         left = __syncthreads_or(left);
         for (int c = threadIdx.x; c < a.cols; c += 256) {
             const int to = c < have ? place(a.pages[row + c]) : -1;
