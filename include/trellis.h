@@ -503,6 +503,8 @@ TRELLIS_API int trellis_kv_fork(int *refs, int *kv_len, int *pages, const int *p
  * num_pages_out pages, and the counts, lengths and table go with them.
  *   refs_out   int32 [num_pages_out]; kv_len_out int32 [seqs]; pages_out int32 [seqs, page_cols], 0 past a
  *              sequence's pages.
+ * A page that something else holds (counted once more) is moved as the others are: it becomes the page of its rank, the number
+ * of pages before it whose count is above 0.
  * Pages that the other cache has no room for are left behind; the sequences that name one, or that name what is no page in
  * use, come out with kv_len 0, no longer counted.  Pages past the last one in use are left as they were.  No output may
  * overlap an input or another output (TRELLIS_ERR_SHAPE).  Two kernels are enqueued.

@@ -30,3 +30,19 @@ def test_a_sequence_that_names_no_page_of_the_pool_ends(bad, col):
     # all sequences give up what they have: nothing is left, and nothing is counted below that
     assert tq.kv_grow(into, refs2, lens2, table2, ints([-100] * 4)).all()
     assert refs2.tolist() == [0] * 12
+
+
+def test_pages_held_elsewhere_move_to_their_rank():
+    """A page counted once more for its holder becomes the page of its rank among those in use."""
+    import trellis_quantized_weight_gb300 as tq
+    cache, into = tq.kv_cache(12, 2, 16, 64), tq.kv_cache(9, 2, 16, 64)
+    for t in cache:
+        t.view(torch.uint8)[:] = torch.randint(0, 256, t.view(torch.uint8).shape, device="cuda", dtype=torch.uint8)
+    refs = ints([0, 3, 0, 0, 1, 1, 0, 0, 2, 0, 1, 0])
+    held = torch.tensor([1, 5, 8, 10], device="cuda")                  # by no sequence, or by one more than their sequences
+    refs2, lens2, table2 = tq.kv_compact(cache, refs, ints([40, 17]), ints([[1, 4, 8], [1, 8, 0]]), into)
+    rank = (refs > 0).cumsum(0) - 1
+    assert lens2.tolist() == [40, 17] and table2.tolist() == [[0, 1, 3], [0, 3, 0]]
+    assert torch.equal(refs2[rank[held]], refs[held])
+    for a, b in zip(cache, into):
+        assert torch.equal(b.view(torch.uint8)[rank[held]], a.view(torch.uint8)[held])

@@ -682,7 +682,7 @@ def kv_fork(cache, refs, kv_len, pages, parents, stream=None):
 def kv_compact(cache, refs, kv_len, pages, into, stream=None):
     """Copy the pages in use, in their order, to the first pages of another cache (of the same heads, page
     size and head width).  Returns its (refs, kv_len, pages); the first cache and its arrays stay as they are.
-    Sequences that name a page which `into` has no
+    Page p becomes page (refs[:p] > 0).sum(), also for whatever else holds it.  Sequences that name a page which `into` has no
     room for, or what is no page in use, come out with kv_len 0."""
     (num_pages, hk, page, d), seqs, cols, index = _require_pool(cache, refs, kv_len, pages)
     shape, where = _require_codes(into)
