@@ -23,10 +23,10 @@ __global__ void __launch_bounds__(256) copy_groups_kernel(CopyBatch b) {
         const unsigned long long nv = n / 8;
         const uint4* s4 = reinterpret_cast<const uint4*>(src);
         uint4* d4 = reinterpret_cast<uint4*>(dst);
-        for (unsigned long long i = t0; i < nv; i += stride) d4[i] = s4[i];
+        for (unsigned long long i = t0; i < nv; i += stride) d4[i] = __ldca(s4 + i);
         done = nv * 8;
     }
-    for (unsigned long long i = done + t0; i < n; i += stride) dst[i] = src[i];
+    for (unsigned long long i = done + t0; i < n; i += stride) dst[i] = __ldca(src + i);
     griddep_launch_dependents();
 }
 

@@ -619,7 +619,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
             for (int i = 0; i < kPieces; ++i) {
                 const int m = x_row + 16 * i;
                 v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (s < s1 && k < a.K && m < a.M) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x8 + static_cast<size_t>(m) * a.K + k));
+                if (s < s1 && k < a.K && m < a.M) v[i] = *reinterpret_cast<const uint4*>(a.x8 + static_cast<size_t>(m) * a.K + k);
             }
         };
         for (int tile = tile0; tile < a.tiles && alive; tile += tile_step, ++d) {
@@ -674,7 +674,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
                     for (int j = 0; j < kStep; ++j) part_sums[j * kRows] = __uint_as_float(v[j / 16][j % 16]);
                 } else {
                     if (a.x_scales != nullptr) {
-                        const float s = lane < kStep && m0 + c + lane < a.M ? __ldg(a.x_scales + m0 + c + lane) : 0.0f;
+                        const float s = lane < kStep && m0 + c + lane < a.M ? a.x_scales[m0 + c + lane] : 0.0f;
 #pragma unroll
                         for (int j = 0; j < kStep; ++j)
                             v[j / 16][j % 16] = __float_as_uint(__uint_as_float(v[j / 16][j % 16]) * __shfl_sync(0xffffffffu, s, j));
@@ -704,7 +704,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
 #pragma unroll
             for (int r = 0; r < kMostParts; ++r)
                 if (r < a.parts) of[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(mine, r) + col * kRows);
-            const float s = a.x_scales != nullptr ? __ldg(a.x_scales + m0 + col) : 1.0f;
+            const float s = a.x_scales != nullptr ? a.x_scales[m0 + col] : 1.0f;
             float4 y = of[0];
 #pragma unroll
             for (int r = 1; r < kMostParts; ++r)
@@ -733,7 +733,7 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
 __global__ void __launch_bounds__(256) q4_widen_kernel(const uint8_t* x, long long count, uint16_t* x16) {
     griddep_wait();
     for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < count; e += static_cast<long long>(gridDim.x) * 256)
-        *reinterpret_cast<uint4*>(x16 + e * 8) = widened(__ldg(reinterpret_cast<const uint2*>(x) + e));
+        *reinterpret_cast<uint4*>(x16 + e * 8) = widened(reinterpret_cast<const uint2*>(x)[e]);
     griddep_launch_dependents();
 }
 

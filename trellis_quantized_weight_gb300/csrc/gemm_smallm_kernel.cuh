@@ -312,7 +312,8 @@ __device__ __forceinline__ void x_block_load(const uint16_t* __restrict__ x, int
         const int e = tid + i * C::NT;
         if (e < C::XV) {
             const int m = e >> 5, c8 = e & 31;
-            v[i] = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K + b * 256 + c8 * 8));
+            // not read-only: a kernel before this one may still be writing it when this grid starts
+            v[i] = __ldca(reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K + b * 256 + c8 * 8));
         }
     }
 }

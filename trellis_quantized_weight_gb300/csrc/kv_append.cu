@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) kv_append_kernel(con
                     for (int p = 0; p < kGroup; ++p) {
                         const int pos = first + (p0 + p) * kPer + sub;
                         raw[p] = make_uint4(0u, 0u, 0u, 0u);
-                        if (pos >= lo && pos < hi) raw[p] = __ldg(reinterpret_cast<const uint4*>(at));
+                        if (pos >= lo && pos < hi) raw[p] = *reinterpret_cast<const uint4*>(at);
                         at += kPer * stride;
                     }
                 };

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(Stream<D, NT>::kThreads, 1) kv_stream_kernel(c
             for (int j = 0; j < KJ; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    raw[nt][j][h] = live ? __ldg(row + 2 * (t + 4 * j) + h) : make_uint4(0u, 0u, 0u, 0u);
+                    raw[nt][j][h] = live ? row[2 * (t + 4 * j) + h] : make_uint4(0u, 0u, 0u, 0u);
         }
     };
     load_queries(walk.u);

@@ -119,7 +119,7 @@ struct Tile {
 
 __device__ __forceinline__ uint4 ldg_once(const uint8_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 // ---- PTX wrappers ------------------------------------------------------------------
@@ -525,9 +525,9 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
                     const int r = r0 + (i0 + i) * kPer, tok = r / a.group;
                     raw[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (tok < v.n)
-                        raw[i] = __ldg(reinterpret_cast<const uint4*>(
+                        raw[i] = reinterpret_cast<const uint4*>(
                             a.q + static_cast<size_t>(v.start + tok) * a.q_stride +
-                            (static_cast<size_t>(v.head) * a.group + (r - tok * a.group)) * D) + c);
+                            (static_cast<size_t>(v.head) * a.group + (r - tok * a.group)) * D)[c];
                 }
 #pragma unroll
                 for (int i = 0; i < kSide; ++i) {
@@ -841,8 +841,8 @@ kv_tile_kernel(const __grid_constant__ AttendArgs a, bool split, unsigned int it
 #pragma unroll
                 for (int p = 0; p < P; ++p) vraw[h][p] = ldg_once(src + (r8 + 8 * h) * D + p * 64);
             const size_t at = unit * (a.l.page_size / kKvBlock) + in_page / kKvBlock;
-            ks = __ldg(a.k_scales + at);
-            vs = __ldg(a.v_scales + at);
+            ks = a.k_scales[at];
+            vs = a.v_scales[at];
         };
         auto store_keys = [&] {
             const uint32_t kdst = sbase + T::kOffK + kst * T::kKPanels * T::kPanel;

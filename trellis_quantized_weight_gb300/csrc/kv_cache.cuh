@@ -33,9 +33,10 @@ struct Seq {
 
 // n <= 0: it has no rows, or a range that is not inside the packed tokens (nothing of it
 // is touched then).  Tokens past the page table are left out of `total`.  The three loads
-// do not wait for one another.
+// do not wait for one another.  (Ordinary loads, here and of the table: trellis_kv_grow may have written both just before,
+// while this grid already lived beside it, so they are not read-only for as long as it lives.)
 __device__ __forceinline__ Seq load_seq(const KvLayout& l, int s) {
-    const int b = __ldg(l.starts + s), e = __ldg(l.starts + s + 1), len = __ldg(l.kv_len + s);
+    const int b = l.starts[s], e = l.starts[s + 1], len = l.kv_len[s];
     const long long most = static_cast<long long>(l.page_cols) << l.page_shift;
     Seq q;
     q.start = b;
@@ -48,7 +49,7 @@ __device__ __forceinline__ Seq load_seq(const KvLayout& l, int s) {
 // Page of column c of sequence s, clamped into the pool: a wrong id reads or
 // writes a wrong page, never outside the cache.
 __device__ __forceinline__ int kv_page_id(const KvLayout& l, int s, int c) {
-    return __ldg(l.pages + static_cast<size_t>(s) * l.page_cols + c);
+    return l.pages[static_cast<size_t>(s) * l.page_cols + c];
 }
 __device__ __forceinline__ int kv_page_of_id(const KvLayout& l, int id) { return min(max(id, 0), l.num_pages - 1); }
 __device__ __forceinline__ int kv_page(const KvLayout& l, int s, int c) { return kv_page_of_id(l, kv_page_id(l, s, c)); }
