@@ -99,8 +99,8 @@ class Layer:
         self.down = Grouped.random(inner, hidden, group, device, g)
 
     def step(self, x, residual, *args, **kw):
-        """x: bf16 [tokens, hidden], what came before, still to be added to the stream `residual`, which is updated in place;
-        the rest as AttentionBlock.step takes it.  bf16 [tokens, hidden], to be added by what comes after."""
+        """x: bf16 [tokens, hidden], what came before, still to be added to the stream `residual`, which is updated in place
+        (in a first layer x is the tokens' embeddings and the stream is zeros); the rest as AttentionBlock.step takes it.  bf16 [tokens, hidden], to be added by what comes after."""
         n, _ = rms_norm(x, self.norms[0], residual=residual, residual_out=residual)
         y = self.block.step(n, *args, **kw)
         codes, scales, _ = rms_norm_q8(y, self.norms[1], residual=residual, residual_out=residual)
@@ -162,10 +162,12 @@ def main(argv=None):
 
     one, starts = torch.ones_like(slot), torch.arange(S * n + 1, device=dev).int()
     row = torch.randn(S * n, args.hidden, device=dev).bfloat16()
-    residual = torch.zeros_like(row)
+    residual = torch.empty_like(row)
 
     def decode():
         kv_grow(cache, refs, kv_len, pages, one)
+        if layer:
+            residual.zero_()                                              # a token's stream begins with its own row
         return run(row, residual, cache, starts, kv_len, pages, which, 1)
 
     stream = torch.cuda.Stream()
