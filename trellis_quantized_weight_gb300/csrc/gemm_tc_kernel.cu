@@ -152,6 +152,7 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uns
     return false;
 }
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) { return mbar_wait_for(bar, parity, kWaitNs); }
+__device__ __forceinline__ bool mbar_wait_unless(bool gave_up, uint32_t bar, uint32_t parity) { return !gave_up && mbar_wait(bar, parity); }
 __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -299,13 +300,15 @@ gemm_tc_kernel(const uint32_t* __restrict__ codes, const uint16_t* __restrict__ 
                 for (int q = 0; q < KB; ++q) ring[d][q] = 0u;
             }
         }
+        // A wait may run out for some lanes of a warp only.  Those go on with the others and wait no more, so that all meet at the
+        // warp barriers; they vote before the results.
         bool alive = true;
         uint32_t carry = 0u;   // word 4k of the block, for the odd stage
-        for (int i0 = 0; i0 < nstages && alive; i0 += D) {
+        for (int i0 = 0; i0 < nstages; i0 += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 const int i = i0 + d;
-                if (i >= nstages || !alive) break;
+                if (i >= nstages) break;
                 const int s = i % kTcStages;
                 const int pre = i + D - 1;
                 if (pre < nstages) tc_load_group<KB>(row_codes, ok, pre, gi, ring[(d + D - 1) % D]);
@@ -344,11 +347,10 @@ gemm_tc_kernel(const uint32_t* __restrict__ codes, const uint16_t* __restrict__ 
                     // one of their phases, slots 0 and 2 never, so no probe
                     // skips a phase of its barrier.
                     if ((d & 1) == 0 && i + 1 >= kTcStages)
-                        alive = mbar_wait(bar_empty + 8 * ((i + 1) % kTcStages), (((i + 1) / kTcStages) + 1) & 1);
+                        alive &= mbar_wait_unless(!alive, bar_empty + 8 * ((i + 1) % kTcStages), (((i + 1) / kTcStages) + 1) & 1);
                 } else {
-                    if (i >= kTcStages) alive = mbar_wait(bar_empty + 8 * s, ((i / kTcStages) + 1) & 1);
+                    if (i >= kTcStages) alive &= mbar_wait_unless(!alive, bar_empty + 8 * s, ((i / kTcStages) + 1) & 1);
                 }
-                if (!alive) break;
                 const uint32_t dst = sbase + kOffA + s * kABytes + a_row_off;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -371,7 +373,7 @@ gemm_tc_kernel(const uint32_t* __restrict__ codes, const uint16_t* __restrict__ 
         }
 
         // -------------------------------------------------------------- epilogue
-        const bool done = alive && mbar_wait(bar_done, 0);
+        const bool done = __all_sync(0xffffffffu, alive && mbar_wait(bar_done, 0));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         // warp w reads TMEM lanes 32*(w%4) .. +31 (its weight rows) and the
         // columns (activation rows) of quarter w/4, 16 at a time
@@ -671,9 +673,9 @@ gemm_tca_kernel(const uint16_t* __restrict__ scales, uint16_t* __restrict__ out,
             const bool probe_slot = 2 * b + 1 >= kS;
             const bool code_ready = mbar_try_wait(bar_code + 8 * c, static_cast<uint32_t>(cpar));
             const bool slot_ready = !probe_slot || mbar_try_wait(bar_empty + 8 * (se + 1), static_cast<uint32_t>(spar));
-            if (!code_ready) alive = mbar_wait(bar_code + 8 * c, static_cast<uint32_t>(cpar));
-            if (alive && !slot_ready) alive = mbar_wait(bar_empty + 8 * (se + 1), static_cast<uint32_t>(spar));
-            if (!alive) break;
+            // (a lane whose wait ran out goes on with the others and waits no more; they vote before the results)
+            if (!code_ready) alive &= mbar_wait_unless(!alive, bar_code + 8 * c, static_cast<uint32_t>(cpar));
+            if (!slot_ready) alive &= mbar_wait_unless(!alive, bar_empty + 8 * (se + 1), static_cast<uint32_t>(spar));
             const uint32_t rb = rb0 + static_cast<uint32_t>(c * S::kCodeBytes);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -725,7 +727,7 @@ gemm_tca_kernel(const uint16_t* __restrict__ scales, uint16_t* __restrict__ out,
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 
         // -------------------------------------------------------------- epilogue
-        const bool done = alive && mbar_wait(bar_done, 0);
+        const bool done = __all_sync(0xffffffffu, alive && mbar_wait(bar_done, 0));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const int sub = warp & 3, colq = warp >> 2;
 #pragma unroll
