@@ -46,3 +46,14 @@ def test_heads_in_place():
     x1, r1 = x.clone(), r.clone()
     tq.rms_norm(x1, w, residual=r1, residual_out=r1, out=x1)
     assert torch.equal(x1, want) and torch.equal(r1, stream)
+
+
+def test_rows_of_no_values_have_no_scale():
+    """The 8-bit form would hand out scales that nothing has written."""
+    import trellis_quantized_weight_gb300 as tq
+    none, w = torch.empty(4, 0).bfloat16().cuda(), torch.empty(0).bfloat16().cuda()
+    with pytest.raises(ValueError):
+        tq.rms_norm_q8(none, w)
+    assert tq.rms_norm(none, w).shape == (4, 0)
+    assert [t.shape for t in tq.rms_norm_q8(none[:0], w)] == [(0, 0), (0,)]
+    assert [t.shape for t in tq.rms_norm_q8(torch.empty(4, 0, 64).bfloat16().cuda(), torch.ones(64).bfloat16().cuda())] == [(4, 0, 64), (4, 0)]

@@ -729,6 +729,8 @@ def _norm(x, weight, eps, residual, residual_out, out, eight, stream):
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     if eight:
+        if width == 0 and rows * heads > 0:
+            raise ValueError("x: rows of no values have no scale")
         codes = _new(shape, _types[4], index, dev, stream)
         scales = _new(shape[:-1], f32, index, dev, stream)
         c_ptr, s_ptr = codes.data_ptr(), scales.data_ptr()
