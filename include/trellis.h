@@ -453,7 +453,7 @@ TRELLIS_API int trellis_lora_add_workspace_size(int M, int K, int N, int R, int 
  *
  *   refs    device, int32 [num_pages]: how many places of the table name each page; 0 is free.
  *           A new pool is all zeros.  A page that something else holds is kept from these calls
- *           by counting it once more.
+ *           by counting it once more (whole pages: a last one's free places still fill).
  *   kv_len, pages  as above; the table names a sequence's pages in its first
  *           ceil(kv_len / page_size) columns, the other columns mean nothing.
  * Free pages are handed out lowest first, to sequences in their order; those that a call gives
@@ -534,9 +534,10 @@ TRELLIS_API int trellis_kv_pages_workspace_size(int seqs, int page_cols, int num
  *   residual_out  bf16 [rows * heads, width]: h, rounded once.
  * y is computed from h before its rounding, sums are fp32 and hold the squares of any h that fp32 holds (an h past that is
  * infinite).  With eps = 0 a row of zeros is NaN.  In the 8-bit form a row counts as not finite where |h * weight| passes 2^128 with
- * |h| below 2^64.  out or residual_out may be x (where that is
- * contiguous) or residual, but not each other; other overlaps of an output are refused (TRELLIS_ERR_SHAPE).  Any width up to 2^20;
- * widths and strides that are multiples of 8, with 16-byte aligned arrays, take wide accesses.
+ * |h| below 2^64.
+ * out or residual_out may be x (where that is contiguous) or residual, but not each other; other overlaps of an output are refused
+ * (TRELLIS_ERR_SHAPE).  Any width up to 2^20; those up to 32768 that are multiples of 8 take wide accesses, with strides that are
+ * and 16-byte aligned arrays.
  * rows == 0 enqueues nothing.  One kernel is enqueued.
  */
 TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const uint16_t *residual,
@@ -555,9 +556,8 @@ TRELLIS_API int trellis_rms_norm(const uint16_t *x, long long x_stride, const ui
  *   x       device, 16-byte aligned: bf16 [M, K] (x_scales NULL), or e4m3 bytes [M, K] with
  *   x_scales  float [M]: x = code * x_scale, as trellis_rms_norm writes them.
  *   out     device, bf16 [M, N], rounded once from fp32 sums; it must not overlap an input (TRELLIS_ERR_SHAPE).
- * Products are exact, sums fp32.  |scale| below 2^120.  Stages of k with groups far from zero take two products (on a run of 16
- * groups in 128 rows, if one of them is).  A row of x that holds an infinity or a NaN has no finite output, and no other row
- * feels it.
+ * Products are exact, sums fp32.  |scale| below 2^120.  A group far from zero takes the stages of k of its run of 16 groups, in
+ * 128 rows, two products.  A row of x that holds an infinity or a NaN has no finite output, and no other row feels it.
  * group: 32, 64 or 128; K a multiple of it, K and N up to 2^20, M up to 65536 (0: nothing is enqueued).
  *   workspace  256-byte aligned, at least trellis_gemm_q4_workspace_size bytes (NULL where that is 0: for bf16
  *           activations, and up to 32 rows); its first 1 MiB is not touched, so a product's workspace will do.

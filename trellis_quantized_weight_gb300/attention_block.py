@@ -100,7 +100,8 @@ class Layer:
 
     def step(self, x, residual, *args, **kw):
         """x: bf16 [tokens, hidden], what came before, still to be added to the stream `residual`, which is updated in place
-        (in a first layer x is the tokens' embeddings and the stream is zeros); the rest as AttentionBlock.step takes it.  bf16 [tokens, hidden], to be added by what comes after."""
+        (in a first layer x is the tokens' embeddings and the stream is zeros); the rest as AttentionBlock.step takes it.
+        bf16 [tokens, hidden], to be added by what comes after."""
         n, _ = rms_norm(x, self.norms[0], residual=residual, residual_out=residual)
         y = self.block.step(n, *args, **kw)
         codes, scales, _ = rms_norm_q8(y, self.norms[1], residual=residual, residual_out=residual)

@@ -10,7 +10,9 @@
 // That rounding is one of 2^-8 of the weight.  Where |bias| > 32 |scale| it would be more than 1% of what the codes
 // say, and all of that in the end, so there a stage has two products: of
 //   bf16(scale c + r), r = bias - o, o = bf16(bias + 8 scale), and of o, the same for all of a group,
-// the second one's weights written when the first one is done.  |r| <= 16 |scale|, since bias is a bf16 number too, and r is one:
+// the second one's weights written when the first one is done.  To look at every group's scale and bias takes 0.3 us of 16.5 at one
+// row, 0.8 of 20 at 64 rows in groups of 32, 235 us instead of 219 at 1999; with all groups far from zero those take 37, 42
+// and 655 us, with one in 10000 28, 30 and 304.  |r| <= 16 |scale|, since bias is a bf16 number too, and r is one:
 // both numbers are multiples of the last bit of the smaller, which is above 2^-8 of that, and so 2^-4 of the scale.
 //
 // A CTA's warps: one loads code tiles, one activation tiles, one issues the products, one keeps tensor
@@ -20,10 +22,10 @@
 // next to each other, so that their codes come from L2), its results leaving while the next tile is under way.
 // Where there are few tiles, a cluster of CTAs shares the k of one and adds its parts in shared memory, in order.
 //
-// Measured: 1999 rows, K = 5120, N = 17408 in groups of 128 203 us, 1.75 PFLOP/s, the tensor cores 89% busy; 64 rows in groups
-// of 32 with biases 19.2 us, one row in groups of 64 with biases 16.2 us (3.1 TB/s): start, first tile and end take 4.5 us of it, the decode
+// Measured: 1999 rows, K = 5120, N = 17408 in groups of 128 205 us, 1.74 PFLOP/s, the tensor cores 86 to 89% busy; 64 rows in groups
+// of 32 with biases 20.0 us, one row in groups of 64 with biases 16.5 us (3.0 TB/s): start, first tile and end take 4.5 us of it, the decode
 // 2 beyond what the copies hide, the rest is the codes' way from cold memory to 136 SMs.  Weights made in registers for mma.sync
-// instead, the k of a tile split over the warps of many small CTAs: 20 to 22 us at one row, 35 at 11 (here 21.0).
+// instead, the k of a tile split over the warps of many small CTAs: 20 to 22 us at one row, 35 at 11 (here 21.3).
 #include <cuda.h>
 #include <cooperative_groups.h>
 #include <mutex>
@@ -227,8 +229,8 @@ __device__ __forceinline__ void weights_of(uint32_t w, uint32_t scale64, uint32_
 }
 // The same where scales are below 1/4, as those of a layer's weights are: a code three bits further up is c 2^-130, its product with
 // 2^130 of the scale is added to the bias (without biases to -8 times the scale, which is exact) in one rounding of the same number.
-// 12 instructions for eight weights, where the other takes 15: one row 16.8 -> 16.4 us, 64 rows 19.4 -> 18.8, 1999 in groups of 32
-// 226 -> 223.5.
+// 12 instructions for eight weights, where the other takes 15: 0.4 us of 16.5 at one row, 0.6 of 20 at 64, 2.5 of 235 at 1999
+// in groups of 32.
 __device__ __forceinline__ void weights_below(uint32_t w, uint32_t scale130, uint32_t bias, uint32_t* p) {
     const uint32_t even = (w << 3) & 0x78787878u, odd = (w >> 1) & 0x78787878u;
 #pragma unroll
@@ -365,12 +367,16 @@ q4_kernel(const __grid_constant__ Q4Args a, const __grid_constant__ CUtensorMap 
         }
     }
     griddep_wait();
-    griddep_launch_dependents();        // the next grid may set itself up meanwhile; it waits for this one's end before it reads
+    // The next grid may set itself up where an SM has no tile of this one (whose CTAs take all of tensor memory, and nearly all
+    // registers); it waits for this one's end before it reads.
+    griddep_launch_dependents();
 
     // Slots are taken in turn: use number i of a ring of n is slot i % n, its phase's parity (i / n) & 1.  A parity tells a
     // phase only from its neighbours, so whoever waits for use i has to know that use i - n is over.  The decoding warps,
     // which meet every fourth stage only, do because a tile has an even number of them: they meet every second code tile
-    // (of a ring of four), and go on by two runs of scales at most (of a ring of two, which is filled in order).
+    // (of a ring of four), and go on by two runs of scales at most (of a ring of two, which is filled in order).  Of the ring of
+    // operand slots a group has waited for the stage four before, four or six slots back from there; that the use before the one
+    // it waits for is over, it knows because commits arrive in the order of their products.
     bool alive = true;
     if (warp == 0) {
         // ---------------------------------------------------------------- code tiles

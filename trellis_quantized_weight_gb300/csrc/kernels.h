@@ -49,9 +49,10 @@ bool smem_opt_in(Kernel kernel, int bytes, std::atomic<unsigned long long>& done
 
 // Launch with programmatic stream serialization: the grid may begin while the
 // previous kernel on the stream is still draining.  Kernels launched this way
-// touch no global memory before griddepcontrol.wait, which returns once the
-// previous grid has completed and its writes are visible, so stream order is
-// kept for every input and output.
+// load and write no global memory before griddepcontrol.wait, which returns once
+// the previous grid has completed and its writes are visible, so stream order is
+// kept for every input and output.  Before it they may fill L2 ahead, and load
+// what no kernel writes (a second launch of one call: what the first has waited for).
 template <class... Params, class... Args>
 cudaError_t launch_programmatic_grid(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
                                      cudaStream_t stream, Args&&... args) {

@@ -8,10 +8,11 @@
 // A row stays in registers between its two reductions (sum of squares and, for the
 // 8-bit form, max|h w|, which are taken together: y's maximum is the product's times
 // rsqrt) and its stores (the 8-bit form takes its products with w a second time there, so that h is at hand where a
-// row's squares are past fp32), so each value is read and written once.  Bound by HBM: 8165 rows of
-// 5120 with a residual to 8 bits 47 us, 6.2 TB/s of the 6.7 that a copy reaches; 7812 rows
-// without one 29 us (4.1 TB/s) to 8 bits and 31 (5.2) to bf16: the chain load, sum, store of a
-// row, with as many rows in flight as there is room for.  One row of 5120: 2.5 us.
+// row's squares are past fp32), so each value is read and written once (rows past 32768 values twice, two bytes at a
+// time: 2000 of 40000 to bf16 233 us).  Bound by HBM: 8165 rows of 5120 with a residual to 8 bits 46.5 us, 6.3 TB/s of
+// the 6.7 that a copy reaches, to bf16 52.4 (6.4); without one 31.0 us (4.0 TB/s) to 8 bits and 32.5 (5.1) to bf16: the
+// chain load, sum, store of a row, with as many rows in flight as there is room for.  2000 tokens of 40 heads of 128: 18.4
+// us to bf16, 20.8 to 8 bits, by instructions (a warp a row).  One row of 5120: 2.5 us.
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "trellis.h"
@@ -359,8 +360,8 @@ cudaError_t launch_rows(const NormArgs& a, const DeviceInfo& dev, cudaStream_t s
     // few rows: one unit a thread where that fits, for the shortest chain
     if (a.rows < dev.num_sms && units <= kMostThreads) return launch<1, kVec, kEight, false, 1024>(a, threads(1), dev, stream);
     // Rows enough for a second one to be on its way while a CTA's first is at work: four units a thread, 1024 threads an SM.
-    // 8165 rows of 5120 with residual to 8 bits 45 us (50 without the second row, two units a thread; 59 with four); without
-    // a residual 27 against 34; two rows ahead 46 to 53.
+    // 8165 rows of 5120 with residual to 8 bits 46 us (50 without the second row, two units a thread; 59 with four); without
+    // a residual 31 against 34; two rows ahead 46 to 53.
     if constexpr (kVec)
         if (units <= 2048 && a.rows >= 2ll * (kAheadThreads / threads(4)) * dev.num_sms)
             return launch<4, kVec, kEight, false, 512, 2>(a, threads(4), dev, stream);
