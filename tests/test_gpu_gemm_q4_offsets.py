@@ -139,3 +139,29 @@ def test_biases_that_are_not_finite_stay_in_their_columns():
     keep[7] = keep[50] = False
     assert torch.equal(got[:, keep], want[:, keep])
     assert torch.all(got[:, 7] == float("inf")) and got[:, 50].isnan().all()
+
+
+def test_captured_and_on_two_streams_at_once():
+    import trellis_quantized_weight_gb300 as tq
+    g = torch.Generator().manual_seed(1)
+    jobs, want = [], []
+    for M, K, N, group in ((3, 5120, 1111, 32), (150, 1280, 3000, 64)):         # a cluster's parts, and whole tiles
+        codes, scales, biases = make(N, K, group, 500, g)
+        biases = torch.where((torch.rand(scales.shape, generator=g) < 0.05).cuda(), biases, (scales.float() * -7.5).bfloat16())
+        jobs.append((torch.randn(M, K, generator=g).bfloat16().cuda(), codes, scales, biases))
+        want.append(tq.gemm_q4(*jobs[-1]))
+    streams = [torch.cuda.Stream(priority=-1) for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[tq.gemm_q4(*jobs[i], stream=streams[i]) for i in range(2)] for _ in range(30)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for pair in got for y, w in zip(pair, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        out = [tq.gemm_q4(*job) for job in jobs]
+    for _ in range(5):
+        for y in out:
+            y.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(out, want))
